@@ -9,6 +9,8 @@
  *   dsa_int8_gemm       : standalone int8 GEMM + dequant to fp16
  *   dsa_mhc             : manifold-constrained hyper-connection mappings
  *   dsa_mla_prolog      : MLA Prolog (q_lora, absorbed query, latent KV rows)
+ *   dsa_kv4_write/_read : latent KV rows into a 4-bit cache, and back to bf16
+ *   dsa_sparse_attn_kv4 : the sparse attention over a 4-bit latent cache
  *
  * Page citations:
  *   [V3.2-PyPTO]  "NPU DeepSeek-V3.2-Exp PyPTO 融合算子开发优化实践",
@@ -42,7 +44,7 @@
  *     the call, which are read as soon as the kernel starts: the weights
  *     w_qb, w_k and w_proj of dsa_indexer_prolog, pos and seq_of_token of
  *     dsa_indexer_topk / dsa_indexer_scores, and q and seq_of_token of
- *     dsa_sparse_attn.  The
+ *     dsa_sparse_attn and dsa_sparse_attn_kv4.  The
  *     kernel enqueued just before such a call must not write them (an event
  *     or a memcpy in between lifts the rule).
  */
@@ -470,6 +472,109 @@ typedef struct {
 
 size_t dsa_mla_prolog_workspace(const dsa_mla_prolog_args* args);
 int dsa_mla_prolog(const dsa_mla_prolog_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 4-bit latent cache.  The pages keep the latent cache in bf16 (1152
+ * bytes a row); this library also reads and writes one whose 512 latent dims
+ * are held in 4 bits, 416 bytes (13 32-byte sectors) a row:
+ *
+ *   bytes   0..255  signed 4-bit codes: the four bytes 4j..4j+3 hold dims
+ *                   8j..8j+7, from the lowest nibble of the first byte:
+ *                   dims 0, 2, 4, 6, 1, 3, 5, 7 of the eight
+ *   bytes 256..287  a scale byte u for each 16 dims, scale =
+ *                   (1 + (u mod 8) / 8) * 2^(u div 8 - 15); u = 255: NaN
+ *   bytes 288..415  the 64 rotary dims, bf16
+ *
+ * A latent value is code * scale, a product of at most 7 significant bits:
+ * bf16 holds it exactly.  A row of zero bytes is a row of zeros.
+ *
+ * Quantiser, per group of 16 dims: a = max |x|; scale = a / 7 rounded to 4
+ * significant bits (nearest even), clamped to [2^-15, 1.75 * 2^16]; code =
+ * rint(clamp(x / scale, -7, 7)), ties to even.  Each value is held to within
+ * half a scale where 2^-15 <= a / 7 <= 1.75 * 2^16.  A group that holds a NaN
+ * or an infinity is stored as NaN (codes 0, u = 255).
+ *
+ * dsa_kv4_write: row i of x (bf16, rows x_stride elements apart) goes to row
+ * slot[i] of the cache.  slot int64 [n]: negative = not written; slots must
+ * not repeat; a slot >= cache_rows is recorded as DSA_ERR_DEVICE_DATA and
+ * that row is not written.  Rows that no slot names stay as they are.
+ * dsa_kv4_read: row i of out (bf16, rows out_stride elements apart; the
+ * columns past 576 stay as they are) receives row slot[i] of the cache.  A
+ * negative slot gives a row of zeros; so does a slot >= cache_rows, which is
+ * recorded as DSA_ERR_DEVICE_DATA.  Slots may repeat.
+ *
+ * Shapes: x, out bf16 [n, 576]; strides multiples of 8, >= 576; kv4 uint8
+ * [cache_rows, 416], cache_rows < 2^31; x, out and kv4 16-byte aligned.
+ * n = 0 is a no-op.  No workspace.  x and out must not overlap the cache.
+ * ---------------------------------------------------------------------- */
+#define DSA_KV4_ROW_BYTES 416
+
+typedef struct {
+  int32_t n;
+  int64_t x_stride;
+  const uint16_t* x;
+  uint8_t* kv4;
+  const int64_t* slot;
+  int64_t cache_rows;
+} dsa_kv4_write_args;
+
+typedef struct {
+  int32_t n;
+  int64_t out_stride;
+  const uint8_t* kv4;
+  const int64_t* slot;
+  int64_t cache_rows;
+  uint16_t* out;
+} dsa_kv4_read_args;
+
+int dsa_kv4_write(const dsa_kv4_write_args* args, void* stream);
+int dsa_kv4_read(const dsa_kv4_read_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Sparse MLA attention over the 4-bit latent cache: dsa_sparse_attn (same
+ * formulas, token layout, sink and lse) with the rows r_j dequantised.
+ *
+ * The products of q with a row and of the probabilities with its values take
+ * the row's values exactly; sums, softmax statistics and lse are fp32, the
+ * probabilities are rounded to bf16 before they meet the values (their sum is
+ * not), and the output is rounded once to bf16.  With several chunks of rows
+ * per token each chunk's partial output is held in bf16 between the two
+ * kernels.
+ *
+ * Shapes: q bf16 [T, H, 576]; kv4 uint8 contiguous [B, max_L, 416]
+ * (cache_rows >= B * max_L) or paged [cache_rows, 416] through block_table
+ * int32 [B, max_blocks], max_L = max_blocks * block_size, any block_size >= 1;
+ * topk_idx int32 [T, topk], entries outside [0, max_L) select nothing; out
+ * bf16 [T, H, 512]; lse fp32 [T, H] or NULL; sink fp32 [H] or NULL, entries
+ * finite or -inf; seq_of_token int32 [T] or NULL.  A selected row whose page
+ * entry is negative, or that lies past cache_rows, is recorded as
+ * DSA_ERR_DEVICE_DATA and reads as a row of zeros.  A token whose sequence lies
+ * outside [0, B) is recorded likewise and reads no row.  A row that nothing
+ * selects is never read.
+ * Supported: 1 <= T <= 65535, 1 <= H <= 1024, 1 <= topk <= 65536, scale
+ * positive and finite; q, kv4 and out 16-byte aligned.
+ * Workspace: dsa_sparse_attn_kv4_workspace() bytes (0 for some shapes),
+ * 256-byte aligned, never in use by two calls that may overlap.
+ * q and seq_of_token are read as soon as the kernel starts (see the note on
+ * programmatic dependent launch above).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t T, B, n_q, H, topk, max_L;
+  float scale;
+  const uint16_t* q;
+  const uint8_t* kv4;
+  int64_t cache_rows;
+  const int32_t* block_table;
+  int32_t block_size, max_blocks;
+  const int32_t* topk_idx;
+  uint16_t* out;
+  float* lse;
+  const float* sink;
+  const int32_t* seq_of_token;
+} dsa_attn_kv4_args;
+
+size_t dsa_sparse_attn_kv4_workspace(const dsa_attn_kv4_args* args);
+int dsa_sparse_attn_kv4(const dsa_attn_kv4_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -30,6 +30,7 @@ __all__ = [
     "indexer_dots", "indexer_scores_token", "topk_indices",
     "sparse_attention_token", "sparse_attention", "cache_rows", "logical_rows", "mhc",
     "rms_norm", "mla_q", "mla_kv", "mla_prolog",
+    "KV4_ROW", "kv4_scale", "kv4_quantise", "kv4_values",
 ]
 
 
@@ -426,3 +427,55 @@ def mla_prolog(p, kv_cache=None):
             if p.slot[t] >= 0:
                 kv_cache[p.slot[t]] = kv[t]
     return {"c_q": c_q, "q_lora": q_lora, "q_lora_scale": q_lora_scale, "q": q, "kv": kv}
+
+
+# ----------------------------------------------------------------------------
+# The 4-bit latent cache (no page has one; the definition is this project's)
+# ----------------------------------------------------------------------------
+KV4_ROW, KV4_GROUP = 416, 16
+KV4_NIBBLE_DIM = (0, 2, 4, 6, 1, 3, 5, 7)  # dim of each nibble of a 4-byte word, from the lowest
+
+
+def kv4_scale(u) -> np.ndarray:
+    """Scale of byte u: (1 + (u mod 8) / 8) 2^(u div 8 - 15); 255 is NaN."""
+    u = np.asarray(u, dtype=np.int64)
+    return np.where(u == 255, np.nan, np.ldexp(1.0 + (u % 8) / 8.0, u // 8 - 15))
+
+
+def kv4_quantise(x: np.ndarray) -> np.ndarray:
+    """Cache rows uint8 [n, 416] of latent rows x (raw bf16 bits uint16
+    [n, 576]): per 16 latent dims the largest |x| / 7 rounded to 4 significant
+    bits (half to even; clamped to [2^-15, 1.75 * 2^16]) is the scale, codes
+    are rint(x / scale) clamped to [-7, 7]; a group with a NaN or an infinity
+    has codes 0 and scale byte 255; the 64 rotary dims are copied."""
+    n = x.shape[0]
+    with np.errstate(invalid="ignore"):  # signalling NaNs
+        g = bf16_bits_to_f64(x[:, :512]).reshape(n, 32, KV4_GROUP)
+    amax = np.abs(g).max(axis=-1)
+    bad = ~np.isfinite(amax)
+    m, e = np.frexp(np.where(bad, 1.0, amax) / 7.0)  # amax / 7 = m 2^e, 1/2 <= m < 1
+    s = np.clip(np.ldexp(np.rint(m * 16.0), e - 4), 2.0 ** -15, 1.75 * 2.0 ** 16)
+    with np.errstate(invalid="ignore"):
+        q = np.clip(np.rint(g / s[..., None]), -7, 7)
+    code = np.where(bad[..., None], 0.0, q).astype(np.int64).reshape(n, 64, 8) & 15
+    word = np.zeros((n, 64), dtype=np.uint32)
+    for nibble, dim in enumerate(KV4_NIBBLE_DIM):
+        word |= (code[:, :, dim] << (4 * nibble)).astype(np.uint32)
+    m, e = np.frexp(s)
+    u = np.where(bad, 255, (e - 1 + 15) * 8 + np.rint(m * 16.0).astype(np.int64) - 8).astype(np.uint8)
+    rope = np.ascontiguousarray(x[:, 512:]).view(np.uint8).reshape(n, 128)
+    return np.concatenate([word.astype("<u4").view(np.uint8).reshape(n, 256), u, rope], axis=1)
+
+
+def kv4_values(rows: np.ndarray) -> np.ndarray:
+    """float64 [n, 576] values of cache rows uint8 [n, 416]."""
+    rows = np.ascontiguousarray(rows)
+    n = rows.shape[0]
+    word = np.ascontiguousarray(rows[:, :256]).view("<u4").astype(np.int64)
+    code = np.empty((n, 64, 8))
+    for nibble, dim in enumerate(KV4_NIBBLE_DIM):
+        c = (word >> (4 * nibble)) & 15
+        code[:, :, dim] = np.where(c >= 8, c - 16, c)
+    lat = code.reshape(n, 32, KV4_GROUP) * kv4_scale(rows[:, 256:288])[..., None]
+    rope = bf16_bits_to_f64(np.ascontiguousarray(rows[:, 288:]).view("<u2"))
+    return np.concatenate([lat.reshape(n, 512), rope], axis=1)

@@ -73,6 +73,25 @@ class MlaArgs(ctypes.Structure):
                 ("cache_rows", ctypes.c_int64)]
 
 
+class Kv4WriteArgs(ctypes.Structure):
+    _fields_ = [("n", c_int), ("x_stride", ctypes.c_int64), ("x", c_ptr), ("kv4", c_ptr), ("slot", c_ptr),
+                ("cache_rows", ctypes.c_int64)]
+
+
+class Kv4ReadArgs(ctypes.Structure):
+    _fields_ = [("n", c_int), ("out_stride", ctypes.c_int64), ("kv4", c_ptr), ("slot", c_ptr),
+                ("cache_rows", ctypes.c_int64), ("out", c_ptr)]
+
+
+class AttnKv4Args(ctypes.Structure):
+    _fields_ = [
+        ("T", c_int), ("B", c_int), ("n_q", c_int), ("H", c_int), ("topk", c_int), ("max_L", c_int),
+        ("scale", ctypes.c_float), ("q", c_ptr), ("kv4", c_ptr), ("cache_rows", ctypes.c_int64),
+        ("block_table", c_ptr), ("block_size", c_int), ("max_blocks", c_int), ("topk_idx", c_ptr), ("out", c_ptr),
+        ("lse", c_ptr), ("sink", c_ptr), ("seq_of_token", c_ptr),
+    ]
+
+
 EXPORTS = [
     "dsa_status_string", "dsa_abi_version", "dsa_get_device_error", "dsa_set_wait_limit_ns",
     "dsa_indexer_prolog_workspace", "dsa_indexer_prolog",
@@ -80,7 +99,10 @@ EXPORTS = [
     "dsa_indexer_scores", "dsa_topk_from_scores",
     "dsa_sparse_attn_workspace", "dsa_sparse_attn", "dsa_indexer_prolog_noalloc", "dsa_act_quant",
     "dsa_int8_gemm", "dsa_mhc", "dsa_mla_prolog_workspace", "dsa_mla_prolog",
+    "dsa_kv4_write", "dsa_kv4_read", "dsa_sparse_attn_kv4_workspace", "dsa_sparse_attn_kv4",
 ]
+
+KV4_ROW_BYTES = 416  # one row of the 4-bit latent cache
 
 _lib = None
 
@@ -130,6 +152,14 @@ def load(path: str = LIB_PATH):
     lib.dsa_mla_prolog_workspace.restype = ctypes.c_size_t
     lib.dsa_mla_prolog.argtypes = [ctypes.POINTER(MlaArgs), c_ptr, ctypes.c_size_t, c_ptr]
     lib.dsa_mla_prolog.restype = c_int
+    lib.dsa_kv4_write.argtypes = [ctypes.POINTER(Kv4WriteArgs), c_ptr]
+    lib.dsa_kv4_write.restype = c_int
+    lib.dsa_kv4_read.argtypes = [ctypes.POINTER(Kv4ReadArgs), c_ptr]
+    lib.dsa_kv4_read.restype = c_int
+    lib.dsa_sparse_attn_kv4_workspace.argtypes = [ctypes.POINTER(AttnKv4Args)]
+    lib.dsa_sparse_attn_kv4_workspace.restype = ctypes.c_size_t
+    lib.dsa_sparse_attn_kv4.argtypes = [ctypes.POINTER(AttnKv4Args), c_ptr, ctypes.c_size_t, c_ptr]
+    lib.dsa_sparse_attn_kv4.restype = c_int
     _lib = lib
     return lib
 
@@ -239,7 +269,8 @@ def dsa_sparse_attn(args: AttnArgs, workspace: Optional[torch.Tensor] = None, st
 def workspace_bytes(kind: str, args) -> int:
     lib = load()
     fn = {"prolog": lib.dsa_indexer_prolog_workspace, "topk": lib.dsa_indexer_topk_workspace,
-          "attn": lib.dsa_sparse_attn_workspace, "mla": lib.dsa_mla_prolog_workspace}[kind]
+          "attn": lib.dsa_sparse_attn_workspace, "mla": lib.dsa_mla_prolog_workspace,
+          "attn_kv4": lib.dsa_sparse_attn_kv4_workspace}[kind]
     return int(fn(ctypes.byref(args)))
 
 
@@ -298,3 +329,85 @@ def dsa_mla_prolog(args: MlaArgs, workspace: Optional[torch.Tensor] = None, stre
     ws, n = _ws(need, device or "cuda", workspace)
     _check(lib.dsa_mla_prolog(ctypes.byref(args), _p(ws), n, _stream(stream)), "dsa_mla_prolog")
     return ws
+
+
+# ----------------------------------------------------- 4-bit latent cache
+def _tensor(name: str, t: torch.Tensor, dtype, shape, device=None, last_dense=False):
+    """Refuses a tensor whose device, type, shape or layout the library would
+    misread (None in a shape matches any size)."""
+    if not t.is_cuda:
+        raise DSAError(f"{name}: not a CUDA tensor")
+    if t.device.index != (torch.cuda.current_device() if device is None else device.index):
+        raise DSAError(f"{name}: on {t.device}, which is not the current device")
+    if t.dtype != dtype:
+        raise DSAError(f"{name}: {t.dtype}, expected {dtype}")
+    if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise DSAError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not (t.stride(-1) == 1 or t.shape[-1] <= 1 if last_dense else t.is_contiguous()):
+        raise DSAError(f"{name}: strides {t.stride()} are not supported")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Distance of a [n, 576] tensor's rows (a single row has none of its own)."""
+    return t.stride(0) if t.shape[0] > 1 else max(576, t.stride(0) // 8 * 8)
+
+
+def dsa_kv4_write(x: torch.Tensor, kv4: torch.Tensor, slot: torch.Tensor, stream=None):
+    """Quantises latent rows x bf16 [n, 576] (any row stride) into rows `slot`
+    int64 [n] of the 4-bit cache kv4 uint8 [rows, 416] (see dsa.h)."""
+    n = slot.shape[0]
+    _tensor("x", x, torch.bfloat16, (n, 576), last_dense=True)
+    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES))
+    _tensor("slot", slot, torch.int64, (n,))
+    args = Kv4WriteArgs(n, _row_stride(x), _p(x), _p(kv4), _p(slot), kv4.shape[0])
+    _check(load().dsa_kv4_write(ctypes.byref(args), _stream(stream)), "dsa_kv4_write")
+
+
+def dsa_kv4_read(kv4: torch.Tensor, slot: torch.Tensor, out: torch.Tensor, stream=None):
+    """Rows `slot` int64 [n] of the 4-bit cache kv4 uint8 [rows, 416] -> out
+    bf16 [n, 576] (any row stride; see dsa.h)."""
+    n = slot.shape[0]
+    _tensor("out", out, torch.bfloat16, (n, 576), last_dense=True)
+    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES))
+    _tensor("slot", slot, torch.int64, (n,))
+    args = Kv4ReadArgs(n, _row_stride(out), _p(kv4), _p(slot), kv4.shape[0], _p(out))
+    _check(load().dsa_kv4_read(ctypes.byref(args), _stream(stream)), "dsa_kv4_read")
+
+
+def attn_kv4_args(T, B, n_q, H, topk, max_L, scale, q, kv4, topk_idx, out, lse=None, block_table=None, block_size=0,
+                  sink=None, seq_of_token=None) -> AttnKv4Args:
+    """Arguments of dsa_sparse_attn_kv4: q bf16 [T, H, 576], kv4 uint8 [rows, 416], topk_idx int32 [T, topk], out
+    bf16 [T, H, 512], lse fp32 [T, H]; block_table int32 [B, max_blocks] for a paged cache; sink fp32 [H];
+    seq_of_token int32 [T] (then n_q is ignored)."""
+    _tensor("q", q, torch.bfloat16, (T, H, 576))
+    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES))
+    _tensor("topk_idx", topk_idx, torch.int32, (T, topk))
+    _tensor("out", out, torch.bfloat16, (T, H, 512))
+    max_blocks = 0
+    if block_table is not None:
+        _tensor("block_table", block_table, torch.int32, (B, None))
+        max_blocks = block_table.shape[1]
+    if lse is not None:
+        _tensor("lse", lse, torch.float32, (T, H))
+    if sink is not None:
+        _tensor("sink", sink, torch.float32, (H,))
+    if seq_of_token is not None:
+        _tensor("seq_of_token", seq_of_token, torch.int32, (T,))
+    args = AttnKv4Args(T, B, n_q, H, topk, max_L, float(scale), _p(q), _p(kv4), kv4.shape[0], _p(block_table),
+                       block_size, max_blocks, _p(topk_idx), _p(out), _p(lse), _p(sink), _p(seq_of_token))
+    args.device = q.device
+    return args
+
+
+def dsa_sparse_attn_kv4(args: AttnKv4Args, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Runs the sparse attention over a 4-bit cache.  Returns the workspace
+    (one is made when none is given and the shape needs one)."""
+    lib = load()
+    if torch.cuda.current_device() != args.device.index:
+        raise DSAError(f"dsa_sparse_attn_kv4: tensors on {args.device}, which is not the current device")
+    if workspace is None:
+        workspace, n = _ws(lib.dsa_sparse_attn_kv4_workspace(ctypes.byref(args)), args.device, None)
+    else:
+        n = workspace.numel() * workspace.element_size()
+    _check(lib.dsa_sparse_attn_kv4(ctypes.byref(args), _p(workspace), n, _stream(stream)), "dsa_sparse_attn_kv4")
+    return workspace

@@ -2,6 +2,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <cfloat>
 #include <cstddef>
 #include <mutex>
 #include "dsa_internal.h"
@@ -391,6 +392,57 @@ int dsa_mla_prolog(const dsa_mla_prolog_args* a, void* ws, size_t ws_bytes, void
   if (st != DSA_OK || a->T == 0) return st;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < mla_workspace(*a)) return DSA_ERR_WORKSPACE;
   return launch_mla(*a, ws, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_kv4_write(const dsa_kv4_write_args* a, void* stream) {
+  if (!a || a->n < 0 || a->cache_rows < 0 || a->x_stride < 576 || a->x_stride % 8 != 0) return DSA_ERR_INVALID_ARG;
+  if (a->cache_rows > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (a->n == 0) return DSA_OK;
+  if (bad_ptr(a->x, 16) || bad_ptr(a->kv4, 16) || bad_ptr(a->slot, 8)) return DSA_ERR_INVALID_ARG;
+  return launch_kv4_write(*a, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_kv4_read(const dsa_kv4_read_args* a, void* stream) {
+  if (!a || a->n < 0 || a->cache_rows < 0 || a->out_stride < 576 || a->out_stride % 8 != 0)
+    return DSA_ERR_INVALID_ARG;
+  if (a->cache_rows > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (a->n == 0) return DSA_OK;
+  if (bad_ptr(a->out, 16) || bad_ptr(a->kv4, 16) || bad_ptr(a->slot, 8)) return DSA_ERR_INVALID_ARG;
+  return launch_kv4_read(*a, static_cast<cudaStream_t>(stream));
+}
+
+static int check_attn_kv4(const dsa_attn_kv4_args* a) {
+  if (!a) return DSA_ERR_INVALID_ARG;
+  {
+    const int st = check_tokens(a->T, a->B, a->n_q, a->seq_of_token);
+    if (st != DSA_OK || a->T == 0) return st;
+  }
+  if (a->H < 1 || a->topk < 1 || a->max_L < 1 || a->cache_rows < 1 || !(a->scale > 0.f) || a->scale > FLT_MAX)
+    return DSA_ERR_INVALID_ARG;
+  if (a->T > 65535 || a->H > 1024 || a->topk > 65536 || a->cache_rows > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (bad_ptr(a->q, 16) || bad_ptr(a->kv4, 16) || bad_ptr(a->topk_idx, 4) || bad_ptr(a->out, 16))
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned(a->lse, 4) || !aligned(a->sink, 4)) return DSA_ERR_INVALID_ARG;
+  if (a->block_table) {
+    if (!aligned(a->block_table, 4) || a->block_size < 1) return DSA_ERR_INVALID_ARG;
+    if (static_cast<long long>(a->max_blocks) * a->block_size != a->max_L) return DSA_ERR_INVALID_ARG;
+  } else if (static_cast<long long>(a->B) * a->max_L > a->cache_rows) {
+    return DSA_ERR_INVALID_ARG;
+  }
+  return DSA_OK;
+}
+
+size_t dsa_sparse_attn_kv4_workspace(const dsa_attn_kv4_args* a) {
+  if (check_attn_kv4(a) != DSA_OK || a->T == 0) return 0;
+  return attn_kv4_workspace(*a);
+}
+
+int dsa_sparse_attn_kv4(const dsa_attn_kv4_args* a, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_attn_kv4(a);
+  if (st != DSA_OK || a->T == 0) return st;
+  const size_t need = attn_kv4_workspace(*a);
+  if (need > 0 && (ws == nullptr || !aligned(ws, 256) || ws_bytes < need)) return DSA_ERR_WORKSPACE;
+  return launch_attn_kv4(*a, ws, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

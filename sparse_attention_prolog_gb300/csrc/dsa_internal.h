@@ -75,5 +75,9 @@ int launch_int8_gemm_tc(const dsa_int8_gemm_args& a, cudaStream_t s);
 int launch_mhc(const dsa_mhc_args& a, cudaStream_t s);
 size_t mla_workspace(const dsa_mla_prolog_args& a);
 int launch_mla(const dsa_mla_prolog_args& a, void* ws, cudaStream_t s);
+int launch_kv4_write(const dsa_kv4_write_args& a, cudaStream_t s);
+int launch_kv4_read(const dsa_kv4_read_args& a, cudaStream_t s);
+size_t attn_kv4_workspace(const dsa_attn_kv4_args& a);
+int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s);
 
 }  // namespace dsa

@@ -3,6 +3,8 @@ sparse attention) over the C ABI.  PyTorch provides device memory and
 streams only; the computation is the library's."""
 from __future__ import annotations
 
+import dataclasses
+
 import numpy as np
 import torch
 
@@ -103,14 +105,35 @@ def is_uniform(inp) -> bool:
     return bool(np.array_equal(inp.seq_of_token, np.repeat(np.arange(inp.B, dtype=np.int32), inp.T // inp.B)))
 
 
+class Kv4Cache:
+    """A latent cache of ``rows`` rows held in 4 bits (416 bytes a row; all
+    zeros at first) and the calls that write and read its rows by slot."""
+
+    def __init__(self, rows: int, device):
+        self.data = torch.zeros(rows, B.KV4_ROW_BYTES, dtype=torch.uint8, device=device)
+
+    def write(self, x: torch.Tensor, slot: torch.Tensor, stream=None):
+        """Quantises x bf16 [n, 576] into the rows slot int64 [n] (-1: skipped)."""
+        B.dsa_kv4_write(x, self.data, slot, stream)
+
+    def read(self, slot: torch.Tensor, out: torch.Tensor = None, stream=None) -> torch.Tensor:
+        """The rows slot int64 [n] as bf16 [n, 576] (-1: zeros)."""
+        if out is None:
+            out = torch.empty(slot.shape[0], 576, dtype=torch.bfloat16, device=self.data.device)
+        B.dsa_kv4_read(self.data, slot, out, stream)
+        return out
+
+
 class DecodeBuffers:
     """Device copies of a workloads.DecodeInputs and the indexer/attention
     outputs.  ``q_idx``/``q_idx_scale``/``w_idx`` may be replaced by the
     prolog's outputs (then pass them in).  The calls get the token map
-    (seq_of_token) when the batch is not uniform, or when ``seq_map``."""
+    (seq_of_token) when the batch is not uniform, or when ``seq_map``.  With
+    ``kv4`` (a Kv4Cache) the attention reads that 4-bit cache in place of
+    ``kv``."""
 
     def __init__(self, inp, device, q_idx=None, q_idx_scale=None, w_idx=None, k_cache=None, k_scale=None,
-                 with_attention=True, keep_scores=False, seq_map=False, q_attn=None, kv=None):
+                 with_attention=True, keep_scores=False, seq_map=False, q_attn=None, kv=None, kv4=None):
         self.inp = inp
         d = device
         self.q_idx = q_idx if q_idx is not None else to_dev(inp.q_idx, d)
@@ -132,19 +155,29 @@ class DecodeBuffers:
         self.with_attention = with_attention
         if with_attention:
             self.q_attn = to_dev(inp.q_attn, d, "bf16") if q_attn is None else q_attn
-            self.kv = to_dev(inp.kv_cache, d, "bf16") if kv is None else kv
+            self.kv4 = kv4
+            self.kv = None if kv4 is not None else to_dev(inp.kv_cache, d, "bf16") if kv is None else kv
             self.out = torch.zeros(T, inp.H, inp.d_v, dtype=torch.bfloat16, device=d)
             self.lse = torch.zeros(T, inp.H, dtype=torch.float32, device=d)
-            self.aargs = B.attn_args(T, inp.B, n_q, inp.H, inp.topk, inp.max_L, inp.scale, self.q_attn,
-                                     self.kv, self.topk_idx, self.out, self.lse, self.block_table, inp.block_size,
-                                     seq_of_token=self.seq)
-            self.aws = torch.zeros(max(B.workspace_bytes("attn", self.aargs), 256), dtype=torch.uint8, device=d)
+            if kv4 is not None:
+                self.aargs = B.attn_kv4_args(T, inp.B, n_q, inp.H, inp.topk, inp.max_L, inp.scale, self.q_attn,
+                                             kv4.data, self.topk_idx, self.out, self.lse, self.block_table,
+                                             inp.block_size, seq_of_token=self.seq)
+            else:
+                self.aargs = B.attn_args(T, inp.B, n_q, inp.H, inp.topk, inp.max_L, inp.scale, self.q_attn,
+                                         self.kv, self.topk_idx, self.out, self.lse, self.block_table,
+                                         inp.block_size, seq_of_token=self.seq)
+            need = B.workspace_bytes("attn" if kv4 is None else "attn_kv4", self.aargs)
+            self.aws = torch.zeros(max(need, 256), dtype=torch.uint8, device=d)
 
     def run_topk(self, stream=None):
         B.dsa_indexer_topk(self.targs, self.tws, stream)
 
     def run_attn(self, stream=None):
-        B.dsa_sparse_attn(self.aargs, self.aws, stream)
+        if self.kv4 is not None:
+            B.dsa_sparse_attn_kv4(self.aargs, self.aws, stream)
+        else:
+            B.dsa_sparse_attn(self.aargs, self.aws, stream)
 
     def run(self, stream=None):
         self.run_topk(stream)
@@ -158,23 +191,39 @@ class DiaBuffers:
     latent cache) -> the Indexer Prolog (fed the MLA Prolog's q_lora and the
     same hidden states x; new keys into the key cache) -> Lightning Indexer
     + top-k -> sparse attention (the MLA Prolog's q over the latent cache).
-    `dia` is a workloads.DiaInputs."""
+    `dia` is a workloads.DiaInputs.
 
-    def __init__(self, dia, device, keep_scores=False):
+    With ``kv4`` the latent cache is held in 4 bits (416 instead of 1152 bytes
+    a row): the prior rows are quantised once here, the MLA Prolog leaves the
+    step's rows in a [T, 576] buffer, dsa_kv4_write puts them into the cache and
+    the attention is dsa_sparse_attn_kv4."""
+
+    def __init__(self, dia, device, keep_scores=False, kv4=False):
         d = device
         inp = dia.decode
         self.dia = dia
         self.k_cache = to_dev(inp.k_cache, d)
         self.k_scale = to_dev(inp.k_scale, d)
         self.kv = to_dev(inp.kv_cache, d, "bf16")
-        self.mla = MlaBuffers(dia.mla, d, self.kv.shape[0], kv_cache=self.kv)
+        self.kv4 = None
+        if kv4:
+            self.kv4 = Kv4Cache(self.kv.shape[0], d)
+            self.kv4.write(self.kv, torch.arange(self.kv.shape[0], dtype=torch.int64, device=d))
+            self.slot = to_dev(dia.mla.slot, d)
+            self.kv = torch.zeros(inp.T, 576, dtype=torch.bfloat16, device=d)
+            mla = dataclasses.replace(dia.mla, slot=np.arange(inp.T, dtype=np.int64))
+        else:
+            mla = dia.mla
+        self.mla = MlaBuffers(mla, d, self.kv.shape[0], kv_cache=self.kv)
         self.pro = PrologBuffers(dia.prolog, d, self.k_cache, self.k_scale, q_lora=self.mla.q_lora,
                                  q_lora_scale=self.mla.q_lora_scale, x=self.mla.x)
         self.buf = DecodeBuffers(inp, d, q_idx=self.pro.q_out, q_idx_scale=self.pro.q_scale_out, w_idx=self.pro.w_out,
                                  k_cache=self.k_cache, k_scale=self.k_scale, keep_scores=keep_scores,
-                                 q_attn=self.mla.q, kv=self.kv)
+                                 q_attn=self.mla.q, kv=self.kv, kv4=self.kv4)
 
     def run(self, stream=None):
         self.mla.run(stream)
+        if self.kv4 is not None:
+            self.kv4.write(self.kv, self.slot, stream)
         self.pro.run(stream)
         self.buf.run(stream)
