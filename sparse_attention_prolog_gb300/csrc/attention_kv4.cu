@@ -4,9 +4,10 @@
 //   out[t,h] = sum_j e^{s_j} v_j / (sum_j e^{s_j} [+ e^{sink[h]}]),
 //   s_j = scale q[t,h] . k_j, k_j the dequantised row, v_j its 512 latent dims
 //
-// One 2-CTA cluster per (token, block of 128 heads, chunk of selected rows);
-// tiles of 128 rows.  An O accumulator [128 x 512] in fp32 fills a CTA's tensor
-// memory, so the two products live in different CTAs:
+// Work items (token, block of 128 heads, chunk of selected rows) go round robin
+// to persistent 2-CTA clusters; an item is a run of tiles of 128 rows.  An O
+// accumulator [128 x 512] in fp32 fills a CTA's tensor memory, so the two
+// products live in different CTAs:
 //
 //   CTA 0: S = q . K^T (M = 128 heads, N = 128 rows, K = 576) and the softmax.
 //          The latent part of q is the A operand in tensor memory (256
@@ -16,13 +17,16 @@
 //   CTA 1: O += P . V with P sent over by CTA 0 (st.async) and the values read
 //          MN-major from the converted rows.
 //
-// Both convert the rows they need from 4 bits to bf16: 16 warps load 64-byte
-// pieces of a row (4 lanes of 16 bytes, 8 rows at a time) into registers one
-// tile ahead, convert (three instructions per pair of dims, exact) and store
-// into the 128B-swizzled layout the MMA reads.  A group of four warps fills one
-// of four slots: a quarter of the dims of all 128 rows in CTA 0, all dims of 32
-// rows in CTA 1, in the order the MMA consumes and frees them; so one tile of
-// buffer keeps the tensor core fed while the next tile is converted.
+// Both load the raw rows they need by TMA row gathers (four rows each) and
+// convert them from 4 bits to bf16, three instructions per pair of dims, exact,
+// into the 128B-swizzled layout the MMA reads, 16 KB units at a time in the
+// order the MMA consumes and frees them: 64 dims of 128 rows in CTA 0, 512 dims
+// of 16 rows in CTA 1.  (Loading the rows into registers instead kept the
+// load/store pipe, which the conversion's stores need, busy for longer than the
+// MMA takes: 4.6 ms for the 4096-token case.)  Unit k of a tile belongs to the
+// warps of group k mod 4.  q goes through the same units of CTA 0, by TMA and
+// then into tensor memory, so the next item's q is on its way while the
+// current item's last tile is multiplied.
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -36,33 +40,39 @@ namespace {
 
 constexpr int kDqk = 576, kDv = 512;
 constexpr int kTile = 128;                 // rows per tile
-constexpr int kSlot = 32768;               // a slot: 128 rows x 128 dims, or 32 rows x 512 dims, bf16
-constexpr int kAtom = 16384;               // 128 rows (or heads) x 128 bytes
-constexpr int kPSlot = 2 * kAtom;          // P [128 heads x 128 rows] bf16
+constexpr int kUnit = 16384;               // 128 rows x 64 dims, or 16 rows x 512 dims, bf16
+constexpr int kUnits = 6;                  // units in flight
+constexpr int kPSlot = 32768;              // P [128 heads x 128 rows] bf16
+constexpr int kRawRow = 288;               // codes and scale bytes of a row
+constexpr int kRawTile = kTile * kRawRow;  // CTA 0: a tile's raw rows
+constexpr int kRawUnit = 16 * kRawRow;     // CTA 1: 16 raw rows
+constexpr int kDescs = 8;
 // 28 warps in seven warpgroups: 0-1 softmax (CTA 0), correction and epilogue
-// (CTA 1); 2-5 conversion; 6 MMA issue and the P-slot relay.  The launch
-// grants 72 registers a thread: 896 x 72 = 256 x 104 + 512 x 64 + 128 x 40.
+// (CTA 1); 2-5 conversion; 6 MMA issue, row gathers, q loads / P-slot relay.
+// The launch grants 72 registers a thread: 896 x 72 = 256 x 80 + 512 x 64 + 128 x 88.
 constexpr int kThreads = 896;
-constexpr int kSoftWarps = 8, kConvWarps = 16, kFirstConv = 8, kMmaWarp = 24, kRelayWarp = 25;
-constexpr int kRegsLaunch = 72, kRegsSoft = 104, kRegsConv = 64, kRegsLast = 40;
+constexpr int kSoftWarps = 8, kConvWarps = 16, kFirstConv = 8, kMmaWarp = 24, kRowWarp = 25, kAuxWarp = 26;
+constexpr int kRegsLaunch = 72, kRegsSoft = 80, kRegsConv = 64, kRegsLast = 88;
 static_assert(256 * kRegsSoft + 512 * kRegsConv + 128 * kRegsLast <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
 constexpr uint32_t kPBytes = 128 * (2 * 128 + 4);  // a P tile and its rescale factors
 constexpr uint32_t kFinalBytes = 128 * 12;         // per head: maximum, two partial sums
 constexpr uint32_t kTmemS = 256;                   // CTA 0: q in columns [0, 256), S in [256, 512)
 
-// Dynamic shared memory.  CTA 0: four K slots, q's rotary part, two rotary K
-// buffers, the row maxima that the two warps of a head exchange.  CTA 1: four V
-// slots (the output staging at the end), two P slots, rescale factors, finals.
-constexpr int kOffQrope = 4 * kSlot, kOffKrope = kOffQrope + kAtom, kOffMax = kOffKrope + 2 * kAtom;
-constexpr int kOffP = 4 * kSlot, kOffAlpha = kOffP + 2 * kPSlot, kOffFinal = kOffAlpha + 1024;
-constexpr int kSmem = 1024 + kOffFinal + 2048;
-static_assert(kOffMax + 2048 <= kSmem - 1024, "CTA 0 fits CTA 1's allocation");
+// Dynamic shared memory, after the units.  CTA 0: q's rotary part, two rotary K
+// buffers, two raw tiles, the row maxima that the two warps of a head exchange.
+// CTA 1: two P slots, the output staging of each column half, raw units, rescale
+// factors, finals.
+constexpr int kOffQrope = kUnits * kUnit, kOffKrope = kOffQrope + kUnit, kOffRaw0 = kOffKrope + 2 * kUnit,
+              kOffMax = kOffRaw0 + 2 * kRawTile, kEnd0 = kOffMax + 2048;
+constexpr int kOffP = kUnits * kUnit, kOffStage = kOffP + 2 * kPSlot, kOffRaw1 = kOffStage + 2 * kUnit,
+              kOffAlpha = kOffRaw1 + kUnits * kRawUnit, kOffFinal = kOffAlpha + 1024, kEnd1 = kOffFinal + 1536;
+constexpr int kSmem = 1024 + (kEnd0 > kEnd1 ? kEnd0 : kEnd1);
+static_assert(kSmem + 2048 <= 232448, "shared memory of a CTA");
 
 struct AttnKv4Params {
-  int T, B, n_q, H, topk, max_L, n_chunks, chunk_rows, head_blocks;
+  int T, B, n_q, H, topk, max_L, n_chunks, chunk_rows, head_blocks, items;
   float scale_log2;
-  const uint16_t* q;
   const uint8_t* kv4;
   int64_t rows;
   const int32_t* block_table;
@@ -77,85 +87,190 @@ struct AttnKv4Params {
   uint32_t* err;
 };
 
-struct __align__(8) Bars {
-  uint64_t full[4], empty[4];      // K (CTA 0) or V (CTA 1) slots
-  uint64_t rfull[2], rempty[2];    // CTA 0: rotary K buffers
-  uint64_t sfull[2], sempty[2];    // CTA 0: S buffers
-  uint64_t pfree[2];               // CTA 0: P slot of CTA 1 free
-  uint64_t mx[4];                  // CTA 0: row maxima exchanged (per warp quadrant)
-  uint64_t pfull[2], pcons[2];     // CTA 1: P slots
-  uint64_t ready[2], odone, ffull; // CTA 1: correction / MMA
-  uint64_t alldone;                // CTA 1: every PV MMA complete
-  uint64_t qready;                 // CTA 0: q is in place
-  uint64_t tiles;                  // the chunk's row count is known
-  uint64_t mdrain;                 // the MMA thread's last commit
+// What every role needs to know of a tile.
+struct __align__(16) Desc {
+  uint32_t valid[4];  // rows that are selected (the others are masked, their values zeros)
+  int rows;           // rows of the tile up to the item's last selected one; 0: the item selects nothing
+  int last;           // the item's last tile
+  int pad[2];
 };
+
+struct __align__(8) Bars {
+  uint64_t full[kUnits], empty[kUnits];      // units (CTA 0: K and q; CTA 1: V)
+  uint64_t rfull[kUnits], rempty[kUnits];    // raw rows (CTA 0: two tiles; CTA 1: units)
+  uint64_t dfull[kDescs], dempty[kDescs];    // tile descriptors
+  uint64_t kpfull[2], kpempty[2];            // CTA 0: rotary K buffers
+  uint64_t sfull[2], sempty[2];              // CTA 0: S buffers
+  uint64_t pfree[2];                         // CTA 0: P slot of CTA 1 free
+  uint64_t mx[4];                            // CTA 0: row maxima exchanged (per warp quadrant)
+  uint64_t qgroup[8], qready, qfree, qpfull; // CTA 0: a q unit read / all of q stored / MMAs done with q; q's rotary part
+  uint64_t cdone;                            // CTA 0: every K unit of the item is converted
+  uint64_t ffree;                            // CTA 0: CTA 1 has read the finals
+  uint64_t pfull[2], pcons[2];               // CTA 1: P slots
+  uint64_t ready[2], odone[2], ffull;        // CTA 1: correction / MMA
+  uint64_t stfull[2], stfree[2];             // CTA 1: output staging of each half
+  uint64_t mdrain;                           // the MMA thread's last commit
+};
+
+// Units of 16 rows that a tile takes in CTA 1: four or eight, so that every group
+// of conversion warps has its share of every tile (a group that sat tiles out
+// could wait for a slot three uses ahead, where its barrier's parity misleads).
+__device__ __forceinline__ int pv_units(int rows) { return rows > kTile / 2 ? 8 : 4; }
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
 
-// The page entry that position s needs (its own sequence number where the
-// cache is contiguous); loaded a tile before page_row() uses it.
-__device__ __forceinline__ int page_of(const AttnKv4Params& P, int b, int s) {
-  if (s < 0 || P.block_table == nullptr) return b;
-  return __ldg(P.block_table + static_cast<size_t>(b) * P.max_blocks + s / P.block_size);
+// One thread of the warp.  (The compiler knows it for one: an MMA then takes half
+// the instructions that it takes under lane == 0.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
 }
-// Physical row of position s (-1: nothing, or recorded and read as zeros).
-__device__ __forceinline__ int page_row(const AttnKv4Params& P, int page, int s) {
-  if (s < 0) return -1;
-  const int64_t row = P.block_table == nullptr ? static_cast<int64_t>(page) * P.max_L + s
-                                               : static_cast<int64_t>(page) * P.block_size + s % P.block_size;
-  if (row < 0 || row >= P.rows || page < 0) {
-    atomicOr(P.err, kErrBadIndex);
-    return -1;
-  }
-  return static_cast<int>(row);
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n}" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+// Four rows r0..r3 of the map's 2-D tensor, from column x on, to consecutive
+// rows of shared memory.
+__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int x, const int (&r)[4], uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+        "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
 
+// After a wait gave up: waits for a copy that completes on `bar`.  The barrier may
+// have moved on to a later use (then the copy has landed, but its parity is gone),
+// so this waits a tenth of a millisecond at most, many times a copy's time.
+__device__ __forceinline__ void drain_copy(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_test(bar, parity) && globaltimer_ns() - t0 < 100000) {}
+}
+
+// Scores of rows that are not selected.
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[32], uint32_t valid) {
+  if (valid == 0xffffffffu) return;
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (!((valid >> k) & 1u)) s[k] = 0xff800000u;
+}
+
+// A counter over a ring of kUnits slots: the slot and the phase of its use.
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void add(uint32_t n) {  // n <= 8
+    slot += n;
+    while (slot >= kUnits) { slot -= kUnits; phase ^= 1; }
+  }
+  __device__ __forceinline__ Ring plus(uint32_t n) const { Ring r = *this; r.add(n); return r; }
+};
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Converts the 32 dims of one 16-byte piece of a raw row and stores them at
+// 16-byte chunks c4..c4+3 of the 128-byte row at dst, swizzled by r7 = row mod 8.
+// The lanes (row = lane / 2, piece = lane mod 2) of a quarter warp read and write
+// all 32 banks once.
+__device__ __forceinline__ void convert_piece(const uint8_t* raw, int piece_off, int scale_off, bool on, uint32_t dst,
+                                              uint32_t c4, uint32_t r7) {
+  uint4 w = *reinterpret_cast<const uint4*>(raw + piece_off);
+  uint32_t sc = *reinterpret_cast<const uint16_t*>(raw + scale_off);
+  if (!on) {
+    w = make_uint4(0, 0, 0, 0);
+    sc = 0;
+  }
+  const Kv4Scale lo = kv4_scale(sc & 255u), hi = kv4_scale(sc >> 8);
+  const uint32_t C = (c4 ^ r7) << 4;
+  st_shared_v4(dst + (C ^ 0), kv4_codes8(w.x, lo));
+  st_shared_v4(dst + (C ^ 16), kv4_codes8(w.y, lo));
+  st_shared_v4(dst + (C ^ 32), kv4_codes8(w.z, hi));
+  st_shared_v4(dst + (C ^ 48), kv4_codes8(w.w, hi));
+}
+
+// Bounded wait for a phase of a barrier, in as little code as will do: the roles
+// of this kernel run at the same time from one instruction cache (with the waits
+// of the other kernels the code was 133 KB and a third of the cache's requests
+// missed; the 4096-token case took 5.97 ms).  `lim` holds the limit and the suspend
+// hint in force, in shared memory.
+struct WaitLimit {
+  uint64_t ns;
+  uint32_t hint;
+  int gave_up;
+};
+template <bool kCluster>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile WaitLimit* lim) {
+  if (kCluster ? mbar_probe_cluster(bar, parity) : mbar_probe(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!(kCluster ? mbar_try_wait_cluster(bar, parity, lim->hint) : mbar_try_wait(bar, parity, lim->hint))) {
+    if (lim->gave_up) return false;
+    if (globaltimer_ns() - t0 > lim->ns) {
+      lim->gave_up = 1;  // reported when the CTA ends
+      return false;
+    }
+  }
+  return true;
+}
+// Waits of one thread, and of a whole warp, whose lanes go on or give up together
+// (a lane that left alone would leave the others at the next warp barrier).
+#define WAIT1(bar, parity) wait_phase<false>(&(bar), (parity), lim)
+#define WAIT(bar, parity) (__all_sync(0xffffffffu, wait_phase<false>(&(bar), (parity), lim)) != 0)
+#define WAIT_CLUSTER(bar, parity) (__all_sync(0xffffffffu, wait_phase<true>(&(bar), (parity), lim)) != 0)
+
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_kv4_kernel(const __grid_constant__ AttnKv4Params P, const __grid_constant__ CUtensorMap tmap_o) {
+    attn_kv4_kernel(const __grid_constant__ AttnKv4Params P, const __grid_constant__ CUtensorMap tmap_q,
+                    const __grid_constant__ CUtensorMap tmap_raw, const __grid_constant__ CUtensorMap tmap_rope,
+                    const __grid_constant__ CUtensorMap tmap_o) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Bars bars;
+  __shared__ Desc descs[kDescs];
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag, last_valid, n_rows_sh;
+  __shared__ WaitLimit wait_limit;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
-  const int chunk = blockIdx.x >> 1, hb = blockIdx.y, t = blockIdx.z;
-  int b = t / P.n_q;
-  bool bad_seq = false;
-  if (P.seq != nullptr) {  // a token outside [0, B) reads no row and gets out = 0
-    b = __ldg(P.seq + t);
-    bad_seq = b < 0 || b >= P.B;
-    if (bad_seq) {
-      if (tid == 0 && rank == 0 && chunk == 0 && hb == 0) atomicOr(P.err, kErrBadIndex);
-      b = 0;
-    }
-  }
-  const int slot_begin = chunk * P.chunk_rows;
-  const int rows_here = bad_seq ? 0 : max(0, min(P.chunk_rows, P.topk - slot_begin));
-  const int32_t* idx_row = P.idx + static_cast<size_t>(t) * P.topk;
-
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
   uint8_t* sP = smem + kOffP;
   float* sAlpha = reinterpret_cast<float*>(smem + kOffAlpha);  // [2][128]
   float* sFinal = reinterpret_cast<float*>(smem + kOffFinal);  // [3][128]: maximum, sum, sum
   float* sMax = reinterpret_cast<float*>(smem + kOffMax);      // [2][2][128]
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) { mbar_init(&bars.full[i], 4); mbar_init(&bars.empty[i], 1); mbar_init(&bars.mx[i], 2); }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&bars.full[i], 4); mbar_init(&bars.empty[i], 1);
+      mbar_init(&bars.rfull[i], 1); mbar_init(&bars.rempty[i], rank == 0 ? kConvWarps : 4);
+    }
+    // descriptors are read by the conversion and softmax / correction warps, the
+    // MMA thread and the q loads (CTA 0) or the relay (CTA 1)
+    for (int i = 0; i < kDescs; ++i) { mbar_init(&bars.dfull[i], 1); mbar_init(&bars.dempty[i], kConvWarps + kSoftWarps + 2); }
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.mx[i], 2);
+    for (int i = 0; i < 8; ++i) mbar_init(&bars.qgroup[i], 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.rfull[i], kConvWarps); mbar_init(&bars.rempty[i], 1);
+      mbar_init(&bars.kpfull[i], 1); mbar_init(&bars.kpempty[i], 1);
       mbar_init(&bars.sfull[i], 1); mbar_init(&bars.sempty[i], kSoftWarps); mbar_init(&bars.pfree[i], 1);
       mbar_init(&bars.pfull[i], 1); mbar_init(&bars.pcons[i], 1); mbar_init(&bars.ready[i], kSoftWarps);
+      mbar_init(&bars.odone[i], 1); mbar_init(&bars.stfull[i], 4); mbar_init(&bars.stfree[i], 1);
     }
-    mbar_init(&bars.odone, 1);
-    mbar_init(&bars.alldone, 1);
+    mbar_init(&bars.qready, kConvWarps);
+    mbar_init(&bars.qfree, 1);
+    mbar_init(&bars.cdone, kConvWarps);
+    mbar_init(&bars.qpfull, 1);
+    mbar_init(&bars.ffree, kSoftWarps);
     mbar_init(&bars.ffull, 1);
-    mbar_init(&bars.qready, kSoftWarps);
-    mbar_init(&bars.tiles, 1);
     mbar_init(&bars.mdrain, 1);
-    last_valid = -1;
-    abort_flag = 0;
+    wait_limit.ns = wait_limit_ns(P.err);
+    wait_limit.hint = static_cast<uint32_t>(wait_limit.ns < kSuspendHintNs ? wait_limit.ns : kSuspendHintNs);
+    wait_limit.gave_up = 0;
     fence_mbar_init();
     if (rank == 1) {
       mbar_arrive_expect_tx(&bars.pfull[0], kPBytes);
@@ -168,448 +283,629 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  volatile int* abort_v = &abort_flag;
+  volatile WaitLimit* lim = &wait_limit;
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  auto row_count = [&]() -> int {  // roles other than the conversion warps
-    if (!mbar_wait_polling<false>(&bars.tiles, 0, P.err, abort_v)) return 0;
-    return n_rows_sh;
-  };
-  const int q_rows = max(0, min(128, P.H - hb * 128));  // real heads of this block
   cluster_sync();  // both CTAs' barriers are initialised before any remote use
   griddep_launch_dependents();
+
+  // The next tile's descriptor, for a whole warp or for one thread.
+  uint32_t dc = 0;
+  auto read_desc = [&](Desc& d) {
+    const Desc& e = descs[dc % kDescs];
+    d.valid[0] = e.valid[0]; d.valid[1] = e.valid[1]; d.valid[2] = e.valid[2]; d.valid[3] = e.valid[3];
+    d.rows = e.rows;
+    d.last = e.last;
+    ++dc;
+  };
+  auto next_desc = [&](Desc& d) -> bool {
+    if (!WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) return false;
+    read_desc(d);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.dempty[(dc - 1) % kDescs]);
+    return true;
+  };
+  auto next_desc1 = [&](Desc& d) -> bool {
+    if (!WAIT1(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) return false;
+    read_desc(d);
+    mbar_arrive(&bars.dempty[(dc - 1) % kDescs]);
+    return true;
+  };
 
   if (warp >= kFirstConv && warp < kFirstConv + kConvWarps) {
     setmaxnreg_dec<kRegsConv>();
     // ------------------------------------------------- conversion (both CTAs)
     const int cw = warp - kFirstConv, grp = cw >> 2, wi = cw & 3;
-    const int rb = rank == 0 ? wi : grp;  // rows [32 rb, 32 rb + 32) of a tile
-    const int dq = rank == 0 ? grp : wi;  // dims [128 dq, 128 dq + 128)
-    const int g = lane & 3, r8 = lane >> 2;
-    griddep_wait();  // the index rows come from the previous kernel
-    // position of this lane's row of tile jj (-1: nothing)
-    auto load_pos = [&](int jj) -> int {
-      const int i = jj * kTile + rb * 32 + lane;
-      const int s = i < rows_here ? __ldg(idx_row + slot_begin + i) : -1;
-      return s < P.max_L ? s : -1;
-    };
-    int s0 = load_pos(0), s1 = load_pos(1), s2 = load_pos(2);
-    int n_rows;
-    {
-      // a valid last slot (every decode chunk) ends the chunk at once; else the
-      // conversion warps find the last valid slot together
-      const int last = rows_here > 0 ? __ldg(idx_row + slot_begin + rows_here - 1) : -1;
-      if (rows_here == 0 || (last >= 0 && last < P.max_L)) {
-        n_rows = rows_here;
-      } else {
-        int mx = -1;
-        for (int i = cw * 32 + lane; i < rows_here; i += kConvWarps * 32) {
-          const int s = __ldg(idx_row + slot_begin + i);
-          if (s >= 0 && s < P.max_L) mx = i;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (lane == 0 && mx >= 0) atomicMax(&last_valid, mx);
-        asm volatile("bar.sync 1, %0;" ::"n"(kConvWarps * 32) : "memory");
-        n_rows = last_valid + 1;
-      }
-      if (cw == 0 && lane == 0) {
-        n_rows_sh = n_rows;
-        mbar_arrive(&bars.tiles);
-      }
-    }
-    const int n_tiles = (n_rows + kTile - 1) / kTile;
-    int page1 = page_of(P, b, s1);
-    uint4 c[4];
-    uint2 rope[4];
-    uint32_t sc[4];
-    const uint8_t* src = P.kv4 + dq * 64 + g * 16;
-    // one piece (8 rows) of a tile: 16 bytes of codes and 2 scale bytes a lane,
-    // and in CTA 0 8 bytes of the rotary dims
-    auto load = [&](int i, int row_l) {
-      const int row = __shfl_sync(0xffffffffu, row_l, i * 8 + r8);
-      c[i] = make_uint4(0, 0, 0, 0);
-      rope[i] = make_uint2(0, 0);
-      sc[i] = 0;
-      if (row >= 0) {
-        const uint8_t* p = src + static_cast<size_t>(row) * kKv4Row;
-        c[i] = __ldg(reinterpret_cast<const uint4*>(p));
-        sc[i] = __ldg(reinterpret_cast<const uint16_t*>(p + (kKv4Scales - dq * 56 - g * 14)));
-        if (rank == 0) rope[i] = __ldg(reinterpret_cast<const uint2*>(p + (kKv4Rope - dq * 32 - g * 8)));
-      }
-    };
-    {
-      const int row0 = page_row(P, page_of(P, b, s0), s0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) load(i, row0);
-    }
-    // this lane's address in a slot: 16-byte chunk kk ^ C of its row
-    const uint32_t C = (g & 2) ^ ((g & 1) << 2) ^ r8;
-    const uint32_t row_bytes = rank == 0 ? rb * 32 * 128 : 0;             // first row of the block in its atom
-    const uint32_t atom = rank == 0 ? (g >> 1) * kAtom : (dq * 2 + (g >> 1)) * 4096;
-    const uint32_t dst = smem_u32(smem) + grp * kSlot + atom + row_bytes + r8 * 128;
-    const uint32_t rdst = smem_u32(smem + kOffKrope) + row_bytes + r8 * 128 + ((((dq * 2) + (g >> 1)) ^ r8) << 4) + (g & 1) * 8;
-    for (int j = 0; j < n_tiles; ++j) {
-      const int row1 = j + 1 < n_tiles ? page_row(P, page1, s1) : -1;
-      s1 = s2;
-      page1 = page_of(P, b, s1);
-      s2 = load_pos(j + 3);
-      const int rows_t = min(kTile, n_rows - j * kTile);
-      const bool used = rb * 32 < rows_t;  // blocks past the last row are not read by the MMA
-      if (rank == 1 && !used) break;       // (only in the last tile)
-      if (!mbar_wait_polling<false>(&bars.empty[grp], (j & 1) ^ 1, P.err, abort_v)) break;
-      if (rank == 0 && !mbar_wait_polling<false>(&bars.rempty[j & 1], ((j >> 1) & 1) ^ 1, P.err, abort_v)) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (used) {
-          Kv4Scale lo = kv4_scale(sc[i] & 255u), hi = kv4_scale(sc[i] >> 8);
-          uint4 w = c[i];
-          if (g & 2) {  // lanes of the second atom store in another order: no bank conflicts
-            const Kv4Scale t0 = lo; lo = hi; hi = t0;
-            w = make_uint4(c[i].z, c[i].w, c[i].x, c[i].y);
-          }
-          const uint32_t d = dst + i * 1024;
-          auto store = [&](uint32_t kk, const uint4& v) {
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d + ((kk ^ C) << 4)), "r"(v.x), "r"(v.y),
-                         "r"(v.z), "r"(v.w) : "memory");
-          };
-          store(0, kv4_codes8(w.x, lo));
-          store(1, kv4_codes8(w.y, lo));
-          store(2, kv4_codes8(w.z, hi));
-          store(3, kv4_codes8(w.w, hi));
-          if (rank == 0)
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(rdst + (j & 1) * kAtom + i * 1024), "r"(rope[i].x),
-                         "r"(rope[i].y) : "memory");
-        }
-        load(i, row1);
-      }
-      fence_proxy_async_smem();  // generic writes -> tensor core reads
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars.full[grp]);
-        if (rank == 0) mbar_arrive(&bars.rfull[j & 1]);
-      }
-    }
-  } else {
+    const int row = lane >> 1, piece = lane & 1;
+    const uint32_t units = smem_u32(smem);
+    Ring uc;          // the tile's (or q's) first unit
+    uint32_t tc = 0;  // tiles
     bool ok = true;
-    int n_rows = -1;  // set by each role where it first needs it
-    if (warp < kSoftWarps) {
-      setmaxnreg_inc<kRegsSoft>();
-      const int hrow = (warp & 3) * 32 + lane, hf = warp >> 2;
+    for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
       if (rank == 0) {
-        // ------------------------------------------------- softmax (CTA 0)
-        // Two threads per head, each 64 of a tile's 128 rows.
-        const uint32_t remote_p = mapa(smem_u32(sP), 1) + hf * kAtom;
-        const uint32_t remote_alpha = mapa(smem_u32(sAlpha), 1);
-        const uint32_t remote_final = mapa(smem_u32(sFinal), 1);
-        const uint32_t remote_pfull[2] = {mapa(smem_u32(&bars.pfull[0]), 1), mapa(smem_u32(&bars.pfull[1]), 1)};
-        const uint32_t remote_ffull = mapa(smem_u32(&bars.ffull), 1);
-        {
-          // q row of this thread's head: 256 latent dims to tensor memory, 32
-          // rotary dims to shared memory
-          const bool real = hrow < q_rows;
-          const uint4* qrow =
-              reinterpret_cast<const uint4*>(P.q + (static_cast<size_t>(t) * P.H + hb * 128 + (real ? hrow : 0)) * kDqk);
-          uint4 rp[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) rp[i] = real ? __ldg(qrow + 64 + hf * 4 + i) : make_uint4(0, 0, 0, 0);
+        // q: units grp and grp + 4 (64 dims of the 128 heads each) from shared to
+        // tensor memory, lane = head
+        if (n > 0) ok = WAIT(bars.qfree, (n - 1) & 1);
+        tc_fence_after();
 #pragma unroll 1
-          for (int a = 0; a < 2; ++a) {
-            uint4 v[16];
+        for (int x = 0; x < 2 && ok; ++x) {
+          const Ring u = uc.plus(grp + 4 * x);
+          // (the slot's previous use first: units 6 and 7 follow q's own first ones)
+          if (!WAIT(bars.empty[u.slot], u.phase ^ 1) || !WAIT(bars.full[u.slot], u.phase)) { ok = false; break; }
+          uint32_t r[32];
+          const uint8_t* src = smem + u.slot * kUnit;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = real ? __ldg(qrow + hf * 32 + a * 16 + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t r[32];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                r[4 * k] = v[x * 8 + k].x; r[4 * k + 1] = v[x * 8 + k].y;
-                r[4 * k + 2] = v[x * 8 + k].z; r[4 * k + 3] = v[x * 8 + k].w;
-              }
-              tmem_st32(tmem + lane_off + hf * 128 + a * 64 + x * 32, r);
-            }
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(&r[4 * k]) = *reinterpret_cast<const uint4*>(src + sw128_off(wi * 32 + lane, k));
+          tmem_st32(tmem + lane_off + (grp + 4 * x) * 32, r);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.qgroup[grp + 4 * x]);
+          if (wi == 0) {  // the four warps have read the unit
+            if (!WAIT(bars.qgroup[grp + 4 * x], n & 1)) { ok = false; break; }
+            if (lane == 0) mbar_arrive(&bars.empty[u.slot]);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(smem + kOffQrope + sw128_off(hrow, hf * 4 + i)) = rp[i];
-          fence_proxy_async_smem();
-          tmem_st_wait();
         }
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.qready);
-        griddep_wait();  // the index rows come from the previous kernel
-        float m_used = neg_inf(), l_sum = 0.f;
-        auto load_idx = [&](int jj, int& lo, int& hi) {
-          const int i = jj * kTile + hf * 64 + lane;
-          lo = i < rows_here ? __ldg(idx_row + slot_begin + i) : -1;
-          hi = i + 32 < rows_here ? __ldg(idx_row + slot_begin + i + 32) : -1;
-        };
-        int nx_lo, nx_hi;
-        load_idx(0, nx_lo, nx_hi);  // before the row count: one round trip
-        n_rows = row_count();
-        const int n_tiles = (n_rows + kTile - 1) / kTile;
-        const uint64_t scale2 = pack_f32x2(P.scale_log2, P.scale_log2);
-        for (int j = 0; j < n_tiles; ++j) {
-          const int sb = j & 1, ph = (j >> 1) & 1;
-          const uint32_t v_lo = __ballot_sync(0xffffffffu, nx_lo >= 0 && nx_lo < P.max_L);
-          const uint32_t v_hi = __ballot_sync(0xffffffffu, nx_hi >= 0 && nx_hi < P.max_L);
-          load_idx(j + 1, nx_lo, nx_hi);
-          ok = mbar_wait_polling<false>(&bars.sfull[sb], ph, P.err, abort_v) && ok;
-          tc_fence_after();
-          uint32_t s[64];
-          {
-            uint32_t(&a)[32] = *reinterpret_cast<uint32_t(*)[32]>(s);
-            uint32_t(&c)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 32);
-            tmem_ld32(tmem + lane_off + kTmemS + sb * kTile + hf * 64, a);
-            tmem_ld32(tmem + lane_off + kTmemS + sb * kTile + hf * 64 + 32, c);
-            tmem_ld_wait();
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.sempty[sb]);
-          if ((v_lo & v_hi) != 0xffffffffu) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if (!((v_lo >> k) & 1u)) s[k] = 0xff800000u;
-              if (!((v_hi >> k) & 1u)) s[32 + k] = 0xff800000u;
+        uc.add(8);
+        // every q unit is released before a K unit waits for a slot: the parity of a
+        // slot's barrier tells its last two uses apart, not its last three
+        if (ok) ok = WAIT(bars.qready, n & 1);
+      }
+      while (ok) {
+        Desc d;
+        if (!next_desc(d)) { ok = false; break; }
+        if (d.rows > 0) {
+          if (rank == 0) {
+            const uint32_t rs = tc & 1;
+            if (!WAIT(bars.rfull[rs], (tc >> 1) & 1)) { ok = false; break; }
+            const uint8_t* raw = smem + kOffRaw0 + rs * kRawTile + (wi * 32 + row) * kRawRow;
+            const bool used = wi * 32 < d.rows;  // blocks past the last row are not read by the MMA
+#pragma unroll 1
+            for (int k = grp; k < 8; k += 4) {
+              const Ring u = uc.plus(k);
+              if (!WAIT(bars.empty[u.slot], u.phase ^ 1)) { ok = false; break; }
+              if (used) {
+                const uint32_t dst = units + u.slot * kUnit + (wi * 32 + row) * 128;
+#pragma unroll 1
+                for (int p = 0; p < 2; ++p)
+                  convert_piece(raw + p * 16 * kRawRow, k * 32 + piece * 16, kKv4Scales + k * 4 + piece * 2, true,
+                                dst + p * 16 * 128, piece * 4, row & 7);
+              }
+              fence_proxy_async_smem();  // generic writes -> tensor core reads
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars.full[u.slot]);
             }
+            if (lane == 0) mbar_arrive(&bars.rempty[rs]);
+            uc.add(8);
+          } else {
+#pragma unroll 1
+            for (int k = grp; k < pv_units(d.rows); k += 4) {
+              const Ring u = uc.plus(k);
+              // in this order: a free unit says that its slot's previous rows were
+              // converted, so that the row barrier is in this use's phase
+              if (!WAIT(bars.empty[u.slot], u.phase ^ 1)) { ok = false; break; }
+              if (!WAIT(bars.rfull[u.slot], u.phase)) { ok = false; break; }
+              const uint8_t* raw = smem + kOffRaw1 + u.slot * kRawUnit + row * kRawRow;
+              const uint32_t vw = k < 4 ? (k < 2 ? d.valid[0] : d.valid[1]) : (k < 6 ? d.valid[2] : d.valid[3]);
+              const bool on = (vw >> ((k & 1) * 16 + row)) & 1u;
+              const uint32_t dst = units + u.slot * kUnit + row * 128;
+              if (k * 16 < d.rows) {
+#pragma unroll 1
+                for (int p = 0; p < 2; ++p) {
+                  const int a = wi * 2 + p;  // 64 dims
+                  convert_piece(raw, a * 32 + piece * 16, kKv4Scales + a * 4 + piece * 2, on, dst + a * 2048, piece * 4,
+                                row & 7);
+                }
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&bars.full[u.slot]);
+                mbar_arrive(&bars.rempty[u.slot]);
+              }
+            }
+            uc.add(pv_units(d.rows));
           }
-          float mt[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-          for (int k = 0; k < 64; ++k) mt[k & 3] = fmaxf(mt[k & 3], __uint_as_float(s[k]));
-          float m_tile = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * P.scale_log2;
-          // the other 64 rows' maximum, from the warp that holds them
-          sMax[(j & 1) * 256 + hf * 128 + hrow] = m_tile;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.mx[warp & 3]);
-          ok = mbar_wait_polling<false>(&bars.mx[warp & 3], j & 1, P.err, abort_v) && ok;
-          m_tile = fmaxf(m_tile, sMax[(j & 1) * 256 + (hf ^ 1) * 128 + hrow]);
-          float alpha = 1.f;
-          if (m_tile > m_used + 8.f) {  // also taken when m_used is -inf
-            alpha = ex2_approx(m_used - m_tile);
-            l_sum *= alpha;
-            m_used = m_tile;
-          }
-          const float msub = m_used == neg_inf() ? 0.f : -m_used;
-          const uint64_t msub2 = pack_f32x2(msub, msub);
-          uint64_t sum2[2] = {0, 0};
-          const uint64_t one2 = pack_f32x2(1.f, 1.f);
-          uint32_t pk[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const uint64_t x = fma_f32x2(pack_f32x2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2, msub2);
-            const float p0 = ex2_approx(lo_f32(x)), p1 = ex2_approx(hi_f32(x));
-            sum2[k & 1] = fma_f32x2(pack_f32x2(p0, p1), one2, sum2[k & 1]);
-            __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-            pk[k] = *reinterpret_cast<uint32_t*>(&pb);
-          }
-          l_sum += (lo_f32(sum2[0]) + hi_f32(sum2[0])) + (lo_f32(sum2[1]) + hi_f32(sum2[1]));
-          ok = mbar_wait_polling<true>(&bars.pfree[sb], ph ^ 1, P.err, abort_v) && ok;
-          if (ok) {
-            const uint32_t prow = remote_p + sb * kPSlot;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              st_async_v4(prow + sw128_off(hrow, k), make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]),
-                          remote_pfull[sb]);
-            if (hf == 0) st_async_b32(remote_alpha + (sb * 128 + hrow) * 4, __float_as_uint(alpha), remote_pfull[sb]);
-          }
+          ++tc;
         }
-        if (hf == 0) st_async_b32(remote_final + hrow * 4, __float_as_uint(m_used), remote_ffull);
-        st_async_b32(remote_final + (128 + hf * 128 + hrow) * 4, __float_as_uint(l_sum), remote_ffull);
-      } else {
-        // ----------------------------------------- correction (CTA 1)
-        n_rows = row_count();
-        const int n_tiles = (n_rows + kTile - 1) / kTile;
-        int consumed = 0;  // odone phases observed
-        for (int j = 0; j < n_tiles && ok; ++j) {
-          const int ps = j & 1;
-          if (!mbar_wait_polling<true>(&bars.pfull[ps], (j >> 1) & 1, P.err, abort_v)) { ok = false; break; }
-          const float alpha = sAlpha[ps * 128 + hrow];
-          const bool need = __any_sync(0xffffffffu, alpha != 1.f) && j > 0;
-          if (need) {
-            // O must hold PV of tile j-1 before it is rescaled.
-            while (consumed < j) {
-              if (!mbar_wait_polling<false>(&bars.odone, consumed & 1, P.err, abort_v)) { ok = false; break; }
-              ++consumed;
-            }
-            if (!ok) break;
+        if (d.last) break;
+      }
+      if (rank == 0 && lane == 0) mbar_arrive(&bars.cdone);
+    }
+  } else if (warp < kSoftWarps) {
+    setmaxnreg_inc<kRegsSoft>();
+    const int hrow = (warp & 3) * 32 + lane, hf = warp >> 2;
+    bool ok = true;
+    uint32_t tc = 0;
+    if (rank == 0) {
+      // ------------------------------------------------- softmax (CTA 0)
+      // Two threads per head, each 64 of a tile's 128 rows.
+      const uint32_t remote_p = mapa(smem_u32(sP), 1) + hf * kUnit;
+      const uint32_t remote_alpha = mapa(smem_u32(sAlpha), 1);
+      const uint32_t remote_final = mapa(smem_u32(sFinal), 1);
+      const uint32_t remote_pfull[2] = {mapa(smem_u32(&bars.pfull[0]), 1), mapa(smem_u32(&bars.pfull[1]), 1)};
+      const uint32_t remote_ffull = mapa(smem_u32(&bars.ffull), 1);
+      const uint64_t scale2 = pack_f32x2(P.scale_log2, P.scale_log2), one2 = pack_f32x2(1.f, 1.f);
+      for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
+        float m_used = neg_inf(), l_sum = 0.f;
+        while (ok) {
+          Desc d;
+          if (!next_desc(d)) { ok = false; break; }
+          if (d.rows > 0) {
+            const uint32_t sb = tc & 1, ph = (tc >> 1) & 1;
+            const uint32_t v_lo = hf ? d.valid[2] : d.valid[0], v_hi = hf ? d.valid[3] : d.valid[1];
+            if (!WAIT(bars.sfull[sb], ph)) { ok = false; break; }
             tc_fence_after();
-            for (int c0 = hf * 256; c0 < hf * 256 + 256; c0 += 32) {
-              uint32_t v[32];
-              tmem_ld32(tmem + lane_off + c0, v);
+            // two passes over the 64 scores, 32 at a time: the maximum, then the
+            // exponentials (reading them twice keeps registers and code small)
+            const uint32_t s_tmem = tmem + lane_off + kTmemS + sb * kTile + hf * 64;
+            float m_tile = neg_inf();
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              uint32_t s[32];
+              tmem_ld32(s_tmem + x * 32, s);
               tmem_ld_wait();
+              mask_scores(s, x ? v_hi : v_lo);
+              float mt[4] = {m_tile, neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-              tmem_st32(tmem + lane_off + c0, v);
+              for (int k = 0; k < 32; ++k) mt[k & 3] = fmaxf(mt[k & 3], __uint_as_float(s[k]));
+              m_tile = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
             }
-            tmem_st_wait();
+            m_tile *= P.scale_log2;
+            // the other 64 rows' maximum, from the warp that holds them
+            sMax[sb * 256 + hf * 128 + hrow] = m_tile;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.mx[warp & 3]);
+            if (!WAIT(bars.mx[warp & 3], tc & 1)) { ok = false; break; }
+            m_tile = fmaxf(m_tile, sMax[sb * 256 + (hf ^ 1) * 128 + hrow]);
+            float alpha = 1.f;
+            if (m_tile > m_used + 8.f) {  // also taken when m_used is -inf
+              alpha = ex2_approx(m_used - m_tile);
+              l_sum *= alpha;
+              m_used = m_tile;
+            }
+            if (!WAIT_CLUSTER(bars.pfree[sb], ph ^ 1)) { ok = false; break; }
+            const float msub = m_used == neg_inf() ? 0.f : -m_used;
+            const uint64_t msub2 = pack_f32x2(msub, msub);
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              uint32_t s[32];
+              tmem_ld32(s_tmem + x * 32, s);
+              tmem_ld_wait();
+              mask_scores(s, x ? v_hi : v_lo);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const uint64_t y =
+                    fma_f32x2(pack_f32x2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2, msub2);
+                const float p0 = ex2_approx(lo_f32(y)), p1 = ex2_approx(hi_f32(y));
+                sum2[k & 1] = fma_f32x2(pack_f32x2(p0, p1), one2, sum2[k & 1]);
+                __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+                s[k] = *reinterpret_cast<uint32_t*>(&pb);
+              }
+              const uint32_t prow = remote_p + sb * kPSlot;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                st_async_v4(prow + sw128_off(hrow, x * 4 + k), make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]),
+                            remote_pfull[sb]);
+            }
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.sempty[sb]);
+            l_sum += (lo_f32(sum2[0]) + hi_f32(sum2[0])) + (lo_f32(sum2[1]) + hi_f32(sum2[1]));
+            if (hf == 0) st_async_b32(remote_alpha + (sb * 128 + hrow) * 4, __float_as_uint(alpha), remote_pfull[sb]);
+            ++tc;
           }
-          fence_proxy_async_smem();  // P arrived through st.async; the MMA reads it
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.ready[ps]);
-          // keep at most one PV completion unobserved
-          while (consumed < j) {
-            if (!mbar_wait_polling<false>(&bars.odone, consumed & 1, P.err, abort_v)) { ok = false; break; }
-            ++consumed;
-          }
+          if (d.last) break;
+        }
+        if (ok && n > 0) ok = WAIT_CLUSTER(bars.ffree, (n - 1) & 1);
+        if (ok) {
+          if (hf == 0) st_async_b32(remote_final + hrow * 4, __float_as_uint(m_used), remote_ffull);
+          st_async_b32(remote_final + (128 + hf * 128 + hrow) * 4, __float_as_uint(l_sum), remote_ffull);
         }
       }
     } else {
-      setmaxnreg_dec<kRegsLast>();
-      if (warp == kMmaWarp && rank == 0) {
-        // ---------------------------------------------- QK^T MMA (CTA 0)
-        if (lane == 0) {
-          n_rows = row_count();
-          const int n_tiles = (n_rows + kTile - 1) / kTile;
-          const uint32_t base = smem_u32(smem);
-          if (n_tiles > 0 && mbar_wait_polling<false>(&bars.qready, 0, P.err, abort_v)) tc_fence_after();
-          for (int j = 0; j < n_tiles && ok; ++j) {
-            const int sb = j & 1;
-            const int rows_t = min(kTile, n_rows - j * kTile);
-            const uint32_t idesc = idesc_f16(128, (rows_t + 31) & ~31, kFmtBF16, 0, 0);
-            const uint32_t d = tmem + kTmemS + sb * kTile;
-            if (!mbar_wait_polling<false>(&bars.sempty[sb], ((j >> 1) & 1) ^ 1, P.err, abort_v)) break;
-            for (int qd = 0; qd < 4 && ok; ++qd) {
-              ok = mbar_wait_polling<false>(&bars.full[qd], j & 1, P.err, abort_v);
+      // ------------------------------- correction and epilogue (CTA 1)
+      const uint32_t remote_ffree = mapa(smem_u32(&bars.ffree), 0);
+      uint32_t consumed = 0;  // odone phases observed
+      uint32_t stores = 0;    // output atoms of this half
+      for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
+        const int chunk = item % P.n_chunks, th = item / P.n_chunks, hb = th % P.head_blocks, t = th / P.head_blocks;
+        bool first = true;
+        while (ok) {
+          Desc d;
+          if (!next_desc(d)) { ok = false; break; }
+          if (d.rows > 0) {
+            const uint32_t ps = tc & 1;
+            if (!WAIT_CLUSTER(bars.pfull[ps], (tc >> 1) & 1)) { ok = false; break; }
+            const float alpha = sAlpha[ps * 128 + hrow];
+            const bool need = __any_sync(0xffffffffu, alpha != 1.f) && !first;
+            if (need) {
+              // O must hold the previous tile's product before it is rescaled.
+              while (ok && consumed < tc) {
+                ok = WAIT(bars.odone[consumed & 1], (consumed >> 1) & 1);
+                ++consumed;
+              }
               if (!ok) break;
               tc_fence_after();
+#pragma unroll 1
+              for (int c0 = hf * 256; c0 < hf * 256 + 256; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(tmem + lane_off + c0, v);
+                tmem_ld_wait();
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint64_t bd = smem_desc(base + qd * kSlot + (kk / 4) * kAtom + (kk % 4) * 32, 16, 1024, kSwizzle128B);
-                mma_ts(d, tmem + qd * 64 + kk * 8, bd, idesc, (qd | kk) != 0 ? 1u : 0u);
+                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                tmem_st32(tmem + lane_off + c0, v);
               }
-              mma_commit(&bars.empty[qd]);
+              tmem_st_wait();
+              tc_fence_before();
             }
-            if (!ok || !mbar_wait_polling<false>(&bars.rfull[sb], (j >> 1) & 1, P.err, abort_v)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t ad = smem_desc(base + kOffQrope + kk * 32, 16, 1024, kSwizzle128B);
-              const uint64_t bd = smem_desc(base + kOffKrope + sb * kAtom + kk * 32, 16, 1024, kSwizzle128B);
-              mma_ss(d, ad, bd, idesc, 1u);
+            fence_proxy_async_smem();  // P arrived through st.async; the MMA reads it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.ready[ps]);
+            // keep at most one completed product unobserved
+            while (ok && consumed < tc) {
+              ok = WAIT(bars.odone[consumed & 1], (consumed >> 1) & 1);
+              ++consumed;
             }
-            mma_commit(&bars.rempty[sb]);
-            mma_commit(&bars.sfull[sb]);
+            ++tc;
+            first = false;
           }
-          // every MMA issued has completed before the tensor memory is freed
-          mma_commit(&bars.mdrain);
-          mbar_drain(&bars.mdrain, 0);
+          if (d.last) break;
         }
-      } else if (warp == kMmaWarp) {
-        // ------------------------------------------------- PV MMA (CTA 1)
-        if (lane == 0) {
-          n_rows = row_count();
-          const int n_tiles = (n_rows + kTile - 1) / kTile;
-          const uint32_t idesc = idesc_f16(128, 256, kFmtBF16, 0, 1);
-          const uint32_t vbase = smem_u32(smem), pbase = smem_u32(sP);
-          for (int j = 0; j < n_tiles && ok; ++j) {
-            const int ps = j & 1;
-            const int rows_t = min(kTile, n_rows - j * kTile);
-            if (!mbar_wait_polling<false>(&bars.ready[ps], (j >> 1) & 1, P.err, abort_v)) break;
-            for (int qd = 0; qd * 32 < rows_t; ++qd) {
-              ok = mbar_wait_polling<false>(&bars.full[qd], j & 1, P.err, abort_v);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {
-                const uint64_t ad =
-                    smem_desc(pbase + ps * kPSlot + (qd >> 1) * kAtom + ((qd & 1) * 2 + kk) * 32, 16, 1024, kSwizzle128B);
-#pragma unroll
-                for (int nh = 0; nh < 2; ++nh) {
-                  const uint64_t bd = smem_desc(vbase + qd * kSlot + nh * 4 * 4096 + kk * 16 * 128, 4096, 1024, kSwizzle128B);
-                  mma_ss(tmem + nh * 256, ad, bd, idesc, (j | qd | kk) != 0 ? 1u : 0u);
-                }
-              }
-              mma_commit(&bars.empty[qd]);
-            }
-            if (!ok) break;
-            mma_commit(&bars.pcons[ps]);
-            mma_commit(&bars.odone);
-            if (j + 1 == n_tiles) mma_commit(&bars.alldone);
+        // Every product is in O and (maximum, sums) of each head have arrived:
+        // normalise, convert to bf16 into a swizzled staging atom and write it
+        // with TMA stores, 64 columns x 128 heads per box (heads past H are
+        // clipped by the tensor map).
+        while (ok && consumed < tc) {
+          ok = WAIT(bars.odone[consumed & 1], (consumed >> 1) & 1);
+          ++consumed;
+        }
+        if (ok) ok = WAIT_CLUSTER(bars.ffull, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const float m = sFinal[hrow], l = sFinal[128 + hrow] + sFinal[256 + hrow];
+        __syncwarp();
+        if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&bars.ffull, kFinalBytes);  // the next item's
+        if (lane == 0) mbar_arrive_remote(remote_ffree);
+        const bool empty = first || l == 0.f;
+        const int h = hb * 128 + hrow;
+        float inv_l = empty ? 0.f : 1.f / l;
+        float lse2 = empty ? neg_inf() : m + log2f(l);  // log2 units
+        if (P.sink != nullptr && P.n_chunks == 1) {
+          // The sink adds 2^s2 to the denominator; taken relative to max(m, s2)
+          // so that neither term overflows.  (Split chunks get it in the merge.)
+          const float s2 = (h < P.H ? __ldg(P.sink + h) : neg_inf()) * 1.4426950408889634f;
+          if (!empty) {
+            const float mx = fmaxf(m, s2);
+            const float den = l * exp2f(m - mx) + exp2f(s2 - mx);
+            inv_l = exp2f(m - mx) / den;
+            lse2 = mx + log2f(den);
+          } else {
+            lse2 = s2;
           }
-          mma_commit(&bars.mdrain);
-          mbar_drain(&bars.mdrain, 0);
         }
-      } else if (warp == kRelayWarp && rank == 1) {
-        // ----------------------------------- relay: P slot consumed -> CTA 0
-        if (lane == 0) {
-          n_rows = row_count();
-          const int n_tiles = (n_rows + kTile - 1) / kTile;
-          const uint32_t remote_pfree[2] = {mapa(smem_u32(&bars.pfree[0]), 0), mapa(smem_u32(&bars.pfree[1]), 0)};
-          for (int j = 0; j + 2 < n_tiles; ++j) {
-            const int ps = j & 1;
-            if (!mbar_wait_polling<false>(&bars.pcons[ps], (j >> 1) & 1, P.err, abort_v)) break;
-            mbar_arrive_expect_tx(&bars.pfull[ps], kPBytes);  // arm the slot's next use
-            mbar_arrive_remote(remote_pfree[ps]);
+        uint8_t* stage = smem + kOffStage + hf * kUnit;
+#pragma unroll 1
+        for (int c0 = hf * 256; c0 < hf * 256 + 256; c0 += 64, ++stores) {  // one atom per round
+          if (stores > 0 && !WAIT(bars.stfree[hf], (stores - 1) & 1)) { ok = false; break; }
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            uint32_t v[32], pk[16];
+            tmem_ld32(tmem + lane_off + c0 + x * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              __nv_bfloat162 w =
+                  __floats2bfloat162_rn(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
+              pk[k] = empty ? 0u : *reinterpret_cast<uint32_t*>(&w);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(stage + sw128_off(hrow, x * 4 + k)) =
+                  make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.stfull[hf]);
+          if ((warp & 3) == 0 && lane == 0) {  // the four warps of this half have written the atom
+            if (WAIT1(bars.stfull[hf], stores & 1)) {
+              tma_store_3d(&tmap_o, stage, c0, hb * 128, P.n_chunks == 1 ? t : t * P.n_chunks + chunk);
+              bulk_commit_group();
+              bulk_wait_group_read0();
+              mbar_arrive(&bars.stfree[hf]);
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        if (hf == 0 && h < P.H) {
+          if (P.n_chunks == 1) {
+            if (P.lse != nullptr) P.lse[static_cast<size_t>(t) * P.H + h] = lse2 * 0.69314718055994531f;
+          } else {
+            P.part_ml[(static_cast<size_t>(t) * P.n_chunks + chunk) * P.H + h] =
+                empty ? make_float2(neg_inf(), 0.f) : make_float2(m, l);
           }
         }
       }
     }
-    if (rank == 1 && warp < kSoftWarps) {
-      // ------------------------------------------------- epilogue (CTA 1)
-      // Every PV product is in O and (maximum, sums) of each head have arrived:
-      // normalise, convert to bf16 into a swizzled staging tile (the free V
-      // slots) and write it with TMA stores, 64 columns x 128 heads per box
-      // (heads past H are clipped by the tensor map).
-      __syncwarp();
-      const bool none = n_rows == 0;
-      if (ok && !none) ok = mbar_wait_polling<false>(&bars.alldone, 0, P.err, abort_v);
-      if (ok) ok = mbar_wait_polling<true>(&bars.ffull, 0, P.err, abort_v);
-      tc_fence_after();
-      const int hrow = (warp & 3) * 32 + lane, half = warp >> 2;
-      const float m = sFinal[hrow], l = sFinal[128 + hrow] + sFinal[256 + hrow];
-      const bool empty = !ok || none || l == 0.f;
-      const int h = hb * 128 + hrow;
-      float inv_l = empty ? 0.f : 1.f / l;
-      float lse2 = empty ? neg_inf() : m + log2f(l);  // log2 units
-      if (P.sink != nullptr && P.n_chunks == 1) {
-        // The sink adds 2^s2 to the denominator; taken relative to max(m, s2) so
-        // that neither term overflows.  (Split chunks get it in the merge.)
-        const float s2 = (h < P.H ? __ldg(P.sink + h) : neg_inf()) * 1.4426950408889634f;
-        if (!empty) {
-          const float mx = fmaxf(m, s2);
-          const float den = l * exp2f(m - mx) + exp2f(s2 - mx);
-          inv_l = exp2f(m - mx) / den;
-          lse2 = mx + log2f(den);
-        } else {
-          lse2 = s2;
+  } else {
+    setmaxnreg_inc<kRegsLast>();
+    if (warp == kRowWarp) {
+      // --------------------------------------------- row gathers (both CTAs)
+      griddep_wait();  // the index rows come from the previous kernel
+      Ring uc;
+      uint32_t tc = 0, n_units = 0;
+      bool ok = true;
+      for (int item = cluster; item < P.items && ok; item += clusters) {
+        const int chunk = item % P.n_chunks, t = item / P.n_chunks / P.head_blocks;
+        int b = t / P.n_q;
+        bool bad_seq = false;
+        if (P.seq != nullptr) {  // a token outside [0, B) reads no row and gets out = 0
+          b = __ldg(P.seq + t);
+          bad_seq = b < 0 || b >= P.B;
+          if (bad_seq && lane == 0) atomicOr(P.err, kErrBadIndex);
         }
-      }
-#pragma unroll 1
-      for (int c0 = half * 256; c0 < half * 256 + 256; c0 += 64) {  // one atom per round
-        uint8_t* stage = smem + (c0 / 64) * kAtom;
+        const int slot_begin = chunk * P.chunk_rows;
+        const int rows_here = bad_seq ? 0 : min(P.chunk_rows, P.topk - slot_begin);
+        const int32_t* idx = P.idx + static_cast<size_t>(t) * P.topk + slot_begin;
+        // the item ends at its last valid slot, found from the end
+        int n_rows = rows_here;
+        if (rows_here > 0) {
+          const int s = __ldg(idx + rows_here - 1);
+          if (s < 0 || s >= P.max_L) {
+            n_rows = 0;
+            for (int end = rows_here; end > 0 && n_rows == 0; end -= 256) {
+              int mx = -1;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t v[32], pk[16];
-          tmem_ld32(tmem + lane_off + c0 + x * 32, v);
-          tmem_ld_wait();
+              for (int x = 0; x < 8; ++x) {
+                const int i = end - 256 + x * 32 + lane;
+                const int v = i >= 0 ? __ldg(idx + i) : -1;
+                if (v >= 0 && v < P.max_L) mx = i;
+              }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            __nv_bfloat162 w = __floats2bfloat162_rn(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
-            pk[k] = empty ? 0u : *reinterpret_cast<uint32_t*>(&w);
+              for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              n_rows = mx + 1;
+            }
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(stage + sw128_off(hrow, x * 4 + k)) =
-                make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
         }
-        // the 4 warps of this half have written the atom: store it while they
-        // convert the next one
-        fence_proxy_async_smem();
-        asm volatile("bar.sync %0, 128;" ::"r"(2 + half) : "memory");
-        if ((warp & 3) == 0 && lane == 0) {
-          tma_store_3d(&tmap_o, stage, c0, hb * 128, P.n_chunks == 1 ? t : t * P.n_chunks + chunk);
-          bulk_commit_group();
+        for (int j0 = 0; ok; j0 += kTile) {
+          const int rows_t = max(0, min(kTile, n_rows - j0));
+          const bool last = j0 + kTile >= n_rows;
+          // rows 4 lane .. 4 lane + 3 of the tile; one that selects nothing is
+          // gathered as row 0 and masked, one that does not exist is recorded too
+          int r[4];
+          uint32_t nib = 0;
+          {
+            int s[4], pg[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int i = j0 + 4 * lane + x;
+              s[x] = i < n_rows ? __ldg(idx + i) : -1;
+              if (s[x] >= P.max_L) s[x] = -1;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              pg[x] = s[x] >= 0 && P.block_table != nullptr
+                          ? __ldg(P.block_table + static_cast<size_t>(b) * P.max_blocks + s[x] / P.block_size) : b;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              r[x] = 0;
+              if (s[x] >= 0) {
+                nib |= 1u << x;
+                const int64_t row = P.block_table != nullptr
+                                        ? static_cast<int64_t>(pg[x]) * P.block_size + s[x] % P.block_size
+                                        : static_cast<int64_t>(b) * P.max_L + s[x];
+                if (pg[x] < 0 || row >= P.rows) atomicOr(P.err, kErrBadIndex);
+                else r[x] = static_cast<int>(row);
+              }
+            }
+          }
+          nib <<= (lane & 7) * 4;
+#pragma unroll
+          for (int o = 4; o; o >>= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
+          const uint32_t di = dc % kDescs;
+          if (!WAIT(bars.dempty[di], ((dc / kDescs) & 1) ^ 1)) { ok = false; break; }
+          if ((lane & 7) == 0) descs[di].valid[lane >> 3] = nib;
+          if (lane == 0) {
+            descs[di].rows = rows_t;
+            descs[di].last = last;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.dfull[di]);
+          ++dc;
+          const int quads = ((rows_t + 15) >> 4) * 4;  // gathers: whole 16-row steps
+          if (rows_t > 0 && rank == 0) {
+            const uint32_t rs = tc & 1, ph = (tc >> 1) & 1;
+            if (!WAIT(bars.rempty[rs], ph ^ 1) || !WAIT(bars.kpempty[rs], ph ^ 1)) { ok = false; break; }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bars.rfull[rs], quads * 4 * kRawRow);
+              mbar_arrive_expect_tx(&bars.kpfull[rs], quads * 4 * 128);
+            }
+            __syncwarp();
+            if (lane < quads) {
+              tma_gather4(smem + kOffRaw0 + rs * kRawTile + lane * 4 * kRawRow, &tmap_raw, 0, r, &bars.rfull[rs]);
+              tma_gather4(smem + kOffKrope + rs * kUnit + lane * 4 * 128, &tmap_rope, kKv4Rope / 2, r, &bars.kpfull[rs]);
+            }
+            ++tc;
+          } else if (rows_t > 0) {
+            for (int k = 0; k < pv_units(rows_t); ++k, uc.add(1)) {
+              if (!WAIT(bars.rempty[uc.slot], uc.phase ^ 1)) { ok = false; break; }
+              if (lane == 0) {
+                if (k * 4 < quads) mbar_arrive_expect_tx(&bars.rfull[uc.slot], kRawUnit);
+                else mbar_arrive(&bars.rfull[uc.slot]);
+              }
+              __syncwarp();
+              if ((lane >> 2) == k && k * 4 < quads)
+                tma_gather4(smem + kOffRaw1 + uc.slot * kRawUnit + (lane & 3) * 4 * kRawRow, &tmap_raw, 0, r,
+                            &bars.rfull[uc.slot]);
+              ++n_units;
+            }
+          }
+          if (last) break;
         }
       }
-      if ((warp & 3) == 0 && lane == 0) bulk_wait_group_read0();
-      if (half == 0 && h < P.H) {
-        if (P.n_chunks == 1) {
-          if (P.lse != nullptr) P.lse[static_cast<size_t>(t) * P.H + h] = lse2 * 0.69314718055994531f;
-        } else {
-          P.part_ml[(static_cast<size_t>(t) * P.n_chunks + chunk) * P.H + h] =
-              empty ? make_float2(neg_inf(), 0.f) : make_float2(m, l);
+      if (lim->gave_up && lane == 0) {  // the copies in flight land before the CTA's memory is given up
+        for (uint32_t i = tc > 2 ? tc - 2 : 0; i < tc; ++i) {
+          mbar_drain(&bars.rfull[i & 1], (i >> 1) & 1);
+          mbar_drain(&bars.kpfull[i & 1], (i >> 1) & 1);
+        }
+        for (uint32_t i = n_units > kUnits ? n_units - kUnits : 0; i < n_units; ++i)
+          mbar_drain(&bars.rfull[i % kUnits], (i / kUnits) & 1);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp && rank == 0) {
+      // ---------------------------------------------- QK^T MMA (CTA 0)
+      if (elect_one()) {
+        Ring uc;
+        uint32_t tc = 0;
+        bool ok = true;
+        const uint32_t base = smem_u32(smem);
+        for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
+          ok = WAIT1(bars.qready, n & 1) && WAIT1(bars.qpfull, n & 1);
+          if (!ok) break;
+          tc_fence_after();
+          uc.add(8);
+          while (ok) {
+            Desc d;
+            if (!next_desc1(d)) { ok = false; break; }
+            if (d.rows > 0) {
+              const uint32_t sb = tc & 1, ph = (tc >> 1) & 1;
+              const uint32_t idesc = idesc_f16(128, (d.rows + 15) & ~15, kFmtBF16, 0, 0);
+              const uint32_t dt = tmem + kTmemS + sb * kTile;
+              if (!WAIT1(bars.sempty[sb], ph ^ 1) || !WAIT1(bars.kpfull[sb], ph)) { ok = false; break; }
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t ad = smem_desc(base + kOffQrope + kk * 32, 16, 1024, kSwizzle128B);
+                const uint64_t bd = smem_desc(base + kOffKrope + sb * kUnit + kk * 32, 16, 1024, kSwizzle128B);
+                mma_ss(dt, ad, bd, idesc, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&bars.kpempty[sb]);
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k, uc.add(1)) {
+                if (!WAIT1(bars.full[uc.slot], uc.phase)) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t bd = smem_desc(base + uc.slot * kUnit, 16, 1024, kSwizzle128B);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) mma_ts(dt, tmem + k * 32 + kk * 8, bd + kk * 2, idesc, 1u);
+                mma_commit(&bars.empty[uc.slot]);
+              }
+              if (!ok) break;
+              mma_commit(&bars.sfull[sb]);
+              ++tc;
+            }
+            if (d.last) break;
+          }
+          mma_commit(&bars.qfree);
+        }
+        // every MMA issued has completed before the tensor memory is freed
+        mma_commit(&bars.mdrain);
+        mbar_drain(&bars.mdrain, 0);
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------- PV MMA (CTA 1)
+      if (elect_one()) {
+        Ring uc;
+        uint32_t tc = 0;
+        bool ok = true;
+        const uint32_t idesc = idesc_f16(128, 256, kFmtBF16, 0, 1);
+        const uint32_t vbase = smem_u32(smem), pbase = smem_u32(sP);
+        for (int item = cluster; item < P.items && ok; item += clusters) {
+          uint32_t acc = 0;  // the item's first product overwrites O
+          while (ok) {
+            Desc d;
+            if (!next_desc1(d)) { ok = false; break; }
+            if (d.rows > 0) {
+              const uint32_t ps = tc & 1;
+              if (!WAIT1(bars.ready[ps], (tc >> 1) & 1)) { ok = false; break; }
+#pragma unroll 1
+              for (int k = 0; k < pv_units(d.rows); ++k, uc.add(1)) {
+                if (!WAIT1(bars.full[uc.slot], uc.phase)) { ok = false; break; }
+                if (k * 16 >= d.rows) {  // past the last row
+                  mma_commit(&bars.empty[uc.slot]);
+                  continue;
+                }
+                tc_fence_after();
+                const uint64_t ad = smem_desc(pbase + ps * kPSlot + (k >> 2) * kUnit + (k & 3) * 32, 16, 1024, kSwizzle128B);
+                const uint64_t bd = smem_desc(vbase + uc.slot * kUnit, 2048, 1024, kSwizzle128B);
+                mma_ss(tmem, ad, bd, idesc, acc);
+                mma_ss(tmem + 256, ad, bd + (4 * 2048 >> 4), idesc, acc);
+                acc = 1;
+                mma_commit(&bars.empty[uc.slot]);
+              }
+              if (!ok) break;
+              mma_commit(&bars.pcons[ps]);
+              mma_commit(&bars.odone[ps]);
+              ++tc;
+            }
+            if (d.last) break;
+          }
+        }
+        mma_commit(&bars.mdrain);
+        mbar_drain(&bars.mdrain, 0);
+      }
+    } else if (warp == kAuxWarp && rank == 0) {
+      // ------------------------------------------------------- q loads (CTA 0)
+      if (elect_one()) {
+        Ring uc, loading;
+        int inflight = 0, rope_loads = 0;
+        bool ok = true;
+        for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
+          const int th = item / P.n_chunks, hb = th % P.head_blocks, t = th / P.head_blocks;
+          // not before the previous item's last unit is converted: a wait for a unit's
+          // slot is by parity, and good for the slot's next use only
+          if (n > 0) ok = WAIT1(bars.cdone, (n - 1) & 1);
+          if (ok) inflight = 0;
+          for (int k = 0; k < 8 && ok; ++k, uc.add(1)) {
+            if (!WAIT1(bars.empty[uc.slot], uc.phase ^ 1)) { ok = false; break; }
+            mbar_arrive_expect_tx(&bars.full[uc.slot], kUnit);
+            mbar_arrive_n(&bars.full[uc.slot], 3);
+            tma_load_3d(smem + uc.slot * kUnit, &tmap_q, k * 64, hb * 128, t, &bars.full[uc.slot]);
+            loading = uc;
+            inflight = inflight < kUnits ? inflight + 1 : kUnits;
+          }
+          if (ok && n > 0) ok = WAIT1(bars.qfree, (n - 1) & 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars.qpfull, kUnit);
+          tma_load_3d(smem + kOffQrope, &tmap_q, 512, hb * 128, t, &bars.qpfull);
+          rope_loads = n + 1;
+          while (ok) {
+            Desc d;
+            if (!next_desc1(d)) { ok = false; break; }
+            if (d.rows > 0) uc.add(8);
+            if (d.last) break;
+          }
+        }
+        if (lim->gave_up) {  // the copies in flight land before the CTA's memory is given up
+          for (; inflight > 0; --inflight) {
+            drain_copy(&bars.full[loading.slot], loading.phase);
+            loading.slot = loading.slot > 0 ? loading.slot - 1 : (loading.phase ^= 1, kUnits - 1);
+          }
+          if (rope_loads > 0) mbar_drain(&bars.qpfull, (rope_loads - 1) & 1);
+        }
+      }
+    } else if (warp == kAuxWarp) {
+      // ----------------------------------- relay: P slot consumed -> CTA 0
+      if (elect_one()) {
+        const uint32_t remote_pfree[2] = {mapa(smem_u32(&bars.pfree[0]), 0), mapa(smem_u32(&bars.pfree[1]), 0)};
+        uint32_t tc = 0;
+        bool ok = true;
+        for (int item = cluster; item < P.items && ok; item += clusters) {
+          while (ok) {
+            Desc d;
+            if (!next_desc1(d)) { ok = false; break; }
+            if (d.rows > 0) {
+              const uint32_t ps = tc & 1;
+              if (!WAIT1(bars.pcons[ps], (tc >> 1) & 1)) { ok = false; break; }
+              mbar_arrive_expect_tx(&bars.pfull[ps], kPBytes);  // arm the slot's next use
+              mbar_arrive_remote(remote_pfree[ps]);
+              ++tc;
+            }
+            if (d.last) break;
+          }
         }
       }
     }
@@ -617,6 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no CTA leaves while its peer may still address it
+  if (tid == 0 && lim->gave_up) atomicOr(P.err, kErrTimeout);
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -654,7 +951,11 @@ __global__ void __launch_bounds__(256) attn_kv4_merge_kernel(const AttnKv4Params
     float Mb = M;
 #pragma unroll
     for (int i = 0; i < kMergeBatch; ++i) Mb = fmaxf(Mb, ml[i].x);
-    if (Mb == neg_inf()) continue;  // nothing visible yet
+    if (Mb == neg_inf()) {  // nothing visible yet (a sum that is not a number stays one)
+#pragma unroll
+      for (int i = 0; i < kMergeBatch; ++i) wsum += ml[i].y;
+      continue;
+    }
     const float r = exp2f(M - Mb);
     wsum *= r;
 #pragma unroll
@@ -696,14 +997,13 @@ __global__ void __launch_bounds__(256) attn_kv4_merge_kernel(const AttnKv4Params
     P.lse[static_cast<size_t>(t) * P.H + h] = wsum == 0.f ? neg_inf() : (M + log2f(wsum)) * 0.69314718055994531f;
 }
 
-// Chunks per token: as many clusters as the GPU holds at once, each a
-// multiple of 64 rows.
+// Chunks per token: as many as the GPU holds clusters for at once, each a
+// multiple of 16 rows (one step of the second product).
 void plan(const dsa_attn_kv4_args& a, int& head_blocks, int& n_chunks, int& chunk_rows) {
   head_blocks = (a.H + 127) / 128;
   const long long pairs = static_cast<long long>(a.T) * head_blocks;
-  const int units = (a.topk + 63) / 64;
   const int target = static_cast<int>(std::max<long long>(1, sm_count() / (2 * pairs)));
-  chunk_rows = (units + target - 1) / target * 64;
+  chunk_rows = ((a.topk + target - 1) / target + 63) / 64 * 64;
   n_chunks = (a.topk + chunk_rows - 1) / chunk_rows;
 }
 
@@ -721,8 +1021,9 @@ int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s) {
   AttnKv4Params P{};
   plan(a, P.head_blocks, P.n_chunks, P.chunk_rows);
   P.T = a.T; P.B = a.B; P.n_q = a.n_q; P.H = a.H; P.topk = a.topk; P.max_L = a.max_L;
+  P.items = a.T * P.head_blocks * P.n_chunks;
   P.scale_log2 = a.scale * 1.4426950408889634f;
-  P.q = a.q; P.kv4 = a.kv4; P.rows = a.cache_rows;
+  P.kv4 = a.kv4; P.rows = a.cache_rows;
   P.block_table = a.block_table; P.block_size = a.block_size; P.max_blocks = a.max_blocks;
   P.idx = a.topk_idx; P.out = a.out; P.lse = a.lse; P.sink = a.sink; P.seq = a.seq_of_token;
   if (P.seq != nullptr) P.n_q = 1;  // ignored with a map
@@ -734,16 +1035,21 @@ int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s) {
   P.err = error_word();
   if (!P.err) return DSA_ERR_CUDA;
 
-  // output (or the chunks' partial outputs): [Z, H, 512] bf16, stored as
-  // 64-column x 128-head boxes; heads past H are clipped by the map
-  alignas(64) CUtensorMap tmap_o;
+  // q [T, H, 576] in 64-dim x 128-head boxes (heads past H read as zeros); the
+  // cache's rows as 208 16-bit words, gathered row by row: codes and scale bytes,
+  // and the rotary dims; the output (or the chunks' partial outputs) [Z, H, 512]
+  // in 64-column x 128-head boxes (heads past H are clipped)
+  alignas(64) CUtensorMap tmap_q, tmap_raw, tmap_rope, tmap_o;
   {
-    const uint64_t z = static_cast<uint64_t>(a.T) * P.n_chunks;
-    const uint64_t dims[3] = {static_cast<uint64_t>(kDv), static_cast<uint64_t>(a.H), z};
-    const uint64_t strides[2] = {static_cast<uint64_t>(kDv) * 2, static_cast<uint64_t>(a.H) * kDv * 2};
-    const uint32_t box[3] = {64, 128, 1};
-    if (!encode_tmap(&tmap_o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, P.n_chunks == 1 ? P.out : P.part_o, dims, strides,
-                     box, 128))
+    const uint64_t H = static_cast<uint64_t>(a.H), T = static_cast<uint64_t>(a.T);
+    const uint64_t dq[3] = {kDqk, H, T}, sq[2] = {kDqk * 2, H * kDqk * 2};
+    const uint64_t dk[2] = {kKv4Row / 2, static_cast<uint64_t>(a.cache_rows)}, sk[1] = {kKv4Row};
+    const uint64_t od[3] = {kDv, H, T * P.n_chunks}, os[2] = {kDv * 2, H * kDv * 2};
+    const uint32_t box[3] = {64, 128, 1}, box_raw[2] = {kRawRow / 2, 1}, box_rope[2] = {kKv4RopeDims, 1};
+    if (!encode_tmap(&tmap_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dq, sq, box, 128) ||
+        !encode_tmap(&tmap_raw, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.kv4, dk, sk, box_raw, 0) ||
+        !encode_tmap(&tmap_rope, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.kv4, dk, sk, box_rope, 128) ||
+        !encode_tmap(&tmap_o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, P.n_chunks == 1 ? P.out : P.part_o, od, os, box, 128))
       return DSA_ERR_CUDA;
   }
   cudaError_t e = cudaFuncSetAttribute(attn_kv4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -756,13 +1062,13 @@ int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s) {
   attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(P.n_chunks * 2, P.head_blocks, a.T);
+  cfg.gridDim = dim3(2 * std::min(P.items, std::max(1, sm_count() / 2)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, attn_kv4_kernel, P, tmap_o);
+  e = cudaLaunchKernelEx(&cfg, attn_kv4_kernel, P, tmap_q, tmap_raw, tmap_rope, tmap_o);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   if (P.n_chunks > 1) {
     cudaLaunchConfig_t c2 = {};
