@@ -41,17 +41,20 @@ namespace {
 constexpr int kDqk = 576, kDv = 512;
 constexpr int kTile = 128;                 // rows per tile
 constexpr int kUnit = 16384;               // 128 rows x 64 dims, or 16 rows x 512 dims, bf16
-constexpr int kUnits = 6;                  // units in flight
+constexpr int kUnits = 4;                  // units in flight, one per group of conversion warps
+constexpr int kRawSlots = 12;              // CTA 1: raw units in flight, three per group
 constexpr int kPSlot = 32768;              // P [128 heads x 128 rows] bf16
 constexpr int kRawRow = 288;               // codes and scale bytes of a row
 constexpr int kRawTile = kTile * kRawRow;  // CTA 0: a tile's raw rows
 constexpr int kRawUnit = 16 * kRawRow;     // CTA 1: 16 raw rows
-constexpr int kDescs = 8;
+constexpr int kDescs = 4;
 // 28 warps in seven warpgroups: 0-1 softmax (CTA 0), correction and epilogue
-// (CTA 1); 2-5 conversion; 6 MMA issue, row gathers, q loads / P-slot relay.
+// (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, q and rotary K loads (CTA 0) or
+// the P-slot relay (CTA 1), raw row loads.
 // The launch grants 72 registers a thread: 896 x 72 = 256 x 80 + 512 x 64 + 128 x 88.
 constexpr int kThreads = 896;
-constexpr int kSoftWarps = 8, kConvWarps = 16, kFirstConv = 8, kMmaWarp = 24, kRowWarp = 25, kAuxWarp = 26;
+constexpr int kSoftWarps = 8, kConvWarps = 16, kFirstConv = 8, kMmaWarp = 24, kRowWarp = 25, kAuxWarp = 26,
+              kRawWarp = 27;
 constexpr int kRegsLaunch = 72, kRegsSoft = 80, kRegsConv = 64, kRegsLast = 88;
 static_assert(256 * kRegsSoft + 512 * kRegsConv + 128 * kRegsLast <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
@@ -66,9 +69,9 @@ constexpr uint32_t kTmemS = 256;                   // CTA 0: q in columns [0, 25
 constexpr int kOffQrope = kUnits * kUnit, kOffKrope = kOffQrope + kUnit, kOffRaw0 = kOffKrope + 2 * kUnit,
               kOffMax = kOffRaw0 + 2 * kRawTile, kEnd0 = kOffMax + 2048;
 constexpr int kOffP = kUnits * kUnit, kOffStage = kOffP + 2 * kPSlot, kOffRaw1 = kOffStage + 2 * kUnit,
-              kOffAlpha = kOffRaw1 + kUnits * kRawUnit, kOffFinal = kOffAlpha + 1024, kEnd1 = kOffFinal + 1536;
+              kOffAlpha = kOffRaw1 + kRawSlots * kRawUnit, kOffFinal = kOffAlpha + 1024, kEnd1 = kOffFinal + 1536;
 constexpr int kSmem = 1024 + (kEnd0 > kEnd1 ? kEnd0 : kEnd1);
-static_assert(kSmem + 2048 <= 232448, "shared memory of a CTA");
+static_assert(kSmem + 1024 + kDescs * 576 <= 232448, "shared memory of a CTA");
 
 struct AttnKv4Params {
   int T, B, n_q, H, topk, max_L, n_chunks, chunk_rows, head_blocks, items;
@@ -87,17 +90,20 @@ struct AttnKv4Params {
   uint32_t* err;
 };
 
-// What every role needs to know of a tile.
-struct __align__(16) Desc {
+// What the roles need to know of a tile, and its physical rows.
+struct Desc {
   uint32_t valid[4];  // rows that are selected (the others are masked, their values zeros)
   int rows;           // rows of the tile up to the item's last selected one; 0: the item selects nothing
   int last;           // the item's last tile
-  int pad[2];
+};
+struct __align__(16) TileDesc {
+  int4 row[kTile / 4];
+  Desc d;
 };
 
 struct __align__(8) Bars {
   uint64_t full[kUnits], empty[kUnits];      // units (CTA 0: K and q; CTA 1: V)
-  uint64_t rfull[kUnits], rempty[kUnits];    // raw rows (CTA 0: two tiles; CTA 1: units)
+  uint64_t rfull[kRawSlots], rempty[kRawSlots];  // raw rows (CTA 0: two tiles; CTA 1: units)
   uint64_t dfull[kDescs], dempty[kDescs];    // tile descriptors
   uint64_t kpfull[2], kpempty[2];            // CTA 0: rotary K buffers
   uint64_t sfull[2], sempty[2];              // CTA 0: S buffers
@@ -112,9 +118,8 @@ struct __align__(8) Bars {
   uint64_t mdrain;                           // the MMA thread's last commit
 };
 
-// Units of 16 rows that a tile takes in CTA 1: four or eight, so that every group
-// of conversion warps has its share of every tile (a group that sat tiles out
-// could wait for a slot three uses ahead, where its barrier's parity misleads).
+// Units of 16 rows that a tile takes in CTA 1: four or eight, a use or two of every
+// slot.
 __device__ __forceinline__ int pv_units(int rows) { return rows > kTile / 2 ? 8 : 4; }
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
@@ -131,11 +136,11 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
 }
 // Four rows r0..r3 of the map's 2-D tensor, from column x on, to consecutive
 // rows of shared memory.
-__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int x, const int (&r)[4], uint64_t* bar) {
+__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int x, const int4& r, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w),
         "r"(smem_u32(bar))
       : "memory");
 }
@@ -154,66 +159,40 @@ __device__ __forceinline__ void drain_copy(uint64_t* bar, uint32_t parity) {
   while (!mbar_test(bar, parity) && globaltimer_ns() - t0 < 100000) {}
 }
 
-// Scores of rows that are not selected.
-__device__ __forceinline__ void mask_scores(uint32_t (&s)[32], uint32_t valid) {
-  if (valid == 0xffffffffu) return;
-#pragma unroll
-  for (int k = 0; k < 32; ++k)
-    if (!((valid >> k) & 1u)) s[k] = 0xff800000u;
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
-
-// A counter over a ring of kUnits slots: the slot and the phase of its use.
-struct Ring {
-  uint32_t slot = 0, phase = 0;
-  __device__ __forceinline__ void add(uint32_t n) {  // n <= 8
-    slot += n;
-    while (slot >= kUnits) { slot -= kUnits; phase ^= 1; }
-  }
-  __device__ __forceinline__ Ring plus(uint32_t n) const { Ring r = *this; r.add(n); return r; }
-};
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Converts the 32 dims of one 16-byte piece of a raw row and stores them at
-// 16-byte chunks c4..c4+3 of the 128-byte row at dst, swizzled by r7 = row mod 8.
-// The lanes (row = lane / 2, piece = lane mod 2) of a quarter warp read and write
-// all 32 banks once.
-__device__ __forceinline__ void convert_piece(const uint8_t* raw, int piece_off, int scale_off, bool on, uint32_t dst,
-                                              uint32_t c4, uint32_t r7) {
-  uint4 w = *reinterpret_cast<const uint4*>(raw + piece_off);
-  uint32_t sc = *reinterpret_cast<const uint16_t*>(raw + scale_off);
-  if (!on) {
-    w = make_uint4(0, 0, 0, 0);
-    sc = 0;
-  }
-  const Kv4Scale lo = kv4_scale(sc & 255u), hi = kv4_scale(sc >> 8);
-  const uint32_t C = (c4 ^ r7) << 4;
-  st_shared_v4(dst + (C ^ 0), kv4_codes8(w.x, lo));
-  st_shared_v4(dst + (C ^ 16), kv4_codes8(w.y, lo));
-  st_shared_v4(dst + (C ^ 32), kv4_codes8(w.z, hi));
-  st_shared_v4(dst + (C ^ 48), kv4_codes8(w.w, hi));
-}
-
-// Bounded wait for a phase of a barrier, in as little code as will do: the roles
-// of this kernel run at the same time from one instruction cache (with the waits
-// of the other kernels the code was 133 KB and a third of the cache's requests
-// missed; the 4096-token case took 5.97 ms).  `lim` holds the limit and the suspend
-// hint in force, in shared memory.
+// Bounded wait for a phase of a barrier, in as little code and as few instructions
+// as will do: the roles of this kernel run at the same time from one instruction
+// cache and one set of schedulers.  (With the other kernels' waits inlined the code
+// was 133 KB and a third of the cache's requests missed: 5.97 ms for the 4096-token
+// case.)  A try blocks in the hardware for a while by itself; every 32nd that fails
+// reads the clock (each one under a limit below 20 us, in failure tests).
 struct WaitLimit {
   uint64_t ns;
-  uint32_t hint;
+  uint32_t mask;
   int gave_up;
 };
 template <bool kCluster>
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile WaitLimit* lim) {
-  if (kCluster ? mbar_probe_cluster(bar, parity) : mbar_probe(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = 0;
 #pragma unroll 1
-  while (!(kCluster ? mbar_try_wait_cluster(bar, parity, lim->hint) : mbar_try_wait(bar, parity, lim->hint))) {
-    if (lim->gave_up) return false;
-    if (globaltimer_ns() - t0 > lim->ns) {
+  for (uint32_t n = 1; !(kCluster ? mbar_probe_cluster(bar, parity) : mbar_probe(bar, parity)); ++n) {
+    if (n & lim->mask) continue;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (lim->gave_up || now - t0 > lim->ns) {
       lim->gave_up = 1;  // reported when the CTA ends
       return false;
     }
@@ -233,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Bars bars;
-  __shared__ Desc descs[kDescs];
+  __shared__ TileDesc descs[kDescs];
   __shared__ uint32_t tmem_base;
   __shared__ WaitLimit wait_limit;
 
@@ -246,13 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sMax = reinterpret_cast<float*>(smem + kOffMax);      // [2][2][128]
 
   if (tid == 0) {
-    for (int i = 0; i < kUnits; ++i) {
-      mbar_init(&bars.full[i], 4); mbar_init(&bars.empty[i], 1);
-      mbar_init(&bars.rfull[i], 1); mbar_init(&bars.rempty[i], rank == 0 ? kConvWarps : 4);
-    }
-    // descriptors are read by the conversion and softmax / correction warps, the
-    // MMA thread and the q loads (CTA 0) or the relay (CTA 1)
-    for (int i = 0; i < kDescs; ++i) { mbar_init(&bars.dfull[i], 1); mbar_init(&bars.dempty[i], kConvWarps + kSoftWarps + 2); }
+    for (int i = 0; i < kUnits; ++i) { mbar_init(&bars.full[i], 4); mbar_init(&bars.empty[i], 1); }
+    for (int i = 0; i < kRawSlots; ++i) { mbar_init(&bars.rfull[i], 1); mbar_init(&bars.rempty[i], rank == 0 ? kConvWarps : 4); }
+    // descriptors are read by the conversion and softmax / correction warps and
+    // three threads: MMA, q and rotary loads / relay, raw row loads
+    for (int i = 0; i < kDescs; ++i) { mbar_init(&bars.dfull[i], 1); mbar_init(&bars.dempty[i], kConvWarps + kSoftWarps + 3); }
     for (int i = 0; i < 4; ++i) mbar_init(&bars.mx[i], 2);
     for (int i = 0; i < 8; ++i) mbar_init(&bars.qgroup[i], 4);
     for (int i = 0; i < 2; ++i) {
@@ -269,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars.ffull, 1);
     mbar_init(&bars.mdrain, 1);
     wait_limit.ns = wait_limit_ns(P.err);
-    wait_limit.hint = static_cast<uint32_t>(wait_limit.ns < kSuspendHintNs ? wait_limit.ns : kSuspendHintNs);
+    wait_limit.mask = wait_limit.ns < kSuspendHintNs ? 0 : 31;
     wait_limit.gave_up = 0;
     fence_mbar_init();
     if (rank == 1) {
@@ -291,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The next tile's descriptor, for a whole warp or for one thread.
   uint32_t dc = 0;
   auto read_desc = [&](Desc& d) {
-    const Desc& e = descs[dc % kDescs];
+    const Desc& e = descs[dc % kDescs].d;
     d.valid[0] = e.valid[0]; d.valid[1] = e.valid[1]; d.valid[2] = e.valid[2]; d.valid[3] = e.valid[3];
     d.rows = e.rows;
     d.last = e.last;
@@ -307,107 +284,119 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto next_desc1 = [&](Desc& d) -> bool {
     if (!WAIT1(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) return false;
     read_desc(d);
-    mbar_arrive(&bars.dempty[(dc - 1) % kDescs]);
     return true;
   };
+  auto free_desc1 = [&]() { mbar_arrive(&bars.dempty[(dc - 1) % kDescs]); };
 
   if (warp >= kFirstConv && warp < kFirstConv + kConvWarps) {
     setmaxnreg_dec<kRegsConv>();
     // ------------------------------------------------- conversion (both CTAs)
+    // Group grp fills slot grp: units grp and grp + 4 of q (by TMA; the group puts
+    // them into tensor memory) and of every tile.  A warp converts two pieces of 16
+    // rows x 64 dims of a unit, a lane 32 dims (16 bytes) of a row; the lanes
+    // (row = lane / 2, half = lane mod 2) of a quarter warp read and write every
+    // bank once.
     const int cw = warp - kFirstConv, grp = cw >> 2, wi = cw & 3;
-    const int row = lane >> 1, piece = lane & 1;
-    const uint32_t units = smem_u32(smem);
-    Ring uc;          // the tile's (or q's) first unit
-    uint32_t tc = 0;  // tiles
+    const int row = lane >> 1, half = lane & 1;
+    uint64_t* const full = &bars.full[grp];
+    uint64_t* const empty = &bars.empty[grp];
+    // CTA 0: rows 32 wi.. of 64 dims; CTA 1: dims 128 wi.. of 16 rows
+    const uint32_t raw_step = rank == 0 ? 16 * kRawRow : 32, scale_step = rank == 0 ? 16 * kRawRow : 4,
+                   dst_step = rank == 0 ? 16 * 128 : 2048;
+    const uint32_t dst0 = smem_u32(smem) + grp * kUnit + (rank == 0 ? wi * 32 * 128 : wi * 2 * 2048) + row * 128 +
+                          (((half * 4) ^ (row & 7)) << 4);
+    const uint32_t raw0 = smem_u32(smem) + (rank == 0 ? kOffRaw0 + (wi * 32 + row) * kRawRow + grp * 32 + half * 16
+                                                      : kOffRaw1 + grp * kRawUnit + row * kRawRow + wi * 64 + half * 16);
+    const uint32_t scale0 = smem_u32(smem) + kKv4Scales + half * 2 +
+                            (rank == 0 ? kOffRaw0 + (wi * 32 + row) * kRawRow + grp * 4
+                                       : kOffRaw1 + grp * kRawUnit + row * kRawRow + wi * 8);
+    uint32_t tc = 0;              // tiles
+    uint32_t uses = 0;            // CTA 1: uses of the slot
+    uint32_t rslot = 0, rphase = 0;  // CTA 1: raw slot of the group's three
     bool ok = true;
+#pragma unroll 1
     for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
       if (rank == 0) {
-        // q: units grp and grp + 4 (64 dims of the 128 heads each) from shared to
-        // tensor memory, lane = head
+        // q: 64 dims of the 128 heads a unit, lane = head
         if (n > 0) ok = WAIT(bars.qfree, (n - 1) & 1);
         tc_fence_after();
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
-          const Ring u = uc.plus(grp + 4 * x);
-          // (the slot's previous use first: units 6 and 7 follow q's own first ones)
-          if (!WAIT(bars.empty[u.slot], u.phase ^ 1) || !WAIT(bars.full[u.slot], u.phase)) { ok = false; break; }
+          if (!WAIT(*full, x)) { ok = false; break; }
+          const uint32_t src = smem_u32(smem) + grp * kUnit;
           uint32_t r[32];
-          const uint8_t* src = smem + u.slot * kUnit;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(&r[4 * k]) = *reinterpret_cast<const uint4*>(src + sw128_off(wi * 32 + lane, k));
+          for (int k = 0; k < 8; ++k) {
+            const uint4 v = lds128(src + sw128_off(wi * 32 + lane, k));
+            r[4 * k] = v.x; r[4 * k + 1] = v.y; r[4 * k + 2] = v.z; r[4 * k + 3] = v.w;
+          }
           tmem_st32(tmem + lane_off + (grp + 4 * x) * 32, r);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.qgroup[grp + 4 * x]);
           if (wi == 0) {  // the four warps have read the unit
             if (!WAIT(bars.qgroup[grp + 4 * x], n & 1)) { ok = false; break; }
-            if (lane == 0) mbar_arrive(&bars.empty[u.slot]);
+            if (lane == 0) mbar_arrive(empty);
           }
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.qready);
-        uc.add(8);
-        // every q unit is released before a K unit waits for a slot: the parity of a
-        // slot's barrier tells its last two uses apart, not its last three
-        if (ok) ok = WAIT(bars.qready, n & 1);
       }
+#pragma unroll 1
       while (ok) {
         Desc d;
         if (!next_desc(d)) { ok = false; break; }
         if (d.rows > 0) {
-          if (rank == 0) {
-            const uint32_t rs = tc & 1;
-            if (!WAIT(bars.rfull[rs], (tc >> 1) & 1)) { ok = false; break; }
-            const uint8_t* raw = smem + kOffRaw0 + rs * kRawTile + (wi * 32 + row) * kRawRow;
-            const bool used = wi * 32 < d.rows;  // blocks past the last row are not read by the MMA
+          if (rank == 0 && !WAIT(bars.rfull[tc & 1], (tc >> 1) & 1)) { ok = false; break; }
+          const int n_x = rank == 0 ? 2 : pv_units(d.rows) / 4;
 #pragma unroll 1
-            for (int k = grp; k < 8; k += 4) {
-              const Ring u = uc.plus(k);
-              if (!WAIT(bars.empty[u.slot], u.phase ^ 1)) { ok = false; break; }
-              if (used) {
-                const uint32_t dst = units + u.slot * kUnit + (wi * 32 + row) * 128;
-#pragma unroll 1
-                for (int p = 0; p < 2; ++p)
-                  convert_piece(raw + p * 16 * kRawRow, k * 32 + piece * 16, kKv4Scales + k * 4 + piece * 2, true,
-                                dst + p * 16 * 128, piece * 4, row & 7);
-              }
-              fence_proxy_async_smem();  // generic writes -> tensor core reads
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars.full[u.slot]);
+          for (int x = 0; x < n_x; ++x) {
+            if (!WAIT(*empty, (uses & 1) ^ 1)) { ok = false; break; }
+            ++uses;
+            uint32_t raw = raw0, scale = scale0, dst = dst0, valid = 0xffffu;
+            bool used;
+            if (rank == 0) {
+              raw += (tc & 1) * kRawTile + x * 128;
+              scale += (tc & 1) * kRawTile + x * 16;
+              used = wi * 32 < d.rows;  // blocks past the last row are not read by the MMA
+            } else {
+              if (!WAIT(bars.rfull[rslot * 4 + grp], rphase)) { ok = false; break; }
+              raw += rslot * 4 * kRawUnit;
+              scale += rslot * 4 * kRawUnit;
+              const int k = grp + 4 * x;
+              const uint32_t vw = x ? (grp < 2 ? d.valid[2] : d.valid[3]) : (grp < 2 ? d.valid[0] : d.valid[1]);
+              valid = (vw >> ((grp & 1) * 16)) & 0xffffu;
+              used = k * 16 < d.rows;
             }
-            if (lane == 0) mbar_arrive(&bars.rempty[rs]);
-            uc.add(8);
-          } else {
+            if (used) {
 #pragma unroll 1
-            for (int k = grp; k < pv_units(d.rows); k += 4) {
-              const Ring u = uc.plus(k);
-              // in this order: a free unit says that its slot's previous rows were
-              // converted, so that the row barrier is in this use's phase
-              if (!WAIT(bars.empty[u.slot], u.phase ^ 1)) { ok = false; break; }
-              if (!WAIT(bars.rfull[u.slot], u.phase)) { ok = false; break; }
-              const uint8_t* raw = smem + kOffRaw1 + u.slot * kRawUnit + row * kRawRow;
-              const uint32_t vw = k < 4 ? (k < 2 ? d.valid[0] : d.valid[1]) : (k < 6 ? d.valid[2] : d.valid[3]);
-              const bool on = (vw >> ((k & 1) * 16 + row)) & 1u;
-              const uint32_t dst = units + u.slot * kUnit + row * 128;
-              if (k * 16 < d.rows) {
-#pragma unroll 1
-                for (int p = 0; p < 2; ++p) {
-                  const int a = wi * 2 + p;  // 64 dims
-                  convert_piece(raw, a * 32 + piece * 16, kKv4Scales + a * 4 + piece * 2, on, dst + a * 2048, piece * 4,
-                                row & 7);
+              for (int p = 0; p < 2; ++p) {
+                uint4 w = lds128(raw);
+                uint32_t sc = lds_u16(scale);
+                if (valid != 0xffffu && !((valid >> row) & 1u)) {  // values of a masked row: zeros
+                  w = make_uint4(0, 0, 0, 0);
+                  sc = 0;
                 }
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(&bars.full[u.slot]);
-                mbar_arrive(&bars.rempty[u.slot]);
+                const Kv4Scale lo = kv4_scale(sc & 255u), hi = kv4_scale(sc >> 8);
+                sts128(dst, kv4_codes8(w.x, lo));
+                sts128(dst ^ 16u, kv4_codes8(w.y, lo));
+                sts128(dst ^ 32u, kv4_codes8(w.z, hi));
+                sts128(dst ^ 48u, kv4_codes8(w.w, hi));
+                raw += raw_step;
+                scale += scale_step;
+                dst += dst_step;
               }
             }
-            uc.add(pv_units(d.rows));
+            fence_proxy_async_smem();  // generic writes -> tensor core reads
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(full);
+              if (rank == 1) mbar_arrive(&bars.rempty[rslot * 4 + grp]);
+            }
+            if (rank == 1 && ++rslot == kRawSlots / 4) { rslot = 0; rphase ^= 1; }
           }
+          if (rank == 0 && lane == 0) mbar_arrive(&bars.rempty[tc & 1]);
           ++tc;
         }
         if (d.last) break;
@@ -428,8 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t remote_pfull[2] = {mapa(smem_u32(&bars.pfull[0]), 1), mapa(smem_u32(&bars.pfull[1]), 1)};
       const uint32_t remote_ffull = mapa(smem_u32(&bars.ffull), 1);
       const uint64_t scale2 = pack_f32x2(P.scale_log2, P.scale_log2), one2 = pack_f32x2(1.f, 1.f);
+#pragma unroll 1
       for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
         float m_used = neg_inf(), l_sum = 0.f;
+#pragma unroll 1
         while (ok) {
           Desc d;
           if (!next_desc(d)) { ok = false; break; }
@@ -438,16 +429,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t v_lo = hf ? d.valid[2] : d.valid[0], v_hi = hf ? d.valid[3] : d.valid[1];
             if (!WAIT(bars.sfull[sb], ph)) { ok = false; break; }
             tc_fence_after();
+            const uint32_t s_tmem = tmem + lane_off + kTmemS + sb * kTile + hf * 64;
+            if ((v_lo & v_hi) != 0xffffffffu) {  // rows that are not selected
+#pragma unroll 1
+              for (int x = 0; x < 2; ++x) {
+                uint32_t s[32];
+                tmem_ld32(s_tmem + x * 32, s);
+                tmem_ld_wait();
+                const uint32_t valid = x ? v_hi : v_lo;
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!((valid >> k) & 1u)) s[k] = 0xff800000u;
+                tmem_st32(s_tmem + x * 32, s);
+              }
+              tmem_st_wait();
+            }
             // two passes over the 64 scores, 32 at a time: the maximum, then the
             // exponentials (reading them twice keeps registers and code small)
-            const uint32_t s_tmem = tmem + lane_off + kTmemS + sb * kTile + hf * 64;
             float m_tile = neg_inf();
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
               uint32_t s[32];
               tmem_ld32(s_tmem + x * 32, s);
               tmem_ld_wait();
-              mask_scores(s, x ? v_hi : v_lo);
               float mt[4] = {m_tile, neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
               for (int k = 0; k < 32; ++k) mt[k & 3] = fmaxf(mt[k & 3], __uint_as_float(s[k]));
@@ -475,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t s[32];
               tmem_ld32(s_tmem + x * 32, s);
               tmem_ld_wait();
-              mask_scores(s, x ? v_hi : v_lo);
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 const uint64_t y =
@@ -511,9 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t remote_ffree = mapa(smem_u32(&bars.ffree), 0);
       uint32_t consumed = 0;  // odone phases observed
       uint32_t stores = 0;    // output atoms of this half
+#pragma unroll 1
       for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
         const int chunk = item % P.n_chunks, th = item / P.n_chunks, hb = th % P.head_blocks, t = th / P.head_blocks;
         bool first = true;
+#pragma unroll 1
         while (ok) {
           Desc d;
           if (!next_desc(d)) { ok = false; break; }
@@ -634,11 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     setmaxnreg_inc<kRegsLast>();
     if (warp == kRowWarp) {
-      // --------------------------------------------- row gathers (both CTAs)
+      // ---------------------------------------------- row lookups (both CTAs)
       griddep_wait();  // the index rows come from the previous kernel
-      Ring uc;
-      uint32_t tc = 0, n_units = 0;
       bool ok = true;
+#pragma unroll 1
       for (int item = cluster; item < P.items && ok; item += clusters) {
         const int chunk = item % P.n_chunks, t = item / P.n_chunks / P.head_blocks;
         int b = t / P.n_q;
@@ -657,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = __ldg(idx + rows_here - 1);
           if (s < 0 || s >= P.max_L) {
             n_rows = 0;
+#pragma unroll 1
             for (int end = rows_here; end > 0 && n_rows == 0; end -= 256) {
               int mx = -1;
 #pragma unroll
@@ -671,25 +676,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        // rows 4 lane .. 4 lane + 3 of a tile, loaded a tile ahead
+        int s[4];
+        auto load_idx = [&](int j0) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int i = j0 + 4 * lane + x;
+            s[x] = i < n_rows ? __ldg(idx + i) : -1;
+          }
+        };
+        load_idx(0);
+#pragma unroll 1
         for (int j0 = 0; ok; j0 += kTile) {
-          const int rows_t = max(0, min(kTile, n_rows - j0));
-          const bool last = j0 + kTile >= n_rows;
-          // rows 4 lane .. 4 lane + 3 of the tile; one that selects nothing is
-          // gathered as row 0 and masked, one that does not exist is recorded too
+          // a row that selects nothing is read as row 0 and masked; one that does
+          // not exist is recorded too
           int r[4];
           uint32_t nib = 0;
+          bool bad = false;
           {
-            int s[4], pg[4];
+            int pg[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int i = j0 + 4 * lane + x;
-              s[x] = i < n_rows ? __ldg(idx + i) : -1;
               if (s[x] >= P.max_L) s[x] = -1;
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
               pg[x] = s[x] >= 0 && P.block_table != nullptr
                           ? __ldg(P.block_table + static_cast<size_t>(b) * P.max_blocks + s[x] / P.block_size) : b;
+            }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               r[x] = 0;
@@ -698,79 +709,96 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t row = P.block_table != nullptr
                                         ? static_cast<int64_t>(pg[x]) * P.block_size + s[x] % P.block_size
                                         : static_cast<int64_t>(b) * P.max_L + s[x];
-                if (pg[x] < 0 || row >= P.rows) atomicOr(P.err, kErrBadIndex);
+                if (pg[x] < 0 || row >= P.rows) bad = true;
                 else r[x] = static_cast<int>(row);
               }
             }
           }
+          load_idx(j0 + kTile);
+          if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(P.err, kErrBadIndex);
           nib <<= (lane & 7) * 4;
 #pragma unroll
           for (int o = 4; o; o >>= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
-          const uint32_t di = dc % kDescs;
-          if (!WAIT(bars.dempty[di], ((dc / kDescs) & 1) ^ 1)) { ok = false; break; }
-          if ((lane & 7) == 0) descs[di].valid[lane >> 3] = nib;
+          const bool last = j0 + kTile >= n_rows;
+          TileDesc& td = descs[dc % kDescs];
+          if (!WAIT(bars.dempty[dc % kDescs], ((dc / kDescs) & 1) ^ 1)) { ok = false; break; }
+          td.row[lane] = make_int4(r[0], r[1], r[2], r[3]);
+          if ((lane & 7) == 0) td.d.valid[lane >> 3] = nib;
           if (lane == 0) {
-            descs[di].rows = rows_t;
-            descs[di].last = last;
+            td.d.rows = max(0, min(kTile, n_rows - j0));
+            td.d.last = last;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.dfull[di]);
+          if (lane == 0) mbar_arrive(&bars.dfull[dc % kDescs]);
           ++dc;
-          const int quads = ((rows_t + 15) >> 4) * 4;  // gathers: whole 16-row steps
-          if (rows_t > 0 && rank == 0) {
-            const uint32_t rs = tc & 1, ph = (tc >> 1) & 1;
-            if (!WAIT(bars.rempty[rs], ph ^ 1) || !WAIT(bars.kpempty[rs], ph ^ 1)) { ok = false; break; }
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&bars.rfull[rs], quads * 4 * kRawRow);
-              mbar_arrive_expect_tx(&bars.kpfull[rs], quads * 4 * 128);
-            }
-            __syncwarp();
-            if (lane < quads) {
-              tma_gather4(smem + kOffRaw0 + rs * kRawTile + lane * 4 * kRawRow, &tmap_raw, 0, r, &bars.rfull[rs]);
-              tma_gather4(smem + kOffKrope + rs * kUnit + lane * 4 * 128, &tmap_rope, kKv4Rope / 2, r, &bars.kpfull[rs]);
-            }
-            ++tc;
-          } else if (rows_t > 0) {
-            for (int k = 0; k < pv_units(rows_t); ++k, uc.add(1)) {
-              if (!WAIT(bars.rempty[uc.slot], uc.phase ^ 1)) { ok = false; break; }
-              if (lane == 0) {
-                if (k * 4 < quads) mbar_arrive_expect_tx(&bars.rfull[uc.slot], kRawUnit);
-                else mbar_arrive(&bars.rfull[uc.slot]);
-              }
-              __syncwarp();
-              if ((lane >> 2) == k && k * 4 < quads)
-                tma_gather4(smem + kOffRaw1 + uc.slot * kRawUnit + (lane & 3) * 4 * kRawRow, &tmap_raw, 0, r,
-                            &bars.rfull[uc.slot]);
-              ++n_units;
-            }
-          }
           if (last) break;
         }
       }
-      if (lim->gave_up && lane == 0) {  // the copies in flight land before the CTA's memory is given up
-        for (uint32_t i = tc > 2 ? tc - 2 : 0; i < tc; ++i) {
-          mbar_drain(&bars.rfull[i & 1], (i >> 1) & 1);
-          mbar_drain(&bars.kpfull[i & 1], (i >> 1) & 1);
+    } else if (warp == kRawWarp) {
+      // --------------------------------------------- raw row loads (both CTAs)
+      if (elect_one()) {
+        uint32_t tc = 0, n_units = 0;
+        uint32_t rslot = 0, rphase = 0;  // CTA 1: slot of each group's three
+        bool ok = true;
+#pragma unroll 1
+        for (int item = cluster; item < P.items && ok; item += clusters) {
+#pragma unroll 1
+          while (ok) {
+            Desc d;
+            if (!next_desc1(d)) { ok = false; break; }
+            const int4* rows = descs[(dc - 1) % kDescs].row;
+            const int quads = ((d.rows + 15) >> 4) * 4;  // whole 16-row steps
+            if (d.rows > 0 && rank == 0) {
+              const uint32_t rs = tc & 1;
+              if (!WAIT1(bars.rempty[rs], ((tc >> 1) & 1) ^ 1)) { ok = false; break; }
+              mbar_arrive_expect_tx(&bars.rfull[rs], quads * 4 * kRawRow);
+              uint8_t* dst = smem + kOffRaw0 + rs * kRawTile;
+#pragma unroll 1
+              for (int q = 0; q < quads; ++q) tma_gather4(dst + q * 4 * kRawRow, &tmap_raw, 0, rows[q], &bars.rfull[rs]);
+              ++tc;
+            } else if (d.rows > 0) {
+#pragma unroll 1
+              for (int k = 0; k < pv_units(d.rows); ++k, ++n_units) {
+                const uint32_t rs = rslot * 4 + (k & 3);
+                if (!WAIT1(bars.rempty[rs], rphase ^ 1)) { ok = false; break; }
+                if (k * 4 < quads) {
+                  mbar_arrive_expect_tx(&bars.rfull[rs], kRawUnit);
+                  uint8_t* dst = smem + kOffRaw1 + rs * kRawUnit;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    tma_gather4(dst + q * 4 * kRawRow, &tmap_raw, 0, rows[k * 4 + q], &bars.rfull[rs]);
+                } else {  // past the last row
+                  mbar_arrive(&bars.rfull[rs]);
+                }
+                if ((k & 3) == 3 && ++rslot == kRawSlots / 4) { rslot = 0; rphase ^= 1; }
+              }
+            }
+            free_desc1();
+            if (d.last) break;
+          }
         }
-        for (uint32_t i = n_units > kUnits ? n_units - kUnits : 0; i < n_units; ++i)
-          mbar_drain(&bars.rfull[i % kUnits], (i / kUnits) & 1);
+        if (lim->gave_up) {  // the copies in flight land before the CTA's memory is given up
+          for (uint32_t i = tc > 2 ? tc - 2 : 0; i < tc; ++i) mbar_drain(&bars.rfull[i & 1], (i >> 1) & 1);
+          for (uint32_t i = n_units > kRawSlots ? n_units - kRawSlots : 0; i < n_units; ++i)
+            mbar_drain(&bars.rfull[i % kRawSlots], (i / kRawSlots) & 1);
+        }
       }
-      __syncwarp();
     } else if (warp == kMmaWarp && rank == 0) {
       // ---------------------------------------------- QK^T MMA (CTA 0)
       if (elect_one()) {
-        Ring uc;
         uint32_t tc = 0;
         bool ok = true;
         const uint32_t base = smem_u32(smem);
+#pragma unroll 1
         for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
           ok = WAIT1(bars.qready, n & 1) && WAIT1(bars.qpfull, n & 1);
           if (!ok) break;
           tc_fence_after();
-          uc.add(8);
+#pragma unroll 1
           while (ok) {
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
+            free_desc1();
             if (d.rows > 0) {
               const uint32_t sb = tc & 1, ph = (tc >> 1) & 1;
               const uint32_t idesc = idesc_f16(128, (d.rows + 15) & ~15, kFmtBF16, 0, 0);
@@ -785,13 +813,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               mma_commit(&bars.kpempty[sb]);
 #pragma unroll 1
-              for (int k = 0; k < 8; ++k, uc.add(1)) {
-                if (!WAIT1(bars.full[uc.slot], uc.phase)) { ok = false; break; }
+              for (int k = 0; k < 8; ++k) {
+                if (!WAIT1(bars.full[k & 3], k >> 2)) { ok = false; break; }
                 tc_fence_after();
-                const uint64_t bd = smem_desc(base + uc.slot * kUnit, 16, 1024, kSwizzle128B);
+                const uint64_t bd = smem_desc(base + (k & 3) * kUnit, 16, 1024, kSwizzle128B);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) mma_ts(dt, tmem + k * 32 + kk * 8, bd + kk * 2, idesc, 1u);
-                mma_commit(&bars.empty[uc.slot]);
+                mma_commit(&bars.empty[k & 3]);
               }
               if (!ok) break;
               mma_commit(&bars.sfull[sb]);
@@ -808,33 +836,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------- PV MMA (CTA 1)
       if (elect_one()) {
-        Ring uc;
-        uint32_t tc = 0;
+        uint32_t tc = 0, uses = 0;  // uses of every slot
         bool ok = true;
         const uint32_t idesc = idesc_f16(128, 256, kFmtBF16, 0, 1);
         const uint32_t vbase = smem_u32(smem), pbase = smem_u32(sP);
+#pragma unroll 1
         for (int item = cluster; item < P.items && ok; item += clusters) {
           uint32_t acc = 0;  // the item's first product overwrites O
+#pragma unroll 1
           while (ok) {
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
+            free_desc1();
             if (d.rows > 0) {
               const uint32_t ps = tc & 1;
               if (!WAIT1(bars.ready[ps], (tc >> 1) & 1)) { ok = false; break; }
 #pragma unroll 1
-              for (int k = 0; k < pv_units(d.rows); ++k, uc.add(1)) {
-                if (!WAIT1(bars.full[uc.slot], uc.phase)) { ok = false; break; }
-                if (k * 16 >= d.rows) {  // past the last row
-                  mma_commit(&bars.empty[uc.slot]);
-                  continue;
+              for (int k = 0; k < pv_units(d.rows); ++k) {
+                if (!WAIT1(bars.full[k & 3], uses & 1)) { ok = false; break; }
+                if (k * 16 < d.rows) {  // (units past the last row change hands all the same)
+                  tc_fence_after();
+                  const uint64_t ad = smem_desc(pbase + ps * kPSlot + (k >> 2) * kUnit + (k & 3) * 32, 16, 1024, kSwizzle128B);
+                  const uint64_t bd = smem_desc(vbase + (k & 3) * kUnit, 2048, 1024, kSwizzle128B);
+                  mma_ss(tmem, ad, bd, idesc, acc);
+                  mma_ss(tmem + 256, ad, bd + (4 * 2048 >> 4), idesc, acc);
+                  acc = 1;
                 }
-                tc_fence_after();
-                const uint64_t ad = smem_desc(pbase + ps * kPSlot + (k >> 2) * kUnit + (k & 3) * 32, 16, 1024, kSwizzle128B);
-                const uint64_t bd = smem_desc(vbase + uc.slot * kUnit, 2048, 1024, kSwizzle128B);
-                mma_ss(tmem, ad, bd, idesc, acc);
-                mma_ss(tmem + 256, ad, bd + (4 * 2048 >> 4), idesc, acc);
-                acc = 1;
-                mma_commit(&bars.empty[uc.slot]);
+                mma_commit(&bars.empty[k & 3]);
+                if ((k & 3) == 3) ++uses;
               }
               if (!ok) break;
               mma_commit(&bars.pcons[ps]);
@@ -848,43 +877,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(&bars.mdrain, 0);
       }
     } else if (warp == kAuxWarp && rank == 0) {
-      // ------------------------------------------------------- q loads (CTA 0)
+      // ---------------------------------------- q and rotary K loads (CTA 0)
       if (elect_one()) {
-        Ring uc, loading;
-        int inflight = 0, rope_loads = 0;
+        uint32_t tc = 0;
+        int q_units = 0, rope_loads = 0;
         bool ok = true;
+#pragma unroll 1
         for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
           const int th = item / P.n_chunks, hb = th % P.head_blocks, t = th / P.head_blocks;
-          // not before the previous item's last unit is converted: a wait for a unit's
-          // slot is by parity, and good for the slot's next use only
+          // not before the previous item's last unit is converted: a wait for a slot is
+          // by parity, and good for its next use only
           if (n > 0) ok = WAIT1(bars.cdone, (n - 1) & 1);
-          if (ok) inflight = 0;
-          for (int k = 0; k < 8 && ok; ++k, uc.add(1)) {
-            if (!WAIT1(bars.empty[uc.slot], uc.phase ^ 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(&bars.full[uc.slot], kUnit);
-            mbar_arrive_n(&bars.full[uc.slot], 3);
-            tma_load_3d(smem + uc.slot * kUnit, &tmap_q, k * 64, hb * 128, t, &bars.full[uc.slot]);
-            loading = uc;
-            inflight = inflight < kUnits ? inflight + 1 : kUnits;
+          q_units = 0;
+#pragma unroll 1
+          for (int k = 0; k < 8 && ok; ++k) {
+            uint64_t* const full = &bars.full[k & 3];
+            if (!WAIT1(bars.empty[k & 3], (k >> 2) ^ 1)) { ok = false; break; }
+            mbar_arrive_expect_tx(full, kUnit);
+            mbar_arrive_n(full, 3);
+            tma_load_3d(smem + (k & 3) * kUnit, &tmap_q, k * 64, hb * 128, t, full);
+            q_units = k + 1;
           }
           if (ok && n > 0) ok = WAIT1(bars.qfree, (n - 1) & 1);
           if (!ok) break;
           mbar_arrive_expect_tx(&bars.qpfull, kUnit);
           tma_load_3d(smem + kOffQrope, &tmap_q, 512, hb * 128, t, &bars.qpfull);
           rope_loads = n + 1;
+#pragma unroll 1
           while (ok) {
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
-            if (d.rows > 0) uc.add(8);
+            if (d.rows > 0) {
+              const uint32_t rs = tc & 1;
+              if (!WAIT1(bars.kpempty[rs], ((tc >> 1) & 1) ^ 1)) { ok = false; break; }
+              const int4* rows = descs[(dc - 1) % kDescs].row;
+              const int quads = ((d.rows + 15) >> 4) * 4;
+              mbar_arrive_expect_tx(&bars.kpfull[rs], quads * 4 * 128);
+              uint8_t* dst = smem + kOffKrope + rs * kUnit;
+#pragma unroll 1
+              for (int q = 0; q < quads; ++q) tma_gather4(dst + q * 512, &tmap_rope, kKv4Rope / 2, rows[q], &bars.kpfull[rs]);
+              ++tc;
+            }
+            free_desc1();
             if (d.last) break;
           }
         }
         if (lim->gave_up) {  // the copies in flight land before the CTA's memory is given up
-          for (; inflight > 0; --inflight) {
-            drain_copy(&bars.full[loading.slot], loading.phase);
-            loading.slot = loading.slot > 0 ? loading.slot - 1 : (loading.phase ^= 1, kUnits - 1);
-          }
+          for (int k = max(0, q_units - 4); k < q_units; ++k) drain_copy(&bars.full[k & 3], k >> 2);
           if (rope_loads > 0) mbar_drain(&bars.qpfull, (rope_loads - 1) & 1);
+          for (uint32_t i = tc > 2 ? tc - 2 : 0; i < tc; ++i) mbar_drain(&bars.kpfull[i & 1], (i >> 1) & 1);
         }
       }
     } else if (warp == kAuxWarp) {
@@ -893,10 +934,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t remote_pfree[2] = {mapa(smem_u32(&bars.pfree[0]), 0), mapa(smem_u32(&bars.pfree[1]), 0)};
         uint32_t tc = 0;
         bool ok = true;
+#pragma unroll 1
         for (int item = cluster; item < P.items && ok; item += clusters) {
+#pragma unroll 1
           while (ok) {
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
+            free_desc1();
             if (d.rows > 0) {
               const uint32_t ps = tc & 1;
               if (!WAIT1(bars.pcons[ps], (tc >> 1) & 1)) { ok = false; break; }
