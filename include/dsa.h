@@ -548,10 +548,9 @@ int dsa_kv4_read(const dsa_kv4_read_args* args, void* stream);
  * bf16 [T, H, 512]; lse fp32 [T, H] or NULL; sink fp32 [H] or NULL, entries
  * finite or -inf; seq_of_token int32 [T] or NULL.  A selected row whose page
  * entry is negative, or that lies past cache_rows, is recorded as
- * DSA_ERR_DEVICE_DATA: row 0 is read in its place, and that token's outputs are
- * unspecified.  A token whose sequence lies outside [0, B) is recorded likewise
- * and gets out = 0.  What a row that nothing selects holds has no effect (row 0
- * may be read and discarded).
+ * DSA_ERR_DEVICE_DATA and reads as a row of zeros.  A token whose sequence lies
+ * outside [0, B) is recorded likewise and reads no row.  A row that nothing
+ * selects is never read.
  * Supported: 1 <= T <= 65535, 1 <= H <= 1024, 1 <= topk <= 65536, scale
  * positive and finite; q, kv4 and out 16-byte aligned.
  * Workspace: dsa_sparse_attn_kv4_workspace() bytes (0 for some shapes),

@@ -14,16 +14,19 @@
 //          columns), its rotary part in shared memory; S is double-buffered in
 //          the other 256 columns.  N = 128 runs at the tensor rate (64.4 of 64
 //          clocks per K = 16 step; N = 64 takes 45 of 32).
-//   CTA 1: O += P . V with P sent over by CTA 0 (st.async) and the values read
-//          MN-major from the converted rows.
+//   CTA 1: O += P . V with P sent over by CTA 0 and the values read MN-major from
+//          the converted rows.  P goes from a staging buffer by bulk copies between
+//          the CTAs' shared memories: 21 bytes a clock, beside the load/store pipe
+//          (st.async from the softmax threads took some 2800 clocks a tile and held
+//          up the conversion's loads and stores behind it; 3.41 ms).
 //
-// Both load the raw rows they need by TMA row gathers (four rows each) and
-// convert them from 4 bits to bf16, three instructions per pair of dims, exact,
+// Both load the raw rows they need with 16-byte asynchronous copies and convert
+// them from 4 bits to bf16, three instructions per pair of dims, exact,
 // into the 128B-swizzled layout the MMA reads, 16 KB units at a time in the
 // order the MMA consumes and frees them: 64 dims of 128 rows in CTA 0, 512 dims
-// of 16 rows in CTA 1.  (Loading the rows into registers instead kept the
-// load/store pipe, which the conversion's stores need, busy for longer than the
-// MMA takes: 4.6 ms for the 4096-token case.)  Unit k of a tile belongs to the
+// of 16 rows in CTA 1.  (TMA row gathers in place of the copies were the bound: a
+// gather of four rows occupies the engine for about 100 clocks, and CTA 0 needs 64
+// a tile; 3.28 ms for the 4096-token case.)  Unit k of a tile belongs to the
 // warps of group k mod 4.  q goes through the same units of CTA 0, by TMA and
 // then into tensor memory, so the next item's q is on its way while the
 // current item's last tile is multiplied.
@@ -48,26 +51,27 @@ constexpr int kRawRow = 288;               // codes and scale bytes of a row
 constexpr int kRawTile = kTile * kRawRow;  // CTA 0: a tile's raw rows
 constexpr int kRawUnit = 16 * kRawRow;     // CTA 1: 16 raw rows
 constexpr int kDescs = 4;
-// 28 warps in seven warpgroups: 0-1 softmax (CTA 0), correction and epilogue
-// (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, q and rotary K loads (CTA 0) or
-// the P-slot relay (CTA 1), raw row loads.
-// The launch grants 72 registers a thread: 896 x 72 = 256 x 80 + 512 x 64 + 128 x 88.
-constexpr int kThreads = 896;
+constexpr uint64_t kTryNs = 40;           // a try of a barrier takes about so long
+// 32 warps in eight warpgroups: 0-1 softmax (CTA 0), correction and epilogue
+// (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, q loads (CTA 0) or the news of
+// P's arrival and use (CTA 1); 7 raw row loads.  The launch grants 64 registers a thread.
+constexpr int kThreads = 1024;
 constexpr int kSoftWarps = 8, kConvWarps = 16, kFirstConv = 8, kMmaWarp = 24, kRowWarp = 25, kAuxWarp = 26,
-              kRawWarp = 27;
-constexpr int kRegsLaunch = 72, kRegsSoft = 80, kRegsConv = 64, kRegsLast = 88;
-static_assert(256 * kRegsSoft + 512 * kRegsConv + 128 * kRegsLast <= kThreads * kRegsLaunch,
+              kSentWarp = 27, kFirstLoad = 28, kLoadWarps = 4;
+constexpr int kRegsLaunch = 64, kRegsSoft = 80, kRegsConv = 56, kRegsLast = 72, kRegsLoad = 56;
+static_assert(256 * kRegsSoft + 512 * kRegsConv + 128 * (kRegsLast + kRegsLoad) <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
 constexpr uint32_t kPBytes = 128 * (2 * 128 + 4);  // a P tile and its rescale factors
 constexpr uint32_t kFinalBytes = 128 * 12;         // per head: maximum, two partial sums
 constexpr uint32_t kTmemS = 256;                   // CTA 0: q in columns [0, 256), S in [256, 512)
 
 // Dynamic shared memory, after the units.  CTA 0: q's rotary part, two rotary K
-// buffers, two raw tiles, the row maxima that the two warps of a head exchange.
+// buffers, two raw tiles, the row maxima that the two warps of a head exchange, P
+// and its rescale factors on their way out.
 // CTA 1: two P slots, the output staging of each column half, raw units, rescale
 // factors, finals.
 constexpr int kOffQrope = kUnits * kUnit, kOffKrope = kOffQrope + kUnit, kOffRaw0 = kOffKrope + 2 * kUnit,
-              kOffMax = kOffRaw0 + 2 * kRawTile, kEnd0 = kOffMax + 2048;
+              kOffMax = kOffRaw0 + 2 * kRawTile, kOffPst = kOffMax + 2048, kEnd0 = kOffPst + kPSlot + 512;
 constexpr int kOffP = kUnits * kUnit, kOffStage = kOffP + 2 * kPSlot, kOffRaw1 = kOffStage + 2 * kUnit,
               kOffAlpha = kOffRaw1 + kRawSlots * kRawUnit, kOffFinal = kOffAlpha + 1024, kEnd1 = kOffFinal + 1536;
 constexpr int kSmem = 1024 + (kEnd0 > kEnd1 ? kEnd0 : kEnd1);
@@ -92,12 +96,12 @@ struct AttnKv4Params {
 
 // What the roles need to know of a tile, and its physical rows.
 struct Desc {
-  uint32_t valid[4];  // rows that are selected (the others are masked, their values zeros)
+  uint32_t valid[4];  // rows that are selected (the others are masked)
   int rows;           // rows of the tile up to the item's last selected one; 0: the item selects nothing
   int last;           // the item's last tile
 };
 struct __align__(16) TileDesc {
-  int4 row[kTile / 4];
+  int row[kTile];  // -1: read as zeros
   Desc d;
 };
 
@@ -108,6 +112,7 @@ struct __align__(8) Bars {
   uint64_t kpfull[2], kpempty[2];            // CTA 0: rotary K buffers
   uint64_t sfull[2], sempty[2];              // CTA 0: S buffers
   uint64_t pfree[2];                         // CTA 0: P slot of CTA 1 free
+  uint64_t pstaged[2], psent;                // CTA 0: half of P staged; P has arrived
   uint64_t mx[4];                            // CTA 0: row maxima exchanged (per warp quadrant)
   uint64_t qgroup[8], qready, qfree, qpfull; // CTA 0: a q unit read / all of q stored / MMAs done with q; q's rotary part
   uint64_t cdone;                            // CTA 0: every K unit of the item is converted
@@ -134,16 +139,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n}" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
-// Four rows r0..r3 of the map's 2-D tensor, from column x on, to consecutive
-// rows of shared memory.
-__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int x, const int4& r, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w),
-        "r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -159,6 +154,11 @@ __device__ __forceinline__ void drain_copy(uint64_t* bar, uint32_t parity) {
   while (!mbar_test(bar, parity) && globaltimer_ns() - t0 < 100000) {}
 }
 
+// Bulk copy to the peer CTA's shared memory, completing on the peer's barrier.
+__device__ __forceinline__ void bulk_s2peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "r"(src), "r"(bytes), "r"(bar) : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -173,48 +173,37 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Bounded wait for a phase of a barrier, in as little code and as few instructions
-// as will do: the roles of this kernel run at the same time from one instruction
-// cache and one set of schedulers.  (With the other kernels' waits inlined the code
-// was 133 KB and a third of the cache's requests missed: 5.97 ms for the 4096-token
-// case.)  A try blocks in the hardware for a while by itself; every 32nd that fails
-// reads the clock (each one under a limit below 20 us, in failure tests).
-struct WaitLimit {
-  uint64_t ns;
-  uint32_t mask;
-  int gave_up;
-};
+// Bounded wait for a phase of a barrier, in as little code as will do: the roles of
+// this kernel run at the same time, and the two CTAs of a cluster, from one
+// instruction cache.  (With the other kernels' waits inlined the code was 133 KB and a
+// third of the cache's requests missed: 5.97 ms for the 4096-token case.)  A try
+// blocks for some 70 clocks by itself; `tries` is how many fill the limit in force.
+// The thread that runs out sets it to 0, and every later wait gives up at once.
 template <bool kCluster>
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile WaitLimit* lim) {
-  uint64_t t0 = 0;
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile uint32_t* tries) {
 #pragma unroll 1
-  for (uint32_t n = 1; !(kCluster ? mbar_probe_cluster(bar, parity) : mbar_probe(bar, parity)); ++n) {
-    if (n & lim->mask) continue;
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (lim->gave_up || now - t0 > lim->ns) {
-      lim->gave_up = 1;  // reported when the CTA ends
+  for (uint32_t n = 0; !(kCluster ? mbar_probe_cluster(bar, parity) : mbar_probe(bar, parity)); ++n)
+    if (n >= *tries) {
+      *tries = 0;  // reported when the CTA ends
       return false;
     }
-  }
   return true;
 }
 // Waits of one thread, and of a whole warp, whose lanes go on or give up together
 // (a lane that left alone would leave the others at the next warp barrier).
-#define WAIT1(bar, parity) wait_phase<false>(&(bar), (parity), lim)
-#define WAIT(bar, parity) (__all_sync(0xffffffffu, wait_phase<false>(&(bar), (parity), lim)) != 0)
-#define WAIT_CLUSTER(bar, parity) (__all_sync(0xffffffffu, wait_phase<true>(&(bar), (parity), lim)) != 0)
+#define WAIT1(bar, parity) wait_phase<false>(&(bar), (parity), tries)
+#define WAIT(bar, parity) (__all_sync(0xffffffffu, wait_phase<false>(&(bar), (parity), tries)) != 0)
+#define WAIT_CLUSTER(bar, parity) (__all_sync(0xffffffffu, wait_phase<true>(&(bar), (parity), tries)) != 0)
 
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kv4_kernel(const __grid_constant__ AttnKv4Params P, const __grid_constant__ CUtensorMap tmap_q,
-                    const __grid_constant__ CUtensorMap tmap_raw, const __grid_constant__ CUtensorMap tmap_rope,
                     const __grid_constant__ CUtensorMap tmap_o) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Bars bars;
   __shared__ TileDesc descs[kDescs];
   __shared__ uint32_t tmem_base;
-  __shared__ WaitLimit wait_limit;
+  __shared__ uint32_t wait_tries;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
@@ -226,28 +215,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kUnits; ++i) { mbar_init(&bars.full[i], 4); mbar_init(&bars.empty[i], 1); }
-    for (int i = 0; i < kRawSlots; ++i) { mbar_init(&bars.rfull[i], 1); mbar_init(&bars.rempty[i], rank == 0 ? kConvWarps : 4); }
-    // descriptors are read by the conversion and softmax / correction warps and
-    // three threads: MMA, q and rotary loads / relay, raw row loads
-    for (int i = 0; i < kDescs; ++i) { mbar_init(&bars.dfull[i], 1); mbar_init(&bars.dempty[i], kConvWarps + kSoftWarps + 3); }
+    // raw rows arrive by the copies of every thread of the load warps (CTA 0) or of
+    // one of them (CTA 1)
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(&bars.rfull[i], rank == 0 ? kLoadWarps * 32 : 32);
+      mbar_init(&bars.rempty[i], rank == 0 ? kConvWarps : 4);
+    }
+    // descriptors are read by the conversion, softmax / correction and load warps
+    // and two threads: MMA, q loads / relay; in CTA 1 a third that tells of P's arrival
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(&bars.dfull[i], 1);
+      mbar_init(&bars.dempty[i], kConvWarps + kSoftWarps + kLoadWarps + 2 + (rank == 0 ? 0 : 1));
+    }
     for (int i = 0; i < 4; ++i) mbar_init(&bars.mx[i], 2);
     for (int i = 0; i < 8; ++i) mbar_init(&bars.qgroup[i], 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.kpfull[i], 1); mbar_init(&bars.kpempty[i], 1);
-      mbar_init(&bars.sfull[i], 1); mbar_init(&bars.sempty[i], kSoftWarps); mbar_init(&bars.pfree[i], 1);
+      mbar_init(&bars.kpfull[i], kLoadWarps * 32); mbar_init(&bars.kpempty[i], 1);
+      mbar_init(&bars.sfull[i], 1); mbar_init(&bars.sempty[i], kSoftWarps); mbar_init(&bars.pfree[i], 1); mbar_init(&bars.pstaged[i], 4);
       mbar_init(&bars.pfull[i], 1); mbar_init(&bars.pcons[i], 1); mbar_init(&bars.ready[i], kSoftWarps);
       mbar_init(&bars.odone[i], 1); mbar_init(&bars.stfull[i], 4); mbar_init(&bars.stfree[i], 1);
     }
     mbar_init(&bars.qready, kConvWarps);
     mbar_init(&bars.qfree, 1);
+    mbar_init(&bars.psent, 1);
     mbar_init(&bars.cdone, kConvWarps);
     mbar_init(&bars.qpfull, 1);
     mbar_init(&bars.ffree, kSoftWarps);
     mbar_init(&bars.ffull, 1);
     mbar_init(&bars.mdrain, 1);
-    wait_limit.ns = wait_limit_ns(P.err);
-    wait_limit.mask = wait_limit.ns < kSuspendHintNs ? 0 : 31;
-    wait_limit.gave_up = 0;
+    wait_tries = static_cast<uint32_t>(min(wait_limit_ns(P.err) / kTryNs + 1, static_cast<uint64_t>(0xffffffffu)));
     fence_mbar_init();
     if (rank == 1) {
       mbar_arrive_expect_tx(&bars.pfull[0], kPBytes);
@@ -260,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  volatile WaitLimit* lim = &wait_limit;
+  volatile uint32_t* tries = &wait_tries;
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
   cluster_sync();  // both CTAs' barriers are initialised before any remote use
   griddep_launch_dependents();
@@ -354,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < n_x; ++x) {
             if (!WAIT(*empty, (uses & 1) ^ 1)) { ok = false; break; }
             ++uses;
-            uint32_t raw = raw0, scale = scale0, dst = dst0, valid = 0xffffu;
+            uint32_t raw = raw0, scale = scale0, dst = dst0;
             bool used;
             if (rank == 0) {
               raw += (tc & 1) * kRawTile + x * 128;
@@ -364,20 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!WAIT(bars.rfull[rslot * 4 + grp], rphase)) { ok = false; break; }
               raw += rslot * 4 * kRawUnit;
               scale += rslot * 4 * kRawUnit;
-              const int k = grp + 4 * x;
-              const uint32_t vw = x ? (grp < 2 ? d.valid[2] : d.valid[3]) : (grp < 2 ? d.valid[0] : d.valid[1]);
-              valid = (vw >> ((grp & 1) * 16)) & 0xffffu;
-              used = k * 16 < d.rows;
+              used = (grp + 4 * x) * 16 < d.rows;
             }
             if (used) {
 #pragma unroll 1
               for (int p = 0; p < 2; ++p) {
-                uint4 w = lds128(raw);
-                uint32_t sc = lds_u16(scale);
-                if (valid != 0xffffu && !((valid >> row) & 1u)) {  // values of a masked row: zeros
-                  w = make_uint4(0, 0, 0, 0);
-                  sc = 0;
-                }
+                const uint4 w = lds128(raw);
+                const uint32_t sc = lds_u16(scale);
                 const Kv4Scale lo = kv4_scale(sc & 255u), hi = kv4_scale(sc >> 8);
                 sts128(dst, kv4_codes8(w.x, lo));
                 sts128(dst ^ 16u, kv4_codes8(w.y, lo));
@@ -411,10 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       // ------------------------------------------------- softmax (CTA 0)
       // Two threads per head, each 64 of a tile's 128 rows.
-      const uint32_t remote_p = mapa(smem_u32(sP), 1) + hf * kUnit;
-      const uint32_t remote_alpha = mapa(smem_u32(sAlpha), 1);
+      const uint32_t stage = smem_u32(smem + kOffPst) + hf * kUnit;
+      float* stage_alpha = reinterpret_cast<float*>(smem + kOffPst + kPSlot);
       const uint32_t remote_final = mapa(smem_u32(sFinal), 1);
-      const uint32_t remote_pfull[2] = {mapa(smem_u32(&bars.pfull[0]), 1), mapa(smem_u32(&bars.pfull[1]), 1)};
       const uint32_t remote_ffull = mapa(smem_u32(&bars.ffull), 1);
       const uint64_t scale2 = pack_f32x2(P.scale_log2, P.scale_log2), one2 = pack_f32x2(1.f, 1.f);
 #pragma unroll 1
@@ -470,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               l_sum *= alpha;
               m_used = m_tile;
             }
-            if (!WAIT_CLUSTER(bars.pfree[sb], ph ^ 1)) { ok = false; break; }
+            if (tc > 0 && !WAIT_CLUSTER(bars.psent, (tc - 1) & 1)) { ok = false; break; }  // the staging is free
             const float msub = m_used == neg_inf() ? 0.f : -m_used;
             const uint64_t msub2 = pack_f32x2(msub, msub);
             uint64_t sum2[2] = {0, 0};
@@ -488,17 +476,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
                 s[k] = *reinterpret_cast<uint32_t*>(&pb);
               }
-              const uint32_t prow = remote_p + sb * kPSlot;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                st_async_v4(prow + sw128_off(hrow, x * 4 + k), make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]),
-                            remote_pfull[sb]);
+                sts128(stage + sw128_off(hrow, x * 4 + k), make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]));
             }
+            if (hf == 0) stage_alpha[hrow] = alpha;
+            fence_proxy_async_smem();  // generic writes -> bulk copy reads
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.sempty[sb]);
+            if (lane == 0) {
+              mbar_arrive(&bars.sempty[sb]);
+              mbar_arrive(&bars.pstaged[hf]);
+            }
             l_sum += (lo_f32(sum2[0]) + hi_f32(sum2[0])) + (lo_f32(sum2[1]) + hi_f32(sum2[1]));
-            if (hf == 0) st_async_b32(remote_alpha + (sb * 128 + hrow) * 4, __float_as_uint(alpha), remote_pfull[sb]);
+            if ((warp & 3) == 0) {  // the four warps of this half have staged it: send it
+              if (!WAIT(bars.pstaged[hf], tc & 1) || !WAIT_CLUSTER(bars.pfree[sb], ph ^ 1)) { ok = false; break; }
+              if (lane == 0) {
+                const uint32_t dst = mapa(smem_u32(sP), 1) + sb * kPSlot + hf * kUnit, bar = mapa(smem_u32(&bars.pfull[sb]), 1);
+                bulk_s2peer(dst, stage, kUnit, bar);
+                if (hf == 0) bulk_s2peer(mapa(smem_u32(sAlpha), 1) + sb * 512, smem_u32(stage_alpha), 512, bar);
+              }
+              __syncwarp();
+            }
             ++tc;
           }
           if (d.last) break;
@@ -547,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_wait();
               tc_fence_before();
             }
-            fence_proxy_async_smem();  // P arrived through st.async; the MMA reads it
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.ready[ps]);
             // keep at most one completed product unobserved
@@ -636,6 +634,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (warp >= kFirstLoad) {
+    setmaxnreg_dec<kRegsLoad>();
+    // --------------------------------------------- raw row loads (both CTAs)
+    // Load warp lw copies rows 32 lw.. of a tile in CTA 0, units lw and lw + 4 (16
+    // rows each) in CTA 1: 16 chunks of codes for two rows, 2 chunks of scale bytes
+    // for 16 rows, 8 chunks of rotary dims for four rows (swizzled) an instruction.
+    const int lw = warp - kFirstLoad;
+    uint32_t tc = 0, rslot = 0, rphase = 0;
+    bool ok = true;
+    auto copy_rows = [&](const int* rows, int n, uint32_t dst) {  // codes and scale bytes of n rows (16 or 32)
+#pragma unroll 4
+      for (int i = 0; i < n / 2; ++i) {
+        const int x = 2 * i + (lane >> 4), r = rows[x];
+        cp_async16(dst + x * kRawRow + (lane & 15) * 16,
+                   P.kv4 + static_cast<size_t>(r < 0 ? 0 : r) * kKv4Row + (lane & 15) * 16, r < 0 ? 0 : 16);
+      }
+#pragma unroll 1
+      for (int i = 0; i < n / 16; ++i) {
+        const int x = 16 * i + (lane >> 1), r = rows[x];
+        cp_async16(dst + x * kRawRow + kKv4Scales + (lane & 1) * 16,
+                   P.kv4 + static_cast<size_t>(r < 0 ? 0 : r) * kKv4Row + kKv4Scales + (lane & 1) * 16, r < 0 ? 0 : 16);
+      }
+    };
+#pragma unroll 1
+    for (int item = cluster; item < P.items && ok; item += clusters) {
+#pragma unroll 1
+      while (ok) {
+        Desc d;
+        if (!WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
+        const int* rows = descs[dc % kDescs].row;
+        read_desc(d);
+        if (d.rows > 0 && rank == 0) {
+          const uint32_t rs = tc & 1, ph = (tc >> 1) & 1;
+          const int n = min(32, ((d.rows + 15) & ~15) - lw * 32);
+          rows += lw * 32;
+          if (!WAIT(bars.kpempty[rs], ph ^ 1)) { ok = false; break; }
+          const uint32_t kp = smem_u32(smem + kOffKrope) + rs * kUnit;
+#pragma unroll 4
+          for (int i = 0; i < n / 4; ++i) {
+            const int x = 4 * i + (lane >> 3), r = rows[x];
+            cp_async16(kp + sw128_off(lw * 32 + x, lane & 7),
+                       P.kv4 + static_cast<size_t>(r < 0 ? 0 : r) * kKv4Row + kKv4Rope + (lane & 7) * 16, r < 0 ? 0 : 16);
+          }
+          cp_async_mbar_arrive(&bars.kpfull[rs]);
+          if (!WAIT(bars.rempty[rs], ph ^ 1)) { ok = false; break; }
+          copy_rows(rows, n, smem_u32(smem + kOffRaw0) + rs * kRawTile + lw * 32 * kRawRow);
+          cp_async_mbar_arrive(&bars.rfull[rs]);
+          ++tc;
+        } else if (d.rows > 0) {
+#pragma unroll 1
+          for (int k = lw; k < pv_units(d.rows); k += 4) {
+            const uint32_t rs = rslot * 4 + lw;
+            if (!WAIT(bars.rempty[rs], rphase ^ 1)) { ok = false; break; }
+            if (k * 16 < d.rows) copy_rows(rows + k * 16, 16, smem_u32(smem + kOffRaw1) + rs * kRawUnit);
+            cp_async_mbar_arrive(&bars.rfull[rs]);
+            if (++rslot == kRawSlots / 4) { rslot = 0; rphase ^= 1; }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.dempty[(dc - 1) % kDescs]);
+        if (d.last) break;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight when the CTA ends
   } else {
     setmaxnreg_inc<kRegsLast>();
     if (warp == kRowWarp) {
@@ -688,8 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_idx(0);
 #pragma unroll 1
         for (int j0 = 0; ok; j0 += kTile) {
-          // a row that selects nothing is read as row 0 and masked; one that does
-          // not exist is recorded too
+          // a slot that selects nothing is masked; a row that does not exist is
+          // recorded and reads as zeros
           int r[4];
           uint32_t nib = 0;
           bool bad = false;
@@ -703,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              r[x] = 0;
+              r[x] = -1;
               if (s[x] >= 0) {
                 nib |= 1u << x;
                 const int64_t row = P.block_table != nullptr
@@ -722,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool last = j0 + kTile >= n_rows;
           TileDesc& td = descs[dc % kDescs];
           if (!WAIT(bars.dempty[dc % kDescs], ((dc / kDescs) & 1) ^ 1)) { ok = false; break; }
-          td.row[lane] = make_int4(r[0], r[1], r[2], r[3]);
+          *reinterpret_cast<int4*>(&td.row[4 * lane]) = make_int4(r[0], r[1], r[2], r[3]);
           if ((lane & 7) == 0) td.d.valid[lane >> 3] = nib;
           if (lane == 0) {
             td.d.rows = max(0, min(kTile, n_rows - j0));
@@ -732,55 +794,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&bars.dfull[dc % kDescs]);
           ++dc;
           if (last) break;
-        }
-      }
-    } else if (warp == kRawWarp) {
-      // --------------------------------------------- raw row loads (both CTAs)
-      if (elect_one()) {
-        uint32_t tc = 0, n_units = 0;
-        uint32_t rslot = 0, rphase = 0;  // CTA 1: slot of each group's three
-        bool ok = true;
-#pragma unroll 1
-        for (int item = cluster; item < P.items && ok; item += clusters) {
-#pragma unroll 1
-          while (ok) {
-            Desc d;
-            if (!next_desc1(d)) { ok = false; break; }
-            const int4* rows = descs[(dc - 1) % kDescs].row;
-            const int quads = ((d.rows + 15) >> 4) * 4;  // whole 16-row steps
-            if (d.rows > 0 && rank == 0) {
-              const uint32_t rs = tc & 1;
-              if (!WAIT1(bars.rempty[rs], ((tc >> 1) & 1) ^ 1)) { ok = false; break; }
-              mbar_arrive_expect_tx(&bars.rfull[rs], quads * 4 * kRawRow);
-              uint8_t* dst = smem + kOffRaw0 + rs * kRawTile;
-#pragma unroll 1
-              for (int q = 0; q < quads; ++q) tma_gather4(dst + q * 4 * kRawRow, &tmap_raw, 0, rows[q], &bars.rfull[rs]);
-              ++tc;
-            } else if (d.rows > 0) {
-#pragma unroll 1
-              for (int k = 0; k < pv_units(d.rows); ++k, ++n_units) {
-                const uint32_t rs = rslot * 4 + (k & 3);
-                if (!WAIT1(bars.rempty[rs], rphase ^ 1)) { ok = false; break; }
-                if (k * 4 < quads) {
-                  mbar_arrive_expect_tx(&bars.rfull[rs], kRawUnit);
-                  uint8_t* dst = smem + kOffRaw1 + rs * kRawUnit;
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    tma_gather4(dst + q * 4 * kRawRow, &tmap_raw, 0, rows[k * 4 + q], &bars.rfull[rs]);
-                } else {  // past the last row
-                  mbar_arrive(&bars.rfull[rs]);
-                }
-                if ((k & 3) == 3 && ++rslot == kRawSlots / 4) { rslot = 0; rphase ^= 1; }
-              }
-            }
-            free_desc1();
-            if (d.last) break;
-          }
-        }
-        if (lim->gave_up) {  // the copies in flight land before the CTA's memory is given up
-          for (uint32_t i = tc > 2 ? tc - 2 : 0; i < tc; ++i) mbar_drain(&bars.rfull[i & 1], (i >> 1) & 1);
-          for (uint32_t i = n_units > kRawSlots ? n_units - kRawSlots : 0; i < n_units; ++i)
-            mbar_drain(&bars.rfull[i % kRawSlots], (i / kRawSlots) & 1);
         }
       }
     } else if (warp == kMmaWarp && rank == 0) {
@@ -804,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t idesc = idesc_f16(128, (d.rows + 15) & ~15, kFmtBF16, 0, 0);
               const uint32_t dt = tmem + kTmemS + sb * kTile;
               if (!WAIT1(bars.sempty[sb], ph ^ 1) || !WAIT1(bars.kpfull[sb], ph)) { ok = false; break; }
+              fence_proxy_async_smem();  // cp.async data -> tensor core reads
               tc_fence_after();
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
@@ -877,9 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(&bars.mdrain, 0);
       }
     } else if (warp == kAuxWarp && rank == 0) {
-      // ---------------------------------------- q and rotary K loads (CTA 0)
+      // ------------------------------------------------------- q loads (CTA 0)
       if (elect_one()) {
-        uint32_t tc = 0;
         int q_units = 0, rope_loads = 0;
         bool ok = true;
 #pragma unroll 1
@@ -907,25 +920,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (ok) {
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
-            if (d.rows > 0) {
-              const uint32_t rs = tc & 1;
-              if (!WAIT1(bars.kpempty[rs], ((tc >> 1) & 1) ^ 1)) { ok = false; break; }
-              const int4* rows = descs[(dc - 1) % kDescs].row;
-              const int quads = ((d.rows + 15) >> 4) * 4;
-              mbar_arrive_expect_tx(&bars.kpfull[rs], quads * 4 * 128);
-              uint8_t* dst = smem + kOffKrope + rs * kUnit;
-#pragma unroll 1
-              for (int q = 0; q < quads; ++q) tma_gather4(dst + q * 512, &tmap_rope, kKv4Rope / 2, rows[q], &bars.kpfull[rs]);
-              ++tc;
-            }
             free_desc1();
             if (d.last) break;
           }
         }
-        if (lim->gave_up) {  // the copies in flight land before the CTA's memory is given up
+        if (*tries == 0) {  // the copies in flight land before the CTA's memory is given up
           for (int k = max(0, q_units - 4); k < q_units; ++k) drain_copy(&bars.full[k & 3], k >> 2);
           if (rope_loads > 0) mbar_drain(&bars.qpfull, (rope_loads - 1) & 1);
-          for (uint32_t i = tc > 2 ? tc - 2 : 0; i < tc; ++i) mbar_drain(&bars.kpfull[i & 1], (i >> 1) & 1);
         }
       }
     } else if (warp == kAuxWarp) {
@@ -952,12 +953,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+    } else if (warp == kSentWarp && rank == 1) {
+      // ------------------------------ P has arrived -> CTA 0: its staging is free
+      if (elect_one()) {
+        const uint32_t remote_psent = mapa(smem_u32(&bars.psent), 0);
+        uint32_t tc = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int item = cluster; item < P.items && ok; item += clusters) {
+#pragma unroll 1
+          while (ok) {
+            Desc d;
+            if (!next_desc1(d)) { ok = false; break; }
+            free_desc1();
+            if (d.rows > 0) {
+              if (!wait_phase<true>(&bars.pfull[tc & 1], (tc >> 1) & 1, tries)) { ok = false; break; }
+              mbar_arrive_remote(remote_psent);
+              ++tc;
+            }
+            if (d.last) break;
+          }
+        }
+      }
     }
   }
   tc_fence_before();
+  if (tid == 0 && *tries == 0) {  // copies to the peer may be in flight: far more time than they take
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 100000) {}
+  }
   __syncthreads();
   cluster_sync();  // no CTA leaves while its peer may still address it
-  if (tid == 0 && lim->gave_up) atomicOr(P.err, kErrTimeout);
+  if (tid == 0 && *tries == 0) atomicOr(P.err, kErrTimeout);
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -1080,19 +1107,15 @@ int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s) {
   if (!P.err) return DSA_ERR_CUDA;
 
   // q [T, H, 576] in 64-dim x 128-head boxes (heads past H read as zeros); the
-  // cache's rows as 208 16-bit words, gathered row by row: codes and scale bytes,
-  // and the rotary dims; the output (or the chunks' partial outputs) [Z, H, 512]
-  // in 64-column x 128-head boxes (heads past H are clipped)
-  alignas(64) CUtensorMap tmap_q, tmap_raw, tmap_rope, tmap_o;
+  // output (or the chunks' partial outputs) [Z, H, 512] in 64-column x 128-head
+  // boxes (heads past H are clipped)
+  alignas(64) CUtensorMap tmap_q, tmap_o;
   {
     const uint64_t H = static_cast<uint64_t>(a.H), T = static_cast<uint64_t>(a.T);
     const uint64_t dq[3] = {kDqk, H, T}, sq[2] = {kDqk * 2, H * kDqk * 2};
-    const uint64_t dk[2] = {kKv4Row / 2, static_cast<uint64_t>(a.cache_rows)}, sk[1] = {kKv4Row};
     const uint64_t od[3] = {kDv, H, T * P.n_chunks}, os[2] = {kDv * 2, H * kDv * 2};
-    const uint32_t box[3] = {64, 128, 1}, box_raw[2] = {kRawRow / 2, 1}, box_rope[2] = {kKv4RopeDims, 1};
+    const uint32_t box[3] = {64, 128, 1};
     if (!encode_tmap(&tmap_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dq, sq, box, 128) ||
-        !encode_tmap(&tmap_raw, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.kv4, dk, sk, box_raw, 0) ||
-        !encode_tmap(&tmap_rope, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.kv4, dk, sk, box_rope, 128) ||
         !encode_tmap(&tmap_o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, P.n_chunks == 1 ? P.out : P.part_o, od, os, box, 128))
       return DSA_ERR_CUDA;
   }
@@ -1112,7 +1135,7 @@ int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, attn_kv4_kernel, P, tmap_q, tmap_raw, tmap_rope, tmap_o);
+  e = cudaLaunchKernelEx(&cfg, attn_kv4_kernel, P, tmap_q, tmap_o);
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   if (P.n_chunks > 1) {
     cudaLaunchConfig_t c2 = {};
