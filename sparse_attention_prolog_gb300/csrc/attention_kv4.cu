@@ -94,15 +94,16 @@ struct AttnKv4Params {
   uint32_t* err;
 };
 
-// What the roles need to know of a tile, and its physical rows.
-struct Desc {
-  uint32_t valid[4];  // rows that are selected (the others are masked)
-  int rows;           // rows of the tile up to the item's last selected one; 0: the item selects nothing
-  int last;           // the item's last tile
-};
+// What the roles need to know of a tile.
 struct __align__(16) TileDesc {
-  int row[kTile];  // -1: read as zeros
-  Desc d;
+  int row[kTile];     // its physical rows; -1: read as zeros
+  uint32_t valid[4];  // rows that are selected (the others are masked)
+  int info;           // rows up to the item's last selected one (0: it selects nothing); + kLast: the item's last tile
+};
+constexpr int kLast = 1 << 16;
+struct Desc {
+  int rows;
+  bool last;
 };
 
 struct __align__(8) Bars {
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one of them (CTA 1)
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(&bars.rfull[i], rank == 0 ? kLoadWarps * 32 : 32);
-      mbar_init(&bars.rempty[i], rank == 0 ? kConvWarps : 4);
+      mbar_init(&bars.rempty[i], rank == 0 ? 2 * kConvWarps : 4);
     }
     // descriptors are read by the conversion, softmax / correction and load warps
     // and two threads: MMA, q loads / relay; in CTA 1 a third that tells of P's arrival
@@ -264,10 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The next tile's descriptor, for a whole warp or for one thread.
   uint32_t dc = 0;
   auto read_desc = [&](Desc& d) {
-    const Desc& e = descs[dc % kDescs].d;
-    d.valid[0] = e.valid[0]; d.valid[1] = e.valid[1]; d.valid[2] = e.valid[2]; d.valid[3] = e.valid[3];
-    d.rows = e.rows;
-    d.last = e.last;
+    const int info = descs[dc % kDescs].info;
+    d.rows = info & (kLast - 1);
+    d.last = info >= kLast;
     ++dc;
   };
   auto next_desc = [&](Desc& d) -> bool {
@@ -296,7 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = lane >> 1, half = lane & 1;
     uint64_t* const full = &bars.full[grp];
     uint64_t* const empty = &bars.empty[grp];
-    // CTA 0: rows 32 wi.. of 64 dims; CTA 1: dims 128 wi.. of 16 rows
+    // CTA 0: rows 32 wi.. of 64 dims; CTA 1: dims 128 wi.. of 16 rows.  What differs
+    // is in these variables: both CTAs run the same loop, which an instruction cache
+    // may then hold once for both.
     const uint32_t raw_step = rank == 0 ? 16 * kRawRow : 32, scale_step = rank == 0 ? 16 * kRawRow : 4,
                    dst_step = rank == 0 ? 16 * 128 : 2048;
     const uint32_t dst0 = smem_u32(smem) + grp * kUnit + (rank == 0 ? wi * 32 * 128 : wi * 2 * 2048) + row * 128 +
@@ -306,9 +308,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t scale0 = smem_u32(smem) + kKv4Scales + half * 2 +
                             (rank == 0 ? kOffRaw0 + (wi * 32 + row) * kRawRow + grp * 4
                                        : kOffRaw1 + grp * kRawUnit + row * kRawRow + wi * 8);
-    uint32_t tc = 0;              // tiles
-    uint32_t uses = 0;            // CTA 1: uses of the slot
-    uint32_t rslot = 0, rphase = 0;  // CTA 1: raw slot of the group's three
+    // raw rows: turn rq of a ring; two turns (units) a raw tile in CTA 0, one a raw
+    // unit in CTA 1
+    const uint32_t rq_shift = rank == 0 ? 1 : 0, rq_end = rank == 0 ? 4 : kRawSlots / 4,
+                   raw_slot = rank == 0 ? kRawTile : 4 * kRawUnit, bar_step = rank == 0 ? 8 : 32,
+                   raw_unit = rank == 0 ? 128 : 0, scale_unit = rank == 0 ? 16 : 0;
+    uint64_t* const rfull0 = rank == 0 ? &bars.rfull[0] : &bars.rfull[grp];
+    const int rempty_off = static_cast<int>(&bars.rempty[0] - &bars.rfull[0]);
+    const int row_first = rank == 0 ? wi * 32 : grp * 16, row_unit = rank == 0 ? 0 : 64;  // of unit x
+    const int one_unit = rank == 0 ? 0 : kTile / 2;  // tiles of so many rows at most take one use of each slot
+    uint32_t uses = 0, rq = 0, rphase = 0;
     bool ok = true;
 #pragma unroll 1
     for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
@@ -344,25 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         Desc d;
         if (!next_desc(d)) { ok = false; break; }
         if (d.rows > 0) {
-          if (rank == 0 && !WAIT(bars.rfull[tc & 1], (tc >> 1) & 1)) { ok = false; break; }
-          const int n_x = rank == 0 ? 2 : pv_units(d.rows) / 4;
+          const int n_x = d.rows > one_unit ? 2 : 1;
 #pragma unroll 1
           for (int x = 0; x < n_x; ++x) {
             if (!WAIT(*empty, (uses & 1) ^ 1)) { ok = false; break; }
             ++uses;
-            uint32_t raw = raw0, scale = scale0, dst = dst0;
-            bool used;
-            if (rank == 0) {
-              raw += (tc & 1) * kRawTile + x * 128;
-              scale += (tc & 1) * kRawTile + x * 16;
-              used = wi * 32 < d.rows;  // blocks past the last row are not read by the MMA
-            } else {
-              if (!WAIT(bars.rfull[rslot * 4 + grp], rphase)) { ok = false; break; }
-              raw += rslot * 4 * kRawUnit;
-              scale += rslot * 4 * kRawUnit;
-              used = (grp + 4 * x) * 16 < d.rows;
-            }
-            if (used) {
+            uint64_t* const rfull = rfull0 + (rq >> rq_shift) * (bar_step / 8);
+            if (!WAIT(*rfull, rphase)) { ok = false; break; }
+            if (row_first + x * row_unit < d.rows) {  // rows past the last one are not read by the MMA
+              uint32_t raw = raw0 + (rq >> rq_shift) * raw_slot + x * raw_unit,
+                       scale = scale0 + (rq >> rq_shift) * raw_slot + x * scale_unit, dst = dst0;
 #pragma unroll 1
               for (int p = 0; p < 2; ++p) {
                 const uint4 w = lds128(raw);
@@ -381,12 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(full);
-              if (rank == 1) mbar_arrive(&bars.rempty[rslot * 4 + grp]);
+              mbar_arrive(rfull + rempty_off);
             }
-            if (rank == 1 && ++rslot == kRawSlots / 4) { rslot = 0; rphase ^= 1; }
+            if (++rq == rq_end) { rq = 0; rphase ^= 1; }
           }
-          if (rank == 0 && lane == 0) mbar_arrive(&bars.rempty[tc & 1]);
-          ++tc;
         }
         if (d.last) break;
       }
@@ -411,10 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         while (ok) {
           Desc d;
-          if (!next_desc(d)) { ok = false; break; }
+          if (!WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
+          const uint32_t v_lo = descs[dc % kDescs].valid[2 * hf], v_hi = descs[dc % kDescs].valid[2 * hf + 1];
+          read_desc(d);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.dempty[(dc - 1) % kDescs]);
           if (d.rows > 0) {
             const uint32_t sb = tc & 1, ph = (tc >> 1) & 1;
-            const uint32_t v_lo = hf ? d.valid[2] : d.valid[0], v_hi = hf ? d.valid[3] : d.valid[1];
             if (!WAIT(bars.sfull[sb], ph)) { ok = false; break; }
             tc_fence_after();
             const uint32_t s_tmem = tmem + lane_off + kTmemS + sb * kTile + hf * 64;
@@ -573,23 +574,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&bars.ffull, kFinalBytes);  // the next item's
         if (lane == 0) mbar_arrive_remote(remote_ffree);
-        const bool empty = first || l == 0.f;
+        // The sink adds 2^s2 to the denominator, all relative to the larger of the
+        // maximum and s2.  (Split chunks get it in the merge.)
         const int h = hb * 128 + hrow;
-        float inv_l = empty ? 0.f : 1.f / l;
-        float lse2 = empty ? neg_inf() : m + log2f(l);  // log2 units
+        float mx = m, num = 1.f, den = l;
         if (P.sink != nullptr && P.n_chunks == 1) {
-          // The sink adds 2^s2 to the denominator; taken relative to max(m, s2)
-          // so that neither term overflows.  (Split chunks get it in the merge.)
           const float s2 = (h < P.H ? __ldg(P.sink + h) : neg_inf()) * 1.4426950408889634f;
-          if (!empty) {
-            const float mx = fmaxf(m, s2);
-            const float den = l * exp2f(m - mx) + exp2f(s2 - mx);
-            inv_l = exp2f(m - mx) / den;
-            lse2 = mx + log2f(den);
-          } else {
-            lse2 = s2;
+          mx = fmaxf(m, s2);
+          if (mx != neg_inf()) {
+            num = ex2_approx(m - mx);
+            den = l * num + ex2_approx(s2 - mx);
           }
         }
+        const float inv_l = den == 0.f ? 0.f : num / den;
+        const float lse2 = den == 0.f ? neg_inf() : mx + log2f(den);  // log2 units
         uint8_t* stage = smem + kOffStage + hf * kUnit;
 #pragma unroll 1
         for (int c0 = hf * 256; c0 < hf * 256 + 256; c0 += 64, ++stores) {  // one atom per round
@@ -603,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 16; ++k) {
               __nv_bfloat162 w =
                   __floats2bfloat162_rn(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
-              pk[k] = empty ? 0u : *reinterpret_cast<uint32_t*>(&w);
+              pk[k] = first ? 0u : *reinterpret_cast<uint32_t*>(&w);  // (no product: O holds an earlier item's)
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -629,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (P.lse != nullptr) P.lse[static_cast<size_t>(t) * P.H + h] = lse2 * 0.69314718055994531f;
           } else {
             P.part_ml[(static_cast<size_t>(t) * P.n_chunks + chunk) * P.H + h] =
-                empty ? make_float2(neg_inf(), 0.f) : make_float2(m, l);
+                make_float2(m, l);
           }
         }
       }
@@ -785,11 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           TileDesc& td = descs[dc % kDescs];
           if (!WAIT(bars.dempty[dc % kDescs], ((dc / kDescs) & 1) ^ 1)) { ok = false; break; }
           *reinterpret_cast<int4*>(&td.row[4 * lane]) = make_int4(r[0], r[1], r[2], r[3]);
-          if ((lane & 7) == 0) td.d.valid[lane >> 3] = nib;
-          if (lane == 0) {
-            td.d.rows = max(0, min(kTile, n_rows - j0));
-            td.d.last = last;
-          }
+          if ((lane & 7) == 0) td.valid[lane >> 3] = nib;
+          if (lane == 0) td.info = max(0, min(kTile, n_rows - j0)) + (last ? kLast : 0);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.dfull[dc % kDescs]);
           ++dc;
