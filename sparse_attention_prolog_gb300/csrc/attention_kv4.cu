@@ -12,24 +12,24 @@
 //   CTA 0: S = q . K^T (M = 128 heads, N = 128 rows, K = 576) and the softmax.
 //          The latent part of q is the A operand in tensor memory (256
 //          columns), its rotary part in shared memory; S is double-buffered in
-//          the other 256 columns.  N = 128 runs at the tensor rate (64.4 of 64
-//          clocks per K = 16 step; N = 64 takes 45 of 32).
+//          the other 256 columns, each buffer filled in two halves of N = 64.
 //   CTA 1: O += P . V with P sent over by CTA 0 and the values read MN-major from
 //          the converted rows.  P goes from a staging buffer by bulk copies between
 //          the CTAs' shared memories: 21 bytes a clock, beside the load/store pipe
 //          (st.async from the softmax threads took some 2800 clocks a tile and held
-//          up the conversion's loads and stores behind it; 3.41 ms).
+//          up the conversion's stores behind it; 3.41 ms for the 4096-token case).
 //
-// Both load the raw rows they need with 16-byte asynchronous copies and convert
-// them from 4 bits to bf16, three instructions per pair of dims, exact,
-// into the 128B-swizzled layout the MMA reads, 16 KB units at a time in the
-// order the MMA consumes and frees them: 64 dims of 128 rows in CTA 0, 512 dims
-// of 16 rows in CTA 1.  (TMA row gathers in place of the copies were the bound: a
-// gather of four rows occupies the engine for about 100 clocks, and CTA 0 needs 64
-// a tile; 3.28 ms for the 4096-token case.)  Unit k of a tile belongs to the
-// warps of group k mod 4.  q goes through the same units of CTA 0, by TMA and
-// then into tensor memory, so the next item's q is on its way while the
-// current item's last tile is multiplied.
+// Both convert the rows from 4 bits to bf16, three instructions per pair of dims,
+// exact, into one of two 64 KB slots (64 rows x 512 dims, 128B-swizzled), which CTA 0
+// reads K-major and CTA 1 MN-major; eight warps fill a slot while the MMA takes the
+// other.  A warp loads its eight rows into registers a tile ahead, two rows of 16
+// lanes an instruction: 584 clocks of the load path for 128 rows.  Measured against
+// it: 16-byte asynchronous copies 812; four lanes a row (which slots of 128 rows x 128
+// dims for N = 128 MMAs ask for) 1854; TMA gathers of four rows 3200, bulk copies of
+// a row 7400.  The 4096-token case took 2.82 to 3.28 ms in those forms; N = 64 costs
+// the tensor core 45 clocks a K = 16 step where N = 128 takes 64 for twice the rows,
+// which was not their bound.  q goes through the same slots of CTA 0, by TMA and then
+// into tensor memory.
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -43,39 +43,35 @@ namespace {
 
 constexpr int kDqk = 576, kDv = 512;
 constexpr int kTile = 128;                 // rows per tile
-constexpr int kUnit = 16384;               // 128 rows x 64 dims, or 16 rows x 512 dims, bf16
-constexpr int kUnits = 4;                  // units in flight, one per group of conversion warps
-constexpr int kRawSlots = 12;              // CTA 1: raw units in flight, three per group
-constexpr int kPSlot = 32768;              // P [128 heads x 128 rows] bf16
-constexpr int kRawRow = 288;               // codes and scale bytes of a row
-constexpr int kRawTile = kTile * kRawRow;  // CTA 0: a tile's raw rows
-constexpr int kRawUnit = 16 * kRawRow;     // CTA 1: 16 raw rows
+constexpr int kAtom = 16384;               // 128 rows (or heads) x 128 bytes
+constexpr int kHalf = 64;                  // rows of a slot
+constexpr int kSlot = 4 * kAtom;           // 64 rows x 512 dims bf16: 8 atoms of 64 rows x 128 bytes
+constexpr int kPSlot = 2 * kAtom;          // P [128 heads x 128 rows] bf16
 constexpr int kDescs = 4;
-constexpr uint64_t kTryNs = 40;           // a try of a barrier takes about so long
-// 32 warps in eight warpgroups: 0-1 softmax (CTA 0), correction and epilogue
-// (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, q loads (CTA 0) or the news of
-// P's arrival and use (CTA 1); 7 raw row loads.  The launch grants 64 registers a thread.
-constexpr int kThreads = 1024;
+constexpr uint64_t kTryNs = 40;            // a try of a barrier takes about so long
+// 28 warps in seven warpgroups: 0-1 softmax (CTA 0), correction and epilogue
+// (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, and q loads and rotary K loads
+// (CTA 0) or the news of P's use and arrival (CTA 1).  The launch grants 72 registers
+// a thread: 896 x 72 = 256 x 80 + 512 x 64 + 128 x 88.
+constexpr int kThreads = 896;
 constexpr int kSoftWarps = 8, kConvWarps = 16, kFirstConv = 8, kMmaWarp = 24, kRowWarp = 25, kAuxWarp = 26,
-              kSentWarp = 27, kFirstLoad = 28, kLoadWarps = 4;
-constexpr int kRegsLaunch = 64, kRegsSoft = 80, kRegsConv = 56, kRegsLast = 72, kRegsLoad = 56;
-static_assert(256 * kRegsSoft + 512 * kRegsConv + 128 * (kRegsLast + kRegsLoad) <= kThreads * kRegsLaunch,
+              kAux2Warp = 27;
+constexpr int kRegsLaunch = 72, kRegsSoft = 80, kRegsConv = 64, kRegsLast = 88;
+static_assert(256 * kRegsSoft + 512 * kRegsConv + 128 * kRegsLast <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
-constexpr uint32_t kPBytes = 128 * (2 * 128 + 4);  // a P tile and its rescale factors
-constexpr uint32_t kFinalBytes = 128 * 12;         // per head: maximum, two partial sums
-constexpr uint32_t kTmemS = 256;                   // CTA 0: q in columns [0, 256), S in [256, 512)
+constexpr uint32_t kPBytes = kPSlot + 512;  // a P tile and its rescale factors
+constexpr uint32_t kFinalBytes = 128 * 16;  // per head: two partial softmaxes' maximum and sum
+constexpr uint32_t kTmemS = 256;            // CTA 0: q in columns [0, 256), S in [256, 512)
 
-// Dynamic shared memory, after the units.  CTA 0: q's rotary part, two rotary K
-// buffers, two raw tiles, the row maxima that the two warps of a head exchange, P
-// and its rescale factors on their way out.
-// CTA 1: two P slots, the output staging of each column half, raw units, rescale
-// factors, finals.
-constexpr int kOffQrope = kUnits * kUnit, kOffKrope = kOffQrope + kUnit, kOffRaw0 = kOffKrope + 2 * kUnit,
-              kOffMax = kOffRaw0 + 2 * kRawTile, kOffPst = kOffMax + 2048, kEnd0 = kOffPst + kPSlot + 512;
-constexpr int kOffP = kUnits * kUnit, kOffStage = kOffP + 2 * kPSlot, kOffRaw1 = kOffStage + 2 * kUnit,
-              kOffAlpha = kOffRaw1 + kRawSlots * kRawUnit, kOffFinal = kOffAlpha + 1024, kEnd1 = kOffFinal + 1536;
+// Dynamic shared memory, after the slots.  CTA 0: q's rotary part, two rotary K
+// buffers, P and its rescale factors on their way out, the running maxima.  CTA 1:
+// two P slots, the output staging, rescale factors, finals.
+constexpr int kOffQrope = 2 * kSlot, kOffKrope = kOffQrope + kAtom, kOffPst = kOffKrope + 2 * kAtom,
+              kOffMax = kOffPst + kPSlot + 512, kEnd0 = kOffMax + 1024;
+constexpr int kOffP = 2 * kSlot, kOffStage = kOffP + 2 * kPSlot, kOffAlpha = kOffStage + kAtom,
+              kOffFinal = kOffAlpha + 1024, kEnd1 = kOffFinal + 2048;
 constexpr int kSmem = 1024 + (kEnd0 > kEnd1 ? kEnd0 : kEnd1);
-static_assert(kSmem + 1024 + kDescs * 576 <= 232448, "shared memory of a CTA");
+static_assert(kSmem + 1024 + kDescs * 544 <= 232448, "shared memory of a CTA");
 
 struct AttnKv4Params {
   int T, B, n_q, H, topk, max_L, n_chunks, chunk_rows, head_blocks, items;
@@ -107,26 +103,20 @@ struct Desc {
 };
 
 struct __align__(8) Bars {
-  uint64_t full[kUnits], empty[kUnits];      // units (CTA 0: K and q; CTA 1: V)
-  uint64_t rfull[kRawSlots], rempty[kRawSlots];  // raw rows (CTA 0: two tiles; CTA 1: units)
-  uint64_t dfull[kDescs], dempty[kDescs];    // tile descriptors
-  uint64_t kpfull[2], kpempty[2];            // CTA 0: rotary K buffers
-  uint64_t sfull[2], sempty[2];              // CTA 0: S buffers
-  uint64_t pfree[2];                         // CTA 0: P slot of CTA 1 free
-  uint64_t pstaged[2], psent;                // CTA 0: half of P staged; P has arrived
-  uint64_t mx[4];                            // CTA 0: row maxima exchanged (per warp quadrant)
-  uint64_t qgroup[8], qready, qfree, qpfull; // CTA 0: a q unit read / all of q stored / MMAs done with q; q's rotary part
-  uint64_t cdone;                            // CTA 0: every K unit of the item is converted
-  uint64_t ffree;                            // CTA 0: CTA 1 has read the finals
-  uint64_t pfull[2], pcons[2];               // CTA 1: P slots
-  uint64_t ready[2], odone[2], ffull;        // CTA 1: correction / MMA
-  uint64_t stfull[2], stfree[2];             // CTA 1: output staging of each half
-  uint64_t mdrain;                           // the MMA thread's last commit
+  uint64_t full[2], empty[2];              // slots (CTA 0: K and q; CTA 1: V)
+  uint64_t dfull[kDescs], dempty[kDescs];  // tile descriptors
+  uint64_t kpfull[2], kpempty[2];          // CTA 0: rotary K buffers
+  uint64_t sfull[2], sempty[2];            // CTA 0: S buffers
+  uint64_t mchain[4];                      // CTA 0: a tile's running maxima are known (per warp quadrant)
+  uint64_t psent[2], pfree[2];             // CTA 0: P has arrived; P slot of CTA 1 free
+  uint64_t qgroup[2], qready, qfree, qpfull;  // CTA 0: a slot of q read; all of q stored; MMAs done with q; its rotary part
+  uint64_t cdone;                          // CTA 0: every slot of the item is converted
+  uint64_t ffree;                          // CTA 0: CTA 1 has read the finals
+  uint64_t pfull[2], pcons[2];             // CTA 1: P slots
+  uint64_t ready[2], odone[2], ffull;      // CTA 1: correction / MMA
+  uint64_t stfull, stfree;                 // CTA 1: output staging
+  uint64_t mdrain;                         // the MMA thread's last commit
 };
-
-// Units of 16 rows that a tile takes in CTA 1: four or eight, a use or two of every
-// slot.
-__device__ __forceinline__ int pv_units(int rows) { return rows > kTile / 2 ? 8 : 4; }
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
 
@@ -146,15 +136,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-
-// After a wait gave up: waits for a copy that completes on `bar`.  The barrier may
-// have moved on to a later use (then the copy has landed, but its parity is gone),
-// so this waits a tenth of a millisecond at most, many times a copy's time.
-__device__ __forceinline__ void drain_copy(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_test(bar, parity) && globaltimer_ns() - t0 < 100000) {}
-}
-
 // Bulk copy to the peer CTA's shared memory, completing on the peer's barrier.
 __device__ __forceinline__ void bulk_s2peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -165,21 +146,27 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// After a wait gave up: waits for a copy that completes on `bar`.  The barrier may
+// have moved on to a later use (then the copy has landed, but its parity is gone),
+// so this waits a tenth of a millisecond at most, many times a copy's time.
+__device__ __forceinline__ void drain_copy(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_test(bar, parity) && globaltimer_ns() - t0 < 100000) {}
+}
+
 // Bounded wait for a phase of a barrier, in as little code as will do: the roles of
 // this kernel run at the same time, and the two CTAs of a cluster, from one
-// instruction cache.  (With the other kernels' waits inlined the code was 133 KB and a
-// third of the cache's requests missed: 5.97 ms for the 4096-token case.)  A try
-// blocks for some 70 clocks by itself; `tries` is how many fill the limit in force.
-// The thread that runs out sets it to 0, and every later wait gives up at once.
+// instruction cache.  (With the other kernels' waits inlined an earlier form was 133
+// KB and a third of the cache's requests missed: 5.97 ms for the 4096-token case;
+// taking 3 KB of code that this case never reaches out of an 78 KB form won 5%.)
+// A try blocks for some 70 clocks by itself; `tries` is how many fill the limit in
+// force.  The thread that runs out sets it to 0, and every later wait gives up at once.
+// A wait is by parity: it tells a phase from the one before and the one after only, so
+// no role may be two uses of a barrier ahead of or behind the one it waits for.
 template <bool kCluster>
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile uint32_t* tries) {
 #pragma unroll 1
@@ -211,38 +198,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
   uint8_t* sP = smem + kOffP;
   float* sAlpha = reinterpret_cast<float*>(smem + kOffAlpha);  // [2][128]
-  float* sFinal = reinterpret_cast<float*>(smem + kOffFinal);  // [3][128]: maximum, sum, sum
-  float* sMax = reinterpret_cast<float*>(smem + kOffMax);      // [2][2][128]
+  float* sFinal = reinterpret_cast<float*>(smem + kOffFinal);  // [4][128]: maximum, sum of each softmax warpgroup
+  float* sMax = reinterpret_cast<float*>(smem + kOffMax);      // [2][128]: running maxima after even / odd tiles
 
   if (tid == 0) {
-    for (int i = 0; i < kUnits; ++i) { mbar_init(&bars.full[i], 4); mbar_init(&bars.empty[i], 1); }
-    // raw rows arrive by the copies of every thread of the load warps (CTA 0) or of
-    // one of them (CTA 1)
-    for (int i = 0; i < kRawSlots; ++i) {
-      mbar_init(&bars.rfull[i], rank == 0 ? kLoadWarps * 32 : 32);
-      mbar_init(&bars.rempty[i], rank == 0 ? 2 * kConvWarps : 4);
-    }
-    // descriptors are read by the conversion, softmax / correction and load warps
-    // and two threads: MMA, q loads / relay; in CTA 1 a third that tells of P's arrival
-    for (int i = 0; i < kDescs; ++i) {
-      mbar_init(&bars.dfull[i], 1);
-      mbar_init(&bars.dempty[i], kConvWarps + kSoftWarps + kLoadWarps + 2 + (rank == 0 ? 0 : 1));
-    }
-    for (int i = 0; i < 4; ++i) mbar_init(&bars.mx[i], 2);
-    for (int i = 0; i < 8; ++i) mbar_init(&bars.qgroup[i], 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.mchain[i], 1);
+    // descriptors are read by the conversion and softmax / correction warps and
+    // three more roles: MMA, q and rotary loads / the two that tell of P
+    for (int i = 0; i < kDescs; ++i) { mbar_init(&bars.dfull[i], 1); mbar_init(&bars.dempty[i], kConvWarps + kSoftWarps + 3); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.kpfull[i], kLoadWarps * 32); mbar_init(&bars.kpempty[i], 1);
-      mbar_init(&bars.sfull[i], 1); mbar_init(&bars.sempty[i], kSoftWarps); mbar_init(&bars.pfree[i], 1); mbar_init(&bars.pstaged[i], 4);
-      mbar_init(&bars.pfull[i], 1); mbar_init(&bars.pcons[i], 1); mbar_init(&bars.ready[i], kSoftWarps);
-      mbar_init(&bars.odone[i], 1); mbar_init(&bars.stfull[i], 4); mbar_init(&bars.stfree[i], 1);
+      mbar_init(&bars.full[i], kConvWarps / 2); mbar_init(&bars.empty[i], 1); mbar_init(&bars.qgroup[i], kConvWarps / 2);
+      mbar_init(&bars.kpfull[i], 32); mbar_init(&bars.kpempty[i], 1);
+      mbar_init(&bars.sfull[i], 1); mbar_init(&bars.sempty[i], 4);
+      mbar_init(&bars.psent[i], 1); mbar_init(&bars.pfree[i], 1); mbar_init(&bars.pfull[i], 1); mbar_init(&bars.pcons[i], 1);
+      mbar_init(&bars.ready[i], kSoftWarps); mbar_init(&bars.odone[i], 1);
     }
     mbar_init(&bars.qready, kConvWarps);
     mbar_init(&bars.qfree, 1);
-    mbar_init(&bars.psent, 1);
-    mbar_init(&bars.cdone, kConvWarps);
     mbar_init(&bars.qpfull, 1);
+    mbar_init(&bars.cdone, kConvWarps);
     mbar_init(&bars.ffree, kSoftWarps);
     mbar_init(&bars.ffull, 1);
+    mbar_init(&bars.stfull, kSoftWarps);
+    mbar_init(&bars.stfree, 1);
     mbar_init(&bars.mdrain, 1);
     wait_tries = static_cast<uint32_t>(min(wait_limit_ns(P.err) / kTryNs + 1, static_cast<uint64_t>(0xffffffffu)));
     fence_mbar_init();
@@ -270,78 +248,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     d.last = info >= kLast;
     ++dc;
   };
-  auto next_desc = [&](Desc& d) -> bool {
-    if (!WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) return false;
-    read_desc(d);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.dempty[(dc - 1) % kDescs]);
-    return true;
-  };
+  auto free_desc = [&]() { mbar_arrive(&bars.dempty[(dc - 1) % kDescs]); };
   auto next_desc1 = [&](Desc& d) -> bool {
     if (!WAIT1(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) return false;
     read_desc(d);
+    free_desc();
     return true;
   };
-  auto free_desc1 = [&]() { mbar_arrive(&bars.dempty[(dc - 1) % kDescs]); };
 
   if (warp >= kFirstConv && warp < kFirstConv + kConvWarps) {
     setmaxnreg_dec<kRegsConv>();
     // ------------------------------------------------- conversion (both CTAs)
-    // Group grp fills slot grp: units grp and grp + 4 of q (by TMA; the group puts
-    // them into tensor memory) and of every tile.  A warp converts two pieces of 16
-    // rows x 64 dims of a unit, a lane 32 dims (16 bytes) of a row; the lanes
-    // (row = lane / 2, half = lane mod 2) of a quarter warp read and write every
-    // bank once.
-    const int cw = warp - kFirstConv, grp = cw >> 2, wi = cw & 3;
-    const int row = lane >> 1, half = lane & 1;
+    // Group grp (eight warps) fills slot grp once for q (by TMA; the group puts it into
+    // tensor memory) and once for every tile, with rows 64 grp.. of it.  A lane
+    // converts 32 dims (16 bytes of codes, piece pc) of rows 2 i + rp of its warp's
+    // eight.  Lanes are numbered, and odd pairs of pieces stored in another order, so
+    // that a quarter warp's stores meet every bank once.
+    const int cw = warp - kFirstConv, grp = cw >> 3, wi = cw & 7;
+    const int pc = ((lane >> 3) << 2) | (lane & 3), rp = (lane >> 2) & 1;
     uint64_t* const full = &bars.full[grp];
     uint64_t* const empty = &bars.empty[grp];
-    // CTA 0: rows 32 wi.. of 64 dims; CTA 1: dims 128 wi.. of 16 rows.  What differs
-    // is in these variables: both CTAs run the same loop, which an instruction cache
-    // may then hold once for both.
-    const uint32_t raw_step = rank == 0 ? 16 * kRawRow : 32, scale_step = rank == 0 ? 16 * kRawRow : 4,
-                   dst_step = rank == 0 ? 16 * 128 : 2048;
-    const uint32_t dst0 = smem_u32(smem) + grp * kUnit + (rank == 0 ? wi * 32 * 128 : wi * 2 * 2048) + row * 128 +
-                          (((half * 4) ^ (row & 7)) << 4);
-    const uint32_t raw0 = smem_u32(smem) + (rank == 0 ? kOffRaw0 + (wi * 32 + row) * kRawRow + grp * 32 + half * 16
-                                                      : kOffRaw1 + grp * kRawUnit + row * kRawRow + wi * 64 + half * 16);
-    const uint32_t scale0 = smem_u32(smem) + kKv4Scales + half * 2 +
-                            (rank == 0 ? kOffRaw0 + (wi * 32 + row) * kRawRow + grp * 4
-                                       : kOffRaw1 + grp * kRawUnit + row * kRawRow + wi * 8);
-    // raw rows: turn rq of a ring; two turns (units) a raw tile in CTA 0, one a raw
-    // unit in CTA 1
-    const uint32_t rq_shift = rank == 0 ? 1 : 0, rq_end = rank == 0 ? 4 : kRawSlots / 4,
-                   raw_slot = rank == 0 ? kRawTile : 4 * kRawUnit, bar_step = rank == 0 ? 8 : 32,
-                   raw_unit = rank == 0 ? 128 : 0, scale_unit = rank == 0 ? 16 : 0;
-    uint64_t* const rfull0 = rank == 0 ? &bars.rfull[0] : &bars.rfull[grp];
-    const int rempty_off = static_cast<int>(&bars.rempty[0] - &bars.rfull[0]);
-    const int row_first = rank == 0 ? wi * 32 : grp * 16, row_unit = rank == 0 ? 0 : 64;  // of unit x
-    const int one_unit = rank == 0 ? 0 : kTile / 2;  // tiles of so many rows at most take one use of each slot
-    uint32_t uses = 0, rq = 0, rphase = 0;
-    bool ok = true;
+    const uint32_t slot = smem_u32(smem) + grp * kSlot;
+    const bool swap = (pc & 2) != 0;
+    const uint32_t dst0 = slot + (pc >> 1) * (kSlot / 8) + (wi * 8 + rp) * 128 +
+                          ((((pc & 1) * 4) ^ (swap ? 2 : 0) ^ rp) << 4);
+    const uint8_t* const src = P.kv4 + pc * 16;
+    const int scale_off = kKv4Scales - pc * 14;
+    const int my_row = grp * kHalf + wi * 8 + rp;
+    uint4 c[4];
+    uint32_t sc[4];
+    auto load = [&](int r, uint4& c, uint32_t& s) {
+      c = make_uint4(0, 0, 0, 0);
+      s = 0;
+      if (r >= 0) {
+        const uint8_t* p = src + static_cast<size_t>(r) * kKv4Row;
+        c = __ldg(reinterpret_cast<const uint4*>(p));
+        s = __ldg(reinterpret_cast<const uint16_t*>(p + scale_off));
+      }
+    };
+    uint32_t uses = 0;
+    Desc cur{0, false};
+    bool ok = WAIT(bars.dfull[0], 0);
+    if (ok) {
+      const int* rows = descs[0].row + my_row;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load(rows[i * 2], c[i], sc[i]);
+      read_desc(cur);
+      __syncwarp();
+      if (lane == 0) free_desc();
+    }
 #pragma unroll 1
     for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
       if (rank == 0) {
-        // q: 64 dims of the 128 heads a unit, lane = head
+        // q: 256 dims of the 128 heads a slot (4 atoms), lane = head, two atoms a warp
         if (n > 0) ok = WAIT(bars.qfree, (n - 1) & 1);
+        if (ok) ok = WAIT(*full, uses & 1);
+        if (!ok) break;
+        ++uses;
         tc_fence_after();
 #pragma unroll 1
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (!WAIT(*full, x)) { ok = false; break; }
-          const uint32_t src = smem_u32(smem) + grp * kUnit;
+        for (int x = 0; x < 2; ++x) {
+          const int a = (wi >> 2) * 2 + x;
           uint32_t r[32];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint4 v = lds128(src + sw128_off(wi * 32 + lane, k));
+            const uint4 v = lds128(slot + a * kAtom + sw128_off((wi & 3) * 32 + lane, k));
             r[4 * k] = v.x; r[4 * k + 1] = v.y; r[4 * k + 2] = v.z; r[4 * k + 3] = v.w;
           }
-          tmem_st32(tmem + lane_off + (grp + 4 * x) * 32, r);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.qgroup[grp + 4 * x]);
-          if (wi == 0) {  // the four warps have read the unit
-            if (!WAIT(bars.qgroup[grp + 4 * x], n & 1)) { ok = false; break; }
-            if (lane == 0) mbar_arrive(empty);
-          }
+          tmem_st32(tmem + lane_off + (grp * 4 + a) * 32, r);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.qgroup[grp]);
+        if (wi == 0) {  // the eight warps have read the slot
+          if (!WAIT(bars.qgroup[grp], n & 1)) { ok = false; break; }
+          if (lane == 0) mbar_arrive(empty);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -350,43 +330,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll 1
       while (ok) {
-        Desc d;
-        if (!next_desc(d)) { ok = false; break; }
-        if (d.rows > 0) {
-          const int n_x = d.rows > one_unit ? 2 : 1;
-#pragma unroll 1
-          for (int x = 0; x < n_x; ++x) {
-            if (!WAIT(*empty, (uses & 1) ^ 1)) { ok = false; break; }
-            ++uses;
-            uint64_t* const rfull = rfull0 + (rq >> rq_shift) * (bar_step / 8);
-            if (!WAIT(*rfull, rphase)) { ok = false; break; }
-            if (row_first + x * row_unit < d.rows) {  // rows past the last one are not read by the MMA
-              uint32_t raw = raw0 + (rq >> rq_shift) * raw_slot + x * raw_unit,
-                       scale = scale0 + (rq >> rq_shift) * raw_slot + x * scale_unit, dst = dst0;
-#pragma unroll 1
-              for (int p = 0; p < 2; ++p) {
-                const uint4 w = lds128(raw);
-                const uint32_t sc = lds_u16(scale);
-                const Kv4Scale lo = kv4_scale(sc & 255u), hi = kv4_scale(sc >> 8);
-                sts128(dst, kv4_codes8(w.x, lo));
-                sts128(dst ^ 16u, kv4_codes8(w.y, lo));
-                sts128(dst ^ 32u, kv4_codes8(w.z, hi));
-                sts128(dst ^ 48u, kv4_codes8(w.w, hi));
-                raw += raw_step;
-                scale += scale_step;
-                dst += dst_step;
-              }
+        const bool more = !cur.last || item + clusters < P.items;  // another tile, maybe of the next item
+        const int* rows = descs[dc % kDescs].row + my_row;
+        if (more && !WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
+        if (cur.rows > 0 && !WAIT(*empty, (uses & 1) ^ 1)) { ok = false; break; }
+        if (my_row - rp < cur.rows) {  // (rows past the last one are not read by the MMA)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t dst = (dst0 + i * 256) ^ (i << 5);
+            Kv4Scale lo = kv4_scale(sc[i] & 255u), hi = kv4_scale(sc[i] >> 8);
+            uint4 w = c[i];
+            if (swap) {
+              const Kv4Scale t = lo; lo = hi; hi = t;
+              w = make_uint4(w.z, w.w, w.x, w.y);
             }
-            fence_proxy_async_smem();  // generic writes -> tensor core reads
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(full);
-              mbar_arrive(rfull + rempty_off);
-            }
-            if (++rq == rq_end) { rq = 0; rphase ^= 1; }
+            sts128(dst, kv4_codes8(w.x, lo));
+            sts128(dst ^ 16u, kv4_codes8(w.y, lo));
+            sts128(dst ^ 32u, kv4_codes8(w.z, hi));
+            sts128(dst ^ 48u, kv4_codes8(w.w, hi));
           }
         }
-        if (d.last) break;
+        if (cur.rows > 0) {
+          fence_proxy_async_smem();  // generic writes -> tensor core reads
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+          ++uses;
+        }
+        const bool last = cur.last;
+        if (more) {
+          // the next tile's rows, in flight while the MMA takes this one (before the
+          // fence they would be waited for there: 950 clocks a tile)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load(rows[i * 2], c[i], sc[i]);
+          read_desc(cur);
+          __syncwarp();
+          if (lane == 0) free_desc();
+        }
+        if (last) break;
       }
       if (rank == 0 && lane == 0) mbar_arrive(&bars.cdone);
     }
@@ -397,47 +377,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t tc = 0;
     if (rank == 0) {
       // ------------------------------------------------- softmax (CTA 0)
-      // Two threads per head, each 64 of a tile's 128 rows.
-      const uint32_t stage = smem_u32(smem + kOffPst) + hf * kUnit;
+      // Two warpgroups take tiles in turn (group hf the tiles of S buffer hf), a
+      // thread a head's 128 scores; the running maximum goes from tile to tile
+      // through shared memory, the sums stay partial until the item ends.
+      const uint32_t stage = smem_u32(smem + kOffPst);
       float* stage_alpha = reinterpret_cast<float*>(smem + kOffPst + kPSlot);
-      const uint32_t remote_final = mapa(smem_u32(sFinal), 1);
+      const uint32_t s_tmem = tmem + lane_off + kTmemS + hf * kTile;
+      const uint32_t remote_p = mapa(smem_u32(sP), 1) + hf * kPSlot, remote_alpha = mapa(smem_u32(sAlpha), 1) + hf * 512,
+                     remote_pfull = mapa(smem_u32(&bars.pfull[hf]), 1);
+      const uint32_t remote_final = mapa(smem_u32(sFinal), 1) + (hf * 256 + hrow) * 4;
       const uint32_t remote_ffull = mapa(smem_u32(&bars.ffull), 1);
       const uint64_t scale2 = pack_f32x2(P.scale_log2, P.scale_log2), one2 = pack_f32x2(1.f, 1.f);
 #pragma unroll 1
       for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
-        float m_used = neg_inf(), l_sum = 0.f;
+        float m_ref = neg_inf(), l_sum = 0.f;  // this group's part: sum relative to m_ref
+        bool first = true;
 #pragma unroll 1
         while (ok) {
           Desc d;
+          const TileDesc& td = descs[dc % kDescs];
           if (!WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
-          const uint32_t v_lo = descs[dc % kDescs].valid[2 * hf], v_hi = descs[dc % kDescs].valid[2 * hf + 1];
           read_desc(d);
+          const bool mine = d.rows > 0 && (tc & 1) == static_cast<uint32_t>(hf);
+          uint4 valid = make_uint4(0, 0, 0, 0);
+          if (mine) valid = *reinterpret_cast<const uint4*>(td.valid);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.dempty[(dc - 1) % kDescs]);
-          if (d.rows > 0) {
-            const uint32_t sb = tc & 1, ph = (tc >> 1) & 1;
-            if (!WAIT(bars.sfull[sb], ph)) { ok = false; break; }
+          if (lane == 0) free_desc();
+          if (mine) {
+            const uint32_t ph = (tc >> 1) & 1;
+            if (!WAIT(bars.sfull[hf], ph)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t s_tmem = tmem + lane_off + kTmemS + sb * kTile + hf * 64;
-            if ((v_lo & v_hi) != 0xffffffffu) {  // rows that are not selected
+            if ((valid.x & valid.y & valid.z & valid.w) != 0xffffffffu) {  // rows that are not selected
 #pragma unroll 1
-              for (int x = 0; x < 2; ++x) {
+              for (int x = 0; x < 4; ++x) {
                 uint32_t s[32];
                 tmem_ld32(s_tmem + x * 32, s);
                 tmem_ld_wait();
-                const uint32_t valid = x ? v_hi : v_lo;
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                  if (!((valid >> k) & 1u)) s[k] = 0xff800000u;
+                  if (!((valid.x >> k) & 1u)) s[k] = 0xff800000u;
                 tmem_st32(s_tmem + x * 32, s);
+                valid = make_uint4(valid.y, valid.z, valid.w, valid.x);
               }
               tmem_st_wait();
             }
-            // two passes over the 64 scores, 32 at a time: the maximum, then the
+            // two passes over the scores, 32 at a time: the maximum, then the
             // exponentials (reading them twice keeps registers and code small)
             float m_tile = neg_inf();
 #pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < 4; ++x) {
               uint32_t s[32];
               tmem_ld32(s_tmem + x * 32, s);
               tmem_ld_wait();
@@ -447,24 +435,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               m_tile = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
             }
             m_tile *= P.scale_log2;
-            // the other 64 rows' maximum, from the warp that holds them
-            sMax[sb * 256 + hf * 128 + hrow] = m_tile;
+            // the running maximum moves only when a tile exceeds it by more than 2^8
+            if (tc > 0 && !WAIT(bars.mchain[warp & 3], (tc - 1) & 1)) { ok = false; break; }
+            const float m_prev = first ? neg_inf() : sMax[((tc - 1) & 1) * 128 + hrow];
+            const float m_new = m_tile > m_prev + 8.f ? m_tile : m_prev;
+            sMax[(tc & 1) * 128 + hrow] = m_new;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.mx[warp & 3]);
-            if (!WAIT(bars.mx[warp & 3], tc & 1)) { ok = false; break; }
-            m_tile = fmaxf(m_tile, sMax[sb * 256 + (hf ^ 1) * 128 + hrow]);
-            float alpha = 1.f;
-            if (m_tile > m_used + 8.f) {  // also taken when m_used is -inf
-              alpha = ex2_approx(m_used - m_tile);
-              l_sum *= alpha;
-              m_used = m_tile;
-            }
-            if (tc > 0 && !WAIT_CLUSTER(bars.psent, (tc - 1) & 1)) { ok = false; break; }  // the staging is free
-            const float msub = m_used == neg_inf() ? 0.f : -m_used;
+            if (lane == 0) mbar_arrive(&bars.mchain[warp & 3]);
+            const float msub = m_new == neg_inf() ? 0.f : -m_new;  // (nothing selected so far: every p is 0)
+            const float alpha = ex2_approx(m_prev + msub);         // 0 from -inf
+            l_sum *= ex2_approx(m_ref + msub);
+            m_ref = m_new;
+            if (tc > 0 && !WAIT_CLUSTER(bars.psent[hf ^ 1], ((tc - 1) >> 1) & 1)) { ok = false; break; }  // the staging is free
+            if (!WAIT_CLUSTER(bars.pfree[hf], ph ^ 1)) { ok = false; break; }
+            stage_alpha[hrow] = first ? 0.f : alpha;
             const uint64_t msub2 = pack_f32x2(msub, msub);
             uint64_t sum2[2] = {0, 0};
+            uint32_t row = stage + hrow * 128, c = (hrow & 7) << 4;
 #pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < 4; ++x) {
               uint32_t s[32];
               tmem_ld32(s_tmem + x * 32, s);
               tmem_ld_wait();
@@ -479,41 +468,42 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                sts128(stage + sw128_off(hrow, x * 4 + k), make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]));
+                sts128(row + (c ^ (k << 4)), make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]));
+              c ^= 64;
+              if (x & 1) {  // an atom of the warp's 32 heads is staged: send it
+                fence_proxy_async_smem();  // generic writes -> bulk copy reads
+                __syncwarp();
+                if (lane == 0) {
+                  const uint32_t off = (x >> 1) * kAtom + (warp & 3) * 4096;
+                  bulk_s2peer(remote_p + off, stage + off, 4096, remote_pfull);
+                  if (x == 1)
+                    bulk_s2peer(remote_alpha + (warp & 3) * 128, smem_u32(stage_alpha) + (warp & 3) * 128, 128, remote_pfull);
+                }
+                row += kAtom;
+              }
             }
-            if (hf == 0) stage_alpha[hrow] = alpha;
-            fence_proxy_async_smem();  // generic writes -> bulk copy reads
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&bars.sempty[sb]);
-              mbar_arrive(&bars.pstaged[hf]);
-            }
+            if (lane == 0) mbar_arrive(&bars.sempty[hf]);
             l_sum += (lo_f32(sum2[0]) + hi_f32(sum2[0])) + (lo_f32(sum2[1]) + hi_f32(sum2[1]));
-            if ((warp & 3) == 0) {  // the four warps of this half have staged it: send it
-              if (!WAIT(bars.pstaged[hf], tc & 1) || !WAIT_CLUSTER(bars.pfree[sb], ph ^ 1)) { ok = false; break; }
-              if (lane == 0) {
-                const uint32_t dst = mapa(smem_u32(sP), 1) + sb * kPSlot + hf * kUnit, bar = mapa(smem_u32(&bars.pfull[sb]), 1);
-                bulk_s2peer(dst, stage, kUnit, bar);
-                if (hf == 0) bulk_s2peer(mapa(smem_u32(sAlpha), 1) + sb * 512, smem_u32(stage_alpha), 512, bar);
-              }
-              __syncwarp();
-            }
+          }
+          if (d.rows > 0) {
+            first = false;
             ++tc;
           }
           if (d.last) break;
         }
         if (ok && n > 0) ok = WAIT_CLUSTER(bars.ffree, (n - 1) & 1);
         if (ok) {
-          if (hf == 0) st_async_b32(remote_final + hrow * 4, __float_as_uint(m_used), remote_ffull);
-          st_async_b32(remote_final + (128 + hf * 128 + hrow) * 4, __float_as_uint(l_sum), remote_ffull);
+          st_async_b32(remote_final, __float_as_uint(m_ref), remote_ffull);
+          st_async_b32(remote_final + 512, __float_as_uint(l_sum), remote_ffull);
         }
       }
     } else {
       // ------------------------------- correction and epilogue (CTA 1)
       const uint32_t remote_ffree = mapa(smem_u32(&bars.ffree), 0);
       uint32_t consumed = 0;  // odone phases observed
-      uint32_t stores = 0;    // output atoms of this half
+      uint32_t stores = 0;    // output atoms
 #pragma unroll 1
       for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
         const int chunk = item % P.n_chunks, th = item / P.n_chunks, hb = th % P.head_blocks, t = th / P.head_blocks;
@@ -521,15 +511,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         while (ok) {
           Desc d;
-          if (!next_desc(d)) { ok = false; break; }
+          if (!WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
+          read_desc(d);
+          __syncwarp();
+          if (lane == 0) free_desc();
           if (d.rows > 0) {
             const uint32_t ps = tc & 1;
             if (!WAIT_CLUSTER(bars.pfull[ps], (tc >> 1) & 1)) { ok = false; break; }
             const float alpha = sAlpha[ps * 128 + hrow];
-            const bool need = __any_sync(0xffffffffu, alpha != 1.f) && !first;
-            if (need) {
+            if (__any_sync(0xffffffffu, alpha != 1.f) && !first) {
               // O must hold the previous tile's product before it is rescaled.
-              while (ok && consumed < tc) {
+              if (consumed < tc) {
                 ok = WAIT(bars.odone[consumed & 1], (consumed >> 1) & 1);
                 ++consumed;
               }
@@ -550,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.ready[ps]);
             // keep at most one completed product unobserved
-            while (ok && consumed < tc) {
+            if (consumed < tc) {
               ok = WAIT(bars.odone[consumed & 1], (consumed >> 1) & 1);
               ++consumed;
             }
@@ -559,64 +551,62 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (d.last) break;
         }
-        // Every product is in O and (maximum, sums) of each head have arrived:
-        // normalise, convert to bf16 into a swizzled staging atom and write it
-        // with TMA stores, 64 columns x 128 heads per box (heads past H are
-        // clipped by the tensor map).
-        while (ok && consumed < tc) {
+        // Every product is in O and the partial softmaxes of each head have arrived:
+        // normalise, convert to bf16 into a swizzled staging atom and write it with
+        // TMA stores, 64 columns x 128 heads per box (heads past H are clipped by the
+        // tensor map), each of the two warps of a head half of the columns.
+        if (ok && consumed < tc) {
           ok = WAIT(bars.odone[consumed & 1], (consumed >> 1) & 1);
           ++consumed;
         }
         if (ok) ok = WAIT_CLUSTER(bars.ffull, n & 1);
         if (!ok) break;
         tc_fence_after();
-        const float m = sFinal[hrow], l = sFinal[128 + hrow] + sFinal[256 + hrow];
+        const float m0 = sFinal[hrow], l0 = sFinal[128 + hrow], m1 = sFinal[256 + hrow], l1 = sFinal[384 + hrow];
         __syncwarp();
         if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&bars.ffull, kFinalBytes);  // the next item's
         if (lane == 0) mbar_arrive_remote(remote_ffree);
+        const float m = fmaxf(m0, m1), mz = m == neg_inf() ? 0.f : m;
+        const float l = l0 * ex2_approx(m0 - mz) + l1 * ex2_approx(m1 - mz);
         // The sink adds 2^s2 to the denominator, all relative to the larger of the
         // maximum and s2.  (Split chunks get it in the merge.)
         const int h = hb * 128 + hrow;
         float mx = m, num = 1.f, den = l;
         if (P.sink != nullptr && P.n_chunks == 1) {
-          const float s2 = (h < P.H ? __ldg(P.sink + h) : neg_inf()) * 1.4426950408889634f;
-          mx = fmaxf(m, s2);
+          const float k2 = (h < P.H ? __ldg(P.sink + h) : neg_inf()) * 1.4426950408889634f;
+          mx = fmaxf(m, k2);
           if (mx != neg_inf()) {
             num = ex2_approx(m - mx);
-            den = l * num + ex2_approx(s2 - mx);
+            den = l * num + ex2_approx(k2 - mx);
           }
         }
         const float inv_l = den == 0.f ? 0.f : num / den;
         const float lse2 = den == 0.f ? neg_inf() : mx + log2f(den);  // log2 units
-        uint8_t* stage = smem + kOffStage + hf * kUnit;
+        const uint32_t row = smem_u32(smem + kOffStage) + hrow * 128, c = ((hf * 4) ^ (hrow & 7)) << 4;
 #pragma unroll 1
-        for (int c0 = hf * 256; c0 < hf * 256 + 256; c0 += 64, ++stores) {  // one atom per round
-          if (stores > 0 && !WAIT(bars.stfree[hf], (stores - 1) & 1)) { ok = false; break; }
-#pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            uint32_t v[32], pk[16];
-            tmem_ld32(tmem + lane_off + c0 + x * 32, v);
-            tmem_ld_wait();
+        for (int c0 = 0; c0 < kDv; c0 += 64, ++stores) {  // one atom per round
+          if (stores > 0 && !WAIT(bars.stfree, (stores - 1) & 1)) { ok = false; break; }
+          uint32_t v[32];
+          tmem_ld32(tmem + lane_off + c0 + hf * 32, v);
+          tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              __nv_bfloat162 w =
-                  __floats2bfloat162_rn(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
-              pk[k] = first ? 0u : *reinterpret_cast<uint32_t*>(&w);  // (no product: O holds an earlier item's)
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(stage + sw128_off(hrow, x * 4 + k)) =
-                  make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+          for (int k = 0; k < 16; ++k) {
+            __nv_bfloat162 w =
+                __floats2bfloat162_rn(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
+            v[k] = first ? 0u : *reinterpret_cast<uint32_t*>(&w);  // (no product: O holds an earlier item's)
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sts128(row + (c ^ (k << 4)), make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.stfull[hf]);
-          if ((warp & 3) == 0 && lane == 0) {  // the four warps of this half have written the atom
-            if (WAIT1(bars.stfull[hf], stores & 1)) {
-              tma_store_3d(&tmap_o, stage, c0, hb * 128, P.n_chunks == 1 ? t : t * P.n_chunks + chunk);
+          if (lane == 0) mbar_arrive(&bars.stfull);
+          if (warp == 0 && lane == 0) {  // the eight warps have written the atom
+            if (WAIT1(bars.stfull, stores & 1)) {
+              tma_store_3d(&tmap_o, smem + kOffStage, c0, hb * 128, P.n_chunks == 1 ? t : t * P.n_chunks + chunk);
               bulk_commit_group();
               bulk_wait_group_read0();
-              mbar_arrive(&bars.stfree[hf]);
+              mbar_arrive(&bars.stfree);
             }
           }
           __syncwarp();
@@ -626,76 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (P.n_chunks == 1) {
             if (P.lse != nullptr) P.lse[static_cast<size_t>(t) * P.H + h] = lse2 * 0.69314718055994531f;
           } else {
-            P.part_ml[(static_cast<size_t>(t) * P.n_chunks + chunk) * P.H + h] =
-                make_float2(m, l);
+            P.part_ml[(static_cast<size_t>(t) * P.n_chunks + chunk) * P.H + h] = make_float2(m, l);
           }
         }
       }
     }
-  } else if (warp >= kFirstLoad) {
-    setmaxnreg_dec<kRegsLoad>();
-    // --------------------------------------------- raw row loads (both CTAs)
-    // Load warp lw copies rows 32 lw.. of a tile in CTA 0, units lw and lw + 4 (16
-    // rows each) in CTA 1: 16 chunks of codes for two rows, 2 chunks of scale bytes
-    // for 16 rows, 8 chunks of rotary dims for four rows (swizzled) an instruction.
-    const int lw = warp - kFirstLoad;
-    uint32_t tc = 0, rslot = 0, rphase = 0;
-    bool ok = true;
-    auto copy_rows = [&](const int* rows, int n, uint32_t dst) {  // codes and scale bytes of n rows (16 or 32)
-#pragma unroll 4
-      for (int i = 0; i < n / 2; ++i) {
-        const int x = 2 * i + (lane >> 4), r = rows[x];
-        cp_async16(dst + x * kRawRow + (lane & 15) * 16,
-                   P.kv4 + static_cast<size_t>(r < 0 ? 0 : r) * kKv4Row + (lane & 15) * 16, r < 0 ? 0 : 16);
-      }
-#pragma unroll 1
-      for (int i = 0; i < n / 16; ++i) {
-        const int x = 16 * i + (lane >> 1), r = rows[x];
-        cp_async16(dst + x * kRawRow + kKv4Scales + (lane & 1) * 16,
-                   P.kv4 + static_cast<size_t>(r < 0 ? 0 : r) * kKv4Row + kKv4Scales + (lane & 1) * 16, r < 0 ? 0 : 16);
-      }
-    };
-#pragma unroll 1
-    for (int item = cluster; item < P.items && ok; item += clusters) {
-#pragma unroll 1
-      while (ok) {
-        Desc d;
-        if (!WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
-        const int* rows = descs[dc % kDescs].row;
-        read_desc(d);
-        if (d.rows > 0 && rank == 0) {
-          const uint32_t rs = tc & 1, ph = (tc >> 1) & 1;
-          const int n = min(32, ((d.rows + 15) & ~15) - lw * 32);
-          rows += lw * 32;
-          if (!WAIT(bars.kpempty[rs], ph ^ 1)) { ok = false; break; }
-          const uint32_t kp = smem_u32(smem + kOffKrope) + rs * kUnit;
-#pragma unroll 4
-          for (int i = 0; i < n / 4; ++i) {
-            const int x = 4 * i + (lane >> 3), r = rows[x];
-            cp_async16(kp + sw128_off(lw * 32 + x, lane & 7),
-                       P.kv4 + static_cast<size_t>(r < 0 ? 0 : r) * kKv4Row + kKv4Rope + (lane & 7) * 16, r < 0 ? 0 : 16);
-          }
-          cp_async_mbar_arrive(&bars.kpfull[rs]);
-          if (!WAIT(bars.rempty[rs], ph ^ 1)) { ok = false; break; }
-          copy_rows(rows, n, smem_u32(smem + kOffRaw0) + rs * kRawTile + lw * 32 * kRawRow);
-          cp_async_mbar_arrive(&bars.rfull[rs]);
-          ++tc;
-        } else if (d.rows > 0) {
-#pragma unroll 1
-          for (int k = lw; k < pv_units(d.rows); k += 4) {
-            const uint32_t rs = rslot * 4 + lw;
-            if (!WAIT(bars.rempty[rs], rphase ^ 1)) { ok = false; break; }
-            if (k * 16 < d.rows) copy_rows(rows + k * 16, 16, smem_u32(smem + kOffRaw1) + rs * kRawUnit);
-            cp_async_mbar_arrive(&bars.rfull[rs]);
-            if (++rslot == kRawSlots / 4) { rslot = 0; rphase ^= 1; }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.dempty[(dc - 1) % kDescs]);
-        if (d.last) break;
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight when the CTA ends
   } else {
     setmaxnreg_inc<kRegsLast>();
     if (warp == kRowWarp) {
@@ -794,44 +719,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp && rank == 0) {
       // ---------------------------------------------- QK^T MMA (CTA 0)
       if (elect_one()) {
-        uint32_t tc = 0;
+        uint32_t tc = 0, uses = 0;  // uses of every slot
         bool ok = true;
         const uint32_t base = smem_u32(smem);
 #pragma unroll 1
         for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
           ok = WAIT1(bars.qready, n & 1) && WAIT1(bars.qpfull, n & 1);
           if (!ok) break;
-          tc_fence_after();
+          ++uses;
 #pragma unroll 1
           while (ok) {
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
-            free_desc1();
             if (d.rows > 0) {
               const uint32_t sb = tc & 1, ph = (tc >> 1) & 1;
-              const uint32_t idesc = idesc_f16(128, (d.rows + 15) & ~15, kFmtBF16, 0, 0);
+              const int rows16 = (d.rows + 15) & ~15;
               const uint32_t dt = tmem + kTmemS + sb * kTile;
               if (!WAIT1(bars.sempty[sb], ph ^ 1) || !WAIT1(bars.kpfull[sb], ph)) { ok = false; break; }
               fence_proxy_async_smem();  // cp.async data -> tensor core reads
               tc_fence_after();
+              {
+                const uint32_t idesc = idesc_f16(128, rows16, kFmtBF16, 0, 0);
+                const uint64_t ad = smem_desc(base + kOffQrope, 16, 1024, kSwizzle128B);
+                const uint64_t bd = smem_desc(base + kOffKrope + sb * kAtom, 16, 1024, kSwizzle128B);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t ad = smem_desc(base + kOffQrope + kk * 32, 16, 1024, kSwizzle128B);
-                const uint64_t bd = smem_desc(base + kOffKrope + sb * kUnit + kk * 32, 16, 1024, kSwizzle128B);
-                mma_ss(dt, ad, bd, idesc, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk) mma_ss(dt, ad + kk * 2, bd + kk * 2, idesc, kk > 0 ? 1u : 0u);
               }
               mma_commit(&bars.kpempty[sb]);
 #pragma unroll 1
-              for (int k = 0; k < 8; ++k) {
-                if (!WAIT1(bars.full[k & 3], k >> 2)) { ok = false; break; }
-                tc_fence_after();
-                const uint64_t bd = smem_desc(base + (k & 3) * kUnit, 16, 1024, kSwizzle128B);
+              for (int x = 0; x < 2; ++x) {
+                if (!WAIT1(bars.full[x], uses & 1)) { ok = false; break; }
+                const int n16 = min(kHalf, rows16 - x * kHalf);
+                if (n16 > 0) {  // (a slot without rows changes hands all the same)
+                  tc_fence_after();
+                  const uint32_t idesc = idesc_f16(128, n16, kFmtBF16, 0, 0);
+                  uint64_t bd = smem_desc(base + x * kSlot, 16, 1024, kSwizzle128B);
+#pragma unroll 1
+                  for (int a = 0; a < 8; ++a, bd += kSlot / 8 >> 4)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_ts(dt, tmem + k * 32 + kk * 8, bd + kk * 2, idesc, 1u);
-                mma_commit(&bars.empty[k & 3]);
+                    for (int kk = 0; kk < 4; ++kk) mma_ts(dt + x * kHalf, tmem + a * 32 + kk * 8, bd + kk * 2, idesc, 1u);
+                }
+                mma_commit(&bars.empty[x]);
               }
               if (!ok) break;
               mma_commit(&bars.sfull[sb]);
+              ++uses;
               ++tc;
             }
             if (d.last) break;
@@ -845,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------- PV MMA (CTA 1)
       if (elect_one()) {
-        uint32_t tc = 0, uses = 0;  // uses of every slot
+        uint32_t tc = 0;
         bool ok = true;
         const uint32_t idesc = idesc_f16(128, 256, kFmtBF16, 0, 1);
         const uint32_t vbase = smem_u32(smem), pbase = smem_u32(sP);
@@ -856,23 +788,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (ok) {
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
-            free_desc1();
             if (d.rows > 0) {
               const uint32_t ps = tc & 1;
               if (!WAIT1(bars.ready[ps], (tc >> 1) & 1)) { ok = false; break; }
 #pragma unroll 1
-              for (int k = 0; k < pv_units(d.rows); ++k) {
-                if (!WAIT1(bars.full[k & 3], uses & 1)) { ok = false; break; }
-                if (k * 16 < d.rows) {  // (units past the last row change hands all the same)
-                  tc_fence_after();
-                  const uint64_t ad = smem_desc(pbase + ps * kPSlot + (k >> 2) * kUnit + (k & 3) * 32, 16, 1024, kSwizzle128B);
-                  const uint64_t bd = smem_desc(vbase + (k & 3) * kUnit, 2048, 1024, kSwizzle128B);
+              for (int x = 0; x < 2; ++x) {
+                if (!WAIT1(bars.full[x], tc & 1)) { ok = false; break; }
+                tc_fence_after();
+                uint64_t ad = smem_desc(pbase + ps * kPSlot + x * kAtom, 16, 1024, kSwizzle128B);
+                uint64_t bd = smem_desc(vbase + x * kSlot, kSlot / 8, 1024, kSwizzle128B);
+#pragma unroll 1
+                for (int r = x * kHalf; r < min(d.rows, (x + 1) * kHalf); r += 16, ad += 2, bd += 16 * 128 >> 4) {
                   mma_ss(tmem, ad, bd, idesc, acc);
-                  mma_ss(tmem + 256, ad, bd + (4 * 2048 >> 4), idesc, acc);
+                  mma_ss(tmem + 256, ad, bd + (4 * (kSlot / 8) >> 4), idesc, acc);
                   acc = 1;
                 }
-                mma_commit(&bars.empty[k & 3]);
-                if ((k & 3) == 3) ++uses;
+                mma_commit(&bars.empty[x]);
               }
               if (!ok) break;
               mma_commit(&bars.pcons[ps]);
@@ -888,70 +819,89 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kAuxWarp && rank == 0) {
       // ------------------------------------------------------- q loads (CTA 0)
       if (elect_one()) {
-        int q_units = 0, rope_loads = 0;
+        uint32_t uses = 0;
+        int q_slots = 0, rope_loads = 0;
         bool ok = true;
 #pragma unroll 1
         for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
           const int th = item / P.n_chunks, hb = th % P.head_blocks, t = th / P.head_blocks;
-          // not before the previous item's last unit is converted: a wait for a slot is
+          // not before the previous item's last slot is converted: a wait for a slot is
           // by parity, and good for its next use only
           if (n > 0) ok = WAIT1(bars.cdone, (n - 1) & 1);
-          q_units = 0;
+          q_slots = 0;
 #pragma unroll 1
-          for (int k = 0; k < 8 && ok; ++k) {
-            uint64_t* const full = &bars.full[k & 3];
-            if (!WAIT1(bars.empty[k & 3], (k >> 2) ^ 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(full, kUnit);
-            mbar_arrive_n(full, 3);
-            tma_load_3d(smem + (k & 3) * kUnit, &tmap_q, k * 64, hb * 128, t, full);
-            q_units = k + 1;
+          for (int k = 0; k < 2 && ok; ++k) {
+            uint64_t* const full = &bars.full[k];
+            if (!WAIT1(bars.empty[k], (uses & 1) ^ 1)) { ok = false; break; }
+            mbar_arrive_expect_tx(full, kSlot);
+            mbar_arrive_n(full, kConvWarps / 2 - 1);
+#pragma unroll 1
+            for (int a = 0; a < 4; ++a)
+              tma_load_3d(smem + k * kSlot + a * kAtom, &tmap_q, k * 256 + a * 64, hb * 128, t, full);
+            q_slots = k + 1;
           }
           if (ok && n > 0) ok = WAIT1(bars.qfree, (n - 1) & 1);
           if (!ok) break;
-          mbar_arrive_expect_tx(&bars.qpfull, kUnit);
+          mbar_arrive_expect_tx(&bars.qpfull, kAtom);
           tma_load_3d(smem + kOffQrope, &tmap_q, 512, hb * 128, t, &bars.qpfull);
           rope_loads = n + 1;
+          ++uses;
 #pragma unroll 1
           while (ok) {
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
-            free_desc1();
+            if (d.rows > 0) ++uses;
             if (d.last) break;
           }
         }
         if (*tries == 0) {  // the copies in flight land before the CTA's memory is given up
-          for (int k = max(0, q_units - 4); k < q_units; ++k) drain_copy(&bars.full[k & 3], k >> 2);
+          for (int k = 0; k < q_slots; ++k) {
+            drain_copy(&bars.full[k], 0);
+            drain_copy(&bars.full[k], 1);
+          }
           if (rope_loads > 0) mbar_drain(&bars.qpfull, (rope_loads - 1) & 1);
         }
       }
-    } else if (warp == kAuxWarp) {
-      // ----------------------------------- relay: P slot consumed -> CTA 0
-      if (elect_one()) {
-        const uint32_t remote_pfree[2] = {mapa(smem_u32(&bars.pfree[0]), 0), mapa(smem_u32(&bars.pfree[1]), 0)};
-        uint32_t tc = 0;
-        bool ok = true;
+    } else if (warp == kAux2Warp && rank == 0) {
+      // ------------------------------------------------ rotary K loads (CTA 0)
+      // 16-byte asynchronous copies, 8 a row, four rows an instruction, swizzled
+      uint32_t tc = 0;
+      bool ok = true;
 #pragma unroll 1
-        for (int item = cluster; item < P.items && ok; item += clusters) {
+      for (int item = cluster; item < P.items && ok; item += clusters) {
 #pragma unroll 1
-          while (ok) {
-            Desc d;
-            if (!next_desc1(d)) { ok = false; break; }
-            free_desc1();
-            if (d.rows > 0) {
-              const uint32_t ps = tc & 1;
-              if (!WAIT1(bars.pcons[ps], (tc >> 1) & 1)) { ok = false; break; }
-              mbar_arrive_expect_tx(&bars.pfull[ps], kPBytes);  // arm the slot's next use
-              mbar_arrive_remote(remote_pfree[ps]);
-              ++tc;
+        while (ok) {
+          Desc d;
+          if (!WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
+          const int* rows = descs[dc % kDescs].row + (lane >> 3);
+          read_desc(d);
+          if (d.rows > 0) {
+            const uint32_t rs = tc & 1;
+            if (!WAIT(bars.kpempty[rs], ((tc >> 1) & 1) ^ 1)) { ok = false; break; }
+            const uint32_t kp = smem_u32(smem + kOffKrope) + rs * kAtom;
+#pragma unroll 4
+            for (int x = lane >> 3; x < ((d.rows + 15) & ~15); x += 4, rows += 4) {
+              const int r = *rows;
+              cp_async16(kp + sw128_off(x, lane & 7),
+                         P.kv4 + static_cast<size_t>(r < 0 ? 0 : r) * kKv4Row + kKv4Rope + (lane & 7) * 16, r < 0 ? 0 : 16);
             }
-            if (d.last) break;
+            cp_async_mbar_arrive(&bars.kpfull[rs]);
+            ++tc;
           }
+          __syncwarp();
+          if (lane == 0) free_desc();
+          if (d.last) break;
         }
       }
-    } else if (warp == kSentWarp && rank == 1) {
-      // ------------------------------ P has arrived -> CTA 0: its staging is free
+      asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight when the CTA ends
+    } else {
+      // CTA 1: P slot consumed -> CTA 0 (the slot is free); P arrived -> CTA 0 (its
+      // staging is free)
       if (elect_one()) {
-        const uint32_t remote_psent = mapa(smem_u32(&bars.psent), 0);
+        const bool arrived = warp == kAux2Warp;
+        const uint32_t remote[2] = {mapa(smem_u32(arrived ? &bars.psent[0] : &bars.pfree[0]), 0),
+                                    mapa(smem_u32(arrived ? &bars.psent[1] : &bars.pfree[1]), 0)};
+        uint64_t* const local = arrived ? bars.pfull : bars.pcons;
         uint32_t tc = 0;
         bool ok = true;
 #pragma unroll 1
@@ -960,10 +910,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (ok) {
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
-            free_desc1();
             if (d.rows > 0) {
-              if (!wait_phase<true>(&bars.pfull[tc & 1], (tc >> 1) & 1, tries)) { ok = false; break; }
-              mbar_arrive_remote(remote_psent);
+              const uint32_t ps = tc & 1;
+              if (!wait_phase<true>(&local[ps], (tc >> 1) & 1, tries)) { ok = false; break; }
+              if (!arrived) mbar_arrive_expect_tx(&bars.pfull[ps], kPBytes);  // arm the slot's next use
+              mbar_arrive_remote(ps ? remote[1] : remote[0]);
               ++tc;
             }
             if (d.last) break;
