@@ -21,8 +21,8 @@
 //
 // Both convert the rows from 4 bits to bf16, three instructions per pair of dims,
 // exact, into one of two 64 KB slots (64 rows x 512 dims, 128B-swizzled), which CTA 0
-// reads K-major and CTA 1 MN-major; eight warps fill a slot while the MMA takes the
-// other.  A warp loads its eight rows into registers a tile ahead, two rows of 16
+// reads K-major and CTA 1 MN-major; sixteen warps fill one while the MMA takes the
+// other.  A warp loads its rows into registers a tile ahead, two rows of 16
 // lanes an instruction: 584 clocks of the load path for 128 rows.  Measured against
 // it: 16-byte asynchronous copies 812; four lanes a row (which slots of 128 rows x 128
 // dims for N = 128 MMAs ask for) 1854; TMA gathers of four rows 3200, bulk copies of
@@ -52,14 +52,14 @@ constexpr uint64_t kTryNs = 40;            // a try of a barrier takes about so 
 // 28 warps in seven warpgroups: 0-1 softmax (CTA 0), correction and epilogue
 // (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, and q loads and rotary K loads
 // (CTA 0) or the news of P's use and arrival (CTA 1).  The launch grants 72 registers
-// a thread: 896 x 72 = 256 x 80 + 512 x 64 + 128 x 88.
+// a thread: 896 x 72 = 256 x 88 + 512 x 64 + 128 x 72.
 constexpr int kThreads = 896;
 constexpr int kSoftWarps = 8, kConvWarps = 16, kFirstConv = 8, kMmaWarp = 24, kRowWarp = 25, kAuxWarp = 26,
               kAux2Warp = 27;
-constexpr int kRegsLaunch = 72, kRegsSoft = 80, kRegsConv = 64, kRegsLast = 88;
+constexpr int kRegsLaunch = 72, kRegsSoft = 88, kRegsConv = 64, kRegsLast = 72;
 static_assert(256 * kRegsSoft + 512 * kRegsConv + 128 * kRegsLast <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
-constexpr uint32_t kPBytes = kPSlot + 512;  // a P tile and its rescale factors
+constexpr uint32_t kPBytes0 = kAtom + 512, kPBytes1 = kAtom;  // the halves of a P tile, the first with the rescale factors
 constexpr uint32_t kFinalBytes = 128 * 16;  // per head: two partial softmaxes' maximum and sum
 constexpr uint32_t kTmemS = 256;            // CTA 0: q in columns [0, 256), S in [256, 512)
 
@@ -108,11 +108,11 @@ struct __align__(8) Bars {
   uint64_t kpfull[2], kpempty[2];          // CTA 0: rotary K buffers
   uint64_t sfull[2], sempty[2];            // CTA 0: S buffers
   uint64_t mchain[4];                      // CTA 0: a tile's running maxima are known (per warp quadrant)
-  uint64_t psent[2], pfree[2];             // CTA 0: P has arrived; P slot of CTA 1 free
+  uint64_t psent[2][2], pfree[2];          // CTA 0: a half of P has arrived; P slot of CTA 1 free
   uint64_t qgroup[2], qready, qfree, qpfull;  // CTA 0: a slot of q read; all of q stored; MMAs done with q; its rotary part
   uint64_t cdone;                          // CTA 0: every slot of the item is converted
   uint64_t ffree;                          // CTA 0: CTA 1 has read the finals
-  uint64_t pfull[2], pcons[2];             // CTA 1: P slots
+  uint64_t pfull[2][2], pcons[2];          // CTA 1: P slots (halves of 64 rows)
   uint64_t ready[2], odone[2], ffull;      // CTA 1: correction / MMA
   uint64_t stfull, stfree;                 // CTA 1: output staging
   uint64_t mdrain;                         // the MMA thread's last commit
@@ -207,10 +207,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // three more roles: MMA, q and rotary loads / the two that tell of P
     for (int i = 0; i < kDescs; ++i) { mbar_init(&bars.dfull[i], 1); mbar_init(&bars.dempty[i], kConvWarps + kSoftWarps + 3); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.full[i], kConvWarps / 2); mbar_init(&bars.empty[i], 1); mbar_init(&bars.qgroup[i], kConvWarps / 2);
+      mbar_init(&bars.full[i], kConvWarps); mbar_init(&bars.empty[i], 1); mbar_init(&bars.qgroup[i], kConvWarps);
       mbar_init(&bars.kpfull[i], 32); mbar_init(&bars.kpempty[i], 1);
       mbar_init(&bars.sfull[i], 1); mbar_init(&bars.sempty[i], 4);
-      mbar_init(&bars.psent[i], 1); mbar_init(&bars.pfree[i], 1); mbar_init(&bars.pfull[i], 1); mbar_init(&bars.pcons[i], 1);
+      mbar_init(&bars.psent[i][0], 1); mbar_init(&bars.psent[i][1], 1); mbar_init(&bars.pfree[i], 1);
+      mbar_init(&bars.pfull[i][0], 1); mbar_init(&bars.pfull[i][1], 1); mbar_init(&bars.pcons[i], 1);
       mbar_init(&bars.ready[i], kSoftWarps); mbar_init(&bars.odone[i], 1);
     }
     mbar_init(&bars.qready, kConvWarps);
@@ -225,8 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait_tries = static_cast<uint32_t>(min(wait_limit_ns(P.err) / kTryNs + 1, static_cast<uint64_t>(0xffffffffu)));
     fence_mbar_init();
     if (rank == 1) {
-      mbar_arrive_expect_tx(&bars.pfull[0], kPBytes);
-      mbar_arrive_expect_tx(&bars.pfull[1], kPBytes);
+      for (int i = 0; i < 2; ++i) {
+        mbar_arrive_expect_tx(&bars.pfull[i][0], kPBytes0);
+        mbar_arrive_expect_tx(&bars.pfull[i][1], kPBytes1);
+      }
       mbar_arrive_expect_tx(&bars.ffull, kFinalBytes);
     }
   }
@@ -259,23 +262,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kFirstConv && warp < kFirstConv + kConvWarps) {
     setmaxnreg_dec<kRegsConv>();
     // ------------------------------------------------- conversion (both CTAs)
-    // Group grp (eight warps) fills slot grp once for q (by TMA; the group puts it into
-    // tensor memory) and once for every tile, with rows 64 grp.. of it.  A lane
-    // converts 32 dims (16 bytes of codes, piece pc) of rows 2 i + rp of its warp's
-    // eight.  Lanes are numbered, and odd pairs of pieces stored in another order, so
-    // that a quarter warp's stores meet every bank once.
-    const int cw = warp - kFirstConv, grp = cw >> 3, wi = cw & 7;
+    // The sixteen warps fill slot 0, then slot 1, four rows of 64 each: once for q (by
+    // TMA; they put it into tensor memory) and once for every tile.  A lane converts
+    // 32 dims (16 bytes of codes, piece pc) of rows 2 i + rp of its warp's four.  Lanes
+    // are numbered, and odd pairs of pieces stored in another order, so that a quarter
+    // warp's stores meet every bank once.
+    const int cw = warp - kFirstConv;
     const int pc = ((lane >> 3) << 2) | (lane & 3), rp = (lane >> 2) & 1;
-    uint64_t* const full = &bars.full[grp];
-    uint64_t* const empty = &bars.empty[grp];
-    const uint32_t slot = smem_u32(smem) + grp * kSlot;
     const bool swap = (pc & 2) != 0;
-    const uint32_t dst0 = slot + (pc >> 1) * (kSlot / 8) + (wi * 8 + rp) * 128 +
-                          ((((pc & 1) * 4) ^ (swap ? 2 : 0) ^ rp) << 4);
+    const int r7 = (cw & 1) * 4 + rp;  // row of i = 0 mod 8
+    const uint32_t slots = smem_u32(smem);
+    const uint32_t dst0 = slots + (pc >> 1) * (kSlot / 8) + (cw * 4 + rp) * 128 +
+                          ((((pc & 1) * 4) ^ (swap ? 2 : 0) ^ r7) << 4);
     const uint8_t* const src = P.kv4 + pc * 16;
     const int scale_off = kKv4Scales - pc * 14;
-    const int my_row = grp * kHalf + wi * 8 + rp;
-    uint4 c[4];
+    const int my_row = cw * 4 + rp;
+    uint4 c[4];  // piece 2 x + i: rows 64 x + 2 i + my_row
     uint32_t sc[4];
     auto load = [&](int r, uint4& c, uint32_t& s) {
       c = make_uint4(0, 0, 0, 0);
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       const int* rows = descs[0].row + my_row;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load(rows[i * 2], c[i], sc[i]);
+      for (int i = 0; i < 4; ++i) load(rows[(i >> 1) * kHalf + (i & 1) * 2], c[i], sc[i]);
       read_desc(cur);
       __syncwarp();
       if (lane == 0) free_desc();
@@ -300,29 +302,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
       if (rank == 0) {
-        // q: 256 dims of the 128 heads a slot (4 atoms), lane = head, two atoms a warp
+        // q: 256 dims of the 128 heads a slot (4 atoms), lane = head, an atom a warp
         if (n > 0) ok = WAIT(bars.qfree, (n - 1) & 1);
-        if (ok) ok = WAIT(*full, uses & 1);
-        if (!ok) break;
-        ++uses;
         tc_fence_after();
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const int a = (wi >> 2) * 2 + x;
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (!WAIT(bars.full[x], uses & 1)) { ok = false; break; }
           uint32_t r[32];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint4 v = lds128(slot + a * kAtom + sw128_off((wi & 3) * 32 + lane, k));
+            const uint4 v = lds128(slots + x * kSlot + (cw >> 2) * kAtom + sw128_off((cw & 3) * 32 + lane, k));
             r[4 * k] = v.x; r[4 * k + 1] = v.y; r[4 * k + 2] = v.z; r[4 * k + 3] = v.w;
           }
-          tmem_st32(tmem + lane_off + (grp * 4 + a) * 32, r);
+          tmem_st32(tmem + lane_off + (x * 4 + (cw >> 2)) * 32, r);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.qgroup[x]);
+          if (cw == 0) {  // all have read the slot
+            if (!WAIT(bars.qgroup[x], n & 1)) { ok = false; break; }
+            if (lane == 0) mbar_arrive(&bars.empty[x]);
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.qgroup[grp]);
-        if (wi == 0) {  // the eight warps have read the slot
-          if (!WAIT(bars.qgroup[grp], n & 1)) { ok = false; break; }
-          if (lane == 0) mbar_arrive(empty);
-        }
+        if (!ok) break;
+        ++uses;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -333,35 +334,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool more = !cur.last || item + clusters < P.items;  // another tile, maybe of the next item
         const int* rows = descs[dc % kDescs].row + my_row;
         if (more && !WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
-        if (cur.rows > 0 && !WAIT(*empty, (uses & 1) ^ 1)) { ok = false; break; }
-        if (my_row - rp < cur.rows) {  // (rows past the last one are not read by the MMA)
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          if (cur.rows > 0) {
+            if (!WAIT(bars.empty[x], (uses & 1) ^ 1)) { ok = false; break; }
+            if (x * kHalf + cw * 4 < cur.rows) {  // (rows past the last one are not read by the MMA)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t dst = (dst0 + i * 256) ^ (i << 5);
-            Kv4Scale lo = kv4_scale(sc[i] & 255u), hi = kv4_scale(sc[i] >> 8);
-            uint4 w = c[i];
-            if (swap) {
-              const Kv4Scale t = lo; lo = hi; hi = t;
-              w = make_uint4(w.z, w.w, w.x, w.y);
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t dst = (dst0 + x * kSlot + i * 256) ^ (i << 5);
+                Kv4Scale lo = kv4_scale(sc[i] & 255u), hi = kv4_scale(sc[i] >> 8);
+                uint4 w = c[i];
+                if (swap) {
+                  const Kv4Scale t = lo; lo = hi; hi = t;
+                  w = make_uint4(w.z, w.w, w.x, w.y);
+                }
+                sts128(dst, kv4_codes8(w.x, lo));
+                sts128(dst ^ 16u, kv4_codes8(w.y, lo));
+                sts128(dst ^ 32u, kv4_codes8(w.z, hi));
+                sts128(dst ^ 48u, kv4_codes8(w.w, hi));
+              }
             }
-            sts128(dst, kv4_codes8(w.x, lo));
-            sts128(dst ^ 16u, kv4_codes8(w.y, lo));
-            sts128(dst ^ 32u, kv4_codes8(w.z, hi));
-            sts128(dst ^ 48u, kv4_codes8(w.w, hi));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.full[x]);  // (the MMA's thread fences the proxies)
           }
+          c[0] = c[2]; c[1] = c[3];
+          sc[0] = sc[2]; sc[1] = sc[3];
         }
-        if (cur.rows > 0) {
-          fence_proxy_async_smem();  // generic writes -> tensor core reads
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full);
-          ++uses;
-        }
+        if (!ok) break;
+        if (cur.rows > 0) ++uses;
         const bool last = cur.last;
         if (more) {
-          // the next tile's rows, in flight while the MMA takes this one (before the
-          // fence they would be waited for there: 950 clocks a tile)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) load(rows[i * 2], c[i], sc[i]);
+          for (int i = 0; i < 4; ++i) load(rows[(i >> 1) * kHalf + (i & 1) * 2], c[i], sc[i]);
           read_desc(cur);
           __syncwarp();
           if (lane == 0) free_desc();
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* stage_alpha = reinterpret_cast<float*>(smem + kOffPst + kPSlot);
       const uint32_t s_tmem = tmem + lane_off + kTmemS + hf * kTile;
       const uint32_t remote_p = mapa(smem_u32(sP), 1) + hf * kPSlot, remote_alpha = mapa(smem_u32(sAlpha), 1) + hf * 512,
-                     remote_pfull = mapa(smem_u32(&bars.pfull[hf]), 1);
+                     remote_pfull = mapa(smem_u32(&bars.pfull[hf][0]), 1);
       const uint32_t remote_final = mapa(smem_u32(sFinal), 1) + (hf * 256 + hrow) * 4;
       const uint32_t remote_ffull = mapa(smem_u32(&bars.ffull), 1);
       const uint64_t scale2 = pack_f32x2(P.scale_log2, P.scale_log2), one2 = pack_f32x2(1.f, 1.f);
@@ -446,42 +450,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float alpha = ex2_approx(m_prev + msub);         // 0 from -inf
             l_sum *= ex2_approx(m_ref + msub);
             m_ref = m_new;
-            if (tc > 0 && !WAIT_CLUSTER(bars.psent[hf ^ 1], ((tc - 1) >> 1) & 1)) { ok = false; break; }  // the staging is free
-            if (!WAIT_CLUSTER(bars.pfree[hf], ph ^ 1)) { ok = false; break; }
-            stage_alpha[hrow] = first ? 0.f : alpha;
+            // the exponentials of 64 rows into registers, then into their half of the
+            // staging once the previous tile's half has gone, and on their way
             const uint64_t msub2 = pack_f32x2(msub, msub);
             uint64_t sum2[2] = {0, 0};
-            uint32_t row = stage + hrow * 128, c = (hrow & 7) << 4;
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
-              uint32_t s[32];
-              tmem_ld32(s_tmem + x * 32, s);
-              tmem_ld_wait();
+            for (int a = 0; a < 2; ++a) {
+              uint32_t pk[32];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const uint64_t y =
-                    fma_f32x2(pack_f32x2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2, msub2);
-                const float p0 = ex2_approx(lo_f32(y)), p1 = ex2_approx(hi_f32(y));
-                sum2[k & 1] = fma_f32x2(pack_f32x2(p0, p1), one2, sum2[k & 1]);
-                __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-                s[k] = *reinterpret_cast<uint32_t*>(&pb);
-              }
+              for (int x = 0; x < 2; ++x) {
+                uint32_t s[32];
+                tmem_ld32(s_tmem + a * kHalf + x * 32, s);
+                tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                sts128(row + (c ^ (k << 4)), make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]));
-              c ^= 64;
-              if (x & 1) {  // an atom of the warp's 32 heads is staged: send it
-                fence_proxy_async_smem();  // generic writes -> bulk copy reads
-                __syncwarp();
-                if (lane == 0) {
-                  const uint32_t off = (x >> 1) * kAtom + (warp & 3) * 4096;
-                  bulk_s2peer(remote_p + off, stage + off, 4096, remote_pfull);
-                  if (x == 1)
-                    bulk_s2peer(remote_alpha + (warp & 3) * 128, smem_u32(stage_alpha) + (warp & 3) * 128, 128, remote_pfull);
+                for (int k = 0; k < 16; ++k) {
+                  const uint64_t y =
+                      fma_f32x2(pack_f32x2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2, msub2);
+                  const float p0 = ex2_approx(lo_f32(y)), p1 = ex2_approx(hi_f32(y));
+                  sum2[k & 1] = fma_f32x2(pack_f32x2(p0, p1), one2, sum2[k & 1]);
+                  __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+                  pk[x * 16 + k] = *reinterpret_cast<uint32_t*>(&pb);
                 }
-                row += kAtom;
               }
+              if (tc > 0 && !WAIT_CLUSTER(bars.psent[hf ^ 1][a], ((tc - 1) >> 1) & 1)) { ok = false; break; }
+              if (a == 0) {
+                if (!WAIT_CLUSTER(bars.pfree[hf], ph ^ 1)) { ok = false; break; }
+                stage_alpha[hrow] = first ? 0.f : alpha;
+              }
+              const uint32_t row = stage + a * kAtom + hrow * 128, c = (hrow & 7) << 4;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                sts128(row + (c ^ (k << 4)), make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]));
+              fence_proxy_async_smem();  // generic writes -> bulk copy reads
+              __syncwarp();
+              if (lane == 0) {
+                const uint32_t off = a * kAtom + (warp & 3) * 4096, bar = remote_pfull + a * 8;
+                bulk_s2peer(remote_p + off, stage + off, 4096, bar);
+                if (a == 0) bulk_s2peer(remote_alpha + (warp & 3) * 128, smem_u32(stage_alpha) + (warp & 3) * 128, 128, bar);
+              }
+              __syncwarp();
             }
+            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.sempty[hf]);
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) free_desc();
           if (d.rows > 0) {
             const uint32_t ps = tc & 1;
-            if (!WAIT_CLUSTER(bars.pfull[ps], (tc >> 1) & 1)) { ok = false; break; }
+            if (!WAIT_CLUSTER(bars.pfull[ps][0], (tc >> 1) & 1)) { ok = false; break; }  // with the rescale factors
             const float alpha = sAlpha[ps * 128 + hrow];
             if (__any_sync(0xffffffffu, alpha != 1.f) && !first) {
               // O must hold the previous tile's product before it is rescaled.
@@ -749,6 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int x = 0; x < 2; ++x) {
                 if (!WAIT1(bars.full[x], uses & 1)) { ok = false; break; }
+                fence_proxy_async_smem();  // generic writes -> tensor core reads
                 const int n16 = min(kHalf, rows16 - x * kHalf);
                 if (n16 > 0) {  // (a slot without rows changes hands all the same)
                   tc_fence_after();
@@ -793,7 +803,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!WAIT1(bars.ready[ps], (tc >> 1) & 1)) { ok = false; break; }
 #pragma unroll 1
               for (int x = 0; x < 2; ++x) {
+                if (x == 1 && !wait_phase<true>(&bars.pfull[ps][1], (tc >> 1) & 1, tries)) { ok = false; break; }
                 if (!WAIT1(bars.full[x], tc & 1)) { ok = false; break; }
+                fence_proxy_async_smem();  // generic writes -> tensor core reads
                 tc_fence_after();
                 uint64_t ad = smem_desc(pbase + ps * kPSlot + x * kAtom, 16, 1024, kSwizzle128B);
                 uint64_t bd = smem_desc(vbase + x * kSlot, kSlot / 8, 1024, kSwizzle128B);
@@ -834,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t* const full = &bars.full[k];
             if (!WAIT1(bars.empty[k], (uses & 1) ^ 1)) { ok = false; break; }
             mbar_arrive_expect_tx(full, kSlot);
-            mbar_arrive_n(full, kConvWarps / 2 - 1);
+            mbar_arrive_n(full, kConvWarps - 1);
 #pragma unroll 1
             for (int a = 0; a < 4; ++a)
               tma_load_3d(smem + k * kSlot + a * kAtom, &tmap_q, k * 256 + a * 64, hb * 128, t, full);
@@ -899,9 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // staging is free)
       if (elect_one()) {
         const bool arrived = warp == kAux2Warp;
-        const uint32_t remote[2] = {mapa(smem_u32(arrived ? &bars.psent[0] : &bars.pfree[0]), 0),
-                                    mapa(smem_u32(arrived ? &bars.psent[1] : &bars.pfree[1]), 0)};
-        uint64_t* const local = arrived ? bars.pfull : bars.pcons;
+        const uint32_t remote = mapa(smem_u32(arrived ? &bars.psent[0][0] : &bars.pfree[0]), 0);
         uint32_t tc = 0;
         bool ok = true;
 #pragma unroll 1
@@ -911,10 +921,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             Desc d;
             if (!next_desc1(d)) { ok = false; break; }
             if (d.rows > 0) {
-              const uint32_t ps = tc & 1;
-              if (!wait_phase<true>(&local[ps], (tc >> 1) & 1, tries)) { ok = false; break; }
-              if (!arrived) mbar_arrive_expect_tx(&bars.pfull[ps], kPBytes);  // arm the slot's next use
-              mbar_arrive_remote(ps ? remote[1] : remote[0]);
+              const uint32_t ps = tc & 1, ph = (tc >> 1) & 1;
+              if (arrived) {
+#pragma unroll 1
+                for (int a = 0; a < 2; ++a) {
+                  if (!wait_phase<true>(&bars.pfull[ps][a], ph, tries)) { ok = false; break; }
+                  mbar_arrive_remote(remote + (ps * 2 + a) * 8);
+                }
+              } else {
+                if (!WAIT1(bars.pcons[ps], ph)) { ok = false; break; }
+                mbar_arrive_expect_tx(&bars.pfull[ps][0], kPBytes0);  // arm the slot's next use
+                mbar_arrive_expect_tx(&bars.pfull[ps][1], kPBytes1);
+                mbar_arrive_remote(remote + ps * 8);
+              }
               ++tc;
             }
             if (d.last) break;
