@@ -114,7 +114,7 @@ struct __align__(8) Bars {
   uint64_t ffree;                          // CTA 0: CTA 1 has read the finals
   uint64_t pfull[2][2], pcons[2];          // CTA 1: P slots (halves of 64 rows)
   uint64_t ready[2], odone[2], ffull;      // CTA 1: correction / MMA
-  uint64_t stfull, stfree;                 // CTA 1: output staging
+  uint64_t stfull[2], stfree[2], stored;     // CTA 1: output staging; an item's P slot is no more needed for it
   uint64_t mdrain;                         // the MMA thread's last commit
 };
 
@@ -201,31 +201,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sFinal = reinterpret_cast<float*>(smem + kOffFinal);  // [4][128]: maximum, sum of each softmax warpgroup
   float* sMax = reinterpret_cast<float*>(smem + kOffMax);      // [2][128]: running maxima after even / odd tiles
 
-  if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&bars.mchain[i], 1);
-    // descriptors are read by the conversion and softmax / correction warps and
-    // three more roles: MMA, q and rotary loads / the two that tell of P
-    for (int i = 0; i < kDescs; ++i) { mbar_init(&bars.dfull[i], 1); mbar_init(&bars.dempty[i], kConvWarps + kSoftWarps + 3); }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.full[i], kConvWarps); mbar_init(&bars.empty[i], 1); mbar_init(&bars.qgroup[i], kConvWarps);
-      mbar_init(&bars.kpfull[i], 32); mbar_init(&bars.kpempty[i], 1);
-      mbar_init(&bars.sfull[i], 1); mbar_init(&bars.sempty[i], 4);
-      mbar_init(&bars.psent[i][0], 1); mbar_init(&bars.psent[i][1], 1); mbar_init(&bars.pfree[i], 1);
-      mbar_init(&bars.pfull[i][0], 1); mbar_init(&bars.pfull[i][1], 1); mbar_init(&bars.pcons[i], 1);
-      mbar_init(&bars.ready[i], kSoftWarps); mbar_init(&bars.odone[i], 1);
+  if (warp == 1) {  // a barrier a lane
+    for (int i = lane; i < static_cast<int>(sizeof(Bars) / 8); i += 32) {
+      uint64_t* const b = reinterpret_cast<uint64_t*>(&bars) + i;
+      auto in = [&](const uint64_t* first, int n) { return b >= first && b < first + n; };
+      uint32_t count = 1;
+      if (in(bars.full, 2) || in(bars.qgroup, 2) || b == &bars.qready || b == &bars.cdone) count = kConvWarps;
+      // descriptors are read by the conversion and softmax / correction warps and
+      // three more roles: MMA, q and rotary loads / the two that tell of P
+      if (in(bars.dempty, kDescs)) count = kConvWarps + kSoftWarps + 3;
+      if (in(bars.kpfull, 2)) count = 32;
+      if (in(bars.sempty, 2)) count = 4;
+      if (in(bars.ready, 2) || b == &bars.ffree || in(bars.stfull, 2)) count = kSoftWarps;
+      mbar_init(b, count);
     }
-    mbar_init(&bars.qready, kConvWarps);
-    mbar_init(&bars.qfree, 1);
-    mbar_init(&bars.qpfull, 1);
-    mbar_init(&bars.cdone, kConvWarps);
-    mbar_init(&bars.ffree, kSoftWarps);
-    mbar_init(&bars.ffull, 1);
-    mbar_init(&bars.stfull, kSoftWarps);
-    mbar_init(&bars.stfree, 1);
-    mbar_init(&bars.mdrain, 1);
-    wait_tries = static_cast<uint32_t>(min(wait_limit_ns(P.err) / kTryNs + 1, static_cast<uint64_t>(0xffffffffu)));
     fence_mbar_init();
-    if (rank == 1) {
+    __syncwarp();
+    if (rank == 1 && lane == 0) {
       for (int i = 0; i < 2; ++i) {
         mbar_arrive_expect_tx(&bars.pfull[i][0], kPBytes0);
         mbar_arrive_expect_tx(&bars.pfull[i][1], kPBytes1);
@@ -233,6 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx(&bars.ffull, kFinalBytes);
     }
   }
+  if (warp == 2 && lane == 0)
+    wait_tries = static_cast<uint32_t>(min(wait_limit_ns(P.err) / kTryNs + 1, static_cast<uint64_t>(0xffffffffu)));
   if (warp == 0) tmem_alloc(&tmem_base, 512);
   tc_fence_before();
   __syncthreads();
@@ -429,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // exponentials (reading them twice keeps registers and code small)
             float m_tile = neg_inf();
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x * 32 < d.rows; ++x) {
               uint32_t s[32];
               tmem_ld32(s_tmem + x * 32, s);
               tmem_ld_wait();
@@ -457,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int a = 0; a < 2; ++a) {
               uint32_t pk[32];
+              if (a * kHalf < d.rows)  // (else the half is sent for its barrier only)
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 uint32_t s[32];
@@ -591,34 +586,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float inv_l = den == 0.f ? 0.f : num / den;
         const float lse2 = den == 0.f ? neg_inf() : mx + log2f(den);  // log2 units
-        const uint32_t row = smem_u32(smem + kOffStage) + hrow * 128, c = ((hf * 4) ^ (hrow & 7)) << 4;
+        // The staging is the V slots after the cluster's last item; else an atom of its
+        // own and the P slot of the item's last tile, which `stored` gives back.
+        const bool final_item = item + clusters >= P.items;
+        const uint32_t c = hrow * 128 + (((hf * 4) ^ (hrow & 7)) << 4);
+        const int z = P.n_chunks == 1 ? t : t * P.n_chunks + chunk;
+        if (first) {  // nothing selected: zeros
+          if (h < P.H) {
+            uint4* o = reinterpret_cast<uint4*>((P.n_chunks == 1 ? P.out : P.part_o) +
+                                                (static_cast<size_t>(z) * P.H + h) * kDv + hf * 256);
 #pragma unroll 1
-        for (int c0 = 0; c0 < kDv; c0 += 64, ++stores) {  // one atom per round
-          if (stores > 0 && !WAIT(bars.stfree, (stores - 1) & 1)) { ok = false; break; }
-          uint32_t v[32];
-          tmem_ld32(tmem + lane_off + c0 + hf * 32, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            __nv_bfloat162 w =
-                __floats2bfloat162_rn(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
-            v[k] = first ? 0u : *reinterpret_cast<uint32_t*>(&w);  // (no product: O holds an earlier item's)
+            for (int k = 0; k < 32; ++k) o[k] = make_uint4(0, 0, 0, 0);
           }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i, ++stores) {  // 64 columns a round
+            // every store of the last item, or the one before last of this, has read its atom
+            const uint32_t before = stores - (i == 0 ? 1 : 2);
+            if (stores > 0 && i != 1 && !WAIT(bars.stfree[before & 1], (before >> 1) & 1)) { ok = false; break; }
+            const int b = i % 3;
+            const uint32_t atom = final_item ? i * kAtom : b == 0 ? kOffStage : kOffP + ((tc - 1) & 1) * kPSlot + (b - 1) * kAtom;
+            const uint32_t row = smem_u32(smem) + atom + c;
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_off + i * 64 + hf * 32, v);
+            tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            sts128(row + (c ^ (k << 4)), make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.stfull);
-          if (warp == 0 && lane == 0) {  // the eight warps have written the atom
-            if (WAIT1(bars.stfull, stores & 1)) {
-              tma_store_3d(&tmap_o, smem + kOffStage, c0, hb * 128, P.n_chunks == 1 ? t : t * P.n_chunks + chunk);
-              bulk_commit_group();
-              bulk_wait_group_read0();
-              mbar_arrive(&bars.stfree);
+            for (int k = 0; k < 16; ++k) {
+              __nv_bfloat162 w =
+                  __floats2bfloat162_rn(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
+              v[k] = *reinterpret_cast<uint32_t*>(&w);
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              sts128(row ^ (k << 4), make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.stfull[stores & 1]);
+            if (warp == 0 && lane == 0) {  // the eight warps have written the atom
+              if (WAIT1(bars.stfull[stores & 1], (stores >> 1) & 1)) {
+                tma_store_3d(&tmap_o, smem + atom, i * 64, hb * 128, z);
+                bulk_commit_group();
+                if (i == 7) {
+                  bulk_wait_group_read0();
+                  mbar_arrive(&bars.stored);
+                } else {
+                  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                }
+                mbar_arrive(&bars.stfree[stores & 1]);
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
         tc_fence_before();
         if (hf == 0 && h < P.H) {
@@ -649,11 +667,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot_begin = chunk * P.chunk_rows;
         const int rows_here = bad_seq ? 0 : min(P.chunk_rows, P.topk - slot_begin);
         const int32_t* idx = P.idx + static_cast<size_t>(t) * P.topk + slot_begin;
+        // rows 4 lane .. 4 lane + 3 of a tile, loaded a tile ahead (the first together
+        // with the item's last slot)
+        int s[4];
+        auto load_idx = [&](int j0, int n) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int i = j0 + 4 * lane + x;
+            s[x] = i < n ? __ldg(idx + i) : -1;
+          }
+        };
+        load_idx(0, rows_here);
         // the item ends at its last valid slot, found from the end
         int n_rows = rows_here;
         if (rows_here > 0) {
-          const int s = __ldg(idx + rows_here - 1);
-          if (s < 0 || s >= P.max_L) {
+          const int last = __ldg(idx + rows_here - 1);
+          if (last < 0 || last >= P.max_L) {
             n_rows = 0;
 #pragma unroll 1
             for (int end = rows_here; end > 0 && n_rows == 0; end -= 256) {
@@ -670,16 +699,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // rows 4 lane .. 4 lane + 3 of a tile, loaded a tile ahead
-        int s[4];
-        auto load_idx = [&](int j0) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int i = j0 + 4 * lane + x;
-            s[x] = i < n_rows ? __ldg(idx + i) : -1;
-          }
-        };
-        load_idx(0);
 #pragma unroll 1
         for (int j0 = 0; ok; j0 += kTile) {
           // a slot that selects nothing is masked; a row that does not exist is
@@ -691,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int pg[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              if (s[x] >= P.max_L) s[x] = -1;
+              if (s[x] < 0 || s[x] >= P.max_L) s[x] = -1;
               pg[x] = s[x] >= 0 && P.block_table != nullptr
                           ? __ldg(P.block_table + static_cast<size_t>(b) * P.max_blocks + s[x] / P.block_size) : b;
             }
@@ -708,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          load_idx(j0 + kTile);
+          load_idx(j0 + kTile, n_rows);
           if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(P.err, kErrBadIndex);
           nib <<= (lane & 7) * 4;
 #pragma unroll
@@ -913,6 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool arrived = warp == kAux2Warp;
         const uint32_t remote = mapa(smem_u32(arrived ? &bars.psent[0][0] : &bars.pfree[0]), 0);
         uint32_t tc = 0;
+        uint32_t filled = 0;  // items that select something
         bool ok = true;
 #pragma unroll 1
         for (int item = cluster; item < P.items && ok; item += clusters) {
@@ -930,6 +950,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               } else {
                 if (!WAIT1(bars.pcons[ps], ph)) { ok = false; break; }
+                // (the item's output is staged in its last tile's slot)
+                if (d.last && !WAIT1(bars.stored, filled++ & 1)) { ok = false; break; }
                 mbar_arrive_expect_tx(&bars.pfull[ps][0], kPBytes0);  // arm the slot's next use
                 mbar_arrive_expect_tx(&bars.pfull[ps][1], kPBytes1);
                 mbar_arrive_remote(remote + ps * 8);
