@@ -178,8 +178,10 @@ def _p(t: Optional[torch.Tensor]):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # (the Stream object of current_stream() costs 2.7 us a call, its handle 0.2)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _ws(nbytes: int, device, ws: Optional[torch.Tensor]):
@@ -332,18 +334,25 @@ def dsa_mla_prolog(args: MlaArgs, workspace: Optional[torch.Tensor] = None, stre
 
 
 # ----------------------------------------------------- 4-bit latent cache
-def _tensor(name: str, t: torch.Tensor, dtype, shape, device=None, last_dense=False):
-    """Refuses a tensor whose device, type, shape or layout the library would
-    misread (None in a shape matches any size)."""
+def _device(name: str, t: torch.Tensor) -> int:
+    """The current device, which has to be the one of t."""
     if not t.is_cuda:
         raise DSAError(f"{name}: not a CUDA tensor")
-    if t.device.index != (torch.cuda.current_device() if device is None else device.index):
+    if t.get_device() != torch.cuda.current_device():
         raise DSAError(f"{name}: on {t.device}, which is not the current device")
-    if t.dtype != dtype:
+    return t.get_device()
+
+
+def _tensor(name: str, t: torch.Tensor, dtype, shape, device: int, last_dense=False):
+    """Refuses a tensor whose device, type, shape or layout the library would
+    misread (None in a shape matches any size)."""
+    if t.get_device() != device:  # (-1 for one that is not a CUDA tensor)
+        raise DSAError(f"{name}: on {t.device}, which is not the current device")
+    if t.dtype is not dtype:
         raise DSAError(f"{name}: {t.dtype}, expected {dtype}")
-    if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+    if t.shape != shape and (t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape))):
         raise DSAError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not (t.stride(-1) == 1 or t.shape[-1] <= 1 if last_dense else t.is_contiguous()):
+    if not t.is_contiguous() and not (last_dense and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
         raise DSAError(f"{name}: strides {t.stride()} are not supported")
 
 
@@ -355,22 +364,24 @@ def _row_stride(t: torch.Tensor) -> int:
 def dsa_kv4_write(x: torch.Tensor, kv4: torch.Tensor, slot: torch.Tensor, stream=None):
     """Quantises latent rows x bf16 [n, 576] (any row stride) into rows `slot`
     int64 [n] of the 4-bit cache kv4 uint8 [rows, 416] (see dsa.h)."""
+    device = _device("slot", slot)
+    _tensor("slot", slot, torch.int64, (None,), device)
     n = slot.shape[0]
-    _tensor("x", x, torch.bfloat16, (n, 576), last_dense=True)
-    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES))
-    _tensor("slot", slot, torch.int64, (n,))
-    args = Kv4WriteArgs(n, _row_stride(x), _p(x), _p(kv4), _p(slot), kv4.shape[0])
+    _tensor("x", x, torch.bfloat16, (n, 576), device, last_dense=True)
+    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES), device)
+    args = Kv4WriteArgs(n, _row_stride(x), x.data_ptr(), kv4.data_ptr(), slot.data_ptr(), kv4.shape[0])
     _check(load().dsa_kv4_write(ctypes.byref(args), _stream(stream)), "dsa_kv4_write")
 
 
 def dsa_kv4_read(kv4: torch.Tensor, slot: torch.Tensor, out: torch.Tensor, stream=None):
     """Rows `slot` int64 [n] of the 4-bit cache kv4 uint8 [rows, 416] -> out
     bf16 [n, 576] (any row stride; see dsa.h)."""
+    device = _device("slot", slot)
+    _tensor("slot", slot, torch.int64, (None,), device)
     n = slot.shape[0]
-    _tensor("out", out, torch.bfloat16, (n, 576), last_dense=True)
-    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES))
-    _tensor("slot", slot, torch.int64, (n,))
-    args = Kv4ReadArgs(n, _row_stride(out), _p(kv4), _p(slot), kv4.shape[0], _p(out))
+    _tensor("out", out, torch.bfloat16, (n, 576), device, last_dense=True)
+    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES), device)
+    args = Kv4ReadArgs(n, _row_stride(out), kv4.data_ptr(), slot.data_ptr(), kv4.shape[0], out.data_ptr())
     _check(load().dsa_kv4_read(ctypes.byref(args), _stream(stream)), "dsa_kv4_read")
 
 
@@ -379,20 +390,21 @@ def attn_kv4_args(T, B, n_q, H, topk, max_L, scale, q, kv4, topk_idx, out, lse=N
     """Arguments of dsa_sparse_attn_kv4: q bf16 [T, H, 576], kv4 uint8 [rows, 416], topk_idx int32 [T, topk], out
     bf16 [T, H, 512], lse fp32 [T, H]; block_table int32 [B, max_blocks] for a paged cache; sink fp32 [H];
     seq_of_token int32 [T] (then n_q is ignored)."""
-    _tensor("q", q, torch.bfloat16, (T, H, 576))
-    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES))
-    _tensor("topk_idx", topk_idx, torch.int32, (T, topk))
-    _tensor("out", out, torch.bfloat16, (T, H, 512))
+    device = _device("q", q)
+    _tensor("q", q, torch.bfloat16, (T, H, 576), device)
+    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES), device)
+    _tensor("topk_idx", topk_idx, torch.int32, (T, topk), device)
+    _tensor("out", out, torch.bfloat16, (T, H, 512), device)
     max_blocks = 0
     if block_table is not None:
-        _tensor("block_table", block_table, torch.int32, (B, None))
+        _tensor("block_table", block_table, torch.int32, (B, None), device)
         max_blocks = block_table.shape[1]
     if lse is not None:
-        _tensor("lse", lse, torch.float32, (T, H))
+        _tensor("lse", lse, torch.float32, (T, H), device)
     if sink is not None:
-        _tensor("sink", sink, torch.float32, (H,))
+        _tensor("sink", sink, torch.float32, (H,), device)
     if seq_of_token is not None:
-        _tensor("seq_of_token", seq_of_token, torch.int32, (T,))
+        _tensor("seq_of_token", seq_of_token, torch.int32, (T,), device)
     args = AttnKv4Args(T, B, n_q, H, topk, max_L, float(scale), _p(q), _p(kv4), kv4.shape[0], _p(block_table),
                        block_size, max_blocks, _p(topk_idx), _p(out), _p(lse), _p(sink), _p(seq_of_token))
     args.device = q.device

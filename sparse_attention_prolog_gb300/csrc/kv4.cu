@@ -9,7 +9,11 @@
 namespace dsa {
 namespace {
 
-constexpr int kWarps = 8;
+// Both kernels are bound by memory.  131071 rows written and read back: 72 us, 5.7 TB/s
+// of the 412 MB that cannot be spared (a plain copy: 6.8 TB/s); 262144 rows read: 68 us,
+// 6.1 TB/s.  Blocks of 4 warps start and end in smaller steps than larger ones
+// (8 warps: 74 and 69 us; 16: 78 and 72).
+constexpr int kWarps = 4;
 
 struct Kv4Params {
   int n;
@@ -31,44 +35,70 @@ __device__ __forceinline__ uint32_t scale_byte(float a) {
   return static_cast<uint32_t>(min(max(r, 0), 254));
 }
 
-// One warp per row, one group of 16 dims per lane.
+// rint(clamp(x / s, -7, 7)) in 4 bits, from r = 1 / s (see kv4_write_kernel).
+__device__ __forceinline__ uint32_t code(float x, float r) {
+  constexpr float kSnap = 0x1.8p11f, kInt = 0x1.8p23f;  // 1.5 * 2^11, 1.5 * 2^23
+  const float q = fminf(fmaxf(fmaf(x, r, kSnap), kSnap - 7.f), kSnap + 7.f);
+  return __float_as_uint(q + (kInt - kSnap)) & 15u;
+}
+
+// A warp per row: a lane takes the 8 dims of 16 bytes from each half of a row, so
+// every load and store of the warp is one run of bytes (a lane per group, whose
+// stores leave gaps, took 89 us for the rows above).  Two lanes share a group;
+// the even one finds the scale of the group in the first half, the odd one that of the
+// second, and they exchange them.
+//
+// x / s is rounded to a code without a division: r = 1/s is off by 2^-24 of its value,
+// x r thus by less than 2^-20.  An x / s that is not halfway between two codes is at least
+// 2^-10 away from it (x has 8 significant bits and s has 4; close to a halfway point x
+// is above s / 4, so x and s times it are multiples of 2^-6 of s's last place, of which s
+// has at most 15), so rounding x r to a multiple of 2^-12 moves halfway points back in
+// place and nothing else past them; the second rounding, to even, is the code.
 __global__ void __launch_bounds__(kWarps * 32) kv4_write_kernel(const Kv4Params P) {
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if (i >= P.n) return;
+  const uint4* xr = reinterpret_cast<const uint4*>(P.x + i * P.stride) + lane;
   const int64_t slot = __ldg(P.slot + i);
+  const uint4 v[2] = {__ldg(xr), __ldg(xr + 32)};
+  uint4 rope = make_uint4(0, 0, 0, 0);
+  if (lane < 8) rope = __ldg(xr + 64);
   if (slot < 0) return;
   if (slot >= P.rows) {
     if (lane == 0) atomicOr(P.err, kErrBadIndex);
     return;
   }
-  const uint4* xr = reinterpret_cast<const uint4*>(P.x + i * P.stride);
-  uint8_t* dst = P.kv4 + slot * kKv4Row;
-  const uint4 v0 = __ldg(xr + 2 * lane), v1 = __ldg(xr + 2 * lane + 1);
-  const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-  uint32_t amax = 0;  // |x| as bf16 bits order like integers
+  uint32_t amax[2];  // |x| as bf16 bits order like integers; both groups of the lane
 #pragma unroll
-  for (int k = 0; k < 8; ++k) amax = __vmaxu2(amax, w[k] & 0x7fff7fffu);
-  amax = max(amax & 0xffffu, amax >> 16);
-  uint32_t u = 255u, c[2] = {0u, 0u};
-  if (amax < 0x7f80u) {  // no NaN, no infinity
-    u = scale_byte(__uint_as_float(amax << 16));
-    const float s = __uint_as_float((u << 20) + (112u << 23));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // dims 2k and 2k+1: nibbles k % 4 and 4 + k % 4 of word k / 4
-      const int lo = __float2int_rn(fminf(fmaxf(bf16lo(w[k]) / s, -7.f), 7.f));
-      const int hi = __float2int_rn(fminf(fmaxf(bf16hi(w[k]) / s, -7.f), 7.f));
-      c[k / 4] |= (static_cast<uint32_t>(lo & 15) | (static_cast<uint32_t>(hi & 15) << 16)) << (4 * (k % 4));
-    }
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t m = 0x7fff7fffu;
+    amax[h] = __vmaxu2(__vmaxu2(v[h].x & m, v[h].y & m), __vmaxu2(v[h].z & m, v[h].w & m));
+    amax[h] = max(amax[h] & 0xffffu, amax[h] >> 16);
   }
-  reinterpret_cast<uint2*>(dst)[lane] = make_uint2(c[0], c[1]);
-  dst[kKv4Scales + lane] = static_cast<uint8_t>(u);
-  if (lane < 8) reinterpret_cast<uint4*>(dst + kKv4Rope)[lane] = __ldg(xr + 64 + lane);
+  const bool odd = lane & 1;
+  uint32_t a = odd ? amax[0] : amax[1];
+  a = max(__shfl_xor_sync(0xffffffffu, a, 1), odd ? amax[1] : amax[0]);
+  const bool ok = a < 0x7f80u;  // no NaN, no infinity
+  const uint32_t u = ok ? scale_byte(__uint_as_float(a << 16)) : 255u;
+  const float r = ok ? __frcp_rn(__uint_as_float((u << 20) + (112u << 23))) : 0.f;
+  const float other = __shfl_xor_sync(0xffffffffu, r, 1);
+  uint8_t* dst = P.kv4 + slot * kKv4Row;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float rh = odd == (h == 1) ? r : other;
+    const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+    uint32_t c = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)  // dims 2k and 2k+1: nibbles k and 4 + k
+      c |= (code(bf16lo(w[k]), rh) | (code(bf16hi(w[k]), rh) << 16)) << (4 * k);
+    reinterpret_cast<uint32_t*>(dst)[h * 32 + lane] = rh == 0.f ? 0u : c;
+  }
+  dst[kKv4Scales + (odd ? 16 : 0) + (lane >> 1)] = static_cast<uint8_t>(u);
+  if (lane < 8) reinterpret_cast<uint4*>(dst + kKv4Rope)[lane] = rope;
 }
 
-// One warp per row, one group of 16 dims per lane.
+// A warp per row, 8 dims of each half per lane, as above.
 __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const Kv4Params P) {
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -79,19 +109,20 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const Kv4Params P
     if (lane == 0) atomicOr(P.err, kErrBadIndex);
     slot = -1;
   }
-  uint4* dst = reinterpret_cast<uint4*>(P.out + i * P.stride);
-  uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0, rope = o0;
+  uint4* dst = reinterpret_cast<uint4*>(P.out + i * P.stride) + lane;
+  uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, rope = o[0];
   if (slot >= 0) {
     const uint8_t* src = P.kv4 + slot * kKv4Row;
-    const uint2 c = *reinterpret_cast<const uint2*>(src + lane * 8);
-    const Kv4Scale s = kv4_scale(src[kKv4Scales + lane]);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(src) + lane;
+    const uint8_t* u = src + kKv4Scales + (lane >> 1);
+    const uint32_t w0 = w[0], w1 = w[32], u0 = u[0], u1 = u[16];
     if (lane < 8) rope = *reinterpret_cast<const uint4*>(src + kKv4Rope + lane * 16);
-    o0 = kv4_codes8(c.x, s);
-    o1 = kv4_codes8(c.y, s);
+    o[0] = kv4_codes8(w0, kv4_scale(u0));
+    o[1] = kv4_codes8(w1, kv4_scale(u1));
   }
-  dst[2 * lane] = o0;
-  dst[2 * lane + 1] = o1;
-  if (lane < 8) dst[64 + lane] = rope;
+  dst[0] = o[0];
+  dst[32] = o[1];
+  if (lane < 8) dst[64] = rope;
 }
 
 int launch(void (*kernel)(const Kv4Params), const Kv4Params& P, cudaStream_t s) {

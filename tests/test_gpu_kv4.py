@@ -98,6 +98,30 @@ def test_read_of_every_byte_value(cuda_lib):
     np.testing.assert_array_equal(out.float().cpu().numpy(), O.kv4_values(rows[slot]).astype(np.float32))
 
 
+def test_every_scale_with_every_value(cuda_lib):
+    """Each of the 255 scales with every bf16 of either sign up to 7 of it (halfway
+    points among them), then each finite bf16 as the largest of a group."""
+    groups = []
+    for u in range(255):
+        s = float(O.kv4_scale(u))
+        top = int(W.f32_to_bf16_bits(np.array([7.0 * s], np.float32))[0])  # (at most 7 significant bits)
+        low = int(W.f32_to_bf16_bits(np.array([s / 8.0], np.float32))[0])
+        v = np.arange(low, top, dtype=np.int64)
+        v = np.concatenate([v, v | 0x8000])
+        v = np.concatenate([v, np.zeros(-len(v) % 15, np.int64)]).reshape(-1, 15)
+        groups.append(np.concatenate([np.full((len(v), 1), top), v], axis=1))
+    rng = np.random.default_rng(5)
+    top = np.arange(0x7f80)[:, None]
+    groups.append(np.concatenate([top, np.maximum(top - rng.integers(0, 600, (0x7f80, 15)), 0)], axis=1))
+    g = rng.permuted(np.concatenate(groups), axis=1)
+    g = np.concatenate([g, np.zeros((-len(g) % 32, 16), np.int64)]).reshape(-1, 512)
+    bits = np.concatenate([g, np.zeros((len(g), 64), np.int64)], axis=1).astype(np.uint16)
+    cache = Kv4Cache(len(bits), DEV)
+    cache.write(to_dev(bits, DEV), torch.arange(len(bits), device=DEV))
+    ok()
+    assert np.array_equal(cache.data.cpu().numpy(), O.kv4_quantise(bits))
+
+
 def test_slots_past_the_cache_are_reported(cuda_lib):
     bits = _rows(6, 3)
     cache = Kv4Cache(5, DEV)
