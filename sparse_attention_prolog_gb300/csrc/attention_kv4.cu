@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 2; ++x) {
           if (cur.rows > 0) {
             if (!WAIT(bars.empty[x], (uses & 1) ^ 1)) { ok = false; break; }
-            if (x * kHalf + cw * 4 < cur.rows) {  // (rows past the last one are not read by the MMA)
+            if (x * kHalf + cw * 4 < cur.rows) {  // (rows past the last 16 are not read by the MMA)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const uint32_t dst = (dst0 + x * kSlot + i * 256) ^ (i << 5);
@@ -737,7 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!WAIT(bars.dempty[dc % kDescs], ((dc / kDescs) & 1) ^ 1)) { ok = false; break; }
           *reinterpret_cast<int4*>(&td.row[4 * lane]) = make_int4(r[0], r[1], r[2], r[3]);
           if ((lane & 7) == 0) td.valid[lane >> 3] = nib;
-          if (lane == 0) td.info = max(0, min(kTile, n_rows - j0)) + (last ? kLast : 0);
+          // (up to a multiple of 16, which the second product reads whole: a zero weight
+          // does not make up for what a NaN left in the slot, so those rows are zeros)
+          if (lane == 0) td.info = max(0, min(kTile, (n_rows - j0 + 15) & ~15)) + (last ? kLast : 0);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.dfull[dc % kDescs]);
           ++dc;
@@ -761,13 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!next_desc1(d)) { ok = false; break; }
             if (d.rows > 0) {
               const uint32_t sb = tc & 1, ph = (tc >> 1) & 1;
-              const int rows16 = (d.rows + 15) & ~15;
               const uint32_t dt = tmem + kTmemS + sb * kTile;
               if (!WAIT1(bars.sempty[sb], ph ^ 1) || !WAIT1(bars.kpfull[sb], ph)) { ok = false; break; }
               fence_proxy_async_smem();  // cp.async data -> tensor core reads
               tc_fence_after();
               {
-                const uint32_t idesc = idesc_f16(128, rows16, kFmtBF16, 0, 0);
+                const uint32_t idesc = idesc_f16(128, d.rows, kFmtBF16, 0, 0);
                 const uint64_t ad = smem_desc(base + kOffQrope, 16, 1024, kSwizzle128B);
                 const uint64_t bd = smem_desc(base + kOffKrope + sb * kAtom, 16, 1024, kSwizzle128B);
 #pragma unroll
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int x = 0; x < 2; ++x) {
                 if (!WAIT1(bars.full[x], uses & 1)) { ok = false; break; }
                 fence_proxy_async_smem();  // generic writes -> tensor core reads
-                const int n16 = min(kHalf, rows16 - x * kHalf);
+                const int n16 = min(kHalf, d.rows - x * kHalf);
                 if (n16 > 0) {  // (a slot without rows changes hands all the same)
                   tc_fence_after();
                   const uint32_t idesc = idesc_f16(128, n16, kFmtBF16, 0, 0);
@@ -911,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!WAIT(bars.kpempty[rs], ((tc >> 1) & 1) ^ 1)) { ok = false; break; }
             const uint32_t kp = smem_u32(smem + kOffKrope) + rs * kAtom;
 #pragma unroll 4
-            for (int x = lane >> 3; x < ((d.rows + 15) & ~15); x += 4, rows += 4) {
+            for (int x = lane >> 3; x < d.rows; x += 4, rows += 4) {
               const int r = *rows;
               cp_async16(kp + sw128_off(x, lane & 7),
                          P.kv4 + static_cast<size_t>(r < 0 ? 0 : r) * kKv4Row + kKv4Rope + (lane & 7) * 16, r < 0 ? 0 : 16);

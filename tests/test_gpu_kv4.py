@@ -358,6 +358,25 @@ def test_nan_rows_count_only_where_selected(cuda_lib):
     assert torch.isnan(buf.out[1]).all() and torch.isnan(buf.lse[1]).all()
 
 
+@pytest.mark.parametrize("topk", [8, 17, 70, 130])
+def test_nothing_is_left_behind_by_other_rows(topk, cuda_lib):
+    """Rows of NaN and infinity fill the shared memory of every SM, in an earlier call
+    and in earlier tokens; tokens that select a few clean rows after them are unhurt."""
+    n_q = 160
+    inp = _batch(1, n_q, [900], topk, 128, 97)
+    inp.kv_cache[400:650] = 0x7fc0
+    inp.kv_cache[650:] = 0x7f80
+    rows = O.kv4_quantise(inp.kv_cache)
+    rng = np.random.default_rng(topk)
+    bad = rng.integers(400, 900, (n_q, topk))
+    _attend(inp, bad, rows=rows, tokens=[])
+    clean = rng.integers(0, 400, (n_q, topk))
+    _attend(inp, clean, rows=rows, tokens=range(0, n_q, 9))
+    for odd in (0, 1):
+        mixed = np.where((np.arange(n_q) // 76 % 2 == odd)[:, None], bad, clean)
+        _attend(inp, mixed, rows=rows, tokens=[t for t in range(n_q) if t // 76 % 2 != odd][::9])
+
+
 def test_rows_past_four_gigabytes(cuda_lib):
     """A cache of 4.6 GB: the byte offsets of its last rows need 33 bits."""
     n = 11_000_000
