@@ -44,7 +44,7 @@
  *     the call, which are read as soon as the kernel starts: the weights
  *     w_qb, w_k and w_proj of dsa_indexer_prolog, pos and seq_of_token of
  *     dsa_indexer_topk / dsa_indexer_scores, and q and seq_of_token of
- *     dsa_sparse_attn and dsa_sparse_attn_kv4.  The
+ *     dsa_sparse_attn.  The
  *     kernel enqueued just before such a call must not write them (an event
  *     or a memcpy in between lifts the rule).
  */
@@ -93,7 +93,8 @@ int dsa_get_device_error(void* stream);
  * call's workspace again before the next one.  Waits are timed on the
  * global timer, so a limit shorter than its tick (about 1 us) runs out at
  * the first tick; under a limit below 20 us a wait never blocks in the
- * hardware.  Synchronous: it takes effect for kernels launched after it
+ * hardware.  (dsa_sparse_attn_kv4 counts tries of some 40 ns each instead,
+ * and needs no zeroed workspace.)  Synchronous: it takes effect for kernels launched after it
  * returns; call it while none of this library's kernels runs.  No
  * counterpart on the pages: a test hook. */
 int dsa_set_wait_limit_ns(uint64_t ns);
@@ -537,9 +538,8 @@ int dsa_kv4_read(const dsa_kv4_read_args* args, void* stream);
  * The products of q with a row and of the probabilities with its values take
  * the row's values exactly; sums, softmax statistics and lse are fp32, the
  * probabilities are rounded to bf16 before they meet the values (their sum is
- * not), and the output is rounded once to bf16.  With several chunks of rows
- * per token each chunk's partial output is held in bf16 between the two
- * kernels.
+ * not), and the output is rounded once to bf16 (the partial outputs of a token
+ * whose rows are split into chunks are fp32).
  *
  * Shapes: q bf16 [T, H, 576]; kv4 uint8 contiguous [B, max_L, 416]
  * (cache_rows >= B * max_L) or paged [cache_rows, 416] through block_table
@@ -555,8 +555,6 @@ int dsa_kv4_read(const dsa_kv4_read_args* args, void* stream);
  * positive and finite; q, kv4 and out 16-byte aligned.
  * Workspace: dsa_sparse_attn_kv4_workspace() bytes (0 for some shapes),
  * 256-byte aligned, never in use by two calls that may overlap.
- * q and seq_of_token are read as soon as the kernel starts (see the note on
- * programmatic dependent launch above).
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t T, B, n_q, H, topk, max_L;

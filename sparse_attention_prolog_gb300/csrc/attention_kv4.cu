@@ -85,8 +85,8 @@ struct AttnKv4Params {
   float* lse;
   const float* sink;
   const int32_t* seq;
-  uint16_t* part_o;  // [T][n_chunks][H][512] bf16, each chunk's O / l, when n_chunks > 1
-  float2* part_ml;   // [T][n_chunks][H]: (maximum, sum) in log2 units
+  float4* part_o;   // [T][n_chunks][512 / 4][H]: each chunk's O, when n_chunks > 1
+  float2* part_ml;  // [T][n_chunks][H]: (maximum, sum) in log2 units
   uint32_t* err;
 };
 
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (last) break;
       }
-      if (rank == 0 && lane == 0) mbar_arrive(&bars.cdone);
+      if (ok && rank == 0 && lane == 0) mbar_arrive(&bars.cdone);
     }
   } else if (warp < kSoftWarps) {
     setmaxnreg_inc<kRegsSoft>();
@@ -590,11 +590,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         // own and the P slot of the item's last tile, which `stored` gives back.
         const bool final_item = item + clusters >= P.items;
         const uint32_t c = hrow * 128 + (((hf * 4) ^ (hrow & 7)) << 4);
-        const int z = P.n_chunks == 1 ? t : t * P.n_chunks + chunk;
-        if (first) {  // nothing selected: zeros
+        if (P.n_chunks > 1) {
+          // A chunk (its cluster's only item) leaves O as it is, in fp32: lanes are heads,
+          // so four columns of 32 heads are a run of 512 bytes, straight from registers.
+          if (!first) {  // (what selects nothing is not read)
+            float4* o = P.part_o + (static_cast<size_t>(t * P.n_chunks + chunk) * (kDv / 4) + hf * (kDv / 8)) * P.H + h;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i, o += 8 * P.H) {
+              uint32_t v[32];
+              tmem_ld32(tmem + lane_off + hf * 256 + i * 32, v);
+              tmem_ld_wait();
+              if (h < P.H)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  o[k * P.H] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                           __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+            }
+            if (warp == 0 && lane == 0) mbar_arrive(&bars.stored);
+          }
+        } else if (first) {  // nothing selected: zeros
           if (h < P.H) {
-            uint4* o = reinterpret_cast<uint4*>((P.n_chunks == 1 ? P.out : P.part_o) +
-                                                (static_cast<size_t>(z) * P.H + h) * kDv + hf * 256);
+            uint4* o = reinterpret_cast<uint4*>(P.out + (static_cast<size_t>(t) * P.H + h) * kDv + hf * 256);
 #pragma unroll 1
             for (int k = 0; k < 32; ++k) o[k] = make_uint4(0, 0, 0, 0);
           }
@@ -624,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bars.stfull[stores & 1]);
             if (warp == 0 && lane == 0) {  // the eight warps have written the atom
               if (WAIT1(bars.stfull[stores & 1], (stores >> 1) & 1)) {
-                tma_store_3d(&tmap_o, smem + atom, i * 64, hb * 128, z);
+                tma_store_3d(&tmap_o, smem + atom, i * 64, hb * 128, t);
                 bulk_commit_group();
                 if (i == 7) {
                   bulk_wait_group_read0();
@@ -798,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (d.last) break;
           }
-          mma_commit(&bars.qfree);
+          if (ok) mma_commit(&bars.qfree);
         }
         // every MMA issued has completed before the tensor memory is freed
         mma_commit(&bars.mdrain);
@@ -851,6 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kAuxWarp && rank == 0) {
       // ------------------------------------------------------- q loads (CTA 0)
       if (elect_one()) {
+        griddep_wait();  // the previous kernel may have written q
         uint32_t uses = 0;
         int q_slots = 0, rope_loads = 0;
         bool ok = true;
@@ -976,84 +993,97 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Merges a token's chunks: out = sum_c w_c O_c / (sum_c w_c [+ 2^(sink - M)])
-// with w_c = l_c 2^(m_c - M) (O_c already divided by l_c).  One warp per
-// (token, head, half of the 512 columns), 8 columns per lane; the loads of a
-// batch of chunks are issued together, so a batch costs one memory round trip.
-constexpr int kMergeBatch = 8;
+// Merges a token's chunks: out = sum_c w_c O_c / (sum_c w_c l_c [+ 2^(sink - M)]) with
+// w_c = 2^(m_c - M).  A block takes 32 heads (a lane each) and 16 kCols columns, so
+// reads are runs of 512 bytes; its warps share the chunks' maxima and sums through
+// shared memory, and the result goes through it to be written in longer runs.  A thread
+// has the loads of kBatch chunks of 4 kCols columns in flight, the first of them before
+// the maxima arrive.
+constexpr int kMergeWarps = 4;
 
-__global__ void __launch_bounds__(256) attn_kv4_merge_kernel(const AttnKv4Params P) {
+template <int kBatch, int kCols>
+__global__ void __launch_bounds__(kMergeWarps * 32) attn_kv4_merge_kernel(const AttnKv4Params P) {
+  extern __shared__ float2 s_ml[];  // [n_chunks][32]
+  __shared__ uint2 s_out[32][kMergeWarps * kCols + 1];
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item = blockIdx.x * 8 + warp;  // (token, head, column half)
-  if (item >= P.T * P.H * 2) return;
-  const int th = item >> 1, half = item & 1;
-  const int t = th / P.H, h = th % P.H;
-  const int col = half * 256 + lane * 8;
-  float acc[8];
+  const int h0 = blockIdx.y * 32, h = min(h0 + lane, P.H - 1), t = blockIdx.z;
+  const int c4 = (blockIdx.x * kMergeWarps + warp) * kCols;
+  const float4* src = P.part_o + (static_cast<size_t>(t) * P.n_chunks * (kDv / 4) + c4) * P.H + h;
+  float4 o[kBatch][kCols];
+  auto load = [&](int c0) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-  float M = neg_inf(), wsum = 0.f;
-  for (int c0 = 0; c0 < P.n_chunks; c0 += kMergeBatch) {
-    float2 ml[kMergeBatch];
-    uint4 raw[kMergeBatch];
+    for (int i = 0; i < kBatch; ++i)
+      if (c0 + i < P.n_chunks)
 #pragma unroll
-    for (int i = 0; i < kMergeBatch; ++i) {
-      ml[i] = make_float2(neg_inf(), 0.f);
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (c0 + i < P.n_chunks) {
-        const size_t row = (static_cast<size_t>(t) * P.n_chunks + c0 + i) * P.H + h;
-        ml[i] = __ldcg(P.part_ml + row);
-        raw[i] = __ldcg(reinterpret_cast<const uint4*>(P.part_o + row * kDv + col));
-      }
-    }
-    float Mb = M;
+        for (int k = 0; k < kCols; ++k) o[i][k] = __ldcg(src + (static_cast<size_t>(c0 + i) * (kDv / 4) + k) * P.H);
+  };
+  load(0);
+  const float2* ml = P.part_ml + static_cast<size_t>(t) * P.n_chunks * P.H + h;
+  for (int c = warp; c < P.n_chunks; c += kMergeWarps) s_ml[c * 32 + lane] = __ldcg(ml + static_cast<size_t>(c) * P.H);
+  __syncthreads();
+  float M = neg_inf();
+#pragma unroll 4
+  for (int c = 0; c < P.n_chunks; ++c) M = fmaxf(M, s_ml[c * 32 + lane].x);
+  const float Mz = M == neg_inf() ? 0.f : M;  // (nothing selected: every weight is 0)
+  float wsum = 0.f;
+  float4 acc[kCols];
 #pragma unroll
-    for (int i = 0; i < kMergeBatch; ++i) Mb = fmaxf(Mb, ml[i].x);
-    if (Mb == neg_inf()) {  // nothing visible yet (a sum that is not a number stays one)
+  for (int k = 0; k < kCols; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = 0; c0 < P.n_chunks; c0 += kBatch) {
+    if (c0 > 0) load(c0);
 #pragma unroll
-      for (int i = 0; i < kMergeBatch; ++i) wsum += ml[i].y;
-      continue;
-    }
-    const float r = exp2f(M - Mb);
-    wsum *= r;
+    for (int i = 0; i < kBatch; ++i) {
+      const float2 c = c0 + i < P.n_chunks ? s_ml[(c0 + i) * 32 + lane] : make_float2(neg_inf(), 0.f);
+      const float w = exp2f(c.x - Mz);
+      wsum = fmaf(w, c.y, wsum);  // (a sum that is not a number stays one)
+      if (w != 0.f) {  // (an empty chunk has no O)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] *= r;
-    M = Mb;
-#pragma unroll
-    for (int i = 0; i < kMergeBatch; ++i) {
-      const float wc = ml[i].y * exp2f(ml[i].x - M);  // 0 for an empty chunk
-      wsum += wc;
-      const uint32_t wds[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        acc[2 * k] = fmaf(wc, bf16lo(wds[k]), acc[2 * k]);
-        acc[2 * k + 1] = fmaf(wc, bf16hi(wds[k]), acc[2 * k + 1]);
+        for (int k = 0; k < kCols; ++k) {
+          acc[k].x = fmaf(w, o[i][k].x, acc[k].x);
+          acc[k].y = fmaf(w, o[i][k].y, acc[k].y);
+          acc[k].z = fmaf(w, o[i][k].z, acc[k].z);
+          acc[k].w = fmaf(w, o[i][k].w, acc[k].w);
+        }
       }
     }
   }
+  float scale = 1.f;
   if (P.sink != nullptr) {
     // one more term 2^s2 in the denominator (a zero-value key); -inf: none
     const float s2 = __ldg(P.sink + h) * 1.4426950408889634f;
     const float mx = fmaxf(M, s2);
     if (mx != neg_inf()) {
-      const float r = exp2f(M - mx);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] *= r;
-      wsum = wsum * r + exp2f(s2 - mx);
+      scale = exp2f(M - mx);
+      wsum = wsum * scale + exp2f(s2 - mx);
       M = mx;
     }
   }
-  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-  uint32_t pk[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    pk[k] = *reinterpret_cast<uint32_t*>(&b2);
-  }
-  *reinterpret_cast<uint4*>(P.out + (static_cast<size_t>(t) * P.H + h) * kDv + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-  if (half == 0 && lane == 0 && P.lse != nullptr)
+  scale = wsum == 0.f ? 0.f : scale / wsum;
+  if (blockIdx.x == 0 && warp == 0 && h0 + lane < P.H && P.lse != nullptr)
     P.lse[static_cast<size_t>(t) * P.H + h] = wsum == 0.f ? neg_inf() : (M + log2f(wsum)) * 0.69314718055994531f;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    const __nv_bfloat162 b0 = __floats2bfloat162_rn(acc[k].x * scale, acc[k].y * scale);
+    const __nv_bfloat162 b1 = __floats2bfloat162_rn(acc[k].z * scale, acc[k].w * scale);
+    s_out[lane][warp * kCols + k] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+  }
+  __syncthreads();
+  uint2* out = reinterpret_cast<uint2*>(P.out) + (static_cast<size_t>(t) * P.H + h0) * (kDv / 4) + blockIdx.x * kMergeWarps * kCols;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    const int i = k * kMergeWarps * 32 + threadIdx.x, head = i / (kMergeWarps * kCols), x = i % (kMergeWarps * kCols);
+    if (h0 + head < P.H) out[static_cast<size_t>(head) * (kDv / 4) + x] = s_out[head][x];
+  }
+}
+
+template <int kBatch, int kCols>
+cudaError_t launch_merge(const AttnKv4Params& P, cudaLaunchConfig_t& cfg) {
+  cfg.gridDim = dim3(kDv / 4 / (kMergeWarps * kCols), (P.H + 31) / 32, P.T);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = static_cast<size_t>(P.n_chunks) * 32 * sizeof(float2);
+  return cudaLaunchKernelEx(&cfg, attn_kv4_merge_kernel<kBatch, kCols>, P);
 }
 
 // Chunks per token: as many as the GPU holds clusters for at once, each a
@@ -1073,7 +1103,7 @@ size_t attn_kv4_workspace(const dsa_attn_kv4_args& a) {
   plan(a, hb, nc, cr);
   if (nc == 1) return 0;
   const size_t heads = static_cast<size_t>(a.T) * nc * a.H;
-  return round_up(heads * kDv * 2, 256) + round_up(heads * sizeof(float2), 256);
+  return round_up(heads * kDv * 4, 256) + round_up(heads * sizeof(float2), 256);
 }
 
 int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s) {
@@ -1087,24 +1117,23 @@ int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s) {
   P.idx = a.topk_idx; P.out = a.out; P.lse = a.lse; P.sink = a.sink; P.seq = a.seq_of_token;
   if (P.seq != nullptr) P.n_q = 1;  // ignored with a map
   if (P.n_chunks > 1) {
-    P.part_o = static_cast<uint16_t*>(ws);
+    P.part_o = static_cast<float4*>(ws);
     P.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) +
-                                          round_up(static_cast<size_t>(a.T) * P.n_chunks * a.H * kDv * 2, 256));
+                                          round_up(static_cast<size_t>(a.T) * P.n_chunks * a.H * kDv * 4, 256));
   }
   P.err = error_word();
   if (!P.err) return DSA_ERR_CUDA;
 
   // q [T, H, 576] in 64-dim x 128-head boxes (heads past H read as zeros); the
-  // output (or the chunks' partial outputs) [Z, H, 512] in 64-column x 128-head
-  // boxes (heads past H are clipped)
+  // output [T, H, 512] in 64-column x 128-head boxes (heads past H are clipped)
   alignas(64) CUtensorMap tmap_q, tmap_o;
   {
     const uint64_t H = static_cast<uint64_t>(a.H), T = static_cast<uint64_t>(a.T);
     const uint64_t dq[3] = {kDqk, H, T}, sq[2] = {kDqk * 2, H * kDqk * 2};
-    const uint64_t od[3] = {kDv, H, T * P.n_chunks}, os[2] = {kDv * 2, H * kDv * 2};
+    const uint64_t od[3] = {kDv, H, T}, os[2] = {kDv * 2, H * kDv * 2};
     const uint32_t box[3] = {64, 128, 1};
     if (!encode_tmap(&tmap_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dq, sq, box, 128) ||
-        !encode_tmap(&tmap_o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, P.n_chunks == 1 ? P.out : P.part_o, od, os, box, 128))
+        !encode_tmap(&tmap_o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, P.out, od, os, box, 128))
       return DSA_ERR_CUDA;
   }
   cudaError_t e = cudaFuncSetAttribute(attn_kv4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -1127,12 +1156,10 @@ int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s) {
   if (e != cudaSuccess) return DSA_ERR_CUDA;
   if (P.n_chunks > 1) {
     cudaLaunchConfig_t c2 = {};
-    c2.gridDim = dim3((a.T * a.H * 2 + 7) / 8);
-    c2.blockDim = dim3(256);
     c2.stream = s;
     c2.attrs = attr;
     c2.numAttrs = 1;
-    e = cudaLaunchKernelEx(&c2, attn_kv4_merge_kernel, P);
+    e = P.n_chunks <= 2 ? launch_merge<2, 4>(P, c2) : P.n_chunks <= 4 ? launch_merge<4, 2>(P, c2) : launch_merge<8, 1>(P, c2);
   }
   return cuda_status(e);
 }
