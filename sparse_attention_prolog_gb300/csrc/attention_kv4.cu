@@ -79,7 +79,8 @@ struct AttnKv4Params {
   const uint8_t* kv4;
   int64_t rows;
   const int32_t* block_table;
-  int block_size, max_blocks;
+  int block_size, max_blocks;  // (a contiguous cache: pages of max_L rows, a sequence each)
+  uint32_t page_mul, page_shift;  // i / block_size = i page_mul >> page_shift for 0 <= i < 2^31
   const int32_t* idx;
   uint16_t* out;
   float* lse;
@@ -467,6 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   pk[x * 16 + k] = *reinterpret_cast<uint32_t*>(&pb);
                 }
               }
+              if (a == 1) {  // S is read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.sempty[hf]);
+              }
               if (tc > 0 && !WAIT_CLUSTER(bars.psent[hf ^ 1][a], ((tc - 1) >> 1) & 1)) { ok = false; break; }
               if (a == 0) {
                 if (!WAIT_CLUSTER(bars.pfree[hf], ph ^ 1)) { ok = false; break; }
@@ -486,9 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
             }
             if (!ok) break;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.sempty[hf]);
             l_sum += (lo_f32(sum2[0]) + hi_f32(sum2[0])) + (lo_f32(sum2[1]) + hi_f32(sum2[1]));
           }
           if (d.rows > 0) {
@@ -683,9 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot_begin = chunk * P.chunk_rows;
         const int rows_here = bad_seq ? 0 : min(P.chunk_rows, P.topk - slot_begin);
         const int32_t* idx = P.idx + static_cast<size_t>(t) * P.topk + slot_begin;
+        const int32_t* table = P.block_table == nullptr ? nullptr : P.block_table + static_cast<size_t>(b) * P.max_blocks;
         // rows 4 lane .. 4 lane + 3 of a tile, loaded a tile ahead (the first together
         // with the item's last slot)
         int s[4];
+        auto page_of = [&](int i) { return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(i)) * P.page_mul) >> P.page_shift); };
         auto load_idx = [&](int j0, int n) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -723,21 +728,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t nib = 0;
           bool bad = false;
           {
-            int pg[4];
+            int pg[4], off[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              if (s[x] < 0 || s[x] >= P.max_L) s[x] = -1;
-              pg[x] = s[x] >= 0 && P.block_table != nullptr
-                          ? __ldg(P.block_table + static_cast<size_t>(b) * P.max_blocks + s[x] / P.block_size) : b;
+              if (s[x] >= P.max_L) s[x] = -1;
+              const int i = page_of(s[x]);
+              off[x] = s[x] - i * P.block_size;
+              pg[x] = s[x] >= 0 && table != nullptr ? __ldg(table + i) : b;
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               r[x] = -1;
               if (s[x] >= 0) {
                 nib |= 1u << x;
-                const int64_t row = P.block_table != nullptr
-                                        ? static_cast<int64_t>(pg[x]) * P.block_size + s[x] % P.block_size
-                                        : static_cast<int64_t>(b) * P.max_L + s[x];
+                const int64_t row = static_cast<int64_t>(pg[x]) * P.block_size + off[x];
                 if (pg[x] < 0 || row >= P.rows) bad = true;
                 else r[x] = static_cast<int>(row);
               }
@@ -914,6 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kAux2Warp && rank == 0) {
       // ------------------------------------------------ rotary K loads (CTA 0)
       // 16-byte asynchronous copies, 8 a row, four rows an instruction, swizzled
+      const uint8_t* const rope_src = P.kv4 + kKv4Rope + (lane & 7) * 16;
       uint32_t tc = 0;
       bool ok = true;
 #pragma unroll 1
@@ -928,11 +933,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t rs = tc & 1;
             if (!WAIT(bars.kpempty[rs], ((tc >> 1) & 1) ^ 1)) { ok = false; break; }
             const uint32_t kp = smem_u32(smem + kOffKrope) + rs * kAtom;
-#pragma unroll 4
-            for (int x = lane >> 3; x < d.rows; x += 4, rows += 4) {
-              const int r = *rows;
-              cp_async16(kp + sw128_off(x, lane & 7),
-                         P.kv4 + static_cast<size_t>(r < 0 ? 0 : r) * kKv4Row + kKv4Rope + (lane & 7) * 16, r < 0 ? 0 : 16);
+#pragma unroll 1
+            for (int x0 = 0; x0 < d.rows; x0 += 16, rows += 16) {
+#pragma unroll
+              for (int x = 0; x < 16; x += 4) {
+                const int r = rows[x];  // (a copy of 0 bytes writes zeros)
+                cp_async16(kp + x0 * 128 + sw128_off(x + (lane >> 3), lane & 7),
+                           rope_src + static_cast<size_t>(max(r, 0)) * kKv4Row, r < 0 ? 0 : 16);
+              }
             }
             cp_async_mbar_arrive(&bars.kpfull[rs]);
             ++tc;
@@ -1113,7 +1121,13 @@ int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s) {
   P.items = a.T * P.head_blocks * P.n_chunks;
   P.scale_log2 = a.scale * 1.4426950408889634f;
   P.kv4 = a.kv4; P.rows = a.cache_rows;
-  P.block_table = a.block_table; P.block_size = a.block_size; P.max_blocks = a.max_blocks;
+  P.block_table = a.block_table; P.block_size = a.block_table ? a.block_size : a.max_L; P.max_blocks = a.max_blocks;
+  // With 2^k >= block_size > 2^(k-1) and m = ceil(2^(31+k) / block_size), i m / 2^(31+k) exceeds
+  // i / block_size by less than i / 2^(31+k) <= 1 / block_size: the quotients are equal.
+  P.page_shift = 0;
+  while ((1u << P.page_shift) < static_cast<uint32_t>(P.block_size)) ++P.page_shift;
+  P.page_shift += 31;
+  P.page_mul = static_cast<uint32_t>(((uint64_t{1} << P.page_shift) + P.block_size - 1) / P.block_size);
   P.idx = a.topk_idx; P.out = a.out; P.lse = a.lse; P.sink = a.sink; P.seq = a.seq_of_token;
   if (P.seq != nullptr) P.n_q = 1;  // ignored with a map
   if (P.n_chunks > 1) {
