@@ -47,7 +47,7 @@ constexpr int kAtom = 16384;               // 128 rows (or heads) x 128 bytes
 constexpr int kHalf = 64;                  // rows of a slot
 constexpr int kSlot = 4 * kAtom;           // 64 rows x 512 dims bf16: 8 atoms of 64 rows x 128 bytes
 constexpr int kPSlot = 2 * kAtom;          // P [128 heads x 128 rows] bf16
-constexpr int kDescs = 4;
+constexpr int kDescs = 8;
 constexpr uint64_t kTryNs = 40;            // a try of a barrier takes about so long
 // 28 warps in seven warpgroups: 0-1 softmax (CTA 0), correction and epilogue
 // (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, and q loads and rotary K loads
@@ -288,11 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = WAIT(bars.dfull[0], 0);
     if (ok) {
       const int* rows = descs[0].row + my_row;
+      int r[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load(rows[(i >> 1) * kHalf + (i & 1) * 2], c[i], sc[i]);
+      for (int i = 0; i < 4; ++i) r[i] = rows[(i >> 1) * kHalf + (i & 1) * 2];
       read_desc(cur);
       __syncwarp();
       if (lane == 0) free_desc();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load(r[i], c[i], sc[i]);
     }
 #pragma unroll 1
     for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
@@ -359,11 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (cur.rows > 0) ++uses;
         const bool last = cur.last;
         if (more) {
+          int r[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) load(rows[(i >> 1) * kHalf + (i & 1) * 2], c[i], sc[i]);
+          for (int i = 0; i < 4; ++i) r[i] = rows[(i >> 1) * kHalf + (i & 1) * 2];
           read_desc(cur);
           __syncwarp();
-          if (lane == 0) free_desc();
+          if (lane == 0) free_desc();  // (before the loads: an arrival waits for those under way)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load(r[i], c[i], sc[i]);
         }
         if (last) break;
       }
