@@ -115,7 +115,8 @@ struct __align__(8) Bars {
   uint64_t ffree;                          // CTA 0: CTA 1 has read the finals
   uint64_t pfull[2][2], pcons[2];          // CTA 1: P slots (halves of 64 rows)
   uint64_t ready[2], odone[2], ffull;      // CTA 1: correction / MMA
-  uint64_t stfull[2], stfree[2], stored;     // CTA 1: output staging; an item's P slot is no more needed for it
+  uint64_t stfull[2], stfree[2], stored;   // CTA 1: output staging; an item's P slot is no more needed for it
+  uint64_t lfull[8];                       // CTA 1: output staging of the cluster's last item
   uint64_t mdrain;                         // the MMA thread's last commit
 };
 
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (in(bars.dempty, kDescs)) count = kConvWarps + kSoftWarps + 3;
       if (in(bars.kpfull, 2)) count = 32;
       if (in(bars.sempty, 2)) count = 4;
-      if (in(bars.ready, 2) || b == &bars.ffree || in(bars.stfull, 2)) count = kSoftWarps;
+      if (in(bars.ready, 2) || b == &bars.ffree || in(bars.stfull, 2) || in(bars.lfull, 8)) count = kSoftWarps;
       mbar_init(b, count);
     }
     fence_mbar_init();
@@ -627,8 +628,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < 8; ++i, ++stores) {  // 64 columns a round
             // every store of the last item, or the one before last of this, has read its atom
+            // (the cluster's last item has one for every round)
             const uint32_t before = stores - (i == 0 ? 1 : 2);
-            if (stores > 0 && i != 1 && !WAIT(bars.stfree[before & 1], (before >> 1) & 1)) { ok = false; break; }
+            if (!final_item && stores > 0 && i != 1 && !WAIT(bars.stfree[before & 1], (before >> 1) & 1)) {
+              ok = false;
+              break;
+            }
             const int b = i % 3;
             const uint32_t atom = final_item ? i * kAtom : b == 0 ? kOffStage : kOffP + ((tc - 1) & 1) * kPSlot + (b - 1) * kAtom;
             const uint32_t row = smem_u32(smem) + atom + c;
@@ -646,15 +651,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               sts128(row ^ (k << 4), make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.stfull[stores & 1]);
+            uint64_t* const full = final_item ? &bars.lfull[i] : &bars.stfull[stores & 1];
+            if (lane == 0) mbar_arrive(full);
             if (warp == 0 && lane == 0) {  // the eight warps have written the atom
-              if (WAIT1(bars.stfull[stores & 1], (stores >> 1) & 1)) {
+              if (wait_phase<false>(full, final_item ? 0 : (stores >> 1) & 1, tries)) {
                 tma_store_3d(&tmap_o, smem + atom, i * 64, hb * 128, t);
                 bulk_commit_group();
                 if (i == 7) {
                   bulk_wait_group_read0();
                   mbar_arrive(&bars.stored);
-                } else {
+                } else if (!final_item) {
                   asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                 }
                 mbar_arrive(&bars.stfree[stores & 1]);
