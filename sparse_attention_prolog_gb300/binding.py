@@ -418,8 +418,14 @@ def dsa_sparse_attn_kv4(args: AttnKv4Args, workspace: Optional[torch.Tensor] = N
     if torch.cuda.current_device() != args.device.index:
         raise DSAError(f"dsa_sparse_attn_kv4: tensors on {args.device}, which is not the current device")
     if workspace is None:
-        workspace, n = _ws(lib.dsa_sparse_attn_kv4_workspace(ctypes.byref(args)), args.device, None)
+        n = lib.dsa_sparse_attn_kv4_workspace(ctypes.byref(args))
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=args.device)
+            if stream is not None:
+                workspace.record_stream(stream)
     else:
         n = workspace.numel() * workspace.element_size()
+        if workspace.get_device() != args.device.index or not workspace.is_contiguous():
+            raise DSAError("dsa_sparse_attn_kv4: the workspace is not contiguous on the tensors' device")
     _check(lib.dsa_sparse_attn_kv4(ctypes.byref(args), _p(workspace), n, _stream(stream)), "dsa_sparse_attn_kv4")
     return workspace

@@ -422,7 +422,37 @@ def test_attention_wrapper_refusals(cuda_lib):
     if B.workspace_bytes("attn_kv4", a):
         with pytest.raises(B.DSAError, match="workspace"):
             B.dsa_sparse_attn_kv4(a, torch.zeros(0, dtype=torch.uint8, device=DEV))
+    a = args(T=1, n_q=1, topk=700, max_L=16, q=torch.zeros(1, 4, 576, dtype=torch.bfloat16, device=DEV),
+             topk_idx=torch.zeros(1, 700, dtype=torch.int32, device=DEV),
+             out=torch.zeros(1, 4, 512, dtype=torch.bfloat16, device=DEV))
+    n = B.workspace_bytes("attn_kv4", a)
+    assert n > 0
+    for bad in (torch.zeros(n, dtype=torch.uint8), torch.zeros(2 * n, dtype=torch.uint8, device=DEV)[::2],
+                torch.zeros(1, dtype=torch.uint8, device=DEV).expand(n)):
+        with pytest.raises(B.DSAError, match="workspace"):
+            B.dsa_sparse_attn_kv4(a, bad)
     ok()
+
+
+def test_a_workspace_of_the_call_s_own_on_a_side_stream(cuda_lib):
+    """Without a workspace each call makes one, which outlives its kernels."""
+    inp = _batch(1, 2, [500], 300, 128, 101)
+    rows = O.kv4_quantise(inp.kv_cache)
+    cache = Kv4Cache(rows.shape[0], DEV)
+    cache.data.copy_(to_dev(rows, DEV))
+    buf = DecodeBuffers(inp, DEV, kv4=cache)
+    idx = _pick(np.random.default_rng(6), inp)
+    buf.topk_idx.copy_(torch.from_numpy(idx.astype(np.int32)))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        B.dsa_sparse_attn_kv4(buf.aargs, stream=s)
+        torch.full((1 << 20,), float("nan"), device=DEV)  # takes freed memory on the current stream
+    ok()
+    out, lse = buf.out.float().cpu().numpy(), buf.lse.cpu().numpy()
+    for t in range(inp.T):
+        vals = O.kv4_values(rows[O.cache_rows(inp, 0, idx[t])])
+        _check_tokens(inp.q_attn[t], vals, inp.scale, out[t], lse[t])
 
 
 # ------------------------------------------------------- streams, graphs, chain
