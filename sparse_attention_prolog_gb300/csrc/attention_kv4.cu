@@ -22,7 +22,7 @@
 // Both convert the rows from 4 bits to bf16, three instructions per pair of dims,
 // exact, into one of two 64 KB slots (64 rows x 512 dims, 128B-swizzled), which CTA 0
 // reads K-major and CTA 1 MN-major; sixteen warps fill one while the MMA takes the
-// other.  A warp loads its rows into registers a tile ahead, two rows of 16
+// other.  A warp loads a slot's rows into registers a tile ahead, two rows of 16
 // lanes an instruction: 584 clocks of the load path for 128 rows.  Measured against
 // it: 16-byte asynchronous copies 812; four lanes a row (which slots of 128 rows x 128
 // dims for N = 128 MMAs ask for) 1854; TMA gathers of four rows 3200, bulk copies of
@@ -31,14 +31,16 @@
 // which was not their bound.  q goes through the same slots of CTA 0, by TMA and then
 // into tensor memory.
 //
-// Measured: 4096 tokens of 128 heads over 2048 of 8192 rows each 2.45 ms, 950 TFLOP/s;
-// 32 sequences of 4096 to 131072 rows 45 us; 8 tokens 25.5 us, one 20.1 us.  The long
+// Measured: 4096 tokens of 128 heads over 2048 of 8192 rows each 2.37 ms, 984 TFLOP/s;
+// 32 sequences of 4096 to 131072 rows 42.5 us; 8 tokens 24.8 us, one 19.7.  The long
 // case is bound by the chain that a buffer of S goes through (products, maximum,
-// exponentials, P on its way) and by instruction fetch: no unit is busy for more than half
-// of the time, and forms with more code in the loops are slower even where they wait
-// less (S in halves of 64 rows 2.91 ms where this took 2.73; slots refilled one by one
-// 2.86 for 2.45).  The short cases are bound by their chain of first steps, each through
-// cold code: indices, rows, q, the products, and 256 KB of O that one SM writes.
+// exponentials, P on its way) and by instruction fetch: no unit is busy for more than two
+// thirds of the time, and forms with more code in the loops are slower even where they wait
+// less (S in halves of 64 rows 2.44 ms where this took 2.35).  Loading all of a tile's
+// rows after its second slot, in less code, took it 2.35 ms, and the 32 sequences, whose
+// rows come from HBM, 46.2 us.  The short cases are bound by their chain of first steps,
+// each through cold code: indices, rows, q, the products, and 256 KB of O that one SM
+// writes.
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -174,25 +176,33 @@ __device__ __forceinline__ void drain_copy(uint64_t* bar, uint32_t parity) {
 // instruction cache.  (With the other kernels' waits inlined an earlier form was 133
 // KB and a third of the cache's requests missed: 5.97 ms for the 4096-token case;
 // taking 3 KB of code that this case never reaches out of an 78 KB form won 5%.)
-// A try blocks for some 70 clocks by itself; `tries` is how many fill the limit in
-// force.  The thread that runs out sets it to 0, and every later wait gives up at once.
+// A try blocks for some 70 clocks by itself; `limit` of them fill the limit in force.
+// Who runs out sets *tries to 0 for the CTA's end and leaves its role; the roles that
+// wait for it run out in their turn.  The lanes of a waiting warp vote on every try, so
+// they go on or give up together (one that left alone would leave the others at the
+// next warp barrier) and the loop's branches are uniform: with the vote after the loop
+// and the limit in shared memory there were 5 KB more of code, and the 4096-token case
+// took 2.45 ms instead of 2.35; with one lane polling for its warp 4.95.
 // A wait is by parity: it tells a phase from the one before and the one after only, so
 // no role may be two uses of a barrier ahead of or behind the one it waits for.
-template <bool kCluster>
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile uint32_t* tries) {
+template <bool kCluster, bool kWarp>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t limit, volatile uint32_t* tries) {
 #pragma unroll 1
-  for (uint32_t n = 0; !(kCluster ? mbar_probe_cluster(bar, parity) : mbar_probe(bar, parity)); ++n)
-    if (n >= *tries) {
-      *tries = 0;  // reported when the CTA ends
+  for (uint32_t n = 0;; ++n) {
+    bool done = kCluster ? mbar_probe_cluster(bar, parity) : mbar_probe(bar, parity);
+    if (kWarp) done = __all_sync(0xffffffffu, done);
+    if (done) return true;
+    if (n >= limit) {
+      *tries = 0;
       return false;
     }
-  return true;
+  }
 }
-// Waits of one thread, and of a whole warp, whose lanes go on or give up together
-// (a lane that left alone would leave the others at the next warp barrier).
-#define WAIT1(bar, parity) wait_phase<false>(&(bar), (parity), tries)
-#define WAIT(bar, parity) (__all_sync(0xffffffffu, wait_phase<false>(&(bar), (parity), tries)) != 0)
-#define WAIT_CLUSTER(bar, parity) (__all_sync(0xffffffffu, wait_phase<true>(&(bar), (parity), tries)) != 0)
+// Waits of one thread, and of a whole warp.
+#define WAIT1(bar, parity) wait_phase<false, false>(&(bar), (parity), limit, tries)
+#define WAIT1_CLUSTER(bar, parity) wait_phase<true, false>(&(bar), (parity), limit, tries)
+#define WAIT(bar, parity) wait_phase<false, true>(&(bar), (parity), limit, tries)
+#define WAIT_CLUSTER(bar, parity) wait_phase<true, true>(&(bar), (parity), limit, tries)
 
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kv4_kernel(const __grid_constant__ AttnKv4Params P, const __grid_constant__ CUtensorMap tmap_q,
@@ -244,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   volatile uint32_t* tries = &wait_tries;
+  const uint32_t limit = wait_tries;
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
   cluster_sync();  // both CTAs' barriers are initialised before any remote use
   griddep_launch_dependents();
@@ -275,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = warp - kFirstConv;
     const int pc = ((lane >> 3) << 2) | (lane & 3), rp = (lane >> 2) & 1;
     const bool swap = (pc & 2) != 0;
+    const uint32_t scale_lo = swap ? 0x4441u : 0x4440u;
     const int r7 = (cw & 1) * 4 + rp;  // row of i = 0 mod 8
     const uint32_t slots = smem_u32(smem);
     const uint32_t dst0 = slots + (pc >> 1) * (kSlot / 8) + (cw * 4 + rp) * 128 +
@@ -342,7 +354,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool more = !cur.last || item + clusters < P.items;  // another tile, maybe of the next item
         const int* rows = descs[dc % kDescs].row + my_row;
         if (more && !WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
-#pragma unroll 1
+        int r[4];
+        Desc nxt{0, false};
+        if (more) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = rows[(i >> 1) * kHalf + (i & 1) * 2];
+          read_desc(nxt);
+          __syncwarp();
+          if (lane == 0) free_desc();  // (before any load: an arrival waits for those under way)
+        }
+#pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (cur.rows > 0) {
             if (!WAIT(bars.empty[x], (uses & 1) ^ 1)) { ok = false; break; }
@@ -350,12 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const uint32_t dst = (dst0 + x * kSlot + i * 256) ^ (i << 5);
-                Kv4Scale lo = kv4_scale(sc[i] & 255u), hi = kv4_scale(sc[i] >> 8);
-                uint4 w = c[i];
-                if (swap) {
-                  const Kv4Scale t = lo; lo = hi; hi = t;
-                  w = make_uint4(w.z, w.w, w.x, w.y);
-                }
+                const Kv4Scale lo = kv4_scale(__byte_perm(sc[2 * x + i], 0, scale_lo)),
+                               hi = kv4_scale(__byte_perm(sc[2 * x + i], 0, scale_lo ^ 1u));
+                uint4 w = c[2 * x + i];
+                if (swap) w = make_uint4(w.z, w.w, w.x, w.y);
                 sts128(dst, kv4_codes8(w.x, lo));
                 sts128(dst ^ 16u, kv4_codes8(w.y, lo));
                 sts128(dst ^ 32u, kv4_codes8(w.z, hi));
@@ -365,22 +384,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.full[x]);  // (the MMA's thread fences the proxies)
           }
-          c[0] = c[2]; c[1] = c[3];
-          sc[0] = sc[2]; sc[1] = sc[3];
+          if (more) {  // the next tile's, as soon as this slot's registers are free
+            load(r[2 * x], c[2 * x], sc[2 * x]);
+            load(r[2 * x + 1], c[2 * x + 1], sc[2 * x + 1]);
+          }
         }
         if (!ok) break;
         if (cur.rows > 0) ++uses;
         const bool last = cur.last;
-        if (more) {
-          int r[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) r[i] = rows[(i >> 1) * kHalf + (i & 1) * 2];
-          read_desc(cur);
-          __syncwarp();
-          if (lane == 0) free_desc();  // (before the loads: an arrival waits for those under way)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) load(r[i], c[i], sc[i]);
-        }
+        cur = nxt;
         if (last) break;
       }
       if (ok && rank == 0 && lane == 0) mbar_arrive(&bars.cdone);
@@ -666,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t* const full = final_item ? &bars.lfull[i] : &bars.stfull[stores & 1];
             if (lane == 0) mbar_arrive(full);
             if (warp == 0 && lane == 0) {  // the eight warps have written the atom
-              if (wait_phase<false>(full, final_item ? 0 : (stores >> 1) & 1, tries)) {
+              if (WAIT1(*full, final_item ? 0 : (stores >> 1) & 1)) {
                 tma_store_3d(&tmap_o, smem + atom, i * 64, hb * 128, t);
                 bulk_commit_group();
                 if (i == 7) {
@@ -867,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!WAIT1(bars.ready[ps], (tc >> 1) & 1)) { ok = false; break; }
 #pragma unroll 1
               for (int x = 0; x < 2; ++x) {
-                if (x == 1 && !wait_phase<true>(&bars.pfull[ps][1], (tc >> 1) & 1, tries)) { ok = false; break; }
+                if (x == 1 && !WAIT1_CLUSTER(bars.pfull[ps][1], (tc >> 1) & 1)) { ok = false; break; }
                 if (!WAIT1(bars.full[x], tc & 1)) { ok = false; break; }
                 fence_proxy_async_smem();  // generic writes -> tensor core reads
                 tc_fence_after();
@@ -995,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (arrived) {
 #pragma unroll 1
                 for (int a = 0; a < 2; ++a) {
-                  if (!wait_phase<true>(&bars.pfull[ps][a], ph, tries)) { ok = false; break; }
+                  if (!WAIT1_CLUSTER(bars.pfull[ps][a], ph)) { ok = false; break; }
                   mbar_arrive_remote(remote + (ps * 2 + a) * 8);
                 }
               } else {
