@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t* const b = reinterpret_cast<uint64_t*>(&bars) + i;
       auto in = [&](const uint64_t* first, int n) { return b >= first && b < first + n; };
       uint32_t count = 1;
-      if (in(bars.full, 2) || in(bars.qgroup, 2) || b == &bars.qready || b == &bars.cdone) count = kConvWarps;
+      if (in(bars.full, 2)) count = kConvWarps / 2;
+      if (in(bars.qgroup, 2) || b == &bars.qready || b == &bars.cdone) count = kConvWarps;
       // descriptors are read by the conversion and softmax / correction warps and
       // three more roles: MMA, q and rotary loads / the two that tell of P
       if (in(bars.dempty, kDescs)) count = kConvWarps + kSoftWarps + 3;
@@ -278,23 +279,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kFirstConv && warp < kFirstConv + kConvWarps) {
     setmaxnreg_dec<kRegsConv>();
     // ------------------------------------------------- conversion (both CTAs)
-    // The sixteen warps fill slot 0, then slot 1, four rows of 64 each: once for q (by
-    // TMA; they put it into tensor memory) and once for every tile.  A lane converts
-    // 32 dims (16 bytes of codes, piece pc) of rows 2 i + rp of its warp's four.  Lanes
-    // are numbered, and odd pairs of pieces stored in another order, so that a quarter
-    // warp's stores meet every bank once.
-    const int cw = warp - kFirstConv;
+    // Eight warps fill a slot, eight rows each, once for q (by TMA; all sixteen put it
+    // into tensor memory) and once for every tile; what a warp does between two fills
+    // goes on while the MMA reads its slot.  A lane converts 32 dims (16 bytes of codes,
+    // piece pc) of rows 2 i + rp of its warp's eight.  Lanes are numbered, and odd pairs
+    // of pieces stored in another order, so that a quarter warp's stores meet every bank
+    // once.
+    const int cw = warp - kFirstConv, g = cw >> 3;  // g: its slot
     const int pc = ((lane >> 3) << 2) | (lane & 3), rp = (lane >> 2) & 1;
     const bool swap = (pc & 2) != 0;
     const uint32_t scale_lo = swap ? 0x4441u : 0x4440u;
-    const int r7 = (cw & 1) * 4 + rp;  // row of i = 0 mod 8
     const uint32_t slots = smem_u32(smem);
-    const uint32_t dst0 = slots + (pc >> 1) * (kSlot / 8) + (cw * 4 + rp) * 128 +
-                          ((((pc & 1) * 4) ^ (swap ? 2 : 0) ^ r7) << 4);
+    const uint32_t dst0 = slots + g * kSlot + (pc >> 1) * (kSlot / 8) + ((cw & 7) * 8 + rp) * 128 +
+                          ((((pc & 1) * 4) ^ (swap ? 2 : 0) ^ rp) << 4);
     const uint8_t* const src = P.kv4 + pc * 16;
     const int scale_off = kKv4Scales - pc * 14;
-    const int my_row = cw * 4 + rp;
-    uint4 c[4];  // piece 2 x + i: rows 64 x + 2 i + my_row
+    const int my_row = cw * 8 + rp;
+    uint4 c[4];  // piece i: row 2 i + my_row
     uint32_t sc[4];
     auto load = [&](int r, uint4& c, uint32_t& s) {
       c = make_uint4(0, 0, 0, 0);
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int* rows = descs[0].row + my_row;
       int r[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = rows[(i >> 1) * kHalf + (i & 1) * 2];
+      for (int i = 0; i < 4; ++i) r[i] = rows[2 * i];
       read_desc(cur);
       __syncwarp();
       if (lane == 0) free_desc();
@@ -351,48 +352,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll 1
       while (ok) {
-        const bool more = !cur.last || item + clusters < P.items;  // another tile, maybe of the next item
-        const int* rows = descs[dc % kDescs].row + my_row;
-        if (more && !WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
-        int r[4];
-        Desc nxt{0, false};
-        if (more) {
+        if (cur.rows > 0) {
+          if (!WAIT(bars.empty[g], (uses & 1) ^ 1)) { ok = false; break; }
+          if (cw * 8 < cur.rows) {  // (rows past the last 16 are not read by the MMA)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) r[i] = rows[(i >> 1) * kHalf + (i & 1) * 2];
-          read_desc(nxt);
-          __syncwarp();
-          if (lane == 0) free_desc();  // (before any load: an arrival waits for those under way)
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (cur.rows > 0) {
-            if (!WAIT(bars.empty[x], (uses & 1) ^ 1)) { ok = false; break; }
-            if (x * kHalf + cw * 4 < cur.rows) {  // (rows past the last 16 are not read by the MMA)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t dst = (dst0 + x * kSlot + i * 256) ^ (i << 5);
-                const Kv4Scale lo = kv4_scale(__byte_perm(sc[2 * x + i], 0, scale_lo)),
-                               hi = kv4_scale(__byte_perm(sc[2 * x + i], 0, scale_lo ^ 1u));
-                uint4 w = c[2 * x + i];
-                if (swap) w = make_uint4(w.z, w.w, w.x, w.y);
-                sts128(dst, kv4_codes8(w.x, lo));
-                sts128(dst ^ 16u, kv4_codes8(w.y, lo));
-                sts128(dst ^ 32u, kv4_codes8(w.z, hi));
-                sts128(dst ^ 48u, kv4_codes8(w.w, hi));
-              }
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t dst = (dst0 + i * 256) ^ (i << 5);
+              const Kv4Scale lo = kv4_scale(__byte_perm(sc[i], 0, scale_lo)),
+                             hi = kv4_scale(__byte_perm(sc[i], 0, scale_lo ^ 1u));
+              uint4 w = c[i];
+              if (swap) w = make_uint4(w.z, w.w, w.x, w.y);
+              sts128(dst, kv4_codes8(w.x, lo));
+              sts128(dst ^ 16u, kv4_codes8(w.y, lo));
+              sts128(dst ^ 32u, kv4_codes8(w.z, hi));
+              sts128(dst ^ 48u, kv4_codes8(w.w, hi));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.full[x]);  // (the MMA's thread fences the proxies)
           }
-          if (more) {  // the next tile's, as soon as this slot's registers are free
-            load(r[2 * x], c[2 * x], sc[2 * x]);
-            load(r[2 * x + 1], c[2 * x + 1], sc[2 * x + 1]);
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.full[g]);  // (the MMA's thread fences the proxies)
+          ++uses;
         }
-        if (!ok) break;
-        if (cur.rows > 0) ++uses;
         const bool last = cur.last;
-        cur = nxt;
+        if (!last || item + clusters < P.items) {  // the next tile's rows, maybe of the next item
+          const int* rows = descs[dc % kDescs].row + my_row;
+          if (!WAIT(bars.dfull[dc % kDescs], (dc / kDescs) & 1)) { ok = false; break; }
+          int r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = rows[2 * i];
+          read_desc(cur);
+          __syncwarp();
+          if (lane == 0) free_desc();  // (before the loads: an arrival waits for those under way)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load(r[i], c[i], sc[i]);
+        }
         if (last) break;
       }
       if (ok && rank == 0 && lane == 0) mbar_arrive(&bars.cdone);
@@ -923,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t* const full = &bars.full[k];
             if (!WAIT1(bars.empty[k], (uses & 1) ^ 1)) { ok = false; break; }
             mbar_arrive_expect_tx(full, kSlot);
-            mbar_arrive_n(full, kConvWarps - 1);
+            mbar_arrive_n(full, kConvWarps / 2 - 1);
 #pragma unroll 1
             for (int a = 0; a < 4; ++a)
               tma_load_3d(smem + k * kSlot + a * kAtom, &tmap_q, k * 256 + a * 64, hb * 128, t, full);
