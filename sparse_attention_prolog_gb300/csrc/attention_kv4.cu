@@ -21,26 +21,24 @@
 //
 // Both convert the rows from 4 bits to bf16, three instructions per pair of dims,
 // exact, into one of two 64 KB slots (64 rows x 512 dims, 128B-swizzled), which CTA 0
-// reads K-major and CTA 1 MN-major; sixteen warps fill one while the MMA takes the
-// other.  A warp loads a slot's rows into registers a tile ahead, two rows of 16
-// lanes an instruction: 584 clocks of the load path for 128 rows.  Measured against
-// it: 16-byte asynchronous copies 812; four lanes a row (which slots of 128 rows x 128
-// dims for N = 128 MMAs ask for) 1854; TMA gathers of four rows 3200, bulk copies of
-// a row 7400.  The 4096-token case took 2.82 to 3.28 ms in those forms; N = 64 costs
-// the tensor core 45 clocks a K = 16 step where N = 128 takes 64 for twice the rows,
-// which was not their bound.  q goes through the same slots of CTA 0, by TMA and then
-// into tensor memory.
+// reads K-major and CTA 1 MN-major; eight warps fill each while the MMA takes the
+// other.  A warp loads its rows into registers a tile ahead, two rows of 16 lanes an
+// instruction: 584 clocks of the load path for 128 rows.  Measured against it: 16-byte
+// asynchronous copies 812; four lanes a row (which slots of 128 rows x 128 dims for
+// N = 128 MMAs ask for) 1854; TMA gathers of four rows 3200, bulk copies of a row 7400.
+// N = 64 costs the tensor core 45 clocks a K = 16 step where N = 128 takes 64 for twice
+// the rows, which is not what bounds it.  q goes through the same slots of CTA 0, by TMA
+// and then into tensor memory.
 //
-// Measured: 4096 tokens of 128 heads over 2048 of 8192 rows each 2.37 ms, 984 TFLOP/s;
-// 32 sequences of 4096 to 131072 rows 42.5 us; 8 tokens 24.8 us, one 19.7.  The long
-// case is bound by the chain that a buffer of S goes through (products, maximum,
-// exponentials, P on its way) and by instruction fetch: no unit is busy for more than two
-// thirds of the time, and forms with more code in the loops are slower even where they wait
-// less (S in halves of 64 rows 2.44 ms where this took 2.35).  Loading all of a tile's
-// rows after its second slot, in less code, took it 2.35 ms, and the 32 sequences, whose
-// rows come from HBM, 46.2 us.  The short cases are bound by their chain of first steps,
-// each through cold code: indices, rows, q, the products, and 256 KB of O that one SM
-// writes.
+// Measured: 4096 tokens of 128 heads over 2048 of 8192 rows each 2.34 ms, 997 TFLOP/s;
+// 32 sequences of 4096 to 131072 rows 42.8 us; 8 tokens 24.7 us, one 19.4.  With the
+// products, the exponentials, the conversion and the row loads taken out the long case
+// still takes 1.9 ms: it is bound by the hand-overs between the roles (a buffer of S from
+// products to exponentials to P on its way) and by instruction fetch.  No unit is busy for
+// more than two thirds of the time, and forms with more code in the loops are slower even
+// where they wait less (S in halves of 64 rows 2.48 ms; slots filled by all sixteen warps
+// in turn 2.38).  The short cases are bound by their chain of first steps, each through
+// cold code: indices, rows, q, the products, and 256 KB of O that one SM writes.
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -58,7 +56,7 @@ constexpr int kAtom = 16384;               // 128 rows (or heads) x 128 bytes
 constexpr int kHalf = 64;                  // rows of a slot
 constexpr int kSlot = 4 * kAtom;           // 64 rows x 512 dims bf16: 8 atoms of 64 rows x 128 bytes
 constexpr int kPSlot = 2 * kAtom;          // P [128 heads x 128 rows] bf16
-constexpr int kDescs = 8;
+constexpr int kDescs = 8;                  // tile descriptors: how far the lookups run ahead of the slowest role
 constexpr uint64_t kTryNs = 40;            // a try of a barrier takes about so long
 // 28 warps in seven warpgroups: 0-1 softmax (CTA 0), correction and epilogue
 // (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, and q loads and rotary K loads
@@ -148,6 +146,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int x, int y, int z) {  // into the L2
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+               ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z) : "memory");
 }
 // Bulk copy to the peer CTA's shared memory, completing on the peer's barrier.
 __device__ __forceinline__ void bulk_s2peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
@@ -927,6 +929,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(smem + kOffQrope, &tmap_q, 512, hb * 128, t, &bars.qpfull);
           rope_loads = n + 1;
           ++uses;
+          if (item + clusters < P.items) {  // the next item's q, for when its turn comes
+            const int next = (item + clusters) / P.n_chunks;
+#pragma unroll 1
+            for (int k = 0; k < kDqk; k += 64)
+              tma_prefetch_3d(&tmap_q, k, next % P.head_blocks * 128, next / P.head_blocks);
+          }
 #pragma unroll 1
           while (ok) {
             Desc d;
