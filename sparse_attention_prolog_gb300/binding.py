@@ -336,11 +336,12 @@ def dsa_mla_prolog(args: MlaArgs, workspace: Optional[torch.Tensor] = None, stre
 # ----------------------------------------------------- 4-bit latent cache
 def _device(name: str, t: torch.Tensor) -> int:
     """The current device, which has to be the one of t."""
-    if not t.is_cuda:
+    device = t.get_device()
+    if device < 0:
         raise DSAError(f"{name}: not a CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
+    if device != torch.cuda.current_device():
         raise DSAError(f"{name}: on {t.device}, which is not the current device")
-    return t.get_device()
+    return device
 
 
 def _tensor(name: str, t: torch.Tensor, dtype, shape, device: int, last_dense=False):
@@ -356,33 +357,43 @@ def _tensor(name: str, t: torch.Tensor, dtype, shape, device: int, last_dense=Fa
         raise DSAError(f"{name}: strides {t.stride()} are not supported")
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Distance of a [n, 576] tensor's rows (a single row has none of its own)."""
-    return t.stride(0) if t.shape[0] > 1 else max(576, t.stride(0) // 8 * 8)
+def _kv4_rows(name: str, t: torch.Tensor, kv4: torch.Tensor, slot: torch.Tensor):
+    """Checks rows t bf16 [n, 576], the cache and the slots: (device, n, row
+    stride of t, rows of the cache).  (One condition for the calls that pass, as a
+    check of each tensor costs as much as a launch.)"""
+    device = _device("slot", slot)
+    shape, cache = t.shape, kv4.shape
+    if not (t.dtype is torch.bfloat16 and kv4.dtype is torch.uint8 and slot.dtype is torch.int64
+            and len(shape) == 2 and shape[1] == 576 and slot.shape == shape[:1]
+            and len(cache) == 2 and cache[1] == KV4_ROW_BYTES
+            and t.get_device() == device and kv4.get_device() == device
+            and t.stride(1) == 1 and kv4.is_contiguous() and slot.is_contiguous()):
+        _tensor("slot", slot, torch.int64, (None,), device)
+        _tensor(name, t, torch.bfloat16, (slot.shape[0], 576), device, last_dense=True)
+        _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES), device)
+    n = shape[0]
+    # (a single row has no stride of its own)
+    return device, n, t.stride(0) if n > 1 else max(576, t.stride(0) // 8 * 8), cache[0]
+
+
+def _stream_of(device: int, stream):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def dsa_kv4_write(x: torch.Tensor, kv4: torch.Tensor, slot: torch.Tensor, stream=None):
     """Quantises latent rows x bf16 [n, 576] (any row stride) into rows `slot`
     int64 [n] of the 4-bit cache kv4 uint8 [rows, 416] (see dsa.h)."""
-    device = _device("slot", slot)
-    _tensor("slot", slot, torch.int64, (None,), device)
-    n = slot.shape[0]
-    _tensor("x", x, torch.bfloat16, (n, 576), device, last_dense=True)
-    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES), device)
-    args = Kv4WriteArgs(n, _row_stride(x), x.data_ptr(), kv4.data_ptr(), slot.data_ptr(), kv4.shape[0])
-    _check(load().dsa_kv4_write(ctypes.byref(args), _stream(stream)), "dsa_kv4_write")
+    device, n, stride, rows = _kv4_rows("x", x, kv4, slot)
+    args = Kv4WriteArgs(n, stride, x.data_ptr(), kv4.data_ptr(), slot.data_ptr(), rows)
+    _check(load().dsa_kv4_write(ctypes.byref(args), _stream_of(device, stream)), "dsa_kv4_write")
 
 
 def dsa_kv4_read(kv4: torch.Tensor, slot: torch.Tensor, out: torch.Tensor, stream=None):
     """Rows `slot` int64 [n] of the 4-bit cache kv4 uint8 [rows, 416] -> out
     bf16 [n, 576] (any row stride; see dsa.h)."""
-    device = _device("slot", slot)
-    _tensor("slot", slot, torch.int64, (None,), device)
-    n = slot.shape[0]
-    _tensor("out", out, torch.bfloat16, (n, 576), device, last_dense=True)
-    _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES), device)
-    args = Kv4ReadArgs(n, _row_stride(out), kv4.data_ptr(), slot.data_ptr(), kv4.shape[0], out.data_ptr())
-    _check(load().dsa_kv4_read(ctypes.byref(args), _stream(stream)), "dsa_kv4_read")
+    device, n, stride, rows = _kv4_rows("out", out, kv4, slot)
+    args = Kv4ReadArgs(n, stride, kv4.data_ptr(), slot.data_ptr(), rows, out.data_ptr())
+    _check(load().dsa_kv4_read(ctypes.byref(args), _stream_of(device, stream)), "dsa_kv4_read")
 
 
 def attn_kv4_args(T, B, n_q, H, topk, max_L, scale, q, kv4, topk_idx, out, lse=None, block_table=None, block_size=0,
@@ -427,5 +438,6 @@ def dsa_sparse_attn_kv4(args: AttnKv4Args, workspace: Optional[torch.Tensor] = N
         n = workspace.numel() * workspace.element_size()
         if workspace.get_device() != args.device.index or not workspace.is_contiguous():
             raise DSAError("dsa_sparse_attn_kv4: the workspace is not contiguous on the tensors' device")
-    _check(lib.dsa_sparse_attn_kv4(ctypes.byref(args), _p(workspace), n, _stream(stream)), "dsa_sparse_attn_kv4")
+    _check(lib.dsa_sparse_attn_kv4(ctypes.byref(args), _p(workspace), n, _stream_of(args.device.index, stream)),
+           "dsa_sparse_attn_kv4")
     return workspace
