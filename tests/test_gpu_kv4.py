@@ -570,6 +570,28 @@ def test_each_call_reads_what_the_one_before_wrote(cuda_lib):
             _check_tokens(q[t], vals, inp.scale, out[t], lse[t])
 
 
+@pytest.mark.parametrize("T,H,topk,rows", [(65535, 1, 3, 5000), (1, 1024, 100, 3000), (2, 130, 3, 1),
+                                           (1, 4, 65536, 70001)])
+def test_largest_and_smallest_sizes(T, H, topk, rows, cuda_lib):
+    """The bounds of the header, one at a time, with lengths of a single row."""
+    rng = np.random.default_rng(T + H)
+    bits = W.f32_to_bf16_bits(rng.standard_normal((rows, 576)).astype(np.float32))
+    held = O.kv4_quantise(bits)
+    q = W.f32_to_bf16_bits(rng.standard_normal((T, H, 576)).astype(np.float32))
+    idx = rng.integers(0, rows, (T, topk)).astype(np.int32)
+    idx[T // 2, 1:] = -1
+    scale = 576 ** -0.5
+    dq, dkv, didx = to_dev(q, DEV).view(torch.bfloat16), to_dev(held, DEV), to_dev(idx, DEV)
+    out = torch.full((T, H, 512), float("nan"), dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, H), float("nan"), dtype=torch.float32, device=DEV)
+    B.dsa_sparse_attn_kv4(B.attn_kv4_args(T, 1, T, H, topk, rows, scale, dq, dkv, didx, out, lse))
+    ok()
+    assert bool(torch.isfinite(lse).all()) and bool(torch.isfinite(out).all())
+    for t in sorted({0, T // 2, T - 1, *rng.integers(0, T, 8).tolist()}):
+        sel = idx[t][idx[t] >= 0]
+        _check_tokens(q[t], O.kv4_values(held[sel]), scale, out[t].float().cpu().numpy(), lse[t].cpu().numpy())
+
+
 @pytest.mark.parametrize("n_q,topk", [(2, 700), (160, 300)])
 def test_wait_limit_runs_out_then_the_next_call_passes(n_q, topk, cuda_lib):
     """With a 1 ns limit after an L2 flush waits give up, in one item and in the
