@@ -30,8 +30,8 @@
 // the rows, which is not what bounds it.  q goes through the same slots of CTA 0, by TMA
 // and then into tensor memory.
 //
-// Measured: 4096 tokens of 128 heads over 2048 of 8192 rows each 2.34 ms, 997 TFLOP/s;
-// 32 sequences of 4096 to 131072 rows 42.8 us; 8 tokens 24.7 us, one 19.4.  With the
+// Measured: 4096 tokens of 128 heads over 2048 of 8192 rows each 2.31 ms, 1012 TFLOP/s;
+// 32 sequences of 4096 to 131072 rows 43.0 us; 8 tokens 24.6 us, one 19.3.  With the
 // products, the exponentials, the conversion and the row loads taken out the long case
 // still takes 1.9 ms: it is bound by the hand-overs between the roles (a buffer of S from
 // products to exponentials to P on its way) and by instruction fetch.  No unit is busy for
@@ -156,6 +156,12 @@ __device__ __forceinline__ void bulk_s2peer(uint32_t dst, uint32_t src, uint32_t
   asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                ::"r"(dst), "r"(src), "r"(bytes), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -229,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t* const b = reinterpret_cast<uint64_t*>(&bars) + i;
       auto in = [&](const uint64_t* first, int n) { return b >= first && b < first + n; };
       uint32_t count = 1;
-      if (in(bars.full, 2)) count = kConvWarps / 2;
-      if (in(bars.qgroup, 2) || b == &bars.qready || b == &bars.cdone) count = kConvWarps;
+      if (in(bars.full, 2) || in(bars.qgroup, 2)) count = kConvWarps / 2;
+      if (b == &bars.qready || b == &bars.cdone) count = kConvWarps;
       // descriptors are read by the conversion and softmax / correction warps and
       // three more roles: MMA, q and rotary loads / the two that tell of P
       if (in(bars.dempty, kDescs)) count = kConvWarps + kSoftWarps + 3;
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kFirstConv && warp < kFirstConv + kConvWarps) {
     setmaxnreg_dec<kRegsConv>();
     // ------------------------------------------------- conversion (both CTAs)
-    // Eight warps fill a slot, eight rows each, once for q (by TMA; all sixteen put it
+    // Eight warps fill a slot, eight rows each, once for q (by TMA; they put it
     // into tensor memory) and once for every tile; what a warp does between two fills
     // goes on while the MMA reads its slot.  A lane converts 32 dims (16 bytes of codes,
     // piece pc) of rows 2 i + rp of its warp's eight.  Lanes are numbered, and odd pairs
@@ -325,27 +331,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
       if (rank == 0) {
-        // q: 256 dims of the 128 heads a slot (4 atoms), lane = head, an atom a warp
+        // q: 256 dims of the 128 heads a slot (4 atoms), lane = head, two atoms a warp, in
+        // 16 registers (in 32, next to a tile's rows, they spill: 2.43 ms for 2.31)
         if (n > 0) ok = WAIT(bars.qfree, (n - 1) & 1);
+        if (!ok || !WAIT(bars.full[g], uses & 1)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll 1
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (!WAIT(bars.full[x], uses & 1)) { ok = false; break; }
-          uint32_t r[32];
+        for (int b = cw & 4, e = b + 4; b < e; ++b) {  // half an atom
+          uint32_t r[16];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint4 v = lds128(slots + x * kSlot + (cw >> 2) * kAtom + sw128_off((cw & 3) * 32 + lane, k));
+          for (int k = 0; k < 4; ++k) {
+            const uint4 v = lds128(slots + g * kSlot + (b >> 1) * kAtom + sw128_off((cw & 3) * 32 + lane, (b & 1) * 4 + k));
             r[4 * k] = v.x; r[4 * k + 1] = v.y; r[4 * k + 2] = v.z; r[4 * k + 3] = v.w;
           }
-          tmem_st32(tmem + lane_off + (x * 4 + (cw >> 2)) * 32, r);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.qgroup[x]);
-          if (cw == 0) {  // all have read the slot
-            if (!WAIT(bars.qgroup[x], n & 1)) { ok = false; break; }
-            if (lane == 0) mbar_arrive(&bars.empty[x]);
-          }
+          tmem_st16(tmem + lane_off + (g * 8 + b) * 16, r);
         }
-        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.qgroup[g]);
+        if ((cw & 7) == 0) {  // all have read the slot
+          if (!WAIT(bars.qgroup[g], n & 1)) { ok = false; break; }
+          if (lane == 0) mbar_arrive(&bars.empty[g]);
+        }
         ++uses;
         tmem_st_wait();
         tc_fence_before();
