@@ -424,16 +424,16 @@ def attn_kv4_args(T, B, n_q, H, topk, max_L, scale, q, kv4, topk_idx, out, lse=N
 
 def dsa_sparse_attn_kv4(args: AttnKv4Args, workspace: Optional[torch.Tensor] = None, stream=None):
     """Runs the sparse attention over a 4-bit cache.  Returns the workspace
-    (one is made when none is given and the shape needs one)."""
+    (one of the stream's own is made when none is given and the shape needs
+    one)."""
     lib = load()
     if torch.cuda.current_device() != args.device.index:
         raise DSAError(f"dsa_sparse_attn_kv4: tensors on {args.device}, which is not the current device")
     if workspace is None:
         n = lib.dsa_sparse_attn_kv4_workspace(ctypes.byref(args))
         if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=args.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            with torch.cuda.stream(stream):  # of the pool whose blocks are free in this stream's order
+                workspace = torch.empty(n, dtype=torch.uint8, device=args.device)
     else:
         n = workspace.numel() * workspace.element_size()
         if workspace.get_device() != args.device.index or not workspace.is_contiguous():
