@@ -117,9 +117,12 @@ class Kv4Cache:
         B.dsa_kv4_write(x, self.data, slot, stream)
 
     def read(self, slot: torch.Tensor, out: torch.Tensor = None, stream=None) -> torch.Tensor:
-        """The rows slot int64 [n] as bf16 [n, 576] (-1: zeros)."""
+        """The rows slot int64 [n] as bf16 [n, 576] (-1: zeros).  A new ``out`` is
+        memory of ``stream``: another stream that uses it waits for this one, and
+        records itself on it (``record_stream``) if it may be dropped before."""
         if out is None:
-            out = torch.empty(slot.shape[0], 576, dtype=torch.bfloat16, device=self.data.device)
+            with torch.cuda.stream(stream):
+                out = torch.empty(slot.shape[0], 576, dtype=torch.bfloat16, device=self.data.device)
         B.dsa_kv4_read(self.data, slot, out, stream)
         return out
 

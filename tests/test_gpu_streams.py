@@ -40,3 +40,24 @@ def test_the_4_bit_attention_s_own_workspace(cuda_lib):
     out, lse = buf.out.float().cpu().numpy(), buf.lse.cpu().numpy()
     for t in range(inp.T):
         _check_tokens(inp.q_attn[t], O.kv4_values(rows[O.cache_rows(inp, 0, idx[t])]), inp.scale, out[t], lse[t])
+
+
+def test_a_read_into_memory_of_its_own(cuda_lib):
+    """The result is dropped at once, while the read may still be writing it."""
+    rng = np.random.default_rng(3)
+    n = 4000
+    bits = rng.standard_normal((n, 576)).astype(np.float32)
+    cache = Kv4Cache(n, DEV)
+    cache.write(torch.from_numpy(bits).to(DEV).bfloat16(), torch.arange(n, device=DEV))
+    slot = torch.arange(n, device=DEV).flip(0)
+    want = cache.read(slot)
+    s = torch.cuda.Stream()
+    address, seen = _freed_block_in_use(n * 576 * 2)
+    got = cache.read(slot, stream=s)
+    assert got.data_ptr() != address
+    with torch.cuda.stream(s):
+        kept = got.clone()
+    del got
+    other = torch.full((n * 576,), 3.0, dtype=torch.bfloat16, device=DEV)  # the current stream gets no block of the read
+    ok()
+    assert torch.equal(kept, want) and bool((seen == 1).all()) and bool((other == 3.0).all())

@@ -17,7 +17,7 @@ SIDE = types.SimpleNamespace(cuda_stream=7)
 class Memory:
     """Stand-in for a device tensor."""
 
-    shape = (4, 576)
+    shape, device = (4, 576), "cuda:0"
 
     def __init__(self, n):
         self.n = n
@@ -68,4 +68,15 @@ def test_workspace_of_the_4_bit_attention(stream, made, monkeypatch):
     args = B.AttnKv4Args()
     args.device = torch.device("cuda", 0)
     B.dsa_sparse_attn_kv4(args, stream=stream)
+    assert made == [stream]
+
+
+@pytest.mark.parametrize("stream", [None, SIDE])
+def test_result_of_a_read(stream, made, monkeypatch):
+    monkeypatch.setattr(B, "dsa_kv4_read", lambda *a: None)
+    cache = pipeline.Kv4Cache(8, "cuda:0")
+    made.clear()
+    cache.read(Memory(4), stream=stream)
+    assert made == [stream]
+    cache.read(Memory(4), out=Memory(4), stream=stream)
     assert made == [stream]
