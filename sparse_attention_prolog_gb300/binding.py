@@ -184,13 +184,17 @@ def _stream(stream=None):
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
-def _ws(nbytes: int, device, ws: Optional[torch.Tensor]):
+def _ws(nbytes: int, device, ws: Optional[torch.Tensor], stream):
+    """A workspace for a call on `stream` and its size.  (A new one comes from the
+    pool of that stream, which also clears it: a block that another stream freed
+    may still be in use there, and its fill might come after the call.)"""
     if nbytes == 0:
         return None, 0
     if ws is not None:
         assert ws.numel() * ws.element_size() >= nbytes
         return ws, ws.numel() * ws.element_size()
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device), nbytes
+    with torch.cuda.stream(stream):
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device), nbytes
 
 
 # ---------------------------------------------------------------- prolog
@@ -209,7 +213,7 @@ def dsa_indexer_prolog(args: PrologArgs, workspace: Optional[torch.Tensor] = Non
                        device=None):
     lib = load()
     need = lib.dsa_indexer_prolog_workspace(ctypes.byref(args))
-    ws, n = _ws(need, device or "cuda", workspace)
+    ws, n = _ws(need, device or "cuda", workspace, stream)
     _check(lib.dsa_indexer_prolog(ctypes.byref(args), _p(ws), n, _stream(stream)), "dsa_indexer_prolog")
     return ws
 
@@ -234,7 +238,7 @@ def topk_args(T, B, n_q, H_I, d_I, topk, max_L, q, q_scale, w, k_cache, k_scale,
 def dsa_indexer_topk(args: TopkArgs, workspace: Optional[torch.Tensor] = None, stream=None, device=None):
     lib = load()
     need = lib.dsa_indexer_topk_workspace(ctypes.byref(args))
-    ws, n = _ws(need, device or "cuda", workspace)
+    ws, n = _ws(need, device or "cuda", workspace, stream)
     _check(lib.dsa_indexer_topk(ctypes.byref(args), _p(ws), n, _stream(stream)), "dsa_indexer_topk")
     return ws
 
@@ -263,7 +267,7 @@ def attn_args(T, B, n_q, H, topk, max_L, scale, q, kv, topk_idx, out, lse=None, 
 def dsa_sparse_attn(args: AttnArgs, workspace: Optional[torch.Tensor] = None, stream=None, device=None):
     lib = load()
     need = lib.dsa_sparse_attn_workspace(ctypes.byref(args))
-    ws, n = _ws(need, device or "cuda", workspace)
+    ws, n = _ws(need, device or "cuda", workspace, stream)
     _check(lib.dsa_sparse_attn(ctypes.byref(args), _p(ws), n, _stream(stream)), "dsa_sparse_attn")
     return ws
 
@@ -328,7 +332,7 @@ def dsa_mla_prolog(args: MlaArgs, workspace: Optional[torch.Tensor] = None, stre
     have been zero-filled before its first use.  Returns the workspace."""
     lib = load()
     need = lib.dsa_mla_prolog_workspace(ctypes.byref(args))
-    ws, n = _ws(need, device or "cuda", workspace)
+    ws, n = _ws(need, device or "cuda", workspace, stream)
     _check(lib.dsa_mla_prolog(ctypes.byref(args), _p(ws), n, _stream(stream)), "dsa_mla_prolog")
     return ws
 

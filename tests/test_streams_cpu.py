@@ -80,3 +80,14 @@ def test_result_of_a_read(stream, made, monkeypatch):
     assert made == [stream]
     cache.read(Memory(4), out=Memory(4), stream=stream)
     assert made == [stream]
+
+
+@pytest.mark.parametrize("stream", [None, SIDE])
+@pytest.mark.parametrize("name", ["dsa_indexer_prolog", "dsa_indexer_topk", "dsa_sparse_attn", "dsa_mla_prolog"])
+def test_workspaces_that_have_to_be_clear(name, stream, made, monkeypatch):
+    """(Made and cleared on the call's stream: the kernels come after the fill.)"""
+    _library(monkeypatch, **{name + "_workspace": lambda a: 4096, name: lambda *a: 0})
+    args = {"dsa_indexer_prolog": B.PrologArgs, "dsa_indexer_topk": B.TopkArgs, "dsa_sparse_attn": B.AttnArgs,
+            "dsa_mla_prolog": B.MlaArgs}[name]()
+    getattr(B, name)(args, stream=stream)
+    assert made == [stream]
