@@ -405,6 +405,10 @@ def attn_kv4_args(T, B, n_q, H, topk, max_L, scale, q, kv4, topk_idx, out, lse=N
     """Arguments of dsa_sparse_attn_kv4: q bf16 [T, H, 576], kv4 uint8 [rows, 416], topk_idx int32 [T, topk], out
     bf16 [T, H, 512], lse fp32 [T, H]; block_table int32 [B, max_blocks] for a paged cache; sink fp32 [H];
     seq_of_token int32 [T] (then n_q is ignored)."""
+    for name, v in (("T", T), ("B", B), ("n_q", n_q), ("H", H), ("topk", topk), ("max_L", max_L),
+                    ("block_size", block_size)):
+        if not -2 ** 31 <= v < 2 ** 31:  # (the C int would take its lower 32 bits)
+            raise DSAError(f"{name}: {v} does not fit 32 bits")
     device = _device("q", q)
     _tensor("q", q, torch.bfloat16, (T, H, 576), device)
     _tensor("kv4", kv4, torch.uint8, (None, KV4_ROW_BYTES), device)

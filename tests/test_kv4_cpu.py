@@ -195,3 +195,26 @@ def test_wrappers_refuse_cpu_tensors():
                  lambda: B.attn_kv4_args(2, 1, 2, 1, 4, 4, 1.0, x[:, None], kv4, slot[:, None].int(), x[:, None])):
         with pytest.raises(B.DSAError, match="not a CUDA tensor"):
             call()
+
+
+def _cpu_attention_args(monkeypatch, **change):
+    """An argument block over CPU tensors (the checks of the tensors left out)."""
+    from sparse_attention_prolog_gb300 import binding as B
+    monkeypatch.setattr(B, "_device", lambda name, t: 0)
+    monkeypatch.setattr(B, "_tensor", lambda *a, **k: None)
+    d = dict(T=2, B=1, n_q=2, H=4, topk=8, max_L=16, scale=0.1, q=torch.zeros(2, 4, 576, dtype=torch.bfloat16),
+             kv4=torch.zeros(16, 416, dtype=torch.uint8), topk_idx=torch.zeros(2, 8, dtype=torch.int32),
+             out=torch.zeros(2, 4, 512, dtype=torch.bfloat16))
+    d.update(change)
+    return B.attn_kv4_args(**d)
+
+
+@pytest.mark.parametrize("name", ["T", "B", "n_q", "H", "topk", "max_L", "block_size"])
+def test_sizes_past_32_bits_are_refused(name, monkeypatch):
+    """(A C int would take their lower 32 bits: another, valid size.)"""
+    from sparse_attention_prolog_gb300 import binding as B
+    _cpu_attention_args(monkeypatch)
+    for value in (2 ** 31, 2 ** 32 + 2, -2 ** 31 - 1):
+        with pytest.raises(B.DSAError, match=name):
+            _cpu_attention_args(monkeypatch, **{name: value})
+    assert getattr(_cpu_attention_args(monkeypatch, **{name: 2 ** 31 - 1}), name) == 2 ** 31 - 1
