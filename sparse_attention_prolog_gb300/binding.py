@@ -177,6 +177,13 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _keep(args, *tensors):
+    """args, holding on to the tensors whose addresses it has (a block may be built
+    from temporaries)."""
+    args.tensors = tensors
+    return args
+
+
 def _stream(stream=None):
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
@@ -201,12 +208,13 @@ def _ws(nbytes: int, device, ws: Optional[torch.Tensor], stream):
 def prolog_args(T, H_I, d_I, d_rope, q_lora, q_lora_scale, w_qb, w_qb_scale, x, w_k, ln_gamma, ln_beta,
                 ln_eps, w_proj, w_scale, pos, rope_cos, rope_sin, rope_interleaved, q_out, q_scale_out,
                 k_cache, k_scale_cache, slot, w_out) -> PrologArgs:
-    return PrologArgs(
+    return _keep(PrologArgs(
         T, H_I, d_I, d_rope, q_lora.shape[1] if T else 0, x.shape[1] if T else 0,
         _p(q_lora), _p(q_lora_scale), _p(w_qb), _p(w_qb_scale), _p(x), _p(w_k), _p(ln_gamma), _p(ln_beta),
         float(ln_eps), _p(w_proj), float(w_scale), _p(pos), _p(rope_cos), _p(rope_sin), rope_cos.shape[0],
         int(rope_interleaved), _p(q_out), _p(q_scale_out), _p(k_cache), _p(k_scale_cache), _p(slot),
-        k_cache.shape[0], _p(w_out))
+        k_cache.shape[0], _p(w_out)), q_lora, q_lora_scale, w_qb, w_qb_scale, x, w_k, ln_gamma, ln_beta, w_proj, pos,
+        rope_cos, rope_sin, q_out, q_scale_out, k_cache, k_scale_cache, slot, w_out)
 
 
 def dsa_indexer_prolog(args: PrologArgs, workspace: Optional[torch.Tensor] = None, stream=None,
@@ -230,9 +238,10 @@ def topk_args(T, B, n_q, H_I, d_I, topk, max_L, q, q_scale, w, k_cache, k_scale,
     """seq_of_token: int32 [T] sequence of each token (then n_q is ignored), or
     None for the uniform batch T = B * n_q."""
     max_blocks = 0 if block_table is None else block_table.shape[1]
-    return TopkArgs(T, B, n_q, H_I, d_I, topk, max_L, _p(q), _p(q_scale), _p(w), _p(k_cache), _p(k_scale),
-                    _p(block_table), block_size, max_blocks, _p(pos), _p(topk_idx), _p(scores_out),
-                    _p(seq_of_token))
+    return _keep(TopkArgs(T, B, n_q, H_I, d_I, topk, max_L, _p(q), _p(q_scale), _p(w), _p(k_cache), _p(k_scale),
+                          _p(block_table), block_size, max_blocks, _p(pos), _p(topk_idx), _p(scores_out),
+                          _p(seq_of_token)),
+                 q, q_scale, w, k_cache, k_scale, block_table, pos, topk_idx, scores_out, seq_of_token)
 
 
 def dsa_indexer_topk(args: TopkArgs, workspace: Optional[torch.Tensor] = None, stream=None, device=None):
@@ -260,8 +269,9 @@ def dsa_topk_from_scores(args: TopkArgs, scores: torch.Tensor, stream=None):
 def attn_args(T, B, n_q, H, topk, max_L, scale, q, kv, topk_idx, out, lse=None, block_table=None,
               block_size=0, d_qk=576, d_v=512, sink=None, seq_of_token=None) -> AttnArgs:
     max_blocks = 0 if block_table is None else block_table.shape[1]
-    return AttnArgs(T, B, n_q, H, d_qk, d_v, topk, max_L, float(scale), _p(q), _p(kv), _p(block_table),
-                    block_size, max_blocks, _p(topk_idx), _p(out), _p(lse), _p(sink), _p(seq_of_token))
+    return _keep(AttnArgs(T, B, n_q, H, d_qk, d_v, topk, max_L, float(scale), _p(q), _p(kv), _p(block_table),
+                          block_size, max_blocks, _p(topk_idx), _p(out), _p(lse), _p(sink), _p(seq_of_token)),
+                 q, kv, block_table, topk_idx, out, lse, sink, seq_of_token)
 
 
 def dsa_sparse_attn(args: AttnArgs, workspace: Optional[torch.Tensor] = None, stream=None, device=None):
@@ -321,10 +331,12 @@ def mla_args(x, w_dq, gamma_q, w_dkv, gamma_kv, rms_eps, w_uq, w_uq_scale, w_uk,
     [H, 128, 512]; outputs q_lora int8 [T, K_q], q_lora_scale fp16 [T], q bf16 [T, H, 576] and the
     kv_cache bf16 [rows, 576] rows at slot (see dsa.h)."""
     T, D_x = x.shape
-    return MlaArgs(T, w_uk.shape[0], w_dq.shape[0], D_x, float(rms_eps), rope_cos.shape[0], int(rope_interleaved),
-                   _p(x), _p(w_dq), _p(gamma_q), _p(w_dkv), _p(gamma_kv), _p(w_uq), _p(w_uq_scale), _p(w_uk),
-                   _p(pos), _p(rope_cos), _p(rope_sin), _p(q_lora), _p(q_lora_scale), _p(q), _p(kv_cache),
-                   _p(slot), kv_cache.shape[0])
+    return _keep(MlaArgs(T, w_uk.shape[0], w_dq.shape[0], D_x, float(rms_eps), rope_cos.shape[0],
+                         int(rope_interleaved), _p(x), _p(w_dq), _p(gamma_q), _p(w_dkv), _p(gamma_kv), _p(w_uq),
+                         _p(w_uq_scale), _p(w_uk), _p(pos), _p(rope_cos), _p(rope_sin), _p(q_lora), _p(q_lora_scale),
+                         _p(q), _p(kv_cache), _p(slot), kv_cache.shape[0]),
+                 x, w_dq, gamma_q, w_dkv, gamma_kv, w_uq, w_uq_scale, w_uk, pos, rope_cos, rope_sin, q_lora,
+                 q_lora_scale, q, kv_cache, slot)
 
 
 def dsa_mla_prolog(args: MlaArgs, workspace: Optional[torch.Tensor] = None, stream=None, device=None):
@@ -427,7 +439,7 @@ def attn_kv4_args(T, B, n_q, H, topk, max_L, scale, q, kv4, topk_idx, out, lse=N
     args = AttnKv4Args(T, B, n_q, H, topk, max_L, float(scale), _p(q), _p(kv4), kv4.shape[0], _p(block_table),
                        block_size, max_blocks, _p(topk_idx), _p(out), _p(lse), _p(sink), _p(seq_of_token))
     args.device = q.device
-    return args
+    return _keep(args, q, kv4, block_table, topk_idx, out, lse, sink, seq_of_token)
 
 
 def dsa_sparse_attn_kv4(args: AttnKv4Args, workspace: Optional[torch.Tensor] = None, stream=None):
