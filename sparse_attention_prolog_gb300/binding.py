@@ -397,8 +397,9 @@ def _stream_of(device: int, stream):
 
 
 def dsa_kv4_write(x: torch.Tensor, kv4: torch.Tensor, slot: torch.Tensor, stream=None):
-    """Quantises latent rows x bf16 [n, 576] (any row stride) into rows `slot`
-    int64 [n] of the 4-bit cache kv4 uint8 [rows, 416] (see dsa.h)."""
+    """Quantises latent rows x bf16 [n, 576] (rows 16-byte aligned, a multiple of 8
+    elements apart) into rows `slot` int64 [n] of the 4-bit cache kv4 uint8
+    [rows, 416] (see dsa.h)."""
     device, n, stride, rows = _kv4_rows("x", x, kv4, slot)
     args = Kv4WriteArgs(n, stride, x.data_ptr(), kv4.data_ptr(), slot.data_ptr(), rows)
     _check(load().dsa_kv4_write(ctypes.byref(args), _stream_of(device, stream)), "dsa_kv4_write")
@@ -406,7 +407,7 @@ def dsa_kv4_write(x: torch.Tensor, kv4: torch.Tensor, slot: torch.Tensor, stream
 
 def dsa_kv4_read(kv4: torch.Tensor, slot: torch.Tensor, out: torch.Tensor, stream=None):
     """Rows `slot` int64 [n] of the 4-bit cache kv4 uint8 [rows, 416] -> out
-    bf16 [n, 576] (any row stride; see dsa.h)."""
+    bf16 [n, 576] (rows 16-byte aligned, a multiple of 8 elements apart; see dsa.h)."""
     device, n, stride, rows = _kv4_rows("out", out, kv4, slot)
     args = Kv4ReadArgs(n, stride, kv4.data_ptr(), slot.data_ptr(), rows, out.data_ptr())
     _check(load().dsa_kv4_read(ctypes.byref(args), _stream_of(device, stream)), "dsa_kv4_read")

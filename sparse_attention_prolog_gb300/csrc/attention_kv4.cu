@@ -57,11 +57,13 @@ constexpr int kHalf = 64;                  // rows of a slot
 constexpr int kSlot = 4 * kAtom;           // 64 rows x 512 dims bf16: 8 atoms of 64 rows x 128 bytes
 constexpr int kPSlot = 2 * kAtom;          // P [128 heads x 128 rows] bf16
 constexpr int kDescs = 8;                  // tile descriptors: how far the lookups run ahead of the slowest role
-constexpr uint64_t kTryNs = 40;            // a try of a barrier takes about so long
+constexpr uint64_t kTryNs = 40;            // a try of a barrier takes about so long, and longer under load
 // 28 warps in seven warpgroups: 0-1 softmax (CTA 0), correction and epilogue
 // (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, and q loads and rotary K loads
 // (CTA 0) or the news of P's use and arrival (CTA 1).  The launch grants 72 registers
-// a thread: 896 x 72 = 256 x 88 + 512 x 64 + 128 x 72.
+// a thread: 896 x 72 = 256 x 88 + 512 x 64 + 128 x 72.  (ptxas spills two words, 40 bytes
+// of stores and 112 of reloads in all; without the softmax or the row lookups none, without
+// the conversion 40 and 100.)
 constexpr int kThreads = 896;
 constexpr int kSoftWarps = 8, kConvWarps = 16, kFirstConv = 8, kMmaWarp = 24, kRowWarp = 25, kAuxWarp = 26,
               kAux2Warp = 27;
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int item = cluster, n = 0; item < P.items && ok; item += clusters, ++n) {
       if (rank == 0) {
         // q: 256 dims of the 128 heads a slot (4 atoms), lane = head, two atoms a warp, in
-        // 16 registers (in 32, next to a tile's rows, they spill: 2.43 ms for 2.31)
+        // 16 registers (in 32, next to a tile's rows: 2.43 ms for 2.31)
         if (n > 0) ok = WAIT(bars.qfree, (n - 1) & 1);
         if (!ok || !WAIT(bars.full[g], uses & 1)) { ok = false; break; }
         tc_fence_after();
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (Rounded to bf16 and through the staging 8 tokens took 24.0 us instead of 24.8
           // and 32 sequences 49.5 instead of 47.2; the output of the 32 was off by 0.0026 of itself
           // instead of 0.0021.)
-          if (!first) {  // (what selects nothing is not read)
+          if (!first) {  // (what selects nothing writes no O: the merge gives it no weight)
             float4* o = P.part_o + (static_cast<size_t>(t * P.n_chunks + chunk) * (kDv / 4) + hf * (kDv / 8)) * P.H + h;
 #pragma unroll 1
             for (int i = 0; i < 8; ++i, o += 8 * P.H) {
@@ -1054,7 +1056,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // reads are runs of 512 bytes; its warps share the chunks' maxima and sums through
 // shared memory, and the result goes through it to be written in longer runs.  A thread
 // has the loads of kBatch chunks of 4 kCols columns in flight, the first of them before
-// the maxima arrive.
+// the maxima arrive.  (The part of a chunk that selects nothing, which nobody wrote, is
+// loaded like the others and left out.)  All chunks in one batch and 32 floats a thread
+// where there are few chunks, batches of eight and one column group where there are many;
+// one call of 128 heads over 2048 rows, us with <2, 4>, <4, 2> and <8, 1>:
+//    2 chunks (38 tokens)  38.5  39.5  42.3     9 (8)   26.4  24.2  23.2
+//    3        (25)         32.7  32.7  34.2    16 (4)   25.5  24.9  22.4
+//    4        (19)         29.4  28.3  29.7    32 (1)   28.3  21.5  19.4
 constexpr int kMergeWarps = 4;
 
 template <int kBatch, int kCols>
@@ -1145,6 +1153,9 @@ cudaError_t launch_merge(const AttnKv4Params& P, cudaLaunchConfig_t& cfg) {
 // Chunks per token: as many as the GPU holds clusters for at once, each a multiple of a
 // slot's 64 rows.  (Blocks of 64 heads in twice the clusters, where there are enough:
 // one token 23.6 us for 21.2, as every row is then converted twice.)
+// Whole chunks per token leave clusters idle just past a count that fills them: 128 heads
+// over 2048 rows take 38.5 us for 38 tokens (two chunks each, every cluster), 50.6 for 39
+// (one each, half of the clusters), 54.1 for 76, 93.0 for 77 (a second round), 102.5 for 152.
 void plan(const dsa_attn_kv4_args& a, int& head_blocks, int& n_chunks, int& chunk_rows) {
   head_blocks = (a.H + 127) / 128;
   const long long pairs = static_cast<long long>(a.T) * head_blocks;

@@ -8,7 +8,6 @@ namespace dsa {
 
 constexpr int kKv4Row = 416;                      // bytes of a row
 constexpr int kKv4Scales = 256, kKv4Rope = 288;   // byte offsets of the scale bytes and the rotary dims
-constexpr int kKv4Dims = 512, kKv4RopeDims = 64, kKv4Group = 16;
 
 // The scale of byte u enters the conversion as 16 s and -24 s, each twice in
 // a register.  s = (1 + m/8) 2^(e-15) with u = 8e + m, so the bits of 16 s in
