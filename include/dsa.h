@@ -93,9 +93,9 @@ int dsa_get_device_error(void* stream);
  * call's workspace again before the next one.  Waits are timed on the
  * global timer, so a limit shorter than its tick (about 1 us) runs out at
  * the first tick; under a limit below 20 us a wait never blocks in the
- * hardware.  (dsa_sparse_attn_kv4 counts tries of some 40 ns each instead:
- * a try takes longer where many warps wait on one SM, so there a limit is a
- * time that a wait lasts at least.  It needs no zeroed workspace.)
+ * hardware.  (dsa_sparse_attn_kv4 counts tries of known length instead: a
+ * wait lasts from the limit, but 4 us at the least, to 3.5 times the limit.
+ * It needs no zeroed workspace.)
  * Synchronous: it takes effect for kernels launched after it returns; call
  * it while none of this library's kernels runs.  No counterpart on the
  * pages: a test hook. */

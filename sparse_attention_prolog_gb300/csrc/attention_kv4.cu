@@ -57,7 +57,10 @@ constexpr int kHalf = 64;                  // rows of a slot
 constexpr int kSlot = 4 * kAtom;           // 64 rows x 512 dims bf16: 8 atoms of 64 rows x 128 bytes
 constexpr int kPSlot = 2 * kAtom;          // P [128 heads x 128 rows] bf16
 constexpr int kDescs = 8;                  // tile descriptors: how far the lookups run ahead of the slowest role
-constexpr uint64_t kTryNs = 40;            // a try of a barrier takes about so long, and longer under load
+// Tries of a barrier, measured at 2070 MHz: by one lane while the others of its warp are
+// parked 56 clocks at the least (186 in this kernel's long calls), by a whole warp 7790.
+constexpr uint64_t kTryNs = 27;
+constexpr uint32_t kWarpTries = 139;       // a warp's try in units of the shortest
 // 28 warps in seven warpgroups: 0-1 softmax (CTA 0), correction and epilogue
 // (CTA 1); 2-5 conversion; 6 MMA issue, row lookups, and q loads and rotary K loads
 // (CTA 0) or the news of P's use and arrival (CTA 1).  The launch grants 72 registers
@@ -186,7 +189,9 @@ __device__ __forceinline__ void drain_copy(uint64_t* bar, uint32_t parity) {
 // instruction cache.  (With the other kernels' waits inlined an earlier form was 133
 // KB and a third of the cache's requests missed: 5.97 ms for the 4096-token case;
 // taking 3 KB of code that this case never reaches out of an 78 KB form won 5%.)
-// A try blocks for some 70 clocks by itself; `limit` of them fill the limit in force.
+// Time is counted in tries, a warp's for kWarpTries of a lane's: `limit` of them last
+// for the limit in force at the least, and for a lane's waits up to 3.5 times it.
+// (Reading the global timer after each failed try instead: 2048 tokens 1305 us for 1204.)
 // Who runs out sets *tries to 0 for the CTA's end and leaves its role; the roles that
 // wait for it run out in their turn.  The lanes of a waiting warp vote on every try, so
 // they go on or give up together (one that left alone would leave the others at the
@@ -198,7 +203,7 @@ __device__ __forceinline__ void drain_copy(uint64_t* bar, uint32_t parity) {
 template <bool kCluster, bool kWarp>
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t limit, volatile uint32_t* tries) {
 #pragma unroll 1
-  for (uint32_t n = 0;; ++n) {
+  for (uint32_t n = 0;; n += kWarp ? kWarpTries : 1) {
     bool done = kCluster ? mbar_probe_cluster(bar, parity) : mbar_probe(bar, parity);
     if (kWarp) done = __all_sync(0xffffffffu, done);
     if (done) return true;
