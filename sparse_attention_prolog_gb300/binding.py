@@ -7,6 +7,7 @@ library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -191,16 +192,24 @@ def _stream(stream=None):
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
+_HERE = contextlib.nullcontext()
+
+
+def pool_of(stream):
+    """Context in which memory is made for a call on `stream` (None: the current
+    one): of that stream's own pool, and filled on it.  A block that another stream
+    freed may still be in use there, and its fill might come after the call."""
+    return _HERE if stream is None else torch.cuda.stream(stream)  # (2.3 us even for None)
+
+
 def _ws(nbytes: int, device, ws: Optional[torch.Tensor], stream):
-    """A workspace for a call on `stream` and its size.  (A new one comes from the
-    pool of that stream, which also clears it: a block that another stream freed
-    may still be in use there, and its fill might come after the call.)"""
+    """A workspace for a call on `stream` and its size."""
     if nbytes == 0:
         return None, 0
     if ws is not None:
         assert ws.numel() * ws.element_size() >= nbytes
         return ws, ws.numel() * ws.element_size()
-    with torch.cuda.stream(stream):
+    with pool_of(stream):
         return torch.zeros(nbytes, dtype=torch.uint8, device=device), nbytes
 
 
@@ -453,7 +462,7 @@ def dsa_sparse_attn_kv4(args: AttnKv4Args, workspace: Optional[torch.Tensor] = N
     if workspace is None:
         n = lib.dsa_sparse_attn_kv4_workspace(ctypes.byref(args))
         if n:
-            with torch.cuda.stream(stream):  # of the pool whose blocks are free in this stream's order
+            with pool_of(stream):
                 workspace = torch.empty(n, dtype=torch.uint8, device=args.device)
     else:
         n = workspace.numel() * workspace.element_size()

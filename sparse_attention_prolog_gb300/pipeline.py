@@ -121,7 +121,7 @@ class Kv4Cache:
         memory of ``stream``: another stream that uses it waits for this one, and
         records itself on it (``record_stream``) if it may be dropped before."""
         if out is None:
-            with torch.cuda.stream(stream):
+            with B.pool_of(stream):
                 out = torch.empty(slot.shape[0], 576, dtype=torch.bfloat16, device=self.data.device)
         B.dsa_kv4_read(self.data, slot, out, stream)
         return out
