@@ -11,6 +11,9 @@
  *   dsa_mla_prolog      : MLA Prolog (q_lora, absorbed query, latent KV rows)
  *   dsa_kv4_write/_read : latent KV rows into a 4-bit cache, and back to bf16
  *   dsa_sparse_attn_kv4 : the sparse attention over a 4-bit latent cache
+ *   dsa_step_maps       : a step's block table and token maps from its lengths
+ *   dsa_latent_attn     : attention over the whole latent cache, no selection
+ *   dsa_add_rmsnorm     : residual addition, RMS norm, bf16 and/or int8 output
  *
  * Page citations:
  *   [V3.2-PyPTO]  "NPU DeepSeek-V3.2-Exp PyPTO 融合算子开发优化实践",
@@ -575,6 +578,161 @@ typedef struct {
 
 size_t dsa_sparse_attn_kv4_workspace(const dsa_attn_kv4_args* args);
 int dsa_sparse_attn_kv4(const dsa_attn_kv4_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Step maps: the tables that a step's calls take (block_table, pos, slot,
+ * seq_of_token, and the token counts and lengths of dsa_latent_attn) from the
+ * lengths of its requests, without a host round trip.  The pages take them as
+ * given; no counterpart there.
+ *
+ * Request b has cached[b] tokens in a paged cache and adds fresh[b] (0: idle).
+ * Its pages ceil(cached / block_size) .. ceil((cached + fresh) / block_size) - 1
+ * are new: the new pages of all requests, in the requests' order, take
+ * free_pages[head], free_pages[head + 1], ... (head = *free_head, or 0 if
+ * free_head is NULL), and only their entries of block_table are written.
+ *
+ *   cu_tokens[b]  = fresh[0] + .. + fresh[b-1]              (b = 0 .. B)
+ *   kv_len[b]     = cached[b] + fresh[b]
+ *   counts        = { tokens of the step, head after it, requests served }
+ *   token t = cu_tokens[b] + i, i < fresh[b]:
+ *     seq_of_token[t] = b, pos[t] = cached[b] + i,
+ *     slot[t] = block_table[b][pos / block_size] * block_size + pos % block_size
+ *   token t past the last one, up to T: the last token's sequence (0 if there
+ *     is none), pos 0, slot -1: padding that the other calls accept (it sees
+ *     one key, and its rows are not written).
+ *
+ * Requests are served in order.  The first one that does not fit (the step's
+ * tokens pass T, its new pages pass the list, its length passes max_blocks *
+ * block_size, or a length is negative) is recorded as DSA_ERR_DEVICE_DATA, and
+ * neither it nor any after it is served: they get no token and no page, and
+ * kv_len = cached.  A negative free_head serves none.  A token whose page entry
+ * is negative gets slot -1, recorded likewise.
+ *
+ * Shapes: cached, fresh int32 [B]; free_pages int32 [n_free] (may be NULL if
+ * n_free = 0), free_head int32 [1] or NULL; block_table int32 [B, max_blocks]
+ * (in and out); cu_tokens int32 [B + 1]; kv_len int32 [B]; counts int32 [3];
+ * seq_of_token, pos int32 [T]; slot int64 [T].  free_head must not be an element
+ * of counts, nor cached be kv_len: outputs are written while inputs are read,
+ * so a loop keeps two of each and swaps them.
+ * Supported: 1 <= B <= 8192, max_blocks * block_size < 2^31, block_size >= 1.
+ * T = 0 is allowed (no request with fresh > 0 is then served).  B = 0 is a
+ * no-op.  No workspace.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t B, T, block_size, max_blocks, n_free;
+  const int32_t* cached;
+  const int32_t* fresh;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  int32_t* block_table;
+  int32_t* cu_tokens;
+  int32_t* kv_len;
+  int32_t* counts;
+  int32_t* seq_of_token;
+  int32_t* pos;
+  int64_t* slot;
+} dsa_step_maps_args;
+
+int dsa_step_maps(const dsa_step_maps_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Latent attention: dsa_sparse_attn without a selection.  The newest tokens of
+ * each sequence attend over every row of its latent cache that they may see,
+ * for layers without an indexer and for contexts no longer than its selection
+ * (the pages' attention of V4-TileLang §Sparse Flash Attention steps 3-8 over
+ * all rows).
+ *
+ *   out[t,h,:] = sum_s softmax_s(scale * q[t,h,:] . KV[s]) KV[s, :512]
+ *
+ * over the rows 0 <= s <= pos(t), pos(t) = kv_len[b] - n_b + i for the i-th of
+ * sequence b's n_b tokens.  lse and sink as in dsa_sparse_attn; a token that
+ * sees no row (kv_len[b] < n_b) gets out = 0 and lse = -inf (or sink[h]).
+ *
+ * Sums, softmax statistics, lse and the partial outputs of split sequences are
+ * fp32; the probabilities are rounded to bf16 before they meet the values
+ * (their sum is not), and the output is rounded once.
+ *
+ * Token layout: cu_tokens int32 [B + 1] (non-decreasing, from 0, at most T):
+ * sequence b has the tokens cu_tokens[b] .. cu_tokens[b+1] - 1; rows of q past
+ * cu_tokens[B] are not read, those of out and lse not written.  NULL: the
+ * uniform batch T = B * n_q.
+ * Shapes: q bf16 [T, H, 576]; kv bf16 contiguous [B, max_L, 576] (cache_rows >=
+ * B * max_L) or paged [cache_rows, 576] through block_table int32 [B,
+ * max_blocks], max_L = max_blocks * block_size; kv_len int32 [B], with the new
+ * tokens' rows (which are in the cache); out bf16 [T, H, 512]; lse fp32 [T, H]
+ * or NULL; sink fp32 [H] or NULL, entries finite or -inf.
+ * Rows at or past kv_len[b] may hold anything.  So may the rows that a token may
+ * not see yet, unless one of its sequence's newer tokens is attended by the same
+ * 128 rows of q (H no multiple of 128): those have to be finite.
+ * A page entry that is negative or names a page past cache_rows, a kv_len
+ * outside [0, max_L] (clamped) and cu_tokens that decrease or leave [0, T]
+ * (clamped) are recorded as DSA_ERR_DEVICE_DATA; rows of such a page read as
+ * zeros.
+ * Supported: T * H < 2^31 - 128, 1 <= H <= 1024, 1 <= B <= 65535, scale positive
+ * and finite, cache_rows < 2^31, block_size 8, 16, 32 or a multiple of 64;
+ * q, kv and out 16-byte aligned.
+ * Workspace: dsa_latent_attn_workspace() bytes, 256-byte aligned, never in use
+ * by two calls that may overlap; it need not be zeroed.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t T, B, n_q, H, max_L;
+  float scale;
+  const uint16_t* q;
+  const uint16_t* kv;
+  int64_t cache_rows;
+  const int32_t* block_table;
+  int32_t block_size, max_blocks;
+  const int32_t* cu_tokens;
+  const int32_t* kv_len;
+  uint16_t* out;
+  float* lse;
+  const float* sink;
+} dsa_latent_attn_args;
+
+size_t dsa_latent_attn_workspace(const dsa_latent_attn_args* args);
+int dsa_latent_attn(const dsa_latent_attn_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Residual addition and RMS norm: what stands between two sublayers, feeding
+ * the prologs (y: their x) and the int8 GEMM (codes, code_scale: its a,
+ * a_scale).  RMSNorm as in dsa_mla_prolog, the quantiser as in dsa_act_quant.
+ *
+ *   h          = x + residual, rounded to the residual's type  (x if NULL)
+ *   z          = h / sqrt(mean(h^2) + eps) * gamma              (fp32)
+ *   residual_out = h;  y = bf16(z)
+ *   code_scale = max |z| / 127  (round_scale != 0: the power of two at or
+ *                above it);  codes = rint(clamp(z / code_scale, -127, 127))
+ *
+ * The norm is taken of h as it is stored, so that adding and normalising in two
+ * calls gives the same.  The codes come from z in fp32, not from y.  A row whose
+ * z is all zeros has code_scale 0 and codes 0; one with a z that is not finite
+ * has a code_scale that is not and codes 0.  The squares are summed in fp32.
+ *
+ * Shapes: x bf16 (x_fp16 = 0) or fp16 (x_fp16 = 1) [T, D], rows x_stride
+ * elements apart; residual and residual_out bf16 (residual_fp32 = 0) or fp32
+ * (1) [T, D], rows residual_stride and residual_out_stride elements apart, both
+ * NULL or both given, and residual_out may be residual (with its stride); gamma
+ * fp32 [D]; y bf16 [T, D] or NULL; codes int8 [T, D] and code_scale fp32 [T],
+ * both NULL or both given; y or codes is given.  Strides are at least D.  Pointers
+ * are aligned to their elements; rows that are all 16-byte aligned (codes: 8)
+ * and D a multiple of 8 are read and written by vectors.  Nothing else overlaps.
+ * Supported: 1 <= D <= 32768, eps >= 0.  T = 0 is a no-op.  No workspace.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t T, D;
+  float eps;
+  int32_t x_fp16, residual_fp32, round_scale;
+  int64_t x_stride, residual_stride, residual_out_stride;
+  const void* x;
+  const void* residual;
+  void* residual_out;
+  const float* gamma;
+  uint16_t* y;
+  int8_t* codes;
+  float* code_scale;
+} dsa_add_rmsnorm_args;
+
+int dsa_add_rmsnorm(const dsa_add_rmsnorm_args* args, void* stream);
 
 #ifdef __cplusplus
 }

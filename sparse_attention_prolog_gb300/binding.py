@@ -93,6 +93,27 @@ class AttnKv4Args(ctypes.Structure):
     ]
 
 
+class StepMapsArgs(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int), ("block_size", c_int), ("max_blocks", c_int), ("n_free", c_int),
+                ("cached", c_ptr), ("fresh", c_ptr), ("free_pages", c_ptr), ("free_head", c_ptr),
+                ("block_table", c_ptr), ("cu_tokens", c_ptr), ("kv_len", c_ptr), ("counts", c_ptr),
+                ("seq_of_token", c_ptr), ("pos", c_ptr), ("slot", c_ptr)]
+
+
+class LatentAttnArgs(ctypes.Structure):
+    _fields_ = [("T", c_int), ("B", c_int), ("n_q", c_int), ("H", c_int), ("max_L", c_int), ("scale", ctypes.c_float),
+                ("q", c_ptr), ("kv", c_ptr), ("cache_rows", ctypes.c_int64), ("block_table", c_ptr),
+                ("block_size", c_int), ("max_blocks", c_int), ("cu_tokens", c_ptr), ("kv_len", c_ptr), ("out", c_ptr),
+                ("lse", c_ptr), ("sink", c_ptr)]
+
+
+class AddRmsnormArgs(ctypes.Structure):
+    _fields_ = [("T", c_int), ("D", c_int), ("eps", ctypes.c_float), ("x_fp16", c_int), ("residual_fp32", c_int),
+                ("round_scale", c_int), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("residual_out_stride", ctypes.c_int64), ("x", c_ptr), ("residual", c_ptr), ("residual_out", c_ptr),
+                ("gamma", c_ptr), ("y", c_ptr), ("codes", c_ptr), ("code_scale", c_ptr)]
+
+
 EXPORTS = [
     "dsa_status_string", "dsa_abi_version", "dsa_get_device_error", "dsa_set_wait_limit_ns",
     "dsa_indexer_prolog_workspace", "dsa_indexer_prolog",
@@ -101,6 +122,7 @@ EXPORTS = [
     "dsa_sparse_attn_workspace", "dsa_sparse_attn", "dsa_indexer_prolog_noalloc", "dsa_act_quant",
     "dsa_int8_gemm", "dsa_mhc", "dsa_mla_prolog_workspace", "dsa_mla_prolog",
     "dsa_kv4_write", "dsa_kv4_read", "dsa_sparse_attn_kv4_workspace", "dsa_sparse_attn_kv4",
+    "dsa_step_maps", "dsa_latent_attn_workspace", "dsa_latent_attn", "dsa_add_rmsnorm",
 ]
 
 KV4_ROW_BYTES = 416  # one row of the 4-bit latent cache
@@ -161,6 +183,14 @@ def load(path: str = LIB_PATH):
     lib.dsa_sparse_attn_kv4_workspace.restype = ctypes.c_size_t
     lib.dsa_sparse_attn_kv4.argtypes = [ctypes.POINTER(AttnKv4Args), c_ptr, ctypes.c_size_t, c_ptr]
     lib.dsa_sparse_attn_kv4.restype = c_int
+    lib.dsa_step_maps.argtypes = [ctypes.POINTER(StepMapsArgs), c_ptr]
+    lib.dsa_step_maps.restype = c_int
+    lib.dsa_latent_attn_workspace.argtypes = [ctypes.POINTER(LatentAttnArgs)]
+    lib.dsa_latent_attn_workspace.restype = ctypes.c_size_t
+    lib.dsa_latent_attn.argtypes = [ctypes.POINTER(LatentAttnArgs), c_ptr, ctypes.c_size_t, c_ptr]
+    lib.dsa_latent_attn.restype = c_int
+    lib.dsa_add_rmsnorm.argtypes = [ctypes.POINTER(AddRmsnormArgs), c_ptr]
+    lib.dsa_add_rmsnorm.restype = c_int
     _lib = lib
     return lib
 
@@ -295,7 +325,7 @@ def workspace_bytes(kind: str, args) -> int:
     lib = load()
     fn = {"prolog": lib.dsa_indexer_prolog_workspace, "topk": lib.dsa_indexer_topk_workspace,
           "attn": lib.dsa_sparse_attn_workspace, "mla": lib.dsa_mla_prolog_workspace,
-          "attn_kv4": lib.dsa_sparse_attn_kv4_workspace}[kind]
+          "attn_kv4": lib.dsa_sparse_attn_kv4_workspace, "latent_attn": lib.dsa_latent_attn_workspace}[kind]
     return int(fn(ctypes.byref(args)))
 
 
@@ -452,22 +482,140 @@ def attn_kv4_args(T, B, n_q, H, topk, max_L, scale, q, kv4, topk_idx, out, lse=N
     return _keep(args, q, kv4, block_table, topk_idx, out, lse, sink, seq_of_token)
 
 
-def dsa_sparse_attn_kv4(args: AttnKv4Args, workspace: Optional[torch.Tensor] = None, stream=None):
-    """Runs the sparse attention over a 4-bit cache.  Returns the workspace
-    (one of the stream's own is made when none is given and the shape needs
-    one)."""
-    lib = load()
+def _run_on(args, fn, size, what: str, workspace, stream):
+    """Calls fn with args, the workspace (one of the stream's own is made when none
+    is given and the shape needs one) and the stream.  Returns the workspace."""
     if torch.cuda.current_device() != args.device.index:
-        raise DSAError(f"dsa_sparse_attn_kv4: tensors on {args.device}, which is not the current device")
+        raise DSAError(f"{what}: tensors on {args.device}, which is not the current device")
     if workspace is None:
-        n = lib.dsa_sparse_attn_kv4_workspace(ctypes.byref(args))
+        n = size(ctypes.byref(args))
         if n:
             with pool_of(stream):
                 workspace = torch.empty(n, dtype=torch.uint8, device=args.device)
     else:
         n = workspace.numel() * workspace.element_size()
         if workspace.get_device() != args.device.index or not workspace.is_contiguous():
-            raise DSAError("dsa_sparse_attn_kv4: the workspace is not contiguous on the tensors' device")
-    _check(lib.dsa_sparse_attn_kv4(ctypes.byref(args), _p(workspace), n, _stream_of(args.device.index, stream)),
-           "dsa_sparse_attn_kv4")
+            raise DSAError(f"{what}: the workspace is not contiguous on the tensors' device")
+    _check(fn(ctypes.byref(args), _p(workspace), n, _stream_of(args.device.index, stream)), what)
     return workspace
+
+
+def dsa_sparse_attn_kv4(args: AttnKv4Args, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Runs the sparse attention over a 4-bit cache.  Returns the workspace
+    (one of the stream's own is made when none is given and the shape needs
+    one)."""
+    lib = load()
+    return _run_on(args, lib.dsa_sparse_attn_kv4, lib.dsa_sparse_attn_kv4_workspace, "dsa_sparse_attn_kv4", workspace,
+                   stream)
+
+
+# ------------------------------------------------------- latent attention
+def _fits_32(**sizes):
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:  # (the C int would take its lower 32 bits)
+            raise DSAError(f"{name}: {v} does not fit 32 bits")
+
+
+def latent_attn_args(T, B, H, max_L, scale, q, kv, kv_len, out, lse=None, cu_tokens=None, n_q=0, block_table=None,
+                     block_size=0, sink=None) -> LatentAttnArgs:
+    """Arguments of dsa_latent_attn: q bf16 [T, H, 576], kv bf16 [rows, 576], kv_len int32 [B], out bf16 [T, H, 512],
+    lse fp32 [T, H]; cu_tokens int32 [B + 1], or None for n_q tokens of each sequence; block_table int32
+    [B, max_blocks] for a paged cache (max_L = max_blocks * block_size); sink fp32 [H] (see dsa.h)."""
+    _fits_32(T=T, B=B, H=H, max_L=max_L, n_q=n_q, block_size=block_size)
+    device = _device("q", q)
+    _tensor("q", q, torch.bfloat16, (T, H, 576), device)
+    _tensor("kv", kv, torch.bfloat16, (None, 576), device)
+    _tensor("kv_len", kv_len, torch.int32, (B,), device)
+    _tensor("out", out, torch.bfloat16, (T, H, 512), device)
+    max_blocks = 0
+    if block_table is not None:
+        _tensor("block_table", block_table, torch.int32, (B, None), device)
+        max_blocks = block_table.shape[1]
+    if lse is not None:
+        _tensor("lse", lse, torch.float32, (T, H), device)
+    if sink is not None:
+        _tensor("sink", sink, torch.float32, (H,), device)
+    if cu_tokens is not None:
+        _tensor("cu_tokens", cu_tokens, torch.int32, (B + 1,), device)
+    args = LatentAttnArgs(T, B, n_q, H, max_L, float(scale), _p(q), _p(kv), kv.shape[0], _p(block_table), block_size,
+                          max_blocks, _p(cu_tokens), _p(kv_len), _p(out), _p(lse), _p(sink))
+    args.device = q.device
+    return _keep(args, q, kv, kv_len, out, lse, cu_tokens, block_table, sink)
+
+
+def dsa_latent_attn(args: LatentAttnArgs, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Runs the attention over the whole latent cache.  Returns the workspace
+    (one of the stream's own is made when none is given)."""
+    lib = load()
+    return _run_on(args, lib.dsa_latent_attn, lib.dsa_latent_attn_workspace, "dsa_latent_attn", workspace, stream)
+
+
+# --------------------------------------------------------------- step maps
+def dsa_step_maps(cached: torch.Tensor, fresh: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
+                  block_size: int, cu_tokens: torch.Tensor, kv_len: torch.Tensor, counts: torch.Tensor,
+                  seq_of_token: torch.Tensor, pos: torch.Tensor, slot: torch.Tensor,
+                  free_head: Optional[torch.Tensor] = None, stream=None):
+    """The tables of a step from its requests' lengths: cached, fresh int32 [B], free_pages int32 [n], free_head int32
+    [1] -> block_table int32 [B, max_blocks] (new pages entered), cu_tokens int32 [B + 1], kv_len int32 [B], counts
+    int32 [3] (tokens, head after the step, requests served), seq_of_token and pos int32 [T], slot int64 [T] (see
+    dsa.h)."""
+    _fits_32(block_size=block_size)
+    device = _device("cached", cached)
+    n, i32 = cached.shape[:1], torch.int32
+    _tensor("cached", cached, i32, (None,), device)
+    _tensor("fresh", fresh, i32, n, device)
+    _tensor("free_pages", free_pages, i32, (None,), device)
+    _tensor("block_table", block_table, i32, (n[0], None), device)
+    _tensor("cu_tokens", cu_tokens, i32, (n[0] + 1,), device)
+    _tensor("kv_len", kv_len, i32, n, device)
+    _tensor("counts", counts, i32, (3,), device)
+    _tensor("slot", slot, torch.int64, (None,), device)
+    _tensor("seq_of_token", seq_of_token, i32, slot.shape, device)
+    _tensor("pos", pos, i32, slot.shape, device)
+    if free_head is not None:
+        _tensor("free_head", free_head, i32, (1,), device)
+    args = StepMapsArgs(n[0], slot.shape[0], block_size, block_table.shape[1], free_pages.shape[0], _p(cached),
+                        _p(fresh), _p(free_pages), _p(free_head), _p(block_table), _p(cu_tokens), _p(kv_len),
+                        _p(counts), _p(seq_of_token), _p(pos), _p(slot))
+    _check(load().dsa_step_maps(ctypes.byref(args), _stream_of(device, stream)), "dsa_step_maps")
+
+
+# --------------------------------------------------- residual and RMS norm
+def _rows(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
+    """Checks a [T, D] tensor whose rows may lie apart: its row stride."""
+    _tensor(name, t, dtype, shape, device, last_dense=True)
+    # (a single row has no stride of its own)
+    return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+
+
+def dsa_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                    residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                    codes: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                    round_scale: bool = False, stream=None):
+    """x bf16 or fp16 [T, D], gamma fp32 [D], residual and residual_out bf16 or fp32 [T, D] (residual_out may be
+    residual) -> residual_out = x + residual, and its RMS norm times gamma as y bf16 [T, D], as codes int8 [T, D] with
+    scale fp32 [T], or both (see dsa.h).  x and the residuals may be rows of wider tensors."""
+    device = _device("x", x)
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16):
+        raise DSAError(f"x: {x.dtype} {tuple(x.shape)}, expected bf16 or fp16 [T, D]")
+    shape = tuple(x.shape)
+    strides = [_rows("x", x, x.dtype, shape, device), 0, 0]
+    _tensor("gamma", gamma, torch.float32, shape[1:], device)
+    if (residual is None) != (residual_out is None) or (codes is None) != (scale is None):
+        raise DSAError("dsa_add_rmsnorm: residual goes with residual_out, codes go with scale")
+    kind = torch.bfloat16
+    if residual is not None:
+        kind = residual.dtype
+        if kind not in (torch.bfloat16, torch.float32):
+            raise DSAError(f"residual: {kind}, expected bf16 or fp32")
+        strides[1] = _rows("residual", residual, kind, shape, device)
+        strides[2] = _rows("residual_out", residual_out, kind, shape, device)
+    if y is not None:
+        _tensor("y", y, torch.bfloat16, shape, device)
+    if codes is not None:
+        _tensor("codes", codes, torch.int8, shape, device)
+        _tensor("scale", scale, torch.float32, shape[:1], device)
+    args = AddRmsnormArgs(*shape, float(eps), int(x.dtype is torch.float16), int(kind is torch.float32),
+                          int(bool(round_scale)), *strides, _p(x), _p(residual), _p(residual_out), _p(gamma), _p(y),
+                          _p(codes), _p(scale))
+    _check(load().dsa_add_rmsnorm(ctypes.byref(args), _stream_of(device, stream)), "dsa_add_rmsnorm")

@@ -445,4 +445,80 @@ int dsa_sparse_attn_kv4(const dsa_attn_kv4_args* a, void* ws, size_t ws_bytes, v
   return launch_attn_kv4(*a, ws, static_cast<cudaStream_t>(stream));
 }
 
+int dsa_step_maps(const dsa_step_maps_args* a, void* stream) {
+  if (!a || a->B < 0 || a->T < 0 || a->n_free < 0) return DSA_ERR_INVALID_ARG;
+  if (a->B == 0) return DSA_OK;
+  if (a->block_size < 1 || a->max_blocks < 1) return DSA_ERR_INVALID_ARG;
+  if (a->B > 8192 || static_cast<long long>(a->max_blocks) * a->block_size > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (bad_ptr(a->cached, 4) || bad_ptr(a->fresh, 4) || bad_ptr(a->block_table, 4) || bad_ptr(a->cu_tokens, 4) ||
+      bad_ptr(a->kv_len, 4) || bad_ptr(a->counts, 4) || !aligned(a->free_pages, 4) || !aligned(a->free_head, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (a->n_free > 0 && a->free_pages == nullptr) return DSA_ERR_INVALID_ARG;
+  if (a->T > 0 && (bad_ptr(a->seq_of_token, 4) || bad_ptr(a->pos, 4) || bad_ptr(a->slot, 8))) return DSA_ERR_INVALID_ARG;
+  // inputs that are read while these outputs are written
+  const int32_t* outs[] = {a->cu_tokens, a->kv_len, a->counts};
+  const size_t lens[] = {static_cast<size_t>(a->B) + 1, static_cast<size_t>(a->B), 3};
+  auto meets = [](const int32_t* x, size_t n, const int32_t* y, size_t m) { return x && x < y + m && y < x + n; };
+  for (int i = 0; i < 3; ++i)
+    if (meets(a->cached, a->B, outs[i], lens[i]) || meets(a->fresh, a->B, outs[i], lens[i]) ||
+        meets(a->free_head, 1, outs[i], lens[i]))
+      return DSA_ERR_INVALID_ARG;
+  return launch_step_maps(*a, static_cast<cudaStream_t>(stream));
+}
+
+static int check_latent_attn(const dsa_latent_attn_args* a) {
+  if (!a || a->T < 0) return DSA_ERR_INVALID_ARG;
+  if (a->T == 0) return DSA_OK;
+  if (a->B < 1 || a->H < 1 || a->max_L < 1 || a->cache_rows < 1 || !(a->scale > 0.f) || a->scale > FLT_MAX)
+    return DSA_ERR_INVALID_ARG;
+  if (a->cu_tokens == nullptr && (a->n_q < 1 || static_cast<long long>(a->B) * a->n_q != a->T)) return DSA_ERR_INVALID_ARG;
+  if (a->B > 65535 || a->H > 1024 || a->cache_rows > INT32_MAX ||
+      static_cast<long long>(a->T) * a->H >= INT32_MAX - 127)
+    return DSA_ERR_UNSUPPORTED;
+  if (bad_ptr(a->q, 16) || bad_ptr(a->kv, 16) || bad_ptr(a->out, 16) || bad_ptr(a->kv_len, 4)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(a->lse, 4) || !aligned(a->sink, 4) || !aligned(a->cu_tokens, 4)) return DSA_ERR_INVALID_ARG;
+  if (a->block_table) {
+    if (!aligned(a->block_table, 4) || a->block_size < 1) return DSA_ERR_INVALID_ARG;
+    if (static_cast<long long>(a->max_blocks) * a->block_size != a->max_L) return DSA_ERR_INVALID_ARG;
+    if (a->block_size % 64 != 0 && a->block_size != 8 && a->block_size != 16 && a->block_size != 32)
+      return DSA_ERR_UNSUPPORTED;
+  } else if (static_cast<long long>(a->B) * a->max_L > a->cache_rows) {
+    return DSA_ERR_INVALID_ARG;
+  }
+  return DSA_OK;
+}
+
+size_t dsa_latent_attn_workspace(const dsa_latent_attn_args* a) {
+  if (check_latent_attn(a) != DSA_OK || a->T == 0) return 0;
+  return latent_attn_workspace(*a);
+}
+
+int dsa_latent_attn(const dsa_latent_attn_args* a, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_latent_attn(a);
+  if (st != DSA_OK || a->T == 0) return st;
+  const size_t need = latent_attn_workspace(*a);
+  if (need > 0 && (ws == nullptr || !aligned(ws, 256) || ws_bytes < need)) return DSA_ERR_WORKSPACE;
+  return launch_latent_attn(*a, ws, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_add_rmsnorm(const dsa_add_rmsnorm_args* a, void* stream) {
+  if (!a || a->T < 0 || !(a->eps >= 0.f) || a->eps > FLT_MAX || (a->x_fp16 & ~1) || (a->residual_fp32 & ~1))
+    return DSA_ERR_INVALID_ARG;
+  if (a->D < 1 || a->D > 32768) return DSA_ERR_UNSUPPORTED;
+  if (a->T == 0) return DSA_OK;
+  const size_t r = a->residual_fp32 ? 4 : 2;
+  if (bad_ptr(a->x, 2) || bad_ptr(a->gamma, 4) || a->x_stride < a->D) return DSA_ERR_INVALID_ARG;
+  if ((a->residual == nullptr) != (a->residual_out == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (a->residual) {
+    if (!aligned(a->residual, r) || !aligned(a->residual_out, r) || a->residual_stride < a->D ||
+        a->residual_out_stride < a->D)
+      return DSA_ERR_INVALID_ARG;
+    if (a->residual == a->residual_out && a->residual_stride != a->residual_out_stride) return DSA_ERR_INVALID_ARG;
+  }
+  if ((a->codes == nullptr) != (a->code_scale == nullptr) || !aligned(a->code_scale, 4) || !aligned(a->y, 2))
+    return DSA_ERR_INVALID_ARG;
+  if (!a->y && !a->codes) return DSA_ERR_INVALID_ARG;
+  return launch_add_rmsnorm(*a, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

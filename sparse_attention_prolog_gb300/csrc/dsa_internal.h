@@ -79,5 +79,9 @@ int launch_kv4_write(const dsa_kv4_write_args& a, cudaStream_t s);
 int launch_kv4_read(const dsa_kv4_read_args& a, cudaStream_t s);
 size_t attn_kv4_workspace(const dsa_attn_kv4_args& a);
 int launch_attn_kv4(const dsa_attn_kv4_args& a, void* ws, cudaStream_t s);
+int launch_step_maps(const dsa_step_maps_args& a, cudaStream_t s);
+int launch_add_rmsnorm(const dsa_add_rmsnorm_args& a, cudaStream_t s);
+size_t latent_attn_workspace(const dsa_latent_attn_args& a);
+int launch_latent_attn(const dsa_latent_attn_args& a, void* ws, cudaStream_t s);
 
 }  // namespace dsa

@@ -1,0 +1,264 @@
+// Residual addition and RMS norm with a bf16 and/or int8 output
+// (dsa_add_rmsnorm).  RMSNorm as in the MLA Prolog, the quantiser as in
+// [V4-TileLang §Activation Quantization] steps 1-3.
+//
+// A row is read once, kept in registers in fp32 (as h, then as z), and written
+// once; between lie two reductions over the row, of h^2 and of max |z|.  So the
+// kernel moves what it cannot do without, and is bound by HBM when there are
+// rows enough and by the launch, one trip to memory and the two reductions when
+// there are few.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include "dsa_internal.h"
+#include "dsa_ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kMaxChunks = 4;  // 8-element chunks of a row that a thread holds
+
+struct NormParams {
+  dsa_add_rmsnorm_args a;
+  int row_threads;  // threads of a row: a warp, or the whole CTA
+  float inv_d;
+};
+
+__device__ __forceinline__ float max_abs_nan(float m, float v) {
+  // as whole numbers: |v| in order, and a NaN above every number
+  return __uint_as_float(max(__float_as_uint(m), __float_as_uint(v) & 0x7fffffffu));
+}
+
+// Sum or maximum over the threads of a row; `part` holds a value per warp.
+template <bool kMax>
+__device__ __forceinline__ float row_reduce(float v, bool one_warp, float* part) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = kMax ? max_abs_nan(v, u) : v + u;
+  }
+  if (one_warp) return v;
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) part[warp] = v;
+  __syncthreads();
+  v = lane < warps ? part[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = kMax ? max_abs_nan(v, u) : v + u;
+  }
+  return v;
+}
+
+template <bool kFp16>
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+  if (kFp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The code of z: rint of the fp32 quotient, in [-127, 127].
+__device__ __forceinline__ uint32_t code_of(float z, float s) {
+  return static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(z / s, -127.f), 127.f))) & 0xffu;
+}
+
+// kVec: D and every row allow vectors of 8 elements; else element by element,
+// neighbouring threads at neighbouring elements.
+template <int kChunks, bool kVec, bool kFp16, bool kRes32>
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
+  __shared__ float part[2][32];
+  const dsa_add_rmsnorm_args& a = P.a;
+  const int n = P.row_threads;
+  const bool one_warp = n == 32;
+  const int me = one_warp ? threadIdx.x & 31 : threadIdx.x;
+  const long long row = one_warp ? static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  griddep_wait();
+  if (row >= a.T) return;  // whole warps, and only where a warp has a row of its own
+  const bool res = a.residual != nullptr;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.x_stride;
+  const uint8_t* rin = static_cast<const uint8_t*>(a.residual) + row * a.residual_stride * (kRes32 ? 4 : 2);
+  uint8_t* rout = static_cast<uint8_t*>(a.residual_out) + row * a.residual_out_stride * (kRes32 ? 4 : 2);
+
+  float h[kChunks][8];
+  if (kVec) {
+    uint4 xv[kChunks];
+    float4 r0[kChunks], r1[kChunks];  // 8 fp32, or 8 bf16 in r0
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int e = (me + k * n) * 8;
+      const bool on = e < a.D;
+      xv[k] = on ? __ldcs(reinterpret_cast<const uint4*>(x + e)) : make_uint4(0, 0, 0, 0);
+      r0[k] = r1[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (res && on) {
+        r0[k] = __ldcs(reinterpret_cast<const float4*>(rin + static_cast<size_t>(e) * (kRes32 ? 4 : 2)));
+        if (kRes32) r1[k] = __ldcs(reinterpret_cast<const float4*>(rin + static_cast<size_t>(e) * 4 + 16));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int e = (me + k * n) * 8;
+      const uint32_t w[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = pair_of<kFp16>(w[i]);
+        h[k][2 * i] = f.x;
+        h[k][2 * i + 1] = f.y;
+      }
+      if (!res) continue;
+      const float b[8] = {r0[k].x, r0[k].y, r0[k].z, r0[k].w, r1[k].x, r1[k].y, r1[k].z, r1[k].w};
+      if (kRes32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] += b[i];
+        if (e < a.D) {
+          float4* o = reinterpret_cast<float4*>(rout + static_cast<size_t>(e) * 4);
+          o[0] = make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
+          o[1] = make_float4(h[k][4], h[k][5], h[k][6], h[k][7]);
+        }
+      } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = pair_of<false>(__float_as_uint(b[i]));
+          o[i] = bf16_pair(h[k][2 * i] + f.x, h[k][2 * i + 1] + f.y);
+          const float2 s = pair_of<false>(o[i]);
+          h[k][2 * i] = s.x;
+          h[k][2 * i + 1] = s.y;
+        }
+        if (e < a.D) *reinterpret_cast<uint4*>(rout + static_cast<size_t>(e) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = me + (k * 8 + i) * n;
+        float v = 0.f;
+        if (e < a.D) {
+          v = kFp16 ? __half2float(__ushort_as_half(x[e])) : __uint_as_float(static_cast<uint32_t>(x[e]) << 16);
+          if (res && kRes32) {
+            v += reinterpret_cast<const float*>(rin)[e];
+            reinterpret_cast<float*>(rout)[e] = v;
+          } else if (res) {
+            const __nv_bfloat16 s =
+                __float2bfloat16_rn(v + __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rin)[e]));
+            reinterpret_cast<__nv_bfloat16*>(rout)[e] = s;
+            v = __bfloat162float(s);
+          }
+        }
+        h[k][i] = v;
+      }
+  }
+
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fmaf(h[k][i], h[k][i], sum);
+  sum = row_reduce<false>(sum, one_warp, part[0]);
+  const float r = 1.f / sqrtf(sum * P.inv_d + a.eps);
+
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    if (kVec) {
+      const int e = (me + k * n) * 8;
+      if (e >= a.D) continue;
+      const float4 g0 = __ldg(reinterpret_cast<const float4*>(a.gamma + e));
+      const float4 g1 = __ldg(reinterpret_cast<const float4*>(a.gamma + e) + 1);
+      const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * r * g[i];
+      if (a.y)
+        *reinterpret_cast<uint4*>(a.y + row * a.D + e) =
+            make_uint4(bf16_pair(h[k][0], h[k][1]), bf16_pair(h[k][2], h[k][3]), bf16_pair(h[k][4], h[k][5]),
+                       bf16_pair(h[k][6], h[k][7]));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max_abs_nan(top, h[k][i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = me + (k * 8 + i) * n;
+        if (e >= a.D) continue;
+        h[k][i] = h[k][i] * r * __ldg(a.gamma + e);
+        if (a.y) reinterpret_cast<__nv_bfloat16*>(a.y)[row * a.D + e] = __float2bfloat16_rn(h[k][i]);
+        top = max_abs_nan(top, h[k][i]);
+      }
+    }
+  }
+  if (a.codes == nullptr) return;
+  top = row_reduce<true>(top, one_warp, part[1]);
+  float s = top / 127.f;
+  const bool fine = s > 0.f && s < __int_as_float(0x7f800000);
+  if (a.round_scale && fine) {
+    int e;
+    const float m = frexpf(s, &e);  // s = m * 2^e, m in [0.5, 1)
+    s = ldexpf(1.f, m == 0.5f ? e - 1 : e);
+  }
+  if (me == 0) a.code_scale[row] = s;
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    if (kVec) {
+      const int e = (me + k * n) * 8;
+      if (e >= a.D) continue;
+      uint2 o = make_uint2(0u, 0u);
+      if (fine) {
+        o.x = code_of(h[k][0], s) | code_of(h[k][1], s) << 8 | code_of(h[k][2], s) << 16 | code_of(h[k][3], s) << 24;
+        o.y = code_of(h[k][4], s) | code_of(h[k][5], s) << 8 | code_of(h[k][6], s) << 16 | code_of(h[k][7], s) << 24;
+      }
+      *reinterpret_cast<uint2*>(a.codes + row * a.D + e) = o;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = me + (k * 8 + i) * n;
+        if (e < a.D) a.codes[row * a.D + e] = fine ? static_cast<int8_t>(code_of(h[k][i], s)) : 0;
+      }
+    }
+  }
+}
+
+template <int kChunks, bool kVec>
+auto pick(bool fp16, bool res32) {
+  return fp16 ? (res32 ? add_rmsnorm_kernel<kChunks, kVec, true, true> : add_rmsnorm_kernel<kChunks, kVec, true, false>)
+              : (res32 ? add_rmsnorm_kernel<kChunks, kVec, false, true> : add_rmsnorm_kernel<kChunks, kVec, false, false>);
+}
+
+}  // namespace
+
+int launch_add_rmsnorm(const dsa_add_rmsnorm_args& a, cudaStream_t s) {
+  const size_t rsize = a.residual_fp32 ? 4 : 2;
+  const bool vec = a.D % 8 == 0 && a.x_stride % 8 == 0 && aligned(a.x, 16) && aligned(a.gamma, 16) &&
+                   aligned(a.residual, 16) && aligned(a.residual_out, 16) && a.residual_stride * rsize % 16 == 0 &&
+                   a.residual_out_stride * rsize % 16 == 0 && aligned(a.y, 16) && aligned(a.codes, 8);
+  const int chunks = (a.D + 7) / 8;
+  // Threads of a row: one chunk each for rows of up to 1024 chunks, so that a row
+  // is one trip to memory; a warp's worth of row (256 elements) is left to one
+  // warp, eight rows to a CTA.
+  int per = 1;
+  while ((chunks + per - 1) / per > 1024) per *= 2;
+  const int n = ((chunks + per - 1) / per + 31) / 32 * 32;
+  const int rows = n == 32 ? 8 : 1;
+  NormParams P{a, n, 1.f / static_cast<float>(a.D)};
+  auto kern = vec ? (per == 1 ? pick<1, true>(a.x_fp16, a.residual_fp32)
+                     : per == 2 ? pick<2, true>(a.x_fp16, a.residual_fp32)
+                                : pick<4, true>(a.x_fp16, a.residual_fp32))
+                  : (per == 1 ? pick<1, false>(a.x_fp16, a.residual_fp32)
+                     : per == 2 ? pick<2, false>(a.x_fp16, a.residual_fp32)
+                                : pick<4, false>(a.x_fp16, a.residual_fp32));
+  static_assert(kMaxChunks * 8 * 1024 >= 32768, "the longest row fits a CTA");
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.T) + rows - 1) / rows));
+  cfg.blockDim = dim3(n * rows);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, P));
+}
+
+}  // namespace dsa

@@ -1,0 +1,215 @@
+// Step maps: the block table and the token maps of a step from the lengths of
+// its requests (dsa_step_maps).
+//
+// Two running sums over the requests (tokens, new pages) decide everything: a
+// token finds its request, and a new page its own, by a binary search of them.
+// B is at most 8192, so every CTA forms both sums itself in shared memory (one
+// read of 8 B bytes, from L2 after the first CTA) and then fills its own stretch
+// of the tables; nothing passes between CTAs, and no page entry that this step
+// writes is read (a new page is looked up in the free list).  What bounds it is
+// the launch and three dependent trips to memory: lengths, page entries, stores.
+#include <cuda_runtime.h>
+#include "dsa_internal.h"
+#include "dsa_ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kMaxRequests = 8192;
+
+struct Sums {  // of a request's tokens and new pages
+  long long tok, page;
+};
+
+__device__ __forceinline__ Sums warp_inclusive(Sums v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, v.tok, o), p = __shfl_up_sync(0xffffffffu, v.page, o);
+    if (lane >= o) {
+      v.tok += t;
+      v.page += p;
+    }
+  }
+  return v;
+}
+
+// The last i of [0, n) with run[i] <= v (run[0] = 0 <= v): of the requests that
+// begin at the same count, the one that is not empty.
+__device__ __forceinline__ int owner(const int* run, int n, int v) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (run[mid] <= v) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(1024) step_maps_kernel(const dsa_step_maps_args P, uint32_t* err) {
+  extern __shared__ int run[];  // tokens before request b [B + 1], then pages before it [B + 1]
+  __shared__ Sums warp_sum[32];
+  __shared__ int cut_sh;       // the first request that is not served
+  __shared__ int total_sh[2];  // tokens and pages of those that are
+  int* run_tok = run;
+  int* run_page = run + P.B + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
+  if (tid == 0) cut_sh = P.B;
+  griddep_wait();
+  const int head = P.free_head == nullptr ? 0 : __ldg(P.free_head);
+  const long long avail = head < 0 ? -1 : static_cast<long long>(P.n_free) - head;
+  const long long most = static_cast<long long>(P.max_blocks) * P.block_size;
+  const int each = (P.B + threads - 1) / threads;  // consecutive requests of a thread
+  const int b0 = min(P.B, tid * each), b1 = min(P.B, b0 + each);
+
+  auto request = [&](int b, int& c, int& f, int& old, int& last) {  // false: its lengths cannot be served
+    c = __ldg(P.cached + b);
+    f = __ldg(P.fresh + b);
+    old = last = 0;
+    if (c < 0 || f < 0 || static_cast<long long>(c) + f > most) return false;
+    old = c / P.block_size + (c % P.block_size != 0);
+    last = (c + f) / P.block_size + ((c + f) % P.block_size != 0);
+    return true;
+  };
+
+  Sums own{0, 0};
+  int first_bad = P.B;
+  for (int b = b0; b < b1; ++b) {
+    int c, f, old, last;
+    if (request(b, c, f, old, last)) {
+      own.tok += f;
+      own.page += last - old;
+    } else {
+      first_bad = min(first_bad, b);
+    }
+  }
+  Sums inc = warp_inclusive(own, lane);
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    Sums w = lane < (threads >> 5) ? warp_sum[lane] : Sums{0, 0};
+    w = warp_inclusive(w, lane);
+    warp_sum[lane] = w;
+  }
+  __syncthreads();
+  Sums at{inc.tok - own.tok, inc.page - own.page};  // before request b0
+  if (warp > 0) {
+    at.tok += warp_sum[warp - 1].tok;
+    at.page += warp_sum[warp - 1].page;
+  }
+  {  // the first request whose running sums pass a limit
+    Sums s = at;
+    for (int b = b0; b < b1 && b < first_bad; ++b) {
+      int c, f, old, last;
+      request(b, c, f, old, last);
+      s.tok += f;
+      s.page += last - old;
+      if (s.tok > P.T || s.page > avail) first_bad = b;
+    }
+  }
+  if (first_bad < P.B) atomicMin(&cut_sh, first_bad);
+  __syncthreads();
+  const int cut = cut_sh;
+  if (tid == 0 && cut == P.B) {
+    const Sums all = warp_sum[31];
+    total_sh[0] = static_cast<int>(all.tok);
+    total_sh[1] = static_cast<int>(all.page);
+  }
+  if (b0 <= cut && cut < b1) {  // sums before the cut
+    Sums s = at;
+    for (int b = b0; b < cut; ++b) {
+      int c, f, old, last;
+      request(b, c, f, old, last);
+      s.tok += f;
+      s.page += last - old;
+    }
+    total_sh[0] = static_cast<int>(s.tok);
+    total_sh[1] = static_cast<int>(s.page);
+  }
+  __syncthreads();
+  const int tokens = total_sh[0], pages = total_sh[1];
+  const bool writer = blockIdx.x == 0;
+  for (int b = b0; b < b1; ++b) {
+    int c, f, old, last;
+    request(b, c, f, old, last);
+    const bool on = b < cut;
+    run_tok[b] = on ? static_cast<int>(at.tok) : tokens;
+    run_page[b] = on ? static_cast<int>(at.page) : pages;
+    if (on) {
+      at.tok += f;
+      at.page += last - old;
+    }
+    if (writer) {
+      P.cu_tokens[b] = run_tok[b];
+      P.kv_len[b] = on ? c + f : c;
+    }
+  }
+  if (tid == 0) {
+    run_tok[P.B] = tokens;
+    run_page[P.B] = pages;
+    if (writer) {
+      P.cu_tokens[P.B] = tokens;
+      P.counts[0] = tokens;
+      P.counts[1] = head + pages;
+      P.counts[2] = cut;
+      if (cut < P.B) atomicOr(err, kErrBadIndex);
+    }
+  }
+  __syncthreads();
+
+  const int stride = gridDim.x * threads;
+  for (int p = blockIdx.x * threads + tid; p < pages; p += stride) {
+    const int b = owner(run_page, P.B, p);
+    const int c = __ldg(P.cached + b);
+    const int j = c / P.block_size + (c % P.block_size != 0) + p - run_page[b];
+    P.block_table[static_cast<size_t>(b) * P.max_blocks + j] = __ldg(P.free_pages + head + p);
+  }
+  const int pad_seq = tokens > 0 ? owner(run_tok, P.B, tokens - 1) : 0;
+  for (int t = blockIdx.x * threads + tid; t < P.T; t += stride) {
+    int seq = pad_seq, pos = 0;
+    int64_t slot = -1;
+    if (t < tokens) {
+      seq = owner(run_tok, P.B, t);
+      const int c = __ldg(P.cached + seq);
+      pos = c + t - run_tok[seq];
+      const int j = pos / P.block_size, old = c / P.block_size + (c % P.block_size != 0);
+      const int page = j < old ? P.block_table[static_cast<size_t>(seq) * P.max_blocks + j]
+                               : __ldg(P.free_pages + head + run_page[seq] + j - old);
+      if (page >= 0)
+        slot = static_cast<int64_t>(page) * P.block_size + pos % P.block_size;
+      else
+        atomicOr(err, kErrBadIndex);
+    }
+    P.seq_of_token[t] = seq;
+    P.pos[t] = pos;
+    P.slot[t] = slot;
+  }
+}
+
+}  // namespace
+
+int launch_step_maps(const dsa_step_maps_args& a, cudaStream_t s) {
+  uint32_t* err = error_word();
+  if (!err) return DSA_ERR_CUDA;
+  const int threads = a.B <= 256 ? 256 : 1024;
+  // every CTA forms the sums again, so none is started for less than two tokens a thread
+  const long long want = (static_cast<long long>(a.T) + 2 * threads - 1) / (2 * threads);
+  const long long most = 2ll * sm_count() * (1024 / threads);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = 2 * (static_cast<size_t>(a.B) + 1) * sizeof(int);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static_assert(2 * (kMaxRequests + 1) * sizeof(int) <= 96 * 1024, "running sums");
+  if (cfg.dynamicSmemBytes > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(step_maps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(cfg.dynamicSmemBytes));
+    if (e != cudaSuccess) return DSA_ERR_CUDA;
+  }
+  return cuda_status(cudaLaunchKernelEx(&cfg, step_maps_kernel, a, err));
+}
+
+}  // namespace dsa
