@@ -661,9 +661,10 @@ int dsa_step_maps(const dsa_step_maps_args* args, void* stream);
  * max_blocks], max_L = max_blocks * block_size; kv_len int32 [B], with the new
  * tokens' rows (which are in the cache); out bf16 [T, H, 512]; lse fp32 [T, H]
  * or NULL; sink fp32 [H] or NULL, entries finite or -inf.
- * Rows at or past kv_len[b] may hold anything.  So may the rows that a token may
- * not see yet, unless one of its sequence's newer tokens is attended by the same
- * 128 rows of q (H no multiple of 128): those have to be finite.
+ * Rows at or past kv_len[b] may hold anything.  A sequence's own newest rows,
+ * which its older new tokens may not see, have to be finite: tokens are
+ * attended in blocks of up to 256 rows of q, and a value that is not finite may
+ * reach every token of a block of which one sees it.
  * A page entry that is negative or names a page past cache_rows, a kv_len
  * outside [0, max_L] (clamped) and cu_tokens that decrease or leave [0, T]
  * (clamped) are recorded as DSA_ERR_DEVICE_DATA; rows of such a page read as

@@ -3,26 +3,41 @@
 // 3-8 with every visible row in place of a selection.
 //
 // The (token, head) rows of a sequence lie behind one another in q and out: they
-// are cut into blocks of 128 rows, whatever H is.  The work is the list of
-// (block, tile of 64 cache rows), block by block; persistent clusters of two
-// CTAs take an equal stretch of it each, so that sequences of any lengths load
-// all SMs evenly.  A block that lies in one stretch is finished there; the parts
-// of one that several clusters share are merged by latent_merge_kernel.
+// are cut into blocks of 128 NP rows, whatever H is.  The work is the list of
+// (block, tile of 128 cache rows), block by block; persistent clusters take an
+// equal stretch of it each, so that sequences of any lengths load all SMs evenly.
+// A block that lies in one stretch is finished there; the parts of one that
+// several clusters share are merged by latent_merge_kernel.
 //
-//   CTA 0  q [128 x 576] in tensor memory, K tiles in shared memory (TMA, one
-//          64-dim atom a box, a ring of 9 slots of 3 atoms), S = q . K^T in three
-//          buffers.  Two softmax warpgroups take the tiles in turn: the running
-//          maximum passes between them as soon as a tile's is known, so one's
-//          exponentials overlap the other's loads; P (bf16) goes straight into
-//          CTA 1's shared memory with st.async, with the factor by which the
-//          maximum's growth scales what is there.
-//   CTA 1  O [128 x 512] fp32 fills its tensor memory; V tiles (the first 512 dims
-//          of the same rows, from L2) in a ring of 6 slots of 4 atoms; O += P . V.
-//          Eight warps rescale O where a maximum grew by more than 2^8, and at a
-//          block's end write it.
+// An O accumulator [128 x 512] in fp32 fills a CTA's tensor memory, so the two
+// products live in different CTAs, and P goes from one to the other:
+//
+//   QK  S = q . K^T (N = 128) and the softmax.  q's latent part is the A operand in
+//       tensor memory (256 columns), its rotary part in shared memory; S takes the
+//       other 256 columns, twice 128.  A thread has half of a row's columns: two
+//       warpgroups, which exchange their maxima, so that a tile's S is read at once
+//       and P follows with little delay.  P (bf16) is staged in shared memory and
+//       sent by bulk copies, 4 KB a warp, with the factors by which the maximum's
+//       growth scales what is in O.
+//   PV  O += P . V, V (the first 512 dims of the same rows, from L2) MN-major.
+//       Eight warps rescale O where a maximum grew by more than 2^8, and write it
+//       at a block's end.
+//
+// What bounds such a kernel first is not a unit but the single threads that feed them:
+// every instruction of theirs takes some five clocks, so their loops are unrolled over a
+// tile's units with slots and phases that need no arithmetic, barriers have constant
+// addresses, and a tile has few units.
+//
+// NP = 1: a cluster is one QK and one PV CTA.  NP = 2: two of each, for sequences
+// of more than 128 rows: the two QK CTAs run one MMA of M = 256 (cta_group::2), each
+// with its own 128 rows of q and half of the tile's K rows, the two PV CTAs likewise
+// with half of V's columns, so that an SM loads half of the bytes for the same
+// products.
 //
 // Rows that no token of a block sees (the end of the last tile: they may hold
 // anything) are cleared in V before the product; their S is not looked at.
+#include <algorithm>
+#include <atomic>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -33,21 +48,46 @@ namespace dsa {
 namespace {
 
 constexpr int kDqk = 576, kDv = 512;
-constexpr int kRows = 64;                  // cache rows of a tile
-constexpr int kAtomBytes = kRows * 128;    // 64 rows x 64 dims
-constexpr int kAtomsK = kDqk / 64, kAtomsV = kDv / 64;
-constexpr int kKAtoms = 3, kKSlots = 9, kKParts = kAtomsK / kKAtoms;  // atoms of a slot, slots, slots of a tile
-constexpr int kVAtoms = 4, kVSlots = 6, kVParts = kAtomsV / kVAtoms;
-constexpr int kSBufs = 3;
-constexpr int kPBytesSlot = 128 * kRows * 2;
-constexpr uint32_t kPTx = kPBytesSlot + 128 * 4;  // P and the rescale factors of a tile
-constexpr uint32_t kTmemS = 288;                  // CTA 0: q in columns [0, 288), then the S buffers
-static_assert(kTmemS + kSBufs * kRows <= 512, "tensor memory of CTA 0");
-constexpr int kThreads = 384;  // 8 softmax / output warps, a loader, an MMA issuer, a relay, one idle
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kRelayWarp = 10;
+constexpr int kTile = 128;                       // cache rows of a tile
+constexpr int kAtomsK = kDqk / 64;               // atoms: 64 dims, 128 bytes a row
+constexpr int kHalfBytes = 128 * 128;            // 64 columns of a P tile
+constexpr uint32_t kTmemS = 256;                 // QK: q's latent part in columns [0, 256), then two S buffers
+constexpr int kThreads = 384;                    // 8 softmax / output warps, a loader, an MMA issuer, two for news
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kNewsWarp = 11;
 // A cluster takes at least this many tiles: splitting further costs more in the
 // merge than it saves.
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 2;
+constexpr int kMaxClusters = 256;
+
+// The rings: slots of a unit, [atoms][rows][128 bytes].  K: one atom (NP = 2: three) of all
+// rows of a CTA's part of the tile; V: 64 rows, the columns of a CTA's part of one N = 256
+// product.  A ring has the units of NP tiles: a slot's number follows from the unit's.
+template <int NP>
+struct Ring {
+  static constexpr int kKRows = kTile / NP, kKAtoms = NP == 1 ? 1 : 3, kKUnits = kAtomsK / kKAtoms;
+  static constexpr int kKBytes = kKAtoms * kKRows * 128, kKSlots = kKUnits * NP;
+  static constexpr int kKLoaders = NP == 1 ? 3 : 1;  // warps that load K, every so manieth unit each
+  static constexpr int kVRows = 64, kVAtoms = 4 / NP, kVUnits = 4;
+  static constexpr int kVBytes = kVAtoms * kVRows * 128, kVSlots = kVUnits * NP;
+};
+constexpr int kMaxKSlots = 9, kMaxVSlots = 8;
+constexpr int kPSlots = 5, kStages = 3;  // slots of half a tile's P, in the PV CTA and where it is staged
+constexpr int kQRounds = 3, kQAtoms = 3; // a block's q comes through the staging slots
+static_assert(kQAtoms == kStages && kQRounds * kQAtoms == kAtomsK, "q's way");
+
+// Shared memory of a QK CTA: K ring, staging slots of P, q's rotary part, OwnQk.  Of a PV
+// CTA: V ring, P slots, the rescale factors.  Behind them, in both, Shared.
+struct OwnQk {
+  float top[2][2][128];      // [tile parity][column half]: a row's maximum in a tile
+  float alpha[kStages][128]; // rescale factors on their way out
+  float2 final_ml[2][128];   // (maximum, sum) of each column half at a block's end
+};
+constexpr int kOffStage = 147456, kOffQrope = kOffStage + kStages * kHalfBytes, kOffOwn = kOffQrope + kHalfBytes;
+constexpr int kOffP = 131072, kOffAlpha = kOffP + kPSlots * kHalfBytes;
+static_assert(Ring<1>::kKSlots * Ring<1>::kKBytes == kOffStage && Ring<2>::kKSlots * Ring<2>::kKBytes == kOffStage, "K ring");
+static_assert(Ring<1>::kVSlots * Ring<1>::kVBytes == kOffP && Ring<2>::kVSlots * Ring<2>::kVBytes == kOffP, "V ring");
+constexpr int kOffShared = kOffOwn + sizeof(OwnQk);
+static_assert(kOffAlpha + kPSlots * 512 <= kOffShared && kOffShared % 16 == 0, "shared memory of a PV CTA");
 
 struct LatentParams {
   int T, B, n_q, H, max_L;
@@ -56,45 +96,42 @@ struct LatentParams {
   int64_t cache_rows;
   const int32_t* block_table;
   int block_size, max_blocks;
-  int box_rows;  // rows of a TMA box: 64, or a smaller page
+  int k_box, v_box;  // rows of a TMA box of K and of V
   const int32_t* cu;
   const int32_t* kv_len;
   __nv_bfloat16* out;
   float* lse;
   const float* sink;
   int clusters;
-  float* part_o;    // [2 clusters][128][512]: a cluster's first and last part
-  float2* part_ml;  // [2 clusters][128]: (maximum, sum) in log2 units
+  float* part_o;    // [2 clusters][64][128 NP][8]: the first and the last part of a stretch, 8 columns of all rows together
+  float2* part_ml;  // [2 clusters][128 NP]: (maximum, sum) in log2 units
+  int block_rows;   // 128 NP
   int4* desc;       // [clusters]: first row, rows, parts of the block that begins at the end of a stretch
   uint32_t* err;
 };
 
 struct __align__(8) Bars {
-  uint64_t kfull[kKSlots], kempty[kKSlots];
-  uint64_t sfull[kSBufs], sempty[kSBufs];
-  uint64_t pfree[2];              // CTA 0: a P slot of CTA 1 is free
-  uint64_t mready[2][4];          // the maximum after a group's tile, per warp
-  uint64_t qfull;                 // a block's q is in tensor memory
-  uint64_t ffree;                 // CTA 0: CTA 1 has read the final (m, l)
-  uint64_t vfull[kVSlots], vempty[kVSlots];
-  uint64_t pfull[2], pcons[2];    // CTA 1: P slots
-  uint64_t oready[2];             // O is scaled for the tile
-  uint64_t odone[2];              // a tile's product is in O (even and odd tiles: a warp may look a tile late)
-  uint64_t ffull;                 // CTA 1: the final (m, l) lie in CTA 0
+  // of the barriers that an MMA waits for, those of the pair's first CTA count for both; full ones tell that a
+  // CTA's own copies are there
+  uint64_t kfull[kMaxKSlots], kempty[kMaxKSlots];
+  uint64_t kpeer[kMaxKSlots], vpeer[kMaxVSlots];  // the second CTA's unit of K or V is there
+  uint64_t sfull[2], sempty[2];
+  uint64_t pfree[kPSlots];        // QK: a P slot of the PV CTA is free
+  uint64_t landed[kStages];       // QK: what a staging slot held has arrived there
+  uint64_t qload, qread;          // QK: three atoms of q are in the staging slots; every warp has read them
+  uint64_t mready[4];             // QK: both halves' maxima are known, per pair of warps
+  uint64_t qfull;                 // a block's q is in place
+  uint64_t ffree;                 // QK: the final (m, l) have been read
+  uint64_t vfull[kMaxVSlots], vempty[kMaxVSlots];
+  uint64_t vclean[kMaxVSlots];    // PV: rows that nothing sees are cleared in a unit
+  uint64_t pfull[kPSlots], pcons[kPSlots];  // PV: P slots
+  uint64_t phalf[2];              // PV: the second half of P has arrived in every CTA
+  uint64_t oready[2];             // PV: O is scaled for the tile, whose first half has arrived
+  uint64_t odone[2];              // PV: a tile's product is in O (even and odd tiles: a warp may look a tile late)
+  uint64_t ffull;                 // PV: the final (m, l) lie in the QK CTA
   uint64_t drain;                 // the MMA thread's last commit
 };
-
-// Shared memory: the ring (CTA 0: K, then OwnA; CTA 1: V, then two P slots), then
-// what both CTAs have.
-constexpr int kRingBytes = kVSlots * kVAtoms * kAtomBytes + 2 * kPBytesSlot;
-struct OwnA {
-  float m[2][128];          // running maximum after a softmax group's latest tile
-  float2 final_ml[2][128];  // (maximum, sum) of each group at a block's end
-};
-constexpr int kOwnA = kKSlots * kKAtoms * kAtomBytes;
-static_assert(kOwnA + sizeof(OwnA) <= kRingBytes, "ring of CTA 0");
 struct __align__(16) Shared {
-  float alpha[2][128];  // CTA 1
   Bars bars;
   long long scan[kThreads / 32];
   long long start_off;
@@ -102,19 +139,22 @@ struct __align__(16) Shared {
   uint32_t tmem;
   int abort_flag;
 };
-constexpr size_t kSmemBytes = 1024 + kRingBytes + sizeof(Shared);  // 1024: to align the ring
+constexpr size_t kSmemBytes = kOffShared + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 
 struct Piece {
-  int row0, rows;  // of q and out
-  int b, len, first_vis;  // sequence, its rows, rows that the block's first row's token sees
-  int in_tok;      // rows of the first token of the sequence before the block: block * 128
-  int vis;         // rows that the block's last token sees
+  int row0, rows;  // of q and out: the block's
+  int b, len;      // sequence, its cache rows
+  int first_vis;   // cache rows that the sequence's first token sees
+  int in_seq;      // rows of the sequence before the block
+  int vis;         // cache rows that the block's last token sees
   int t0, t1;      // tiles
   bool begins, ends;
 };
 
+template <int NP>
 struct Walker {
+  static constexpr int kBlock = 128 * NP;
   long long left;
   int b, blk, off;
   int n, c0, len, nt, nb;
@@ -128,8 +168,8 @@ struct Walker {
       n = P.n_q;
     }
     len = min(max(__ldg(P.kv_len + b), 0), P.max_L);
-    nt = max(1, (len + kRows - 1) / kRows);
-    nb = (n * P.H + 127) / 128;
+    nt = max(1, (len - 1) / kTile + 1);
+    nb = (n * P.H + kBlock - 1) / kBlock;
   }
   __device__ __forceinline__ void start(const LatentParams& P, int b0, long long at, long long count) {
     left = count;
@@ -150,14 +190,14 @@ struct Walker {
     }
     p.b = b;
     p.len = len;
-    p.row0 = c0 * P.H + blk * 128;
-    p.rows = min(128, n * P.H - blk * 128);
-    p.in_tok = blk * 128;
+    p.row0 = c0 * P.H + blk * kBlock;
+    p.rows = min(kBlock, n * P.H - blk * kBlock);
+    p.in_seq = blk * kBlock;
     p.first_vis = len - n + 1;
-    p.vis = max(0, p.first_vis + (blk * 128 + p.rows - 1) / P.H);
+    p.vis = max(0, p.first_vis + (blk * kBlock + p.rows - 1) / P.H);
     const int stop = static_cast<int>(min(static_cast<long long>(nt), off + left));
     p.t0 = off;
-    p.t1 = max(off, min(stop, (p.vis + kRows - 1) / kRows));
+    p.t1 = max(off, min(stop, (p.vis + kTile - 1) / kTile));
     p.begins = off == 0;
     p.ends = stop == nt;
     left -= stop - off;
@@ -170,18 +210,25 @@ struct Walker {
   }
 };
 
-// Row of the cache at which rows s .. s + box_rows of a sequence lie; cache_rows
-// (past the map: read as zeros) where there are none.
+// Row of the cache at which the rows from s on of a sequence lie (a box of them, in
+// one page); cache_rows (past the map: read as zeros) where there are none.
 __device__ __forceinline__ int box_row(const LatentParams& P, const Piece& p, int s, bool report) {
-  if (P.block_table == nullptr) return p.b * P.max_L + s;  // below cache_rows, so it fits
   const int none = static_cast<int>(P.cache_rows);
   if (s >= p.len) return none;
+  if (P.block_table == nullptr) return p.b * P.max_L + s;  // below cache_rows, so it fits
   const int page = __ldg(P.block_table + static_cast<size_t>(p.b) * P.max_blocks + s / P.block_size);
   if (page < 0 || (static_cast<int64_t>(page) + 1) * P.block_size > P.cache_rows) {
     if (report) atomicOr(P.err, kErrBadIndex);
     return none;
   }
   return page * P.block_size + s % P.block_size;
+}
+
+// One thread of the warp (the compiler knows it for one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t v;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(v));
+  return v != 0;
 }
 
 // mbar_wait_polling for a whole warp: all lanes get the same answer, so that what
@@ -204,6 +251,79 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
   }
 }
 
+// Arrives on a barrier of another CTA without ordering this thread's own writes before
+// it: for news of what copies and products did, which this thread learned from a
+// barrier.  (With .release.cluster an arrival takes 500 ns, and a thread that sends two
+// or four a tile holds the whole pipeline up: 2.1 us a tile with nothing else to do.)
+__device__ __forceinline__ void arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// The same for one thread.  (Not inlined: the loops of the threads that wait stay short.)
+template <bool kCluster>
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort_flag) {
+  return mbar_wait_polling<kCluster>(bar, parity, err, abort_flag);
+}
+template <bool kCluster>
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort_flag) {
+  if (kCluster ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)) return true;
+  return wait_on<kCluster>(bar, parity, err, abort_flag);
+}
+
+// Tiled load of the box [atoms][rows][64 dims] at an atom and a row.
+__device__ __forceinline__ void load_box(void* dst, const void* map, int atom, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(atom), "r"(smem_u32(bar))
+      : "memory");
+}
+// Shared memory of this CTA -> of another of the cluster, counted on its barrier.
+__device__ __forceinline__ void bulk_to_peer(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "r"(smem_u32(src)), "r"(bytes), "r"(bar) : "memory");
+}
+
+// Bytes that arrive with half i % 2 of tile i / 2: the first has the rescale factors.
+__device__ __forceinline__ uint32_t p_bytes(int i) { return kHalfBytes + (i % 2 == 0 ? 512 : 0); }
+
+template <int NP>
+__device__ __forceinline__ void alloc_tmem(uint32_t* result) {
+  if (NP == 1) {
+    tmem_alloc(result, 512);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(result)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int NP>
+__device__ __forceinline__ void free_tmem(uint32_t addr) {
+  if (NP == 1) tmem_dealloc(addr, 512);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(addr) : "memory");
+}
+// The pair's (or the CTA's) product with A in shared or in tensor memory.
+template <int NP>
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if (NP == 1) mma_ss(d, a, b, idesc, add);
+  else
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+template <int NP>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if (NP == 1) mma_ts(d, a, b, idesc, add);
+  else
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+// Arrives on the barrier, in every CTA of the pair, when the products issued so far are complete.
+template <int NP>
+__device__ __forceinline__ void commit(uint64_t* bar, uint16_t mask) {
+  if (NP == 1) mma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"(mask) : "memory");
+}
+
 __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
@@ -215,43 +335,64 @@ __device__ __forceinline__ void st_global_v8(float* p, const uint32_t* r) {
                : "memory");
 }
 
+template <int NP>
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_attn_kernel(const __grid_constant__ LatentParams P, const __grid_constant__ CUtensorMap kv_map) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* ring = smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u;
-  Shared& sh = *reinterpret_cast<Shared*>(ring + kRingBytes);
-  OwnA& own = *reinterpret_cast<OwnA*>(ring + kOwnA);
+    latent_attn_kernel(const __grid_constant__ LatentParams P, const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
+  using R = Ring<NP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0) {  // (swizzled tiles; it starts at a multiple, as the kernel has no other)
+    if (threadIdx.x == 0) atomicOr(P.err, kErrTimeout);
+    return;
+  }
+  Shared& sh = *reinterpret_cast<Shared*>(smem + kOffShared);
+  OwnQk& own = *reinterpret_cast<OwnQk*>(smem + kOffOwn);
   Bars& bars = sh.bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
-  const int cluster = blockIdx.x >> 1;
-  uint8_t* sP = ring + kVSlots * kVAtoms * kAtomBytes;  // CTA 1
+  const int role = rank / NP, side = rank % NP;  // 0: QK, 1: PV; which 128 rows of the block
+  const uint32_t first = role * NP;              // rank of the pair's first CTA, which issues its products
+  const int cluster = blockIdx.x / (2 * NP);
   volatile int* abort_v = &sh.abort_flag;
 
   if (tid == 0) {
-    for (int i = 0; i < kKSlots; ++i) { mbar_init(&bars.kfull[i], 1); mbar_init(&bars.kempty[i], 1); }
-    for (int i = 0; i < kSBufs; ++i) { mbar_init(&bars.sfull[i], 1); mbar_init(&bars.sempty[i], 4); }
-    for (int i = 0; i < kVSlots; ++i) { mbar_init(&bars.vfull[i], 1); mbar_init(&bars.vempty[i], 1); }
+    for (int i = 0; i < kMaxKSlots; ++i) {
+      mbar_init(&bars.kfull[i], 1);
+      mbar_init(&bars.kpeer[i], 1);
+      mbar_init(&bars.kempty[i], 1);
+    }
+    for (int i = 0; i < kMaxVSlots; ++i) {
+      mbar_init(&bars.vfull[i], 1);
+      mbar_init(&bars.vpeer[i], 1);
+      mbar_init(&bars.vempty[i], 1);
+      mbar_init(&bars.vclean[i], 8 * NP);
+    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.sfull[i], 1);
+      mbar_init(&bars.sempty[i], 8 * NP);
+      mbar_init(&bars.phalf[i], NP);
+      mbar_init(&bars.oready[i], 8 * NP);
+      mbar_init(&bars.odone[i], 1);
+    }
+    for (int i = 0; i < kPSlots; ++i) {
       mbar_init(&bars.pfree[i], 1);
       mbar_init(&bars.pfull[i], 1);
       mbar_init(&bars.pcons[i], 1);
-      mbar_init(&bars.oready[i], 8);
-      mbar_init(&bars.odone[i], 1);
-      for (int w = 0; w < 4; ++w) mbar_init(&bars.mready[i][w], 1);
     }
-    mbar_init(&bars.qfull, 8);
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars.landed[i], 1);
+    mbar_init(&bars.qload, 1);
+    mbar_init(&bars.qread, 8);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.mready[i], 2);
+    mbar_init(&bars.qfull, 8 * NP);
     mbar_init(&bars.ffree, 8);
     mbar_init(&bars.ffull, 8);
     mbar_init(&bars.drain, 1);
     sh.abort_flag = 0;
     fence_mbar_init();
-    if (rank == 1) {
-      mbar_arrive_expect_tx(&bars.pfull[0], kPTx);
-      mbar_arrive_expect_tx(&bars.pfull[1], kPTx);
-    }
+    if (role == 1)
+      for (int i = 0; i < kPSlots; ++i) mbar_arrive_expect_tx(&bars.pfull[i], p_bytes(i));
   }
-  if (warp == 0) tmem_alloc(&sh.tmem, 512);
+  if (warp == 0) alloc_tmem<NP>(&sh.tmem);
   griddep_wait();
 
   // ------------------------------------------------ this cluster's stretch
@@ -259,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b0 = min(P.B, tid * each), b1 = min(P.B, b0 + each);
   long long mine = 0;
   bool bad = false;
-  Walker w;
+  Walker<NP> w;
   for (w.b = b0; w.b < b1; ++w.b) {
     w.load(P);
     mine += static_cast<long long>(w.nb) * w.nt;
@@ -287,8 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += sh.scan[i];
   }
   const long long active = max(1ll, min(static_cast<long long>(P.clusters), total / kMinTiles));
-  const long long lo = cluster < active ? total * cluster / active : total;
-  const long long hi = cluster < active ? total * (cluster + 1) / active : total;
+  // stretch c begins at share c + min(c, rest)
+  const long long share = total / active, rest = total - share * active;
+  const long long lo = cluster < active ? share * cluster + min(static_cast<long long>(cluster), rest) : total;
+  const long long hi = cluster < active ? lo + share + (cluster < rest ? 1 : 0) : total;
   if (lo < hi && before <= lo && lo < before + mine) {
     long long at = lo - before;
     for (w.b = b0; w.b < b1; ++w.b) {
@@ -306,146 +449,195 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem = sh.tmem;
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  cluster_sync();  // the stretch is known; both CTAs' barriers are initialised before any remote use
+  cluster_sync();  // the stretch is known; every CTA's barriers are initialised before any remote use
   w.start(P, sh.start_b, sh.start_off, hi - lo);
   Piece p;
+  // arrives on a barrier of the pair's first CTA; with own_writes, those are visible there
+  auto arrive_first = [&](uint64_t* bar, bool own_writes) {
+    if (NP == 1) mbar_arrive(bar);
+    else if (own_writes) mbar_arrive_remote(mapa(smem_u32(bar), first));
+    else arrive_remote_relaxed(mapa(smem_u32(bar), first));
+  };
 
-  if (warp < 8 && rank == 0) {
-    // ------------------------------------------------------- softmax (CTA 0)
-    const int g = warp >> 2, wq = warp & 3;
+  if (warp < 8 && role == 0) {
+    // ------------------------------------------------------------- softmax
+    const int g = warp >> 2, wq = warp & 3;  // half of the columns, quadrant of the rows
     const int row = wq * 32 + lane;
     const float ninf = -__int_as_float(0x7f800000);
-    const uint32_t remote_p = mapa(smem_u32(sP + g * kPBytesSlot), 1);
-    const uint32_t remote_alpha = mapa(smem_u32(&sh.alpha[g][row]), 1);
-    const uint32_t remote_pfull = mapa(smem_u32(&bars.pfull[g]), 1);
-    const uint32_t remote_ffull = mapa(smem_u32(&bars.ffull), 1);
-    int G = 0, pieces = 0;  // tiles and blocks so far
+    const uint32_t peer = NP + side;
+    const uint32_t peer_p = mapa(smem_u32(smem + kOffP + wq * 4096), peer);
+    const uint32_t peer_alpha = mapa(smem_u32(smem + kOffAlpha + wq * 128), peer);
+    const uint32_t peer_pfull = mapa(smem_u32(&bars.pfull[0]), peer);
+    const uint32_t peer_ffull = mapa(smem_u32(&bars.ffull), peer);
+    const uint64_t scale2 = pack_f32x2(P.scale_log2, P.scale_log2), one2 = pack_f32x2(1.f, 1.f);
+    int G = 0, pieces = 0, rounds = 0;  // tiles, blocks and loads of q so far
+    auto fetch_q = [&](const Piece& b) {  // four rows a lane
+      const int64_t from = static_cast<int64_t>(b.row0) + side * 128 + lane * 4;
+      const int64_t n = min(static_cast<int64_t>(4), static_cast<int64_t>(b.row0) + b.rows - from);
+      if (n > 0) prefetch_l2(P.q + from * kDqk, static_cast<uint32_t>(n) * (kDqk * 2));
+    };
     bool ok = true;
     while (ok && w.next(P, p)) {
-      const int nt = p.t1 - p.t0;
+      const int nt = p.t1 - p.t0, in_block = side * 128 + row;
       if (nt > 0) {
-        // q: this thread's row, atoms [5g, 5 + 4g): global -> tensor memory
-        const uint4* qrow = reinterpret_cast<const uint4*>(P.q + static_cast<size_t>(p.row0 + row) * kDqk);
-        const bool real = row < p.rows;
-#pragma unroll 1
-        for (int a = 5 * g; a < 5 + 4 * g; ++a) {
-          uint32_t r[32];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 v = real ? __ldg(qrow + a * 8 + c) : make_uint4(0, 0, 0, 0);
-            r[4 * c] = v.x; r[4 * c + 1] = v.y; r[4 * c + 2] = v.z; r[4 * c + 3] = v.w;
-          }
-          tmem_st32(tmem + lane_off + a * 32, r);
+        // q, three atoms at a time through the staging slots (free once what they held
+        // has arrived): this row's latent atoms into tensor memory, half of them each
+        // group, the rotary atom into its own place.  The products that read the last
+        // block's are complete: every warp has seen its last S.
+        if (warp == 7) {  // the later rounds' rows and the next block's come from the L2
+          if (G == 0) fetch_q(p);
+          Walker<NP> after = w;
+          Piece next;
+          if (after.next(P, next)) fetch_q(next);
         }
+        if (warp == 0) {
+          for (int i = 0; ok && i < kStages; ++i) {
+            const int last = 2 * G - 1 - i;  // the last half that was staged, and the two before
+            ok = last < 0 || warp_wait<false>(&bars.landed[last % kStages], (last / kStages) & 1, P.err, abort_v);
+          }
+        }
+        for (int r = 0; ok && r < kQRounds; ++r, ++rounds) {
+          if (warp == 0) {
+            ok = rounds == 0 || warp_wait<false>(&bars.qread, (rounds & 1) ^ 1, P.err, abort_v);
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bars.qload, kQAtoms * kHalfBytes);
+              load_box(smem + kOffStage, &q_map, r * kQAtoms, p.row0 + side * 128, &bars.qload);
+            }
+          }
+          ok = warp_wait<false>(&bars.qload, rounds & 1, P.err, abort_v);
+          if (!ok) break;
+#pragma unroll 1
+          for (int i = 0; i < kQAtoms; ++i) {
+            const int a = r * kQAtoms + i;
+            if ((a & 1) != g) continue;
+            const uint8_t* src = smem + kOffStage + i * kHalfBytes;
+            uint32_t v[32];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4*>(src + sw128_off(row, c));
+              v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
+            }
+            if (a < kAtomsK - 1) {
+              tmem_st32(tmem + lane_off + a * 32, v);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(smem + kOffQrope + sw128_off(row, c)) =
+                    make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+              fence_proxy_async_smem();
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.qread);
+        }
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.qfull);
+        if (lane == 0) arrive_first(&bars.qfull, true);
       }
-      const int vis = p.first_vis + (p.in_tok + row) / P.H;  // rows that this row's token sees
-      float m_used = ninf, l_sum = 0.f;
+      const int vis = p.first_vis + (p.in_seq + in_block) / P.H;  // rows that this row's token sees
+      float m_used = ninf;
+      uint64_t l_two = 0;  // two partial sums
       for (int j = 0; j < nt; ++j, ++G) {
-        const int sb = G % kSBufs;
-        const uint32_t sph = (G / kSBufs) & 1;
-        if ((G & 1) != g) {
-          // the other group's tile; the block's last one also says that q is read
-          if (j + 1 == nt) {
-            if (!warp_wait<false>(&bars.sfull[sb], sph, P.err, abort_v)) { ok = false; break; }
-          }
-          continue;
-        }
-        if (!warp_wait<false>(&bars.sfull[sb], sph, P.err, abort_v)) { ok = false; break; }
+        const int par = G & 1, at = 2 * G + g, ps = at % kPSlots, st = at % kStages;
+        if (!warp_wait<false>(&bars.sfull[par], (G >> 1) & 1, P.err, abort_v)) { ok = false; break; }
         tc_fence_after();
-        float x[kRows];
-        {
-          uint32_t s0[32], s1[32];
-          tmem_ld32(tmem + lane_off + kTmemS + sb * kRows, s0);
-          tmem_ld32(tmem + lane_off + kTmemS + sb * kRows + 32, s1);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            x[k] = __uint_as_float(s0[k]);
-            x[32 + k] = __uint_as_float(s1[k]);
-          }
-        }
+        uint32_t s0[32], s1[32];
+        tmem_ld32(tmem + lane_off + kTmemS + par * kTile + g * 64, s0);
+        tmem_ld32(tmem + lane_off + kTmemS + par * kTile + g * 64 + 32, s1);
+        tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.sempty[sb]);
-        const int lim = vis - (p.t0 + j) * kRows;  // columns that this row sees
-        if (!__all_sync(0xffffffffu, lim >= kRows)) {
+        if (lane == 0) arrive_first(&bars.sempty[par], false);
+        const int lim = vis - (p.t0 + j) * kTile - g * 64;  // columns that this row sees
+        if (!__all_sync(0xffffffffu, lim >= 64)) {
 #pragma unroll
-          for (int k = 0; k < kRows; ++k)
-            if (k >= lim) x[k] = ninf;
+          for (int k = 0; k < 32; ++k) {
+            if (k >= lim) s0[k] = __float_as_uint(ninf);
+            if (32 + k >= lim) s1[k] = __float_as_uint(ninf);
+          }
         }
-        float mt = ninf;
+        float mx[4] = {ninf, ninf, ninf, ninf};
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) mt = fmaxf(mt, x[k]);
-        mt *= P.scale_log2;
-        float m_prev = ninf;
-        if (j > 0) {
-          if (!warp_wait<false>(&bars.mready[g ^ 1][wq], ((G - 1) >> 1) & 1, P.err, abort_v)) { ok = false; break; }
-          m_prev = own.m[g ^ 1][row];
-        }
-        float alpha = 1.f, m_now = m_prev;
-        if (mt > m_prev + 8.f) {  // also taken when m_prev is -inf
-          m_now = mt;
-          alpha = ex2_approx(m_prev - mt);
-        }
-        own.m[g][row] = m_now;
+        for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], fmaxf(__uint_as_float(s0[k]), __uint_as_float(s1[k])));
+        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        own.top[par][g][row] = mt;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.mready[g][wq]);
-        if (m_now != m_used) {
-          l_sum *= ex2_approx(m_used - m_now);  // (0 at the first)
-          m_used = m_now;
+        if (lane == 0) mbar_arrive(&bars.mready[wq]);
+        if (!warp_wait<false>(&bars.mready[wq], par, P.err, abort_v)) { ok = false; break; }
+        mt = fmaxf(mt, own.top[par][g ^ 1][row]) * P.scale_log2;
+        float alpha = 1.f;
+        if (mt > m_used + 8.f) {  // also taken when m_used is -inf
+          alpha = ex2_approx(m_used - mt);
+          m_used = mt;
+          l_two = fma_f32x2(l_two, pack_f32x2(alpha, alpha), 0);
         }
+        const float shift = m_used == ninf ? 0.f : -m_used;
+        const uint64_t shift2 = pack_f32x2(shift, shift);
         uint32_t pk[32];
-        float lt = 0.f;
-        const float shift = m_now == ninf ? 0.f : m_now;
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          const float p0 = ex2_approx(fmaf(x[2 * k], P.scale_log2, -shift));
-          const float p1 = ex2_approx(fmaf(x[2 * k + 1], P.scale_log2, -shift));
-          lt += p0 + p1;
+          const uint64_t x = k < 16 ? pack_f32x2(__uint_as_float(s0[(2 * k) & 31]), __uint_as_float(s0[(2 * k + 1) & 31]))
+                                    : pack_f32x2(__uint_as_float(s1[(2 * k) & 31]), __uint_as_float(s1[(2 * k + 1) & 31]));
+          const uint64_t y = fma_f32x2(x, scale2, shift2);
+          const float p0 = ex2_approx(lo_f32(y)), p1 = ex2_approx(hi_f32(y));
+          l_two = fma_f32x2(pack_f32x2(p0, p1), one2, l_two);
           const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
           pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
         }
-        l_sum += lt;
-        if (!warp_wait<true>(&bars.pfree[g], ((G >> 1) & 1) ^ 1, P.err, abort_v)) { ok = false; break; }
+        if (!warp_wait<false>(&bars.landed[st], ((at / kStages) & 1) ^ 1, P.err, abort_v) ||
+            !warp_wait<false>(&bars.pfree[ps], ((at / kPSlots) & 1) ^ 1, P.err, abort_v)) {
+          ok = false;
+          break;
+        }
+        uint8_t* stage = smem + kOffStage + st * kHalfBytes;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          st_async_v4(remote_p + sw128_off(row, c), make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]),
-                      remote_pfull);
-        st_async_b32(remote_alpha, __float_as_uint(alpha), remote_pfull);
+          *reinterpret_cast<uint4*>(stage + sw128_off(row, c)) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        if (g == 0) own.alpha[st][row] = alpha;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_to_peer(peer_p + ps * kHalfBytes, stage + wq * 4096, 4096, peer_pfull + ps * 8);
+          if (g == 0) bulk_to_peer(peer_alpha + ps * 512, &own.alpha[st][wq * 32], 128, peer_pfull + ps * 8);
+        }
       }
       if (!ok) break;
       if (!warp_wait<true>(&bars.ffree, (pieces & 1) ^ 1, P.err, abort_v)) { ok = false; break; }
-      own.final_ml[g][row] = make_float2(m_used, l_sum);
+      own.final_ml[g][row] = make_float2(m_used, lo_f32(l_two) + hi_f32(l_two));
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(remote_ffull);
+      if (lane == 0) mbar_arrive_remote(peer_ffull);
       ++pieces;
     }
-    if (!ok) __nanosleep(100000);  // stores on their way to CTA 1 land before either CTA leaves
+    if (!ok) __nanosleep(100000);  // copies on their way to the PV CTA land before either CTA leaves
   } else if (warp < 8) {
-    // ----------------------------------------- O: scaling and output (CTA 1)
+    // ------------------------------------------------ O: scaling and output
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const float ninf = -__int_as_float(0x7f800000);
-    const uint32_t remote_final = mapa(smem_u32(&own.final_ml[0][0]), 0);
-    const uint32_t remote_ffree = mapa(smem_u32(&bars.ffree), 0);
+    const float* alphas = reinterpret_cast<const float*>(smem + kOffAlpha);
+    const uint32_t peer_final = mapa(smem_u32(&own.final_ml[0][0]), side);
+    const uint32_t peer_ffree = mapa(smem_u32(&bars.ffree), side);
     int G = 0, pieces = 0, done = 0;  // tiles, blocks, products seen complete
     bool ok = true;
     int tail_row0 = 0, tail_rows = 0, tail_parts = 0;  // the block that this stretch ends inside of
     long long at = lo;
+    auto wait_products = [&](int n) {
+      while (ok && done < n) {
+        ok = warp_wait<false>(&bars.odone[done & 1], (done >> 1) & 1, P.err, abort_v);
+        done += ok;
+      }
+    };
     while (ok && w.next(P, p)) {
-      const int nt = p.t1 - p.t0;
+      const int nt = p.t1 - p.t0, in_block = side * 128 + row;
       for (int j = 0; j < nt; ++j, ++G) {
-        const int ps = G & 1;
-        if (!warp_wait<true>(&bars.pfull[ps], (G >> 1) & 1, P.err, abort_v)) { ok = false; break; }
-        const float alpha = sh.alpha[ps][row];
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          while (ok && done < G) {  // O holds the products before this tile
-            ok = warp_wait<false>(&bars.odone[done & 1], (done >> 1) & 1, P.err, abort_v);
-            done += ok;
-          }
+        const int par = G & 1, ps = 2 * G % kPSlots;
+        if (!warp_wait<false>(&bars.pfull[ps], (2 * G / kPSlots) & 1, P.err, abort_v)) { ok = false; break; }
+        const float alpha = alphas[ps * 128 + row];
+        const bool rescaled = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+        if (rescaled) {
+          wait_products(G);  // O holds the products before this tile
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -460,50 +652,50 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();
           tc_fence_before();
         }
-        const int live = p.vis - (p.t0 + j) * kRows;  // rows of the tile that the block sees
-        if (live < kRows) {
-          const int pair = G % (kVSlots / kVParts);
-          const uint32_t vph = (G / (kVSlots / kVParts)) & 1;
-          for (int i = 0; ok && i < kVParts; ++i)
-            ok = warp_wait<false>(&bars.vfull[pair * kVParts + i], vph, P.err, abort_v);
-          if (!ok) break;
-          uint8_t* v = ring + pair * kAtomsV * kAtomBytes;
-          for (int i = tid; i < (kRows - live) * kAtomsV * 8; i += 256)
-            *reinterpret_cast<uint4*>(v + ((i >> 3) % kAtomsV) * kAtomBytes + (live + i / (kAtomsV * 8)) * 128 +
-                                      (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();  // P arrived through st.async, zeros by plain stores; the MMA reads both
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.oready[ps]);
-        while (ok && done < G) {  // at most one product's completion stays unseen
-          ok = warp_wait<false>(&bars.odone[done & 1], (done >> 1) & 1, P.err, abort_v);
-          done += ok;
+        if (lane == 0) arrive_first(&bars.oready[par], rescaled);
+        const int live = p.vis - (p.t0 + j) * kTile;  // rows of the tile that the block sees
+        if (live < kTile) {
+          // (with the products before complete, every unit before this tile's has been there: a
+          // wait below cannot take an older phase for its own)
+          wait_products(G);
+          for (int u = live / R::kVRows * 2; ok && u < R::kVUnits; ++u) {
+            const int slot = (G * R::kVUnits + u) % R::kVSlots;
+            ok = warp_wait<false>(&bars.vfull[slot], (NP == 1 ? G : G >> 1) & 1, P.err, abort_v);
+            if (!ok) break;
+            const int from = max(0, live - u / 2 * R::kVRows), rows = R::kVRows - from;
+            for (int i = tid; i < rows * R::kVAtoms * 8; i += 256)
+              *reinterpret_cast<uint4*>(smem + slot * R::kVBytes + i / (8 * rows) * (R::kVRows * 128) +
+                                        (from + (i >> 3) % rows) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_first(&bars.vclean[slot], true);
+          }
         }
         if (!ok) break;
+        wait_products(G);  // at most one product's completion stays unseen
+        if (!ok) break;
       }
-      while (ok && done < G) {
-        ok = warp_wait<false>(&bars.odone[done & 1], (done >> 1) & 1, P.err, abort_v);
-        done += ok;
-      }
+      wait_products(G);
       if (ok) ok = warp_wait<true>(&bars.ffull, pieces & 1, P.err, abort_v);
       if (!ok) break;
       tc_fence_after();
-      const float2 f0 = ld_cluster_f32x2(remote_final + row * 8);
-      const float2 f1 = ld_cluster_f32x2(remote_final + (128 + row) * 8);
+      const float2 f0 = ld_cluster_f32x2(peer_final + row * 8);
+      const float2 f1 = ld_cluster_f32x2(peer_final + (128 + row) * 8);
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(remote_ffree);
+      if (lane == 0) mbar_arrive_remote(peer_ffree);
       ++pieces;
       float m = fmaxf(f0.x, f1.x);
       // (a sum of 0 says that nothing was seen; one that is not a number stays so)
       float l = (f0.y == 0.f ? 0.f : f0.y * ex2_approx(f0.x - m)) + (f1.y == 0.f ? 0.f : f1.y * ex2_approx(f1.x - m));
       const bool empty = l == 0.f || nt == 0;
       const bool whole = p.begins && p.ends;
-      const size_t orow = static_cast<size_t>(p.row0) + row;
+      const size_t orow = static_cast<size_t>(p.row0) + in_block;
       if (whole) {
         float factor = empty ? 0.f : 1.f / l, lse2 = empty ? ninf : m + log2f(l);
         if (P.sink != nullptr) {
           // the sink adds 2^s2 to the denominator, taken relative to max(m, s2)
-          const float s2 = __ldg(P.sink + (p.in_tok + row) % P.H) * 1.4426950408889634f;
+          const float s2 = __ldg(P.sink + (p.in_seq + in_block) % P.H) * 1.4426950408889634f;
           if (empty) {
             lse2 = s2;
           } else {
@@ -512,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             lse2 = mx + log2f(den);
           }
         }
-        if (row < p.rows && half == 0 && P.lse != nullptr) P.lse[orow] = lse2 * 0.69314718055994531f;
+        if (in_block < p.rows && half == 0 && P.lse != nullptr) P.lse[orow] = lse2 * 0.69314718055994531f;
         __nv_bfloat16* o = P.out + orow * kDv;
 #pragma unroll 1
         for (int c0 = half * 256; c0 < half * 256 + 256; c0 += 32) {
@@ -524,33 +716,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             const __nv_bfloat162 pb = __floats2bfloat162_rn(__uint_as_float(v[2 * k]) * factor, __uint_as_float(v[2 * k + 1]) * factor);
             pk[k] = empty ? 0u : *reinterpret_cast<const uint32_t*>(&pb);
           }
-          if (row < p.rows) {
+          if (in_block < p.rows) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               *reinterpret_cast<uint4*>(o + c0 + 8 * k) = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
           }
         }
       } else {
-        const int slot = 2 * cluster + (p.begins ? 1 : 0);
-        if (half == 0) P.part_ml[static_cast<size_t>(slot) * 128 + row] = make_float2(empty ? ninf : m, empty ? 0.f : l);
-        float* o = P.part_o + (static_cast<size_t>(slot) * 128 + row) * kDv;
+        const size_t part = 2 * cluster + (p.begins ? 1 : 0);
+        if (half == 0) P.part_ml[part * (128 * NP) + in_block] = make_float2(empty ? ninf : m, empty ? 0.f : l);
+        float* o = P.part_o + part * (128 * NP) * kDv + in_block * 8;
         if (__any_sync(0xffffffffu, !empty)) {
 #pragma unroll 1
-          for (int c0 = half * 256; c0 < half * 256 + 256; c0 += 32) {
-            uint32_t v[32];
-            tmem_ld32(tmem + lane_off + c0, v);
+          for (int c0 = half * 256; c0 < half * 256 + 256; c0 += 64) {
+            uint32_t v0[32], v1[32];
+            tmem_ld32(tmem + lane_off + c0, v0);
+            tmem_ld32(tmem + lane_off + c0 + 32, v1);
             tmem_ld_wait();
-            if (row < p.rows && !empty) {
+            if (in_block < p.rows && !empty) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) st_global_v8(o + c0 + 8 * k, v + 8 * k);
+              for (int k = 0; k < 4; ++k) {
+                st_global_v8(o + (c0 / 8 + k) * (128 * NP * 8), v0 + 8 * k);
+                st_global_v8(o + (c0 / 8 + 4 + k) * (128 * NP * 8), v1 + 8 * k);
+              }
             }
           }
         }
         if (p.begins) {
           // the block ends in the stretch that holds its last tile
-          long long e = at + w.nt;
-          int parts = 1;
-          while (total * (cluster + parts) / active < e) ++parts;
+          const long long last = at + w.nt - 1, edge = (share + 1) * rest;
+          const long long holder = last < edge ? last / (share + 1) : rest + (last - edge) / share;
+          const int parts = static_cast<int>(holder) - cluster + 1;
           tail_row0 = p.row0;
           tail_rows = p.rows;
           tail_parts = parts;
@@ -559,225 +755,487 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       at += (p.ends ? w.nt : w.off) - p.t0;
     }
-    if (tid == 0) P.desc[cluster] = make_int4(tail_row0, tail_rows, tail_parts, 0);
-  } else if (warp == kLoadWarp) {
-    // ------------------------------------------------ K (CTA 0) or V (CTA 1)
-    const int atoms = rank == 0 ? kKAtoms : kVAtoms, parts = rank == 0 ? kKParts : kVParts;
-    const int slots = rank == 0 ? kKSlots : kVSlots;
-    uint64_t* full = rank == 0 ? bars.kfull : bars.vfull;
-    uint64_t* empty = rank == 0 ? bars.kempty : bars.vempty;
-    const int boxes = kRows / P.box_rows;  // boxes of an atom: 1, or a page each
-    int slot = 0, issued = 0;
-    uint32_t ph = 0;
+    if (tid == 0 && side == 0) P.desc[cluster] = make_int4(tail_row0, tail_rows, tail_parts, 0);
+  } else if (warp == kLoadWarp || (NP == 1 && role == 0 && warp > kMmaWarp)) {
+    // ------------------------------------------------------------ K or V
+    // Each lane has a box of the tile's rows (a page, or all rows of a unit): it looks up the
+    // next tile's while it issues this one's.
+    const int box = role == 0 ? P.k_box : P.v_box, tile_rows = role == 0 ? R::kKRows : kTile;
+    const int boxes = tile_rows / box, skip = role == 0 ? side * R::kKRows : 0;  // boxes of a tile's rows that this CTA loads
+    const bool report = role == 1 && side == 0;  // (a PV CTA looks up every row)
+    const bool plain = box == (role == 0 ? R::kKRows : R::kVRows);  // a box has all rows of a unit, and its atoms
+    const int which = warp == kLoadWarp ? 0 : warp - kMmaWarp;
+    int G = 0, issued = 0;
     bool ok = true;
+    auto look_up = [&](int t) {
+      return t < p.t1 && lane < boxes ? box_row(P, p, t * kTile + skip + lane * box, report) : 0;
+    };
     while (ok && w.next(P, p)) {
-      int row = lane < boxes && p.t0 < p.t1 ? box_row(P, p, p.t0 * kRows + lane * P.box_rows, rank == 0) : 0;
-      for (int t = p.t0; ok && t < p.t1; ++t) {
-        const int here = row;
-        if (t + 1 < p.t1 && lane < boxes) row = box_row(P, p, (t + 1) * kRows + lane * P.box_rows, rank == 0);
-        for (int part = 0; part < parts; ++part) {
-          if (lane == 0) {
-            ok = mbar_wait_polling<false>(&empty[slot], ph ^ 1, P.err, abort_v);
-            if (ok) mbar_arrive_expect_tx(&full[slot], atoms * kAtomBytes);
+      if (p.t0 >= p.t1) continue;
+      int row = look_up(p.t0);
+      for (int t = p.t0; t < p.t1; ++t, ++G) {
+        const int next_row = look_up(t + 1);
+        if (lane < boxes) {
+          const int ring = NP == 1 ? 0 : G & 1;
+          const uint32_t use = ((NP == 1 ? G : G >> 1) & 1) ^ 1;
+          if (role == 0) {
+#pragma unroll
+            for (int i = 0; i < R::kKUnits / R::kKLoaders; ++i) {
+              const int u = i * R::kKLoaders + which, slot = ring * R::kKUnits + u;
+              ok = ok && thread_wait<false>(&bars.kempty[slot], use, P.err, abort_v);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(&bars.kfull[slot], R::kKBytes);
+              uint8_t* dst = smem + slot * R::kKBytes + lane * box * 128;
+              if (plain) {
+                load_box(dst, &k_map, u * R::kKAtoms, row, &bars.kfull[slot]);
+              } else {
+#pragma unroll
+                for (int a = 0; a < R::kKAtoms; ++a)
+                  load_box(dst + a * R::kKRows * 128, &k_map, u * R::kKAtoms + a, row, &bars.kfull[slot]);
+              }
+              ++issued;
+            }
+          } else {
+            const int per = boxes / 2, group = lane >= per;  // boxes of a unit; this lane's is in the units of rows 64 group ..
+#pragma unroll
+            for (int u = 0; u < R::kVUnits; ++u) {
+              const int slot = ring * R::kVUnits + u, atom = (u & 1) * 4 + side * R::kVAtoms;
+              ok = ok && thread_wait<false>(&bars.vempty[slot], use, P.err, abort_v);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(&bars.vfull[slot], R::kVBytes);
+              uint8_t* dst = smem + slot * R::kVBytes + (lane - group * per) * box * 128;
+              if (group == u >> 1) {
+                if (plain) {
+                  load_box(dst, &v_map, atom, row, &bars.vfull[slot]);
+                } else {
+#pragma unroll
+                  for (int a = 0; a < R::kVAtoms; ++a)
+                    load_box(dst + a * R::kVRows * 128, &v_map, atom + a, row, &bars.vfull[slot]);
+                }
+              }
+              ++issued;
+            }
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          if (lane < boxes) {
-            uint8_t* dst = ring + slot * atoms * kAtomBytes + lane * P.box_rows * 128;
-            for (int a = 0; a < atoms; ++a)
-              tma_load_2d(dst + a * kAtomBytes, &kv_map, (part * atoms + a) * 64, here, &full[slot]);
-          }
-          __syncwarp();
-          ++issued;
-          if (++slot == slots) { slot = 0; ph ^= 1; }
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        row = next_row;
       }
     }
     if (!ok && lane == 0) {  // copies in flight land before the CTA leaves
-      for (int i = max(0, issued - slots); i < issued; ++i) mbar_drain(&full[i % slots], (i / slots) & 1);
+      const int loaders = role == 0 ? R::kKLoaders : 1, slots = (role == 0 ? R::kKSlots : R::kVSlots) / loaders;
+      uint64_t* full = role == 0 ? bars.kfull : bars.vfull;
+      for (int i = max(0, issued - slots); i < issued; ++i)
+        if (!mbar_drain(&full[i % slots * loaders + which], (i / slots) & 1)) break;
     }
-  } else if (warp == kMmaWarp && lane == 0) {
+  } else if (warp == kMmaWarp && side == 0 && elect_one()) {
+    const uint16_t both = role == 0 ? 3 : 12;
     bool ok = true;
-    int G = 0, slot = 0, pieces = 0;
-    uint32_t ph = 0;
-    if (rank == 0) {
+    int G = 0;
+    if (role == 0) {
       // ------------------------------------------------------ S = q . K^T
-      const uint32_t idesc = idesc_f16(128, kRows, kFmtBF16, 0, 0);
+      const uint32_t idesc = idesc_f16(128 * NP, kTile, kFmtBF16, 0, 0);
+      const uint64_t k_desc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint64_t qrope_desc = smem_desc(smem_u32(smem + kOffQrope), 16, 1024, kSwizzle128B);
+      int blocks = 0;
       while (ok && w.next(P, p)) {
         if (p.t0 >= p.t1) continue;
-        ok = mbar_wait_polling<false>(&bars.qfull, pieces & 1, P.err, abort_v);
-        ++pieces;
+        ok = thread_wait<NP == 2>(&bars.qfull, blocks & 1, P.err, abort_v);
+        ++blocks;
         for (int t = p.t0; ok && t < p.t1; ++t, ++G) {
-          const int sb = G % kSBufs;
-          ok = mbar_wait_polling<false>(&bars.sempty[sb], ((G / kSBufs) & 1) ^ 1, P.err, abort_v);
-          for (int part = 0; ok && part < kKParts; ++part) {
-            ok = mbar_wait_polling<false>(&bars.kfull[slot], ph, P.err, abort_v);
+          const uint32_t s = tmem + kTmemS + (G & 1) * kTile;
+          const int ring = NP == 1 ? 0 : G & 1;
+          const uint32_t use = (NP == 1 ? G : G >> 1) & 1;
+          ok = thread_wait<false>(&bars.sempty[G & 1], ((G >> 1) & 1) ^ 1, P.err, abort_v);
+#pragma unroll
+          for (int u = 0; u < R::kKUnits; ++u) {
+            const int slot = ring * R::kKUnits + u;
+            ok = ok && thread_wait<false>(&bars.kfull[slot], use, P.err, abort_v);
+            if (NP == 2) ok = ok && thread_wait<false>(&bars.kpeer[slot], use, P.err, abort_v);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t base = smem_u32(ring + slot * kKAtoms * kAtomBytes);
+            const uint64_t kd = k_desc + ((slot * R::kKBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kKAtoms * 4; ++kk) {
-              const uint64_t bd = smem_desc(base + (kk / 4) * kAtomBytes + (kk % 4) * 32, 16, 1024, kSwizzle128B);
-              mma_ts(tmem + kTmemS + sb * kRows, tmem + (part * kKAtoms * 4 + kk) * 8, bd, idesc,
-                     part > 0 || kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < R::kKAtoms * 4; ++kk) {
+              const int step = u * R::kKAtoms * 4 + kk;
+              const uint64_t bd = kd + (((kk / 4) * (R::kKRows * 128) + (kk % 4) * 32) >> 4);
+              if (step < 32)
+                product_ts<NP>(s, tmem + step * 8, bd, idesc, step > 0 ? 1u : 0u);
+              else
+                product_ss<NP>(s, qrope_desc + (((kk % 4) * 32) >> 4), bd, idesc, 1u);
             }
-            mma_commit(&bars.kempty[slot]);
-            if (++slot == kKSlots) { slot = 0; ph ^= 1; }
+            commit<NP>(&bars.kempty[slot], both);
           }
-          if (ok) mma_commit(&bars.sfull[sb]);
+          if (ok) commit<NP>(&bars.sfull[G & 1], both);
         }
       }
     } else {
       // ------------------------------------------------------- O += P . V
-      const uint32_t idesc = idesc_f16(128, 256, kFmtBF16, 0, 1);
+      const uint32_t idesc = idesc_f16(128 * NP, 256, kFmtBF16, 0, 1);
+      const uint64_t v_desc = smem_desc(smem_u32(smem), R::kVRows * 128, 1024, kSwizzle128B);
+      const uint64_t p_desc = smem_desc(smem_u32(smem + kOffP), 16, 1024, kSwizzle128B);
+      uint32_t cleaned = 0;  // the phase of each slot's vclean
+      int ps = 0;            // slot of the next half of P, and its phase
+      uint32_t p_use = 0;
       while (ok && w.next(P, p)) {
         for (int t = p.t0; ok && t < p.t1; ++t, ++G) {
-          const int ps = G & 1;
-          ok = mbar_wait_polling<false>(&bars.oready[ps], (G >> 1) & 1, P.err, abort_v);
-          const uint32_t pbase = smem_u32(sP + ps * kPBytesSlot);
-          for (int part = 0; ok && part < kVParts; ++part) {
-            ok = mbar_wait_polling<false>(&bars.vfull[slot], ph, P.err, abort_v);
-            if (!ok) break;
-            fence_proxy_async_smem();
-            tc_fence_after();
-            const uint32_t vbase = smem_u32(ring + slot * kVAtoms * kAtomBytes);
+          const int par = G & 1, ring = NP == 1 ? 0 : par, live = p.vis - t * kTile;
+          const uint32_t use = (NP == 1 ? G : G >> 1) & 1;
+          ok = thread_wait<NP == 2>(&bars.oready[par], (G >> 1) & 1, P.err, abort_v);
 #pragma unroll
-            for (int kk = 0; kk < kRows / 16; ++kk) {
-              const uint64_t ad = smem_desc(pbase + kk * 32, 16, 1024, kSwizzle128B);
-              const uint64_t bd = smem_desc(vbase + kk * 16 * 128, kAtomBytes, 1024, kSwizzle128B);
-              mma_ss(tmem + part * 256, ad, bd, idesc, t > p.t0 || kk > 0 ? 1u : 0u);
+          for (int u = 0; u < R::kVUnits; ++u) {
+            const int slot = ring * R::kVUnits + u;
+            if (u == R::kVUnits / 2) {
+              if (NP == 1) ok = ok && thread_wait<false>(&bars.pfull[ps], p_use, P.err, abort_v);
+              else ok = ok && thread_wait<false>(&bars.phalf[par], (G >> 1) & 1, P.err, abort_v);
             }
-            mma_commit(&bars.vempty[slot]);
-            if (++slot == kVSlots) { slot = 0; ph ^= 1; }
+            ok = ok && thread_wait<false>(&bars.vfull[slot], use, P.err, abort_v);
+            if (NP == 2) ok = ok && thread_wait<false>(&bars.vpeer[slot], use, P.err, abort_v);
+            if (ok && (u / 2 + 1) * R::kVRows > live) {  // rows that nothing sees: cleared first
+              ok = thread_wait<NP == 2>(&bars.vclean[slot], (cleaned >> slot) & 1, P.err, abort_v);
+              cleaned ^= 1u << slot;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t pd = p_desc + ((ps * kHalfBytes) >> 4), vd = v_desc + ((slot * R::kVBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < R::kVRows / 16; ++kk)
+              product_ss<NP>(tmem + (u & 1) * 256, pd + ((kk * 32) >> 4), vd + ((kk * 16 * 128) >> 4), idesc,
+                             u > 1 || kk > 0 || t > p.t0 ? 1u : 0u);
+            commit<NP>(&bars.vempty[slot], both);
+            if (u & 1) {
+              commit<NP>(&bars.pcons[ps], both);
+              if (++ps == kPSlots) { ps = 0; p_use ^= 1; }
+            }
           }
-          if (ok) {
-            mma_commit(&bars.pcons[ps]);
-            mma_commit(&bars.odone[ps]);
-          }
+          if (ok) commit<NP>(&bars.odone[par], both);
         }
       }
     }
     // every product issued has completed before the tensor memory is freed
-    mma_commit(&bars.drain);
+    commit<NP>(&bars.drain, both);
     mbar_drain(&bars.drain, 0);
-  } else if (warp == kRelayWarp && lane == 0 && rank == 1) {
-    // ------------------------------------- a P slot is consumed -> CTA 0
-    const uint32_t remote_pfree[2] = {mapa(smem_u32(&bars.pfree[0]), 0), mapa(smem_u32(&bars.pfree[1]), 0)};
+  } else if (warp == kRelayWarp && role == 1 && elect_one()) {
+    // -- to the QK CTA: a half of P has arrived, its staging slot is free; a P slot is
+    // consumed, and free.  (Pairs) to the first CTA: the second half has arrived.
+    const uint32_t peer_pfree = mapa(smem_u32(&bars.pfree[0]), side), peer_landed = mapa(smem_u32(&bars.landed[0]), side);
+    const uint32_t first_phalf = mapa(smem_u32(&bars.phalf[0]), first);
+    int landed = 0, consumed = 0, end = 0;  // halves
+    int l_slot = 0, l_stage = 0, c_slot = 0;
+    uint32_t l_use = 0, c_use = 0;
     bool ok = true;
-    int G = 0;
     while (ok && w.next(P, p)) {
-      for (int t = p.t0; ok && t < p.t1; ++t, ++G) {
-        ok = mbar_wait_polling<false>(&bars.pcons[G & 1], (G >> 1) & 1, P.err, abort_v);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&bars.pfull[G & 1], kPTx);  // for the slot's next use
-        mbar_arrive_remote(remote_pfree[G & 1]);
+      end += 2 * (p.t1 - p.t0);
+      int idle = 0;
+      uint64_t since = 0;
+      while (consumed < end) {
+        bool any = false;
+        if (landed < end && mbar_test(&bars.pfull[l_slot], l_use)) {
+          arrive_remote_relaxed(peer_landed + l_stage * 8);
+          if (NP == 2 && (landed & 1)) arrive_remote_relaxed(first_phalf + (landed >> 1 & 1) * 8);
+          ++landed;
+          if (++l_slot == kPSlots) { l_slot = 0; l_use ^= 1; }
+          if (++l_stage == kStages) l_stage = 0;
+          any = true;
+        }
+        if (consumed < landed && mbar_test(&bars.pcons[c_slot], c_use)) {
+          mbar_arrive_expect_tx(&bars.pfull[c_slot], p_bytes(consumed + kPSlots));  // for the slot's next use
+          arrive_remote_relaxed(peer_pfree + c_slot * 8);
+          ++consumed;
+          if (++c_slot == kPSlots) { c_slot = 0; c_use ^= 1; }
+          any = true;
+        }
+        if (any) {
+          idle = 0;
+        } else if (++idle % 64 == 0) {
+          const uint64_t now = globaltimer_ns();
+          if (idle == 64) since = now;
+          const bool late = now - since > wait_limit_ns(P.err);
+          if (late) atomicOr(P.err, kErrTimeout);
+          if (late || *abort_v) {
+            *abort_v = 1;
+            ok = false;
+            break;
+          }
+        }
       }
     }
+  } else if (NP == 2 && warp == kNewsWarp && side == 1 && elect_one()) {
+    // ------------- a unit of this CTA's half has arrived -> the first CTA
+    const int units = role == 0 ? R::kKUnits : R::kVUnits, slots = role == 0 ? R::kKSlots : R::kVSlots;
+    uint64_t* full = role == 0 ? bars.kfull : bars.vfull;
+    const uint32_t peer = mapa(smem_u32(role == 0 ? bars.kpeer : bars.vpeer), first);
+    int slot = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    while (ok && w.next(P, p))
+      for (int i = 0; ok && i < (p.t1 - p.t0) * units; ++i) {
+        ok = thread_wait<false>(&full[slot], ph, P.err, abort_v);
+        if (!ok) break;
+        arrive_remote_relaxed(peer + slot * 8);
+        if (++slot == slots) { slot = 0; ph ^= 1; }
+      }
   }
   griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // no CTA leaves while its peer may still address it
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  cluster_sync();  // no CTA leaves while another may still address it
+  if (warp == 0) free_tmem<NP>(tmem);
 }
 
-// Merges the parts of the block that cluster blockIdx.x's stretch ends inside of:
-// out = sum_c 2^(m_c - M) O_c / (sum_c 2^(m_c - M) l_c [+ 2^(sink - M)]).  A warp
-// takes half a row, 8 columns a lane; the loads of a batch of parts are issued
-// before any is used.
-constexpr int kMergeBatch = 4;
+// Merges the parts of the blocks that clusters' stretches end inside of:
+// out = sum_c 2^(m_c - M) O_c / (sum_c 2^(m_c - M) l_c [+ 2^(sink - M)]).  An item is 32
+// rows (a lane each) x 8 columns of a block.  Of a block of few parts a warp takes an
+// item with all of them; of one of many, eight warps take an eighth each and their sums
+// meet in shared memory.  Four parts are in flight at a time.
+constexpr int kMergeBatch = 4, kMergeWarps = 8, kFewParts = 8;
 
-__global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant__ LatentParams P) {
-  griddep_wait();
-  const int4 d = __ldcg(P.desc + blockIdx.x);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item = blockIdx.y * 8 + warp, row = item >> 1, half = item & 1;
-  if (d.z == 0 || row >= d.y) return;
-  const int col = half * 256 + lane * 8;
+struct Merged {
+  float acc[8], sum, top;  // sum_c 2^(m_c - top) O_c and l_c
+};
+
+// Adds the parts first, first + step, .. < d.z of the block that begins in cluster c's stretch.
+__device__ __forceinline__ void add_parts(const LatentParams& P, Merged& s, const int4& d, int c, int chunk, int row, int first, int step) {
   const float ninf = -__int_as_float(0x7f800000);
-  float acc[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-  float M = ninf, sum = 0.f;
-  for (int c0 = 0; c0 < d.z; c0 += kMergeBatch) {
+  for (int c0 = first; c0 < d.z; c0 += kMergeBatch * step) {
     float2 ml[kMergeBatch];
     float4 v0[kMergeBatch], v1[kMergeBatch];
 #pragma unroll
-    for (int i = 0; i < kMergeBatch; ++i) {
-      const int c = c0 + i;
-      ml[i] = make_float2(ninf, 0.f);
-      v0[i] = v1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c < d.z) {
-        const size_t at = static_cast<size_t>(c == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + c)) * 128 + row;
-        ml[i] = __ldcg(P.part_ml + at);
-        const float4* o = reinterpret_cast<const float4*>(P.part_o + at * kDv + col);
-        v0[i] = __ldcg(o);
-        v1[i] = __ldcg(o + 1);
+    for (int b = 0; b < kMergeBatch; ++b) {
+      const int part = c0 + b * step;
+      ml[b] = make_float2(ninf, 0.f);
+      v0[b] = v1[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < d.y && part < d.z) {
+        const size_t at = part == 0 ? 2 * c + 1 : 2 * (c + part);
+        ml[b] = __ldcg(P.part_ml + at * P.block_rows + row);
+        const float4* o = reinterpret_cast<const float4*>(P.part_o + ((at * (kDv / 8) + chunk) * P.block_rows + row) * 8);
+        v0[b] = __ldcg(o);
+        v1[b] = __ldcg(o + 1);
       }
     }
-    float Mb = M;
+    float top = s.top;
 #pragma unroll
-    for (int i = 0; i < kMergeBatch; ++i)
-      if (ml[i].y != 0.f) Mb = fmaxf(Mb, ml[i].x);
-    const float shift = Mb == ninf ? 0.f : Mb;
-    const float r = exp2f(M - shift);
-    sum *= r;
+    for (int b = 0; b < kMergeBatch; ++b)
+      if (ml[b].y != 0.f) top = fmaxf(top, ml[b].x);
+    const float shift = top == ninf ? 0.f : top, r = exp2f(s.top - shift);
+    s.top = top;
+    s.sum *= r;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] *= r;
-    M = Mb;
+    for (int k = 0; k < 8; ++k) s.acc[k] *= r;
 #pragma unroll
-    for (int i = 0; i < kMergeBatch; ++i) {
-      if (ml[i].y == 0.f) continue;  // nothing seen: its O was not written
-      const float wc = exp2f(ml[i].x - shift);
-      sum = fmaf(wc, ml[i].y, sum);
-      const float v[8] = {v0[i].x, v0[i].y, v0[i].z, v0[i].w, v1[i].x, v1[i].y, v1[i].z, v1[i].w};
+    for (int b = 0; b < kMergeBatch; ++b) {
+      if (ml[b].y == 0.f) continue;  // nothing seen: its O was not written
+      const float f = exp2f(ml[b].x - shift);
+      s.sum = fmaf(f, ml[b].y, s.sum);
+      const float v[8] = {v0[b].x, v0[b].y, v0[b].z, v0[b].w, v1[b].x, v1[b].y, v1[b].z, v1[b].w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = fmaf(wc, v[k], acc[k]);
+      for (int k = 0; k < 8; ++k) s.acc[k] = fmaf(f, v[k], s.acc[k]);
     }
   }
+}
+
+// The output of an item's row, with the sink as one more term 2^s2 of the denominator.
+__device__ __forceinline__ void finish_row(const LatentParams& P, Merged& s, const int4& d, int chunk, int row) {
+  if (row >= d.y) return;
+  const float ninf = -__int_as_float(0x7f800000);
   const int orow = d.x + row;
   if (P.sink != nullptr) {
-    const float s2 = __ldg(P.sink + orow % P.H) * 1.4426950408889634f;
-    if (s2 != ninf) {
-      if (sum != 0.f) {
-        const float mx = fmaxf(M, s2), r = exp2f(M - mx);
+    const float s2 = __ldg(P.sink + orow % P.H) * 1.4426950408889634f, top = s.sum != 0.f ? fmaxf(s.top, s2) : s2;
+    const float shift = top == ninf ? 0.f : top, r = s.sum != 0.f ? exp2f(s.top - shift) : 0.f;
+    s.sum = s.sum * r + exp2f(s2 - shift);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] *= r;
-        sum = sum * r + exp2f(s2 - mx);
-        M = mx;
-      } else {
-        M = s2;
-        sum = 1.f;
-      }
-    }
+    for (int k = 0; k < 8; ++k) s.acc[k] *= r;
+    s.top = top;
   }
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  const float inv = s.sum != 0.f ? 1.f / s.sum : 0.f;
   uint32_t pk[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 pb = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    const __nv_bfloat162 pb = __floats2bfloat162_rn(s.acc[2 * k] * inv, s.acc[2 * k + 1] * inv);
     pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
   }
-  *reinterpret_cast<uint4*>(P.out + static_cast<size_t>(orow) * kDv + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-  if (half == 0 && lane == 0 && P.lse != nullptr)
-    P.lse[orow] = sum != 0.f ? (M + log2f(sum)) * 0.69314718055994531f : ninf;
+  *reinterpret_cast<uint4*>(P.out + static_cast<size_t>(orow) * kDv + chunk * 8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  if (chunk == 0 && P.lse != nullptr) P.lse[orow] = s.sum != 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : ninf;
 }
 
-// Clusters of a call: one for each pair of SMs, but no more than the most tiles
+__global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __grid_constant__ LatentParams P) {
+  __shared__ float sums[kMergeWarps][10][32];  // a warp's 8 columns, sum and maximum
+  __shared__ int4 descs[kMaxClusters];
+  __shared__ int begin[kMaxClusters + 1];  // steps of the CTAs before a cluster's block: eight items, or one of many parts
+  __shared__ int warp_total[kMergeWarps];
+  static_assert(kMaxClusters == 32 * kMergeWarps, "a thread per cluster");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float ninf = -__int_as_float(0x7f800000);
+  constexpr int kChunks = kDv / 8;
+  griddep_wait();
+  {
+    int4 d = make_int4(0, 0, 0, 0);
+    if (threadIdx.x < P.clusters) d = __ldcg(P.desc + threadIdx.x);
+    const int items = d.z == 0 ? 0 : (d.y + 31) / 32 * kChunks;
+    const int steps = d.z > kFewParts ? items : (items + kMergeWarps - 1) / kMergeWarps;
+    int inc = steps;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_total[warp] = inc;
+    descs[threadIdx.x] = d;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) inc += warp_total[i];
+    begin[threadIdx.x + 1] = inc;
+    if (threadIdx.x == 0) begin[0] = 0;
+    __syncthreads();
+  }
+  const int all = begin[kMaxClusters];
+  for (int step = blockIdx.x; step < all; step += gridDim.x) {
+    int c = 0;  // the last cluster whose steps begin at or before it
+#pragma unroll
+    for (int o = kMaxClusters / 2; o; o >>= 1)
+      if (begin[c + o] <= step) c += o;
+    const int4 d = descs[c];
+    const int at = step - begin[c];
+    Merged s;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s.acc[k] = 0.f;
+    s.sum = 0.f;
+    s.top = ninf;
+    if (d.z <= kFewParts) {
+      const int item = at * kMergeWarps + warp, chunk = item % kChunks, row = item / kChunks * 32 + lane;
+      add_parts(P, s, d, c, chunk, row, 0, 1);
+      finish_row(P, s, d, chunk, row);
+      continue;
+    }
+    const int chunk = at % kChunks, row = at / kChunks * 32 + lane;
+    add_parts(P, s, d, c, chunk, row, warp, kMergeWarps);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sums[warp][k][lane] = s.acc[k];
+    sums[warp][8][lane] = s.sum;
+    sums[warp][9][lane] = s.top;
+    __syncthreads();
+    if (warp == 0) {
+      s.top = ninf;
+#pragma unroll
+      for (int u = 0; u < kMergeWarps; ++u)
+        if (sums[u][8][lane] != 0.f) s.top = fmaxf(s.top, sums[u][9][lane]);
+      const float shift = s.top == ninf ? 0.f : s.top;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s.acc[k] = 0.f;
+      s.sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < kMergeWarps; ++u) {
+        const float su = sums[u][8][lane];
+        if (su == 0.f) continue;
+        const float f = exp2f(sums[u][9][lane] - shift);
+        s.sum = fmaf(f, su, s.sum);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s.acc[k] = fmaf(f, sums[u][k][lane], s.acc[k]);
+      }
+      finish_row(P, s, d, chunk, row);
+    }
+    __syncthreads();
+  }
+}
+
+// Whether a call's blocks are 256 rows (NP = 2): where a sequence has more than 128 rows
+// on average.  Two blocks of 128 rows read the cache twice.
+bool paired(const dsa_latent_attn_args& a) { return static_cast<long long>(a.T) * a.H > 128ll * a.B; }
+
+template <int NP>
+cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2 * NP;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2 * NP * clusters);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Clusters that the current device holds at once.
+template <int NP>
+int resident_clusters() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  int d = -1;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return 1;
+  int n = known[d].load();
+  if (n == 0) {
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config<NP>(1, attr);
+    if (cudaFuncSetAttribute(latent_attn_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBytes)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<NP>, &cfg) != cudaSuccess || n < 1)
+      n = 1;
+    known[d].store(n);
+  }
+  return n;
+}
+
+// Clusters of a call: as many as the device holds, but no more than the most tiles
 // that the shape allows can keep busy.
 int cluster_count(const dsa_latent_attn_args& a) {
-  const long long blocks = (static_cast<long long>(a.T) * a.H + 127) / 128 + a.B;
-  const long long tiles = blocks * ((static_cast<long long>(a.max_L) + kRows - 1) / kRows);
-  const long long most = sm_count() / 2, want = tiles / kMinTiles;
-  return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+  const int block = paired(a) ? 256 : 128;
+  const long long blocks = (static_cast<long long>(a.T) * a.H + block - 1) / block + a.B;
+  const long long tiles = blocks * ((static_cast<long long>(a.max_L) + kTile - 1) / kTile);
+  const long long most = paired(a) ? resident_clusters<2>() : resident_clusters<1>(), want = tiles / kMinTiles;
+  return static_cast<int>(std::min<long long>(kMaxClusters, std::max(1ll, std::min(want, most))));
+}
+
+struct Workspace {
+  size_t ml, desc, bytes;  // the partial outputs come first
+  Workspace(int clusters, int block) {
+    const size_t parts = static_cast<size_t>(clusters) * 2 * block;
+    ml = round_up(parts * kDv * sizeof(float), 256);
+    desc = ml + round_up(parts * sizeof(float2), 256);
+    bytes = desc + round_up(static_cast<size_t>(clusters) * sizeof(int4), 256);
+  }
+};
+
+// The rows of a box: what a unit has, or less where pages are smaller.
+int box_rows(const dsa_latent_attn_args& a, int unit) {
+  if (a.block_table != nullptr)
+    while (a.block_size % unit != 0) unit /= 2;
+  return unit;
+}
+
+// A map of rows of 576 values as [atom][row][64 values].
+bool encode_boxes(CUtensorMap& map, const uint16_t* base, int64_t rows, int box, int atoms) {
+  const uint64_t dims[3] = {64, static_cast<uint64_t>(rows), kAtomsK};
+  const uint64_t strides[2] = {kDqk * 2, 128};
+  const uint32_t b[3] = {64, static_cast<uint32_t>(box), static_cast<uint32_t>(atoms)};
+  return encode_tmap(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, b, 128);
+}
+
+template <int NP>
+int launch(LatentParams& P, const dsa_latent_attn_args& a, cudaStream_t s) {
+  using R = Ring<NP>;
+  P.k_box = box_rows(a, R::kKRows);
+  P.v_box = box_rows(a, R::kVRows);
+  alignas(64) CUtensorMap k_map, v_map, q_map;
+  if (!encode_boxes(k_map, a.kv, a.cache_rows, P.k_box, P.k_box == R::kKRows ? R::kKAtoms : 1) ||
+      !encode_boxes(v_map, a.kv, a.cache_rows, P.v_box, P.v_box == R::kVRows ? R::kVAtoms : 1) ||
+      !encode_boxes(q_map, a.q, static_cast<int64_t>(a.T) * a.H, 128, kQAtoms))
+    return DSA_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = config<NP>(P.clusters, attr);
+  cfg.stream = s;
+  if (cudaFuncSetAttribute(latent_attn_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmemBytes)) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return cuda_status(cudaLaunchKernelEx(&cfg, latent_attn_kernel<NP>, P, k_map, v_map, q_map));
 }
 
 }  // namespace
 
 size_t latent_attn_workspace(const dsa_latent_attn_args& a) {
-  const size_t n = cluster_count(a);
-  return round_up(n * 2 * 128 * kDv * sizeof(float), 256) + round_up(n * 2 * 128 * sizeof(float2), 256) +
-         round_up(n * sizeof(int4), 256);
+  return Workspace(cluster_count(a), paired(a) ? 256 : 128).bytes;
 }
 
 int launch_latent_attn(const dsa_latent_attn_args& a, void* ws, cudaStream_t s) {
@@ -787,56 +1245,33 @@ int launch_latent_attn(const dsa_latent_attn_args& a, void* ws, cudaStream_t s) 
   P.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
   P.cache_rows = a.cache_rows;
   P.block_table = a.block_table; P.block_size = a.block_size; P.max_blocks = a.max_blocks;
-  P.box_rows = a.block_table != nullptr && a.block_size < kRows ? a.block_size : kRows;
   P.cu = a.cu_tokens;
   P.kv_len = a.kv_len;
   P.out = reinterpret_cast<__nv_bfloat16*>(a.out);
   P.lse = a.lse;
   P.sink = a.sink;
   P.clusters = cluster_count(a);
-  uint8_t* at = static_cast<uint8_t*>(ws);
-  P.part_o = reinterpret_cast<float*>(at);
-  at += round_up(static_cast<size_t>(P.clusters) * 2 * 128 * kDv * sizeof(float), 256);
-  P.part_ml = reinterpret_cast<float2*>(at);
-  at += round_up(static_cast<size_t>(P.clusters) * 2 * 128 * sizeof(float2), 256);
-  P.desc = reinterpret_cast<int4*>(at);
+  P.block_rows = paired(a) ? 256 : 128;
+  const Workspace at(P.clusters, P.block_rows);
+  P.part_o = static_cast<float*>(ws);
+  P.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + at.ml);
+  P.desc = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + at.desc);
   P.err = error_word();
   if (!P.err) return DSA_ERR_CUDA;
-  alignas(64) CUtensorMap kv_map;
-  {
-    const uint64_t dims[2] = {static_cast<uint64_t>(kDqk), static_cast<uint64_t>(a.cache_rows)};
-    const uint64_t strides[1] = {static_cast<uint64_t>(kDqk) * 2};
-    const uint32_t box[2] = {64, static_cast<uint32_t>(P.box_rows)};
-    if (!encode_tmap(&kv_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.kv, dims, strides, box, 128)) return DSA_ERR_CUDA;
-  }
-  cudaError_t e = cudaFuncSetAttribute(latent_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
-  if (e != cudaSuccess) return DSA_ERR_CUDA;
+  const int st = paired(a) ? launch<2>(P, a, s) : launch<1>(P, a, s);
+  if (st != DSA_OK || P.clusters == 1) return st;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(2 * P.clusters);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  // no more CTAs than items: the most that the clusters can leave
+  const long long items = static_cast<long long>(P.clusters) * (P.block_rows / 32) * (kDv / 8), most = 4ll * sm_count();
+  cfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most));
+  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel, P, kv_map);
-  if (e != cudaSuccess) return DSA_ERR_CUDA;
-  if (P.clusters > 1) {
-    cudaLaunchConfig_t c2 = {};
-    c2.gridDim = dim3(P.clusters, 32);
-    c2.blockDim = dim3(256);
-    c2.stream = s;
-    c2.attrs = attr;
-    c2.numAttrs = 1;
-    e = cudaLaunchKernelEx(&c2, latent_merge_kernel, P);
-  }
-  return cuda_status(e);
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, latent_merge_kernel, P));
 }
 
 }  // namespace dsa
