@@ -23,6 +23,11 @@
 //       Eight warps rescale O where a maximum grew by more than 2^8, and write it
 //       at a block's end.
 //
+// With NP = 1, a warp of the PV CTA fetches the rows of later tiles into the L2: the K ring
+// is one tile, and HBM's latency beside the products is longer than a tile's time (538 ->
+// 502 us for 32 sequences of 4096 to 131072 rows; from the QK CTA, whose own copies then
+// wait behind the fetches, it costs more than it gives).
+//
 // What bounds such a kernel first is not a unit but the single threads that feed them:
 // every instruction of theirs takes some five clocks, so their loops are unrolled over a
 // tile's units with slots and phases that need no arithmetic, barriers have constant
@@ -57,22 +62,26 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kNewsWarp = 11;
 // A cluster takes at least this many tiles: splitting further costs more in the
 // merge than it saves.
 constexpr int kMinTiles = 2;
+// What a block costs beside its tiles (its q, its output, the pipeline's start), in tiles:
+// stretches are equal with it counted in front of each block.
+constexpr int kStart = 3;
 constexpr int kMaxClusters = 256;
 
-// The rings: slots of a unit, [atoms][rows][128 bytes].  K: one atom (NP = 2: three) of all
-// rows of a CTA's part of the tile; V: 64 rows, the columns of a CTA's part of one N = 256
-// product.  A ring has the units of NP tiles: a slot's number follows from the unit's.
+// The rings: slots of a unit, [atoms][rows][128 bytes].  K: three atoms of all rows of a
+// CTA's part of the tile; V: 64 rows, the columns of a CTA's part of one N = 256 product.
+// A ring has the units of NP tiles: a slot's number follows from the unit's.
 template <int NP>
 struct Ring {
-  static constexpr int kKRows = kTile / NP, kKAtoms = NP == 1 ? 1 : 3, kKUnits = kAtomsK / kKAtoms;
+  static constexpr int kKRows = kTile / NP, kKAtoms = 3, kKUnits = kAtomsK / kKAtoms;
   static constexpr int kKBytes = kKAtoms * kKRows * 128, kKSlots = kKUnits * NP;
-  static constexpr int kKLoaders = NP == 1 ? 3 : 1;  // warps that load K, every so manieth unit each
+  static constexpr int kKLoaders = NP == 1 ? 3 : 1;  // warps that load K, a share of a unit's atoms each
   static constexpr int kVRows = 64, kVAtoms = 4 / NP, kVUnits = 4;
   static constexpr int kVBytes = kVAtoms * kVRows * 128, kVSlots = kVUnits * NP;
 };
-constexpr int kMaxKSlots = 9, kMaxVSlots = 8;
+constexpr int kMaxKSlots = 6, kMaxVSlots = 8;
 constexpr int kPSlots = 5, kStages = 3;  // slots of half a tile's P, in the PV CTA and where it is staged
 constexpr int kQRounds = 3, kQAtoms = 3; // a block's q comes through the staging slots
+constexpr int kAhead = 3;  // tiles between V's loads and the rows that are fetched into the L2
 static_assert(kQAtoms == kStages && kQRounds * kQAtoms == kAtomsK, "q's way");
 
 // Shared memory of a QK CTA: K ring, staging slots of P, q's rotary part, OwnQk.  Of a PV
@@ -93,6 +102,7 @@ struct LatentParams {
   int T, B, n_q, H, max_L;
   float scale_log2;
   const __nv_bfloat16* q;
+  const __nv_bfloat16* kv;
   int64_t cache_rows;
   const int32_t* block_table;
   int block_size, max_blocks;
@@ -138,6 +148,7 @@ struct __align__(16) Shared {
   int start_b;
   uint32_t tmem;
   int abort_flag;
+  volatile int progress;  // tiles whose loads have begun, but one
 };
 constexpr size_t kSmemBytes = kOffShared + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
@@ -150,6 +161,7 @@ struct Piece {
   int vis;         // cache rows that the block's last token sees
   int t0, t1;      // tiles
   bool begins, ends;
+  int to_end;      // of the block's share of the work, what is left for later stretches
 };
 
 template <int NP>
@@ -168,7 +180,7 @@ struct Walker {
       n = P.n_q;
     }
     len = min(max(__ldg(P.kv_len + b), 0), P.max_L);
-    nt = max(1, (len - 1) / kTile + 1);
+    nt = max(1, (len - 1) / kTile + 1) + kStart;  // kStart empty ones in front
     nb = (n * P.H + kBlock - 1) / kBlock;
   }
   __device__ __forceinline__ void start(const LatentParams& P, int b0, long long at, long long count) {
@@ -182,31 +194,36 @@ struct Walker {
     off = static_cast<int>(at % nt);
   }
   __device__ __forceinline__ bool next(const LatentParams& P, Piece& p) {
-    if (left <= 0) return false;
-    while (blk >= nb) {
-      if (++b >= P.B) return false;
-      blk = 0;
-      load(P);
+    while (true) {
+      if (left <= 0) return false;
+      while (blk >= nb) {
+        if (++b >= P.B) return false;
+        blk = 0;
+        load(P);
+      }
+      const int from = off, stop = static_cast<int>(min(static_cast<long long>(nt), off + left));
+      const int block = blk;
+      left -= stop - from;
+      off = stop;
+      if (off == nt) {
+        off = 0;
+        ++blk;
+      }
+      if (stop <= kStart) continue;  // none of the block's tiles: it begins in the next stretch
+      p.b = b;
+      p.len = len;
+      p.row0 = c0 * P.H + block * kBlock;
+      p.rows = min(kBlock, n * P.H - block * kBlock);
+      p.in_seq = block * kBlock;
+      p.first_vis = len - n + 1;
+      p.vis = max(0, p.first_vis + (block * kBlock + p.rows - 1) / P.H);
+      p.t0 = max(0, from - kStart);
+      p.t1 = max(p.t0, min(stop - kStart, (p.vis + kTile - 1) / kTile));
+      p.begins = from <= kStart;
+      p.ends = stop == nt;
+      p.to_end = nt - stop;
+      return true;
     }
-    p.b = b;
-    p.len = len;
-    p.row0 = c0 * P.H + blk * kBlock;
-    p.rows = min(kBlock, n * P.H - blk * kBlock);
-    p.in_seq = blk * kBlock;
-    p.first_vis = len - n + 1;
-    p.vis = max(0, p.first_vis + (blk * kBlock + p.rows - 1) / P.H);
-    const int stop = static_cast<int>(min(static_cast<long long>(nt), off + left));
-    p.t0 = off;
-    p.t1 = max(off, min(stop, (p.vis + kTile - 1) / kTile));
-    p.begins = off == 0;
-    p.ends = stop == nt;
-    left -= stop - off;
-    off = stop;
-    if (off == nt) {
-      off = 0;
-      ++blk;
-    }
-    return true;
   }
 };
 
@@ -300,20 +317,30 @@ __device__ __forceinline__ void free_tmem(uint32_t addr) {
   if (NP == 1) tmem_dealloc(addr, 512);
   else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(addr) : "memory");
 }
-// The pair's (or the CTA's) product with A in shared or in tensor memory.
-template <int NP>
-__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-  if (NP == 1) mma_ss(d, a, b, idesc, add);
+// The pair's (or the CTA's) product with A in shared (its descriptor's low word) or in
+// tensor memory; kAdd: to what D holds.  All descriptors here have the same high word but
+// V's; 32-bit additions and a constant predicate keep an MMA at a few instructions.
+template <int NP, bool kAdd>
+__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc) {
+  if (NP == 1)
+    asm volatile("{\n.reg .pred p;\n.reg .b64 x, y;\nsetp.ne.b32 p, %6, 0;\nmov.b64 x, {%1, %2};\nmov.b64 y, {%3, %4};\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}"
+                 ::"r"(d), "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "n"(kAdd ? 1 : 0) : "memory");
   else
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+    asm volatile("{\n.reg .pred p;\n.reg .b64 x, y;\nsetp.ne.b32 p, %6, 0;\nmov.b64 x, {%1, %2};\nmov.b64 y, {%3, %4};\n"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %5, p;\n}"
+                 ::"r"(d), "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "n"(kAdd ? 1 : 0) : "memory");
 }
-template <int NP>
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-  if (NP == 1) mma_ts(d, a, b, idesc, add);
+template <int NP, bool kAdd>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc) {
+  if (NP == 1)
+    asm volatile("{\n.reg .pred p;\n.reg .b64 y;\nsetp.ne.b32 p, %5, 0;\nmov.b64 y, {%2, %3};\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "n"(kAdd ? 1 : 0) : "memory");
   else
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+    asm volatile("{\n.reg .pred p;\n.reg .b64 y;\nsetp.ne.b32 p, %5, 0;\nmov.b64 y, {%2, %3};\n"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], y, %4, p;\n}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "n"(kAdd ? 1 : 0) : "memory");
 }
 // Arrives on the barrier, in every CTA of the pair, when the products issued so far are complete.
 template <int NP>
@@ -357,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kMaxKSlots; ++i) {
-      mbar_init(&bars.kfull[i], 1);
+      mbar_init(&bars.kfull[i], R::kKLoaders);
       mbar_init(&bars.kpeer[i], 1);
       mbar_init(&bars.kempty[i], 1);
     }
@@ -388,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars.ffull, 8);
     mbar_init(&bars.drain, 1);
     sh.abort_flag = 0;
+    sh.progress = 0;
     fence_mbar_init();
     if (role == 1)
       for (int i = 0; i < kPSlots; ++i) mbar_arrive_expect_tx(&bars.pfull[i], p_bytes(i));
@@ -427,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (i < warp) before += sh.scan[i];
     total += sh.scan[i];
   }
-  const long long active = max(1ll, min(static_cast<long long>(P.clusters), total / kMinTiles));
+  const long long active = max(1ll, min(static_cast<long long>(P.clusters), total / (kMinTiles + kStart)));
   // stretch c begins at share c + min(c, rest)
   const long long share = total / active, rest = total - share * active;
   const long long lo = cluster < active ? share * cluster + min(static_cast<long long>(cluster), rest) : total;
@@ -622,7 +650,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int G = 0, pieces = 0, done = 0;  // tiles, blocks, products seen complete
     bool ok = true;
     int tail_row0 = 0, tail_rows = 0, tail_parts = 0;  // the block that this stretch ends inside of
-    long long at = lo;
     auto wait_products = [&](int n) {
       while (ok && done < n) {
         ok = warp_wait<false>(&bars.odone[done & 1], (done >> 1) & 1, P.err, abort_v);
@@ -743,8 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (p.begins) {
-          // the block ends in the stretch that holds its last tile
-          const long long last = at + w.nt - 1, edge = (share + 1) * rest;
+          // the block ends in the stretch that holds its last tile; this stretch ends with this piece
+          const long long last = hi - 1 + p.to_end, edge = (share + 1) * rest;
           const long long holder = last < edge ? last / (share + 1) : rest + (last - edge) / share;
           const int parts = static_cast<int>(holder) - cluster + 1;
           tail_row0 = p.row0;
@@ -753,7 +780,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      at += (p.ends ? w.nt : w.off) - p.t0;
     }
     if (tid == 0 && side == 0) P.desc[cluster] = make_int4(tail_row0, tail_rows, tail_parts, 0);
   } else if (warp == kLoadWarp || (NP == 1 && role == 0 && warp > kMmaWarp)) {
@@ -775,23 +801,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       int row = look_up(p.t0);
       for (int t = p.t0; t < p.t1; ++t, ++G) {
         const int next_row = look_up(t + 1);
+        if (lane == 0) sh.progress = G;
         if (lane < boxes) {
           const int ring = NP == 1 ? 0 : G & 1;
           const uint32_t use = ((NP == 1 ? G : G >> 1) & 1) ^ 1;
           if (role == 0) {
 #pragma unroll
-            for (int i = 0; i < R::kKUnits / R::kKLoaders; ++i) {
-              const int u = i * R::kKLoaders + which, slot = ring * R::kKUnits + u;
+            for (int u = 0; u < R::kKUnits; ++u) {
+              constexpr int kAtoms = R::kKAtoms / R::kKLoaders;
+              const int slot = ring * R::kKUnits + u;
               ok = ok && thread_wait<false>(&bars.kempty[slot], use, P.err, abort_v);
               if (!ok) break;
-              if (lane == 0) mbar_arrive_expect_tx(&bars.kfull[slot], R::kKBytes);
-              uint8_t* dst = smem + slot * R::kKBytes + lane * box * 128;
+              if (lane == 0) mbar_arrive_expect_tx(&bars.kfull[slot], R::kKBytes / R::kKLoaders);
+              uint8_t* dst = smem + slot * R::kKBytes + (which * kAtoms * R::kKRows + lane * box) * 128;
               if (plain) {
-                load_box(dst, &k_map, u * R::kKAtoms, row, &bars.kfull[slot]);
+                load_box(dst, &k_map, u * R::kKAtoms + which * kAtoms, row, &bars.kfull[slot]);
               } else {
 #pragma unroll
-                for (int a = 0; a < R::kKAtoms; ++a)
-                  load_box(dst + a * R::kKRows * 128, &k_map, u * R::kKAtoms + a, row, &bars.kfull[slot]);
+                for (int a = 0; a < kAtoms; ++a)
+                  load_box(dst + a * R::kKRows * 128, &k_map, u * R::kKAtoms + which * kAtoms + a, row, &bars.kfull[slot]);
               }
               ++issued;
             }
@@ -823,10 +851,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && lane == 0) {  // copies in flight land before the CTA leaves
-      const int loaders = role == 0 ? R::kKLoaders : 1, slots = (role == 0 ? R::kKSlots : R::kVSlots) / loaders;
+      const int slots = role == 0 ? R::kKSlots : R::kVSlots;
       uint64_t* full = role == 0 ? bars.kfull : bars.vfull;
       for (int i = max(0, issued - slots); i < issued; ++i)
-        if (!mbar_drain(&full[i % slots * loaders + which], (i / slots) & 1)) break;
+        if (!mbar_drain(&full[i % slots], (i / slots) & 1)) break;
     }
   } else if (warp == kMmaWarp && side == 0 && elect_one()) {
     const uint16_t both = role == 0 ? 3 : 12;
@@ -836,7 +864,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------ S = q . K^T
       const uint32_t idesc = idesc_f16(128 * NP, kTile, kFmtBF16, 0, 0);
       const uint64_t k_desc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-      const uint64_t qrope_desc = smem_desc(smem_u32(smem + kOffQrope), 16, 1024, kSwizzle128B);
+      const uint32_t k_lo = static_cast<uint32_t>(k_desc), k_hi = static_cast<uint32_t>(k_desc >> 32);
+      const uint32_t qrope_lo = k_lo + (kOffQrope >> 4);
       int blocks = 0;
       while (ok && w.next(P, p)) {
         if (p.t0 >= p.t1) continue;
@@ -854,15 +883,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (NP == 2) ok = ok && thread_wait<false>(&bars.kpeer[slot], use, P.err, abort_v);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t kd = k_desc + ((slot * R::kKBytes) >> 4);
+            const uint32_t kd = k_lo + ((slot * R::kKBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < R::kKAtoms * 4; ++kk) {
               const int step = u * R::kKAtoms * 4 + kk;
-              const uint64_t bd = kd + (((kk / 4) * (R::kKRows * 128) + (kk % 4) * 32) >> 4);
-              if (step < 32)
-                product_ts<NP>(s, tmem + step * 8, bd, idesc, step > 0 ? 1u : 0u);
+              const uint32_t bd = kd + (((kk / 4) * (R::kKRows * 128) + (kk % 4) * 32) >> 4);
+              if (step == 0)
+                product_ts<NP, false>(s, tmem, bd, k_hi, idesc);
+              else if (step < 32)
+                product_ts<NP, true>(s, tmem + step * 8, bd, k_hi, idesc);
               else
-                product_ss<NP>(s, qrope_desc + (((kk % 4) * 32) >> 4), bd, idesc, 1u);
+                product_ss<NP, true>(s, qrope_lo + (((kk % 4) * 32) >> 4), k_hi, bd, k_hi, idesc);
             }
             commit<NP>(&bars.kempty[slot], both);
           }
@@ -874,6 +905,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_f16(128 * NP, 256, kFmtBF16, 0, 1);
       const uint64_t v_desc = smem_desc(smem_u32(smem), R::kVRows * 128, 1024, kSwizzle128B);
       const uint64_t p_desc = smem_desc(smem_u32(smem + kOffP), 16, 1024, kSwizzle128B);
+      const uint32_t v_lo = static_cast<uint32_t>(v_desc), v_hi = static_cast<uint32_t>(v_desc >> 32);
+      const uint32_t p_lo = static_cast<uint32_t>(p_desc), p_hi = static_cast<uint32_t>(p_desc >> 32);
       uint32_t cleaned = 0;  // the phase of each slot's vclean
       int ps = 0;            // slot of the next half of P, and its phase
       uint32_t p_use = 0;
@@ -897,11 +930,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             tc_fence_after();
-            const uint64_t pd = p_desc + ((ps * kHalfBytes) >> 4), vd = v_desc + ((slot * R::kVBytes) >> 4);
+            const uint32_t pd = p_lo + ((ps * kHalfBytes) >> 4), vd = v_lo + ((slot * R::kVBytes) >> 4);
+            const uint32_t d = tmem + (u & 1) * 256;
+            if (u < 2 && t == p.t0)
+              product_ss<NP, false>(d, pd, p_hi, vd, v_hi, idesc);
+            else
+              product_ss<NP, true>(d, pd, p_hi, vd, v_hi, idesc);
 #pragma unroll
-            for (int kk = 0; kk < R::kVRows / 16; ++kk)
-              product_ss<NP>(tmem + (u & 1) * 256, pd + ((kk * 32) >> 4), vd + ((kk * 16 * 128) >> 4), idesc,
-                             u > 1 || kk > 0 || t > p.t0 ? 1u : 0u);
+            for (int kk = 1; kk < R::kVRows / 16; ++kk)
+              product_ss<NP, true>(d, pd + ((kk * 32) >> 4), p_hi, vd + ((kk * 16 * 128) >> 4), v_hi, idesc);
             commit<NP>(&bars.vempty[slot], both);
             if (u & 1) {
               commit<NP>(&bars.pcons[ps], both);
@@ -958,6 +995,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
         }
+      }
+    }
+  } else if (NP == 1 && warp == kNewsWarp && role == 1) {
+    // --- the tile kAhead on from V's: its rows into the L2, 8 a lane (they lie in one page).
+    // No one waits for this warp: it leaves when the others are late.
+    bool ok = true;
+    int G = 0;
+    while (ok && w.next(P, p)) {
+      for (int t = p.t0; ok && t < p.t1; ++t, ++G) {
+        const int row = lane < kTile / 8 ? box_row(P, p, t * kTile + lane * 8, false) : static_cast<int>(P.cache_rows);
+        const uint64_t since = globaltimer_ns();
+        while (ok && G > sh.progress + kAhead) {
+          __nanosleep(64);
+          ok = !*abort_v && globaltimer_ns() - since <= wait_limit_ns(P.err);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && row < P.cache_rows)
+          prefetch_l2(P.kv + static_cast<size_t>(row) * kDqk, static_cast<uint32_t>(min(static_cast<int64_t>(8), P.cache_rows - row)) * (kDqk * 2));
       }
     }
   } else if (NP == 2 && warp == kNewsWarp && side == 1 && elect_one()) {
@@ -1219,7 +1274,7 @@ int launch(LatentParams& P, const dsa_latent_attn_args& a, cudaStream_t s) {
   P.k_box = box_rows(a, R::kKRows);
   P.v_box = box_rows(a, R::kVRows);
   alignas(64) CUtensorMap k_map, v_map, q_map;
-  if (!encode_boxes(k_map, a.kv, a.cache_rows, P.k_box, P.k_box == R::kKRows ? R::kKAtoms : 1) ||
+  if (!encode_boxes(k_map, a.kv, a.cache_rows, P.k_box, P.k_box == R::kKRows ? R::kKAtoms / R::kKLoaders : 1) ||
       !encode_boxes(v_map, a.kv, a.cache_rows, P.v_box, P.v_box == R::kVRows ? R::kVAtoms : 1) ||
       !encode_boxes(q_map, a.q, static_cast<int64_t>(a.T) * a.H, 128, kQAtoms))
     return DSA_ERR_CUDA;
@@ -1243,6 +1298,7 @@ int launch_latent_attn(const dsa_latent_attn_args& a, void* ws, cudaStream_t s) 
   P.T = a.T; P.B = a.B; P.n_q = a.n_q; P.H = a.H; P.max_L = a.max_L;
   P.scale_log2 = a.scale * 1.4426950408889634f;
   P.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+  P.kv = reinterpret_cast<const __nv_bfloat16*>(a.kv);
   P.cache_rows = a.cache_rows;
   P.block_table = a.block_table; P.block_size = a.block_size; P.max_blocks = a.max_blocks;
   P.cu = a.cu_tokens;
