@@ -43,6 +43,7 @@
 // anything) are cleared in V before the product; their S is not looked at.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -62,9 +63,6 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kNewsWarp = 11;
 // A cluster takes at least this many tiles: splitting further costs more in the
 // merge than it saves.
 constexpr int kMinTiles = 2;
-// What a block costs beside its tiles (its q, its output, the pipeline's start), in tiles:
-// stretches are equal with it counted in front of each block.
-constexpr int kStart = 3;
 constexpr int kMaxClusters = 256;
 
 // The rings: slots of a unit, [atoms][rows][128 bytes].  K: three atoms of all rows of a
@@ -167,6 +165,10 @@ struct Piece {
 template <int NP>
 struct Walker {
   static constexpr int kBlock = 128 * NP;
+  // What a block costs beside its tiles (its q, its output, the pipeline's start), in
+  // tiles: stretches are equal with it counted in front of each block.  (Without: 16 heads
+  // over 700 to 9000 rows 88 us in place of 80, 4 x 2 tokens at 64K 115 in place of 109.)
+  static constexpr int kStart = 2 + 2 * NP;
   long long left;
   int b, blk, off;
   int n, c0, len, nt, nb;
@@ -421,7 +423,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kPSlots; ++i) mbar_arrive_expect_tx(&bars.pfull[i], p_bytes(i));
   }
   if (warp == 0) alloc_tmem<NP>(&sh.tmem);
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for below
   griddep_wait();
+  griddep_launch_dependents();  // the merge's CTAs come as these leave, and wait for the last
 
   // ------------------------------------------------ this cluster's stretch
   const int each = (P.B + kThreads - 1) / kThreads;
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (i < warp) before += sh.scan[i];
     total += sh.scan[i];
   }
-  const long long active = max(1ll, min(static_cast<long long>(P.clusters), total / (kMinTiles + kStart)));
+  const long long active = max(1ll, min(static_cast<long long>(P.clusters), total / (kMinTiles + Walker<NP>::kStart)));
   // stretch c begins at share c + min(c, rest)
   const long long share = total / active, rest = total - share * active;
   const long long lo = cluster < active ? share * cluster + min(static_cast<long long>(cluster), rest) : total;
@@ -477,7 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem = sh.tmem;
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  cluster_sync();  // the stretch is known; every CTA's barriers are initialised before any remote use
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA's barriers are initialised
+  __syncthreads();                                                      // the stretch is known
   w.start(P, sh.start_b, sh.start_off, hi - lo);
   Piece p;
   // arrives on a barrier of the pair's first CTA; with own_writes, those are visible there
@@ -1031,7 +1037,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++slot == slots) { slot = 0; ph ^= 1; }
       }
   }
-  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no CTA leaves while another may still address it
@@ -1040,57 +1045,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merges the parts of the blocks that clusters' stretches end inside of:
 // out = sum_c 2^(m_c - M) O_c / (sum_c 2^(m_c - M) l_c [+ 2^(sink - M)]).  An item is 32
-// rows (a lane each) x 8 columns of a block.  Of a block of few parts a warp takes an
-// item with all of them; of one of many, eight warps take an eighth each and their sums
-// meet in shared memory.  Four parts are in flight at a time.
-constexpr int kMergeBatch = 4, kMergeWarps = 8, kFewParts = 8;
+// rows (a lane each) x 8 columns of a block.  Of a block of few parts a warp takes an item
+// with all of them, four in flight at a time; of one of many (one long sequence), eight
+// warps take an eighth each of the parts of 4 columns, ten in flight, and their sums meet
+// in shared memory.
+constexpr int kMergeWarps = 8, kFewParts = 16;
 
+template <int kCols>
 struct Merged {
-  float acc[8], sum, top;  // sum_c 2^(m_c - top) O_c and l_c
+  float acc[kCols], sum, top;  // sum_c 2^(m_c - top) O_c and l_c
+  __device__ __forceinline__ Merged() : sum(0.f), top(-INFINITY) {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
+  }
 };
 
 // Adds the parts first, first + step, .. < d.z of the block that begins in cluster c's stretch.
-__device__ __forceinline__ void add_parts(const LatentParams& P, Merged& s, const int4& d, int c, int chunk, int row, int first, int step) {
+template <int kCols, int kBatch>
+__device__ __forceinline__ void add_parts(const LatentParams& P, Merged<kCols>& s, const int4& d, int c, int col, int row, int first, int step) {
   const float ninf = -__int_as_float(0x7f800000);
-  for (int c0 = first; c0 < d.z; c0 += kMergeBatch * step) {
-    float2 ml[kMergeBatch];
-    float4 v0[kMergeBatch], v1[kMergeBatch];
+  for (int c0 = first; c0 < d.z; c0 += kBatch * step) {
+    float2 ml[kBatch];
+    float4 v[kBatch][kCols / 4];
 #pragma unroll
-    for (int b = 0; b < kMergeBatch; ++b) {
+    for (int b = 0; b < kBatch; ++b) {
       const int part = c0 + b * step;
       ml[b] = make_float2(ninf, 0.f);
-      v0[b] = v1[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kCols / 4; ++k) v[b][k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < d.y && part < d.z) {
         const size_t at = part == 0 ? 2 * c + 1 : 2 * (c + part);
         ml[b] = __ldcg(P.part_ml + at * P.block_rows + row);
-        const float4* o = reinterpret_cast<const float4*>(P.part_o + ((at * (kDv / 8) + chunk) * P.block_rows + row) * 8);
-        v0[b] = __ldcg(o);
-        v1[b] = __ldcg(o + 1);
+        const float4* o = reinterpret_cast<const float4*>(P.part_o + ((at * (kDv / 8) + col / 8) * P.block_rows + row) * 8 + col % 8);
+#pragma unroll
+        for (int k = 0; k < kCols / 4; ++k) v[b][k] = __ldcg(o + k);
       }
     }
     float top = s.top;
 #pragma unroll
-    for (int b = 0; b < kMergeBatch; ++b)
+    for (int b = 0; b < kBatch; ++b)
       if (ml[b].y != 0.f) top = fmaxf(top, ml[b].x);
     const float shift = top == ninf ? 0.f : top, r = exp2f(s.top - shift);
     s.top = top;
     s.sum *= r;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s.acc[k] *= r;
+    for (int k = 0; k < kCols; ++k) s.acc[k] *= r;
 #pragma unroll
-    for (int b = 0; b < kMergeBatch; ++b) {
+    for (int b = 0; b < kBatch; ++b) {
       if (ml[b].y == 0.f) continue;  // nothing seen: its O was not written
       const float f = exp2f(ml[b].x - shift);
       s.sum = fmaf(f, ml[b].y, s.sum);
-      const float v[8] = {v0[b].x, v0[b].y, v0[b].z, v0[b].w, v1[b].x, v1[b].y, v1[b].z, v1[b].w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s.acc[k] = fmaf(f, v[k], s.acc[k]);
+      for (int k = 0; k < kCols / 4; ++k) {
+        s.acc[4 * k] = fmaf(f, v[b][k].x, s.acc[4 * k]);
+        s.acc[4 * k + 1] = fmaf(f, v[b][k].y, s.acc[4 * k + 1]);
+        s.acc[4 * k + 2] = fmaf(f, v[b][k].z, s.acc[4 * k + 2]);
+        s.acc[4 * k + 3] = fmaf(f, v[b][k].w, s.acc[4 * k + 3]);
+      }
     }
   }
 }
 
 // The output of an item's row, with the sink as one more term 2^s2 of the denominator.
-__device__ __forceinline__ void finish_row(const LatentParams& P, Merged& s, const int4& d, int chunk, int row) {
+template <int kCols>
+__device__ __forceinline__ void finish_row(const LatentParams& P, Merged<kCols>& s, const int4& d, int col, int row) {
   if (row >= d.y) return;
   const float ninf = -__int_as_float(0x7f800000);
   const int orow = d.x + row;
@@ -1099,22 +1117,22 @@ __device__ __forceinline__ void finish_row(const LatentParams& P, Merged& s, con
     const float shift = top == ninf ? 0.f : top, r = s.sum != 0.f ? exp2f(s.top - shift) : 0.f;
     s.sum = s.sum * r + exp2f(s2 - shift);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s.acc[k] *= r;
+    for (int k = 0; k < kCols; ++k) s.acc[k] *= r;
     s.top = top;
   }
   const float inv = s.sum != 0.f ? 1.f / s.sum : 0.f;
-  uint32_t pk[4];
+  uint2* o = reinterpret_cast<uint2*>(P.out + static_cast<size_t>(orow) * kDv + col);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 pb = __floats2bfloat162_rn(s.acc[2 * k] * inv, s.acc[2 * k + 1] * inv);
-    pk[k] = *reinterpret_cast<const uint32_t*>(&pb);
+  for (int k = 0; k < kCols / 4; ++k) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(s.acc[4 * k] * inv, s.acc[4 * k + 1] * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(s.acc[4 * k + 2] * inv, s.acc[4 * k + 3] * inv);
+    o[k] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
-  *reinterpret_cast<uint4*>(P.out + static_cast<size_t>(orow) * kDv + chunk * 8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-  if (chunk == 0 && P.lse != nullptr) P.lse[orow] = s.sum != 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : ninf;
+  if (col == 0 && P.lse != nullptr) P.lse[orow] = s.sum != 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : ninf;
 }
 
 __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __grid_constant__ LatentParams P) {
-  __shared__ float sums[kMergeWarps][10][32];  // a warp's 8 columns, sum and maximum
+  __shared__ float sums[kMergeWarps][6][32];  // a warp's 4 columns, sum and maximum
   __shared__ int4 descs[kMaxClusters];
   __shared__ int begin[kMaxClusters + 1];  // steps of the CTAs before a cluster's block: eight items, or one of many parts
   __shared__ int warp_total[kMergeWarps];
@@ -1127,7 +1145,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
     int4 d = make_int4(0, 0, 0, 0);
     if (threadIdx.x < P.clusters) d = __ldcg(P.desc + threadIdx.x);
     const int items = d.z == 0 ? 0 : (d.y + 31) / 32 * kChunks;
-    const int steps = d.z > kFewParts ? items : (items + kMergeWarps - 1) / kMergeWarps;
+    const int steps = d.z > kFewParts ? 2 * items : (items + kMergeWarps - 1) / kMergeWarps;
     int inc = steps;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1150,43 +1168,39 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
       if (begin[c + o] <= step) c += o;
     const int4 d = descs[c];
     const int at = step - begin[c];
-    Merged s;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s.acc[k] = 0.f;
-    s.sum = 0.f;
-    s.top = ninf;
     if (d.z <= kFewParts) {
-      const int item = at * kMergeWarps + warp, chunk = item % kChunks, row = item / kChunks * 32 + lane;
-      add_parts(P, s, d, c, chunk, row, 0, 1);
-      finish_row(P, s, d, chunk, row);
+      const int item = at * kMergeWarps + warp, col = item % kChunks * 8, row = item / kChunks * 32 + lane;
+      Merged<8> s;
+      add_parts<8, 4>(P, s, d, c, col, row, 0, 1);
+      finish_row(P, s, d, col, row);
       continue;
     }
-    const int chunk = at % kChunks, row = at / kChunks * 32 + lane;
-    add_parts(P, s, d, c, chunk, row, warp, kMergeWarps);
+    const int col = at % (2 * kChunks) * 4, row = at / (2 * kChunks) * 32 + lane;
+    {
+      Merged<4> s;
+      add_parts<4, 10>(P, s, d, c, col, row, warp, kMergeWarps);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sums[warp][k][lane] = s.acc[k];
-    sums[warp][8][lane] = s.sum;
-    sums[warp][9][lane] = s.top;
+      for (int k = 0; k < 4; ++k) sums[warp][k][lane] = s.acc[k];
+      sums[warp][4][lane] = s.sum;
+      sums[warp][5][lane] = s.top;
+    }
     __syncthreads();
     if (warp == 0) {
-      s.top = ninf;
+      Merged<4> s;
 #pragma unroll
       for (int u = 0; u < kMergeWarps; ++u)
-        if (sums[u][8][lane] != 0.f) s.top = fmaxf(s.top, sums[u][9][lane]);
+        if (sums[u][4][lane] != 0.f) s.top = fmaxf(s.top, sums[u][5][lane]);
       const float shift = s.top == ninf ? 0.f : s.top;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s.acc[k] = 0.f;
-      s.sum = 0.f;
-#pragma unroll
       for (int u = 0; u < kMergeWarps; ++u) {
-        const float su = sums[u][8][lane];
+        const float su = sums[u][4][lane];
         if (su == 0.f) continue;
-        const float f = exp2f(sums[u][9][lane] - shift);
+        const float f = exp2f(sums[u][5][lane] - shift);
         s.sum = fmaf(f, su, s.sum);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s.acc[k] = fmaf(f, sums[u][k][lane], s.acc[k]);
+        for (int k = 0; k < 4; ++k) s.acc[k] = fmaf(f, sums[u][k][lane], s.acc[k]);
       }
-      finish_row(P, s, d, chunk, row);
+      finish_row(P, s, d, col, row);
     }
     __syncthreads();
   }
