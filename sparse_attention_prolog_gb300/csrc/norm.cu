@@ -20,7 +20,7 @@ constexpr int kMaxChunks = 4;  // 8-element chunks of a row that a thread holds
 
 struct NormParams {
   dsa_add_rmsnorm_args a;
-  int row_threads;  // threads of a row: a warp, or the whole CTA
+  int row_threads;  // threads of a row: 8, 16 or 32 (several rows a CTA), or the whole CTA
   float inv_d;
 };
 
@@ -29,24 +29,20 @@ __device__ __forceinline__ float max_abs_nan(float m, float v) {
   return __uint_as_float(max(__float_as_uint(m), __float_as_uint(v) & 0x7fffffffu));
 }
 
-// Sum or maximum over the threads of a row; `part` holds a value per warp.
+// Sum or maximum over the n threads of a row; `part` holds a value per warp of the CTA's.
 template <bool kMax>
-__device__ __forceinline__ float row_reduce(float v, bool one_warp, float* part) {
+__device__ __forceinline__ float row_reduce(float v, int n, float* part) {
+  auto join = [](float x, float y) { return kMax ? max_abs_nan(x, y) : x + y; };
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = kMax ? max_abs_nan(v, u) : v + u;
-  }
-  if (one_warp) return v;
+  for (int o = 16; o; o >>= 1)
+    if (o < n) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (n <= 32) return v;
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) part[warp] = v;
   __syncthreads();
   v = lane < warps ? part[lane] : 0.f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = kMax ? max_abs_nan(v, u) : v + u;
-  }
+  for (int o = 16; o; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -65,18 +61,42 @@ __device__ __forceinline__ uint32_t code_of(float z, float s) {
   return static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(z / s, -127.f), 127.f))) & 0xffu;
 }
 
+// The codes of 8 values.  A division costs as much as the rest of an element: t = z (1/s)
+// is within 127 * 2^-22 < 2^-14 of z / s, so its nearest whole number is the quotient's
+// unless t lies that near to a tie; then all 8 are divided (225 -> 196 us for 16384 rows
+// of 7168).  Adding 1.5 * 2^23 rounds to a whole number, ties to even, and leaves it in the
+// low byte.  |z| <= 127 s (1 + 2^-23): nothing has to be clamped.
+__device__ __forceinline__ uint2 codes_of(const float (&z)[8], float s, float r) {
+  constexpr float kRound = 12582912.f;
+  uint32_t c[8];
+  bool near = !(s > 1e-30f);  // (1 / s would leave fp32's range)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = z[i] * r, u = t + kRound;
+    near |= fabsf(fabsf(t - (u - kRound)) - 0.5f) < 1.f / 16384;
+    c[i] = __float_as_uint(u);
+  }
+  if (near)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = code_of(z[i], s);
+  auto four = [&](int i) {
+    return __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040), __byte_perm(c[i + 2], c[i + 3], 0x0040), 0x5410);
+  };
+  return make_uint2(four(0), four(4));
+}
+
 // kVec: D and every row allow vectors of 8 elements; else element by element,
 // neighbouring threads at neighbouring elements.
-template <int kChunks, bool kVec, bool kFp16, bool kRes32>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
+template <int kChunks, int kThreads, bool kVec, bool kFp16, bool kRes32>
+__global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const NormParams P) {
   __shared__ float part[2][32];
   const dsa_add_rmsnorm_args& a = P.a;
   const int n = P.row_threads;
-  const bool one_warp = n == 32;
-  const int me = one_warp ? threadIdx.x & 31 : threadIdx.x;
-  const long long row = one_warp ? static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  const int me = n <= 32 ? threadIdx.x % n : threadIdx.x;
+  const long long at = n <= 32 ? static_cast<long long>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n : blockIdx.x;
   griddep_wait();
-  if (row >= a.T) return;  // whole warps, and only where a warp has a row of its own
+  const int D = at < a.T ? a.D : 0;  // (a row past the last: its threads only take part in the reductions)
+  const long long row = min(at, static_cast<long long>(a.T) - 1);
   const bool res = a.residual != nullptr;
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.x_stride;
   const uint8_t* rin = static_cast<const uint8_t*>(a.residual) + row * a.residual_stride * (kRes32 ? 4 : 2);
@@ -89,7 +109,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       const int e = (me + k * n) * 8;
-      const bool on = e < a.D;
+      const bool on = e < D;
       xv[k] = on ? __ldcs(reinterpret_cast<const uint4*>(x + e)) : make_uint4(0, 0, 0, 0);
       r0[k] = r1[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (res && on) {
@@ -112,7 +132,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
       if (kRes32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[k][i] += b[i];
-        if (e < a.D) {
+        if (e < D) {
           float4* o = reinterpret_cast<float4*>(rout + static_cast<size_t>(e) * 4);
           o[0] = make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
           o[1] = make_float4(h[k][4], h[k][5], h[k][6], h[k][7]);
@@ -127,7 +147,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
           h[k][2 * i] = s.x;
           h[k][2 * i + 1] = s.y;
         }
-        if (e < a.D) *reinterpret_cast<uint4*>(rout + static_cast<size_t>(e) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (e < D) *reinterpret_cast<uint4*>(rout + static_cast<size_t>(e) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   } else {
@@ -137,7 +157,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
       for (int i = 0; i < 8; ++i) {
         const int e = me + (k * 8 + i) * n;
         float v = 0.f;
-        if (e < a.D) {
+        if (e < D) {
           v = kFp16 ? __half2float(__ushort_as_half(x[e])) : __uint_as_float(static_cast<uint32_t>(x[e]) << 16);
           if (res && kRes32) {
             v += reinterpret_cast<const float*>(rin)[e];
@@ -158,7 +178,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
   for (int k = 0; k < kChunks; ++k)
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum = fmaf(h[k][i], h[k][i], sum);
-  sum = row_reduce<false>(sum, one_warp, part[0]);
+  sum = row_reduce<false>(sum, n, part[0]);
   const float r = 1.f / sqrtf(sum * P.inv_d + a.eps);
 
   float top = 0.f;
@@ -166,7 +186,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
   for (int k = 0; k < kChunks; ++k) {
     if (kVec) {
       const int e = (me + k * n) * 8;
-      if (e >= a.D) continue;
+      if (e >= D) continue;
       const float4 g0 = __ldg(reinterpret_cast<const float4*>(a.gamma + e));
       const float4 g1 = __ldg(reinterpret_cast<const float4*>(a.gamma + e) + 1);
       const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
@@ -182,7 +202,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int e = me + (k * 8 + i) * n;
-        if (e >= a.D) continue;
+        if (e >= D) continue;
         h[k][i] = h[k][i] * r * __ldg(a.gamma + e);
         if (a.y) reinterpret_cast<__nv_bfloat16*>(a.y)[row * a.D + e] = __float2bfloat16_rn(h[k][i]);
         top = max_abs_nan(top, h[k][i]);
@@ -190,7 +210,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
     }
   }
   if (a.codes == nullptr) return;
-  top = row_reduce<true>(top, one_warp, part[1]);
+  top = row_reduce<true>(top, n, part[1]);
   float s = top / 127.f;
   const bool fine = s > 0.f && s < __int_as_float(0x7f800000);
   if (a.round_scale && fine) {
@@ -198,32 +218,30 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormParams P) {
     const float m = frexpf(s, &e);  // s = m * 2^e, m in [0.5, 1)
     s = ldexpf(1.f, m == 0.5f ? e - 1 : e);
   }
-  if (me == 0) a.code_scale[row] = s;
+  const float inv_s = 1.f / s;
+  if (me == 0 && D > 0) a.code_scale[row] = s;
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     if (kVec) {
       const int e = (me + k * n) * 8;
-      if (e >= a.D) continue;
-      uint2 o = make_uint2(0u, 0u);
-      if (fine) {
-        o.x = code_of(h[k][0], s) | code_of(h[k][1], s) << 8 | code_of(h[k][2], s) << 16 | code_of(h[k][3], s) << 24;
-        o.y = code_of(h[k][4], s) | code_of(h[k][5], s) << 8 | code_of(h[k][6], s) << 16 | code_of(h[k][7], s) << 24;
-      }
-      *reinterpret_cast<uint2*>(a.codes + row * a.D + e) = o;
+      if (e >= D) continue;
+      *reinterpret_cast<uint2*>(a.codes + row * a.D + e) = fine ? codes_of(h[k], s, inv_s) : make_uint2(0u, 0u);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int e = me + (k * 8 + i) * n;
-        if (e < a.D) a.codes[row * a.D + e] = fine ? static_cast<int8_t>(code_of(h[k][i], s)) : 0;
+        if (e < D) a.codes[row * a.D + e] = fine ? static_cast<int8_t>(code_of(h[k][i], s)) : 0;
       }
     }
   }
 }
 
-template <int kChunks, bool kVec>
+template <int kChunks, int kThreads, bool kVec>
 auto pick(bool fp16, bool res32) {
-  return fp16 ? (res32 ? add_rmsnorm_kernel<kChunks, kVec, true, true> : add_rmsnorm_kernel<kChunks, kVec, true, false>)
-              : (res32 ? add_rmsnorm_kernel<kChunks, kVec, false, true> : add_rmsnorm_kernel<kChunks, kVec, false, false>);
+  return fp16 ? (res32 ? add_rmsnorm_kernel<kChunks, kThreads, kVec, true, true>
+                       : add_rmsnorm_kernel<kChunks, kThreads, kVec, true, false>)
+              : (res32 ? add_rmsnorm_kernel<kChunks, kThreads, kVec, false, true>
+                       : add_rmsnorm_kernel<kChunks, kThreads, kVec, false, false>);
 }
 
 }  // namespace
@@ -234,20 +252,25 @@ int launch_add_rmsnorm(const dsa_add_rmsnorm_args& a, cudaStream_t s) {
                    aligned(a.residual, 16) && aligned(a.residual_out, 16) && a.residual_stride * rsize % 16 == 0 &&
                    a.residual_out_stride * rsize % 16 == 0 && aligned(a.y, 16) && aligned(a.codes, 8);
   const int chunks = (a.D + 7) / 8;
-  // Threads of a row: one chunk each for rows of up to 1024 chunks, so that a row
-  // is one trip to memory; a warp's worth of row (256 elements) is left to one
-  // warp, eight rows to a CTA.
+  // Threads of a row.  Few rows: one chunk each, so that a row is one trip to memory (8 rows
+  // of 7168 2.7 us).  Rows enough to fill the SMs: four chunks each, so that more rows are
+  // on their way while others reduce.  Rows of up to 32 chunks: 8 to 32 threads, several
+  // rows a CTA.
+  const bool many = a.T > 4 * sm_count();
   int per = 1;
   while ((chunks + per - 1) / per > 1024) per *= 2;
-  const int n = ((chunks + per - 1) / per + 31) / 32 * 32;
-  const int rows = n == 32 ? 8 : 1;
+  if (many && vec && chunks > 256 && chunks <= 2048) per = 4;
+  int n = ((chunks + per - 1) / per + 31) / 32 * 32;
+  if (n == 32) n = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
+  const int rows = n <= 32 ? 256 / n : 1;
   NormParams P{a, n, 1.f / static_cast<float>(a.D)};
-  auto kern = vec ? (per == 1 ? pick<1, true>(a.x_fp16, a.residual_fp32)
-                     : per == 2 ? pick<2, true>(a.x_fp16, a.residual_fp32)
-                                : pick<4, true>(a.x_fp16, a.residual_fp32))
-                  : (per == 1 ? pick<1, false>(a.x_fp16, a.residual_fp32)
-                     : per == 2 ? pick<2, false>(a.x_fp16, a.residual_fp32)
-                                : pick<4, false>(a.x_fp16, a.residual_fp32));
+  const bool f = a.x_fp16, r = a.residual_fp32;
+  auto kern = !vec ? (per == 1 ? pick<1, 1024, false>(f, r) : per == 2 ? pick<2, 1024, false>(f, r) : pick<4, 1024, false>(f, r))
+              : per == 1 ? pick<1, 1024, true>(f, r)
+              : per == 2 ? pick<2, 1024, true>(f, r)
+              : n <= 256 ? pick<4, 256, true>(f, r)
+              : n <= 512 ? pick<4, 512, true>(f, r)
+                         : pick<4, 1024, true>(f, r);
   static_assert(kMaxChunks * 8 * 1024 >= 32768, "the longest row fits a CTA");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
