@@ -551,6 +551,10 @@ def dsa_latent_attn(args: LatentAttnArgs, workspace: Optional[torch.Tensor] = No
 
 
 # --------------------------------------------------------------- step maps
+def _plain(t: torch.Tensor, dtype, device: int) -> bool:
+    return t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+
+
 def dsa_step_maps(cached: torch.Tensor, fresh: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
                   block_size: int, cu_tokens: torch.Tensor, kv_len: torch.Tensor, counts: torch.Tensor,
                   seq_of_token: torch.Tensor, pos: torch.Tensor, slot: torch.Tensor,
@@ -559,31 +563,38 @@ def dsa_step_maps(cached: torch.Tensor, fresh: torch.Tensor, free_pages: torch.T
     [1] -> block_table int32 [B, max_blocks] (new pages entered), cu_tokens int32 [B + 1], kv_len int32 [B], counts
     int32 [3] (tokens, head after the step, requests served), seq_of_token and pos int32 [T], slot int64 [T] (see
     dsa.h)."""
-    _fits_32(block_size=block_size)
     device = _device("cached", cached)
-    n, i32 = cached.shape[:1], torch.int32
-    _tensor("cached", cached, i32, (None,), device)
-    _tensor("fresh", fresh, i32, n, device)
-    _tensor("free_pages", free_pages, i32, (None,), device)
-    _tensor("block_table", block_table, i32, (n[0], None), device)
-    _tensor("cu_tokens", cu_tokens, i32, (n[0] + 1,), device)
-    _tensor("kv_len", kv_len, i32, n, device)
-    _tensor("counts", counts, i32, (3,), device)
-    _tensor("slot", slot, torch.int64, (None,), device)
-    _tensor("seq_of_token", seq_of_token, i32, slot.shape, device)
-    _tensor("pos", pos, i32, slot.shape, device)
-    if free_head is not None:
-        _tensor("free_head", free_head, i32, (1,), device)
-    args = StepMapsArgs(n[0], slot.shape[0], block_size, block_table.shape[1], free_pages.shape[0], _p(cached),
-                        _p(fresh), _p(free_pages), _p(free_head), _p(block_table), _p(cu_tokens), _p(kv_len),
-                        _p(counts), _p(seq_of_token), _p(pos), _p(slot))
+    n, i32, tokens, table = cached.shape, torch.int32, slot.shape, block_table.shape
+    # (one condition for the calls that pass, as a check of each tensor costs as much as a launch)
+    if not (len(n) == len(tokens) == 1 and fresh.shape == n and kv_len.shape == n and seq_of_token.shape == tokens
+            and pos.shape == tokens and len(table) == 2 and table[0] == n[0] and len(free_pages.shape) == 1
+            and cu_tokens.shape == (n[0] + 1,) and counts.shape == (3,) and slot.dtype is torch.int64
+            and -2 ** 31 <= block_size < 2 ** 31 and (free_head is None or _plain(free_head, i32, device) and free_head.shape == (1,))
+            and _plain(cached, i32, device) and _plain(fresh, i32, device) and _plain(free_pages, i32, device)
+            and _plain(block_table, i32, device) and _plain(cu_tokens, i32, device) and _plain(kv_len, i32, device)
+            and _plain(counts, i32, device) and _plain(seq_of_token, i32, device) and _plain(pos, i32, device)
+            and _plain(slot, torch.int64, device)):
+        _fits_32(block_size=block_size)
+        _tensor("cached", cached, i32, (None,), device)
+        _tensor("slot", slot, torch.int64, (None,), device)
+        for name, t, shape in (("fresh", fresh, n), ("free_pages", free_pages, (None,)),
+                               ("block_table", block_table, (n[0], None)), ("cu_tokens", cu_tokens, (n[0] + 1,)),
+                               ("kv_len", kv_len, n), ("counts", counts, (3,)), ("seq_of_token", seq_of_token, tokens),
+                               ("pos", pos, tokens), ("free_head", free_head, (1,))):
+            if t is not None:
+                _tensor(name, t, i32, shape, device)
+    args = StepMapsArgs(n[0], tokens[0], block_size, table[1], free_pages.shape[0], cached.data_ptr(), fresh.data_ptr(),
+                        free_pages.data_ptr(), None if free_head is None else free_head.data_ptr(),
+                        block_table.data_ptr(), cu_tokens.data_ptr(), kv_len.data_ptr(), counts.data_ptr(),
+                        seq_of_token.data_ptr(), pos.data_ptr(), slot.data_ptr())
     _check(load().dsa_step_maps(ctypes.byref(args), _stream_of(device, stream)), "dsa_step_maps")
 
 
 # --------------------------------------------------- residual and RMS norm
 def _rows(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
     """Checks a [T, D] tensor whose rows may lie apart: its row stride."""
-    _tensor(name, t, dtype, shape, device, last_dense=True)
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device and t.stride(1) == 1):
+        _tensor(name, t, dtype, tuple(shape), device, last_dense=True)
     # (a single row has no stride of its own)
     return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
 
@@ -596,26 +607,30 @@ def dsa_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: 
     residual) -> residual_out = x + residual, and its RMS norm times gamma as y bf16 [T, D], as codes int8 [T, D] with
     scale fp32 [T], or both (see dsa.h).  x and the residuals may be rows of wider tensors."""
     device = _device("x", x)
-    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16):
-        raise DSAError(f"x: {x.dtype} {tuple(x.shape)}, expected bf16 or fp16 [T, D]")
-    shape = tuple(x.shape)
-    strides = [_rows("x", x, x.dtype, shape, device), 0, 0]
-    _tensor("gamma", gamma, torch.float32, shape[1:], device)
+    shape, kind, bf16 = x.shape, x.dtype, torch.bfloat16
+    if len(shape) != 2 or kind is not bf16 and kind is not torch.float16:
+        raise DSAError(f"x: {kind} {tuple(shape)}, expected bf16 or fp16 [T, D]")
     if (residual is None) != (residual_out is None) or (codes is None) != (scale is None):
         raise DSAError("dsa_add_rmsnorm: residual goes with residual_out, codes go with scale")
-    kind = torch.bfloat16
+    T, D = shape
+    r_kind, strides = bf16, (_rows("x", x, kind, shape, device), 0, 0)
     if residual is not None:
-        kind = residual.dtype
-        if kind not in (torch.bfloat16, torch.float32):
-            raise DSAError(f"residual: {kind}, expected bf16 or fp32")
-        strides[1] = _rows("residual", residual, kind, shape, device)
-        strides[2] = _rows("residual_out", residual_out, kind, shape, device)
-    if y is not None:
-        _tensor("y", y, torch.bfloat16, shape, device)
-    if codes is not None:
+        r_kind = residual.dtype
+        if r_kind is not bf16 and r_kind is not torch.float32:
+            raise DSAError(f"residual: {r_kind}, expected bf16 or fp32")
+        strides = (strides[0], _rows("residual", residual, r_kind, shape, device),
+                   _rows("residual_out", residual_out, r_kind, shape, device))
+    if not (gamma.shape == (D,) and _plain(gamma, torch.float32, device)):
+        _tensor("gamma", gamma, torch.float32, (D,), device)
+    if y is not None and not (y.shape == shape and _plain(y, bf16, device)):
+        _tensor("y", y, bf16, shape, device)
+    if codes is not None and not (codes.shape == shape and scale.shape == (T,) and _plain(codes, torch.int8, device)
+                                  and _plain(scale, torch.float32, device)):
         _tensor("codes", codes, torch.int8, shape, device)
-        _tensor("scale", scale, torch.float32, shape[:1], device)
-    args = AddRmsnormArgs(*shape, float(eps), int(x.dtype is torch.float16), int(kind is torch.float32),
-                          int(bool(round_scale)), *strides, _p(x), _p(residual), _p(residual_out), _p(gamma), _p(y),
-                          _p(codes), _p(scale))
+        _tensor("scale", scale, torch.float32, (T,), device)
+    args = AddRmsnormArgs(T, D, eps, kind is not bf16, r_kind is not bf16, bool(round_scale), *strides, x.data_ptr(),
+                          None if residual is None else residual.data_ptr(),
+                          None if residual is None else residual_out.data_ptr(), gamma.data_ptr(),
+                          None if y is None else y.data_ptr(), None if codes is None else codes.data_ptr(),
+                          None if codes is None else scale.data_ptr())
     _check(load().dsa_add_rmsnorm(ctypes.byref(args), _stream_of(device, stream)), "dsa_add_rmsnorm")
