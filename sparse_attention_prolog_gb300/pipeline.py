@@ -67,12 +67,14 @@ class PrologBuffers:
 
 class MlaBuffers:
     """Device copies of a workloads.MlaInputs plus the MLA Prolog's outputs
-    (q_lora, q_lora_scale, q) and a latent cache of ``cache_rows`` rows."""
+    (q_lora, q_lora_scale, q) and a latent cache of ``cache_rows`` rows.  x, pos
+    and slot may be given as device tensors (another kernel's outputs)."""
 
-    def __init__(self, p, device, cache_rows: int, kv_fill: float = 0.0, kv_cache: torch.Tensor = None):
+    def __init__(self, p, device, cache_rows: int, kv_fill: float = 0.0, kv_cache: torch.Tensor = None,
+                 x: torch.Tensor = None, pos: torch.Tensor = None, slot: torch.Tensor = None):
         self.p = p
         d = device
-        self.x = to_dev(p.x, d, "bf16")
+        self.x = to_dev(p.x, d, "bf16") if x is None else x
         self.w_dq = to_dev(p.w_dq, d, "bf16")
         self.gamma_q = to_dev(p.gamma_q, d)
         self.w_dkv = to_dev(p.w_dkv, d, "bf16")
@@ -80,10 +82,10 @@ class MlaBuffers:
         self.w_uq = to_dev(p.w_uq, d)
         self.w_uq_scale = to_dev(p.w_uq_scale, d)
         self.w_uk = to_dev(p.w_uk, d, "bf16")
-        self.pos = to_dev(p.pos, d)
+        self.pos = to_dev(p.pos, d) if pos is None else pos
         self.rope_cos = to_dev(p.rope_cos, d)
         self.rope_sin = to_dev(p.rope_sin, d)
-        self.slot = to_dev(p.slot, d)
+        self.slot = to_dev(p.slot, d) if slot is None else slot
         self.q_lora = torch.zeros(p.T, p.K_q, dtype=torch.int8, device=d)
         self.q_lora_scale = torch.zeros(p.T, dtype=torch.float16, device=d)
         self.q = torch.zeros(p.T, p.H, 576, dtype=torch.bfloat16, device=d)
@@ -230,3 +232,69 @@ class DiaBuffers:
             self.kv4.write(self.kv, self.slot, stream)
         self.pro.run(stream)
         self.buf.run(stream)
+
+
+class StepMaps:
+    """The tables of the steps of ``B`` requests over a paged cache, kept on the
+    device: a block table, a list of free pages and the lengths.  Each run()
+    adds fresh int32 [B] tokens to the requests and leaves what the step's calls
+    take: block_table, cu_tokens, kv_len, seq_of_token, pos and slot (T rows; see
+    dsa_step_maps), counts (tokens, free pages taken so far, requests served).
+    A step reads one set of lengths and writes the other, and sets its free head
+    from its counts, so a captured run() has to be of an even number of steps."""
+
+    def __init__(self, B_: int, T: int, block_size: int, max_blocks: int, free_pages: torch.Tensor):
+        d = free_pages.device
+        i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device=d)  # noqa: E731
+        self.block_size = block_size
+        self.free_pages = free_pages
+        self.block_table = torch.full((B_, max_blocks), -1, dtype=torch.int32, device=d)
+        self.lens = [i32(B_), i32(B_)]
+        self.counts = [i32(3), i32(3)]
+        self.cu_tokens, self.seq_of_token, self.pos = i32(B_ + 1), i32(T), i32(T)
+        self.slot = torch.zeros(T, dtype=torch.int64, device=d)
+        self.step = 0  # which set the next run reads
+
+    @property
+    def kv_len(self) -> torch.Tensor:
+        """The lengths after the latest step (a view that the next step keeps)."""
+        return self.lens[self.step]
+
+    def run(self, fresh: torch.Tensor, stream=None):
+        now, then = self.step, 1 - self.step
+        B.dsa_step_maps(self.lens[now], fresh, self.free_pages, self.block_table, self.block_size, self.cu_tokens,
+                        self.lens[then], self.counts[then], self.seq_of_token, self.pos, self.slot,
+                        free_head=self.counts[now][1:2], stream=stream)
+        self.step = then
+
+
+class DenseBuffers:
+    """One decode step of a layer without an indexer: the residual addition and
+    RMS norm of the hidden states (their output is the MLA Prolog's x) -> the MLA
+    Prolog (positions and cache rows from the step maps) -> attention over the
+    whole latent cache of each request.  ``p`` is a workloads.MlaInputs whose x,
+    pos and slot are not used; T = p.T rows, of which a step may fill fewer (the
+    maps' padding).  ``x`` and ``residual`` bf16 [T, D_x] are the step's inputs,
+    ``residual`` is updated in place."""
+
+    def __init__(self, p, maps: StepMaps, kv_cache: torch.Tensor, gamma: torch.Tensor, scale: float, eps: float = 1e-6):
+        d = kv_cache.device
+        self.maps, self.gamma, self.eps, self.scale, self.kv_cache = maps, gamma, eps, scale, kv_cache
+        self.x = torch.zeros(p.T, p.D_x, dtype=torch.bfloat16, device=d)
+        self.residual = torch.zeros_like(self.x)
+        self.mla = MlaBuffers(p, d, kv_cache.shape[0], kv_cache=kv_cache, x=torch.zeros_like(self.x), pos=maps.pos,
+                              slot=maps.slot)
+        self.out = torch.zeros(p.T, p.H, 512, dtype=torch.bfloat16, device=d)
+        self.lse = torch.zeros(p.T, p.H, dtype=torch.float32, device=d)
+        B_, blocks = maps.block_table.shape
+        self.aargs = [B.latent_attn_args(p.T, B_, p.H, blocks * maps.block_size, scale, self.mla.q, kv_cache, lens,
+                                         self.out, self.lse, cu_tokens=maps.cu_tokens, block_table=maps.block_table,
+                                         block_size=maps.block_size) for lens in maps.lens]
+        self.aws = torch.empty(B.workspace_bytes("latent_attn", self.aargs[0]), dtype=torch.uint8, device=d)
+
+    def run(self, fresh: torch.Tensor, stream=None):
+        """fresh int32 [B]: the tokens that each request adds, in x's row order."""
+        self.maps.run(fresh, stream)
+        B.dsa_add_rmsnorm(self.x, self.gamma, self.eps, self.residual, self.residual, self.mla.x, stream=stream)
+        self.mla.run(stream)
+        B.dsa_latent_attn(self.aargs[self.maps.step], self.aws, stream)
