@@ -49,7 +49,8 @@
  *     dsa_indexer_topk / dsa_indexer_scores, and q and seq_of_token of
  *     dsa_sparse_attn.  The
  *     kernel enqueued just before such a call must not write them (an event
- *     or a memcpy in between lifts the rule).
+ *     or a memcpy in between lifts the rule).  dsa_step_maps writes pos and
+ *     seq_of_token: it is called before a prolog, not between one and these.
  */
 #ifndef DSA_H_
 #define DSA_H_
@@ -654,8 +655,8 @@ int dsa_step_maps(const dsa_step_maps_args* args, void* stream);
  *
  * Token layout: cu_tokens int32 [B + 1] (non-decreasing, from 0, at most T):
  * sequence b has the tokens cu_tokens[b] .. cu_tokens[b+1] - 1; rows of q past
- * cu_tokens[B] are not read, those of out and lse not written.  NULL: the
- * uniform batch T = B * n_q.
+ * cu_tokens[B] may hold anything, those of out and lse are not written.  NULL:
+ * the uniform batch T = B * n_q.
  * Shapes: q bf16 [T, H, 576]; kv bf16 contiguous [B, max_L, 576] (cache_rows >=
  * B * max_L) or paged [cache_rows, 576] through block_table int32 [B,
  * max_blocks], max_L = max_blocks * block_size; kv_len int32 [B], with the new
@@ -669,7 +670,7 @@ int dsa_step_maps(const dsa_step_maps_args* args, void* stream);
  * outside [0, max_L] (clamped) and cu_tokens that decrease or leave [0, T]
  * (clamped) are recorded as DSA_ERR_DEVICE_DATA; rows of such a page read as
  * zeros.
- * Supported: T * H < 2^31 - 128, 1 <= H <= 1024, 1 <= B <= 65535, scale positive
+ * Supported: T * H < 2^31 - 256, 1 <= H <= 1024, 1 <= B <= 65535, scale positive
  * and finite, cache_rows < 2^31, block_size 8, 16, 32 or a multiple of 64;
  * q, kv and out 16-byte aligned.
  * Workspace: dsa_latent_attn_workspace() bytes, 256-byte aligned, never in use

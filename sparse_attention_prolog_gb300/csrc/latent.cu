@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t peer_ffull = mapa(smem_u32(&bars.ffull), peer);
     const uint64_t scale2 = pack_f32x2(P.scale_log2, P.scale_log2), one2 = pack_f32x2(1.f, 1.f);
     int G = 0, pieces = 0, rounds = 0;  // tiles, blocks and loads of q so far
+    bool loading = false;               // (warp 0) a load of q is on its way
     auto fetch_q = [&](const Piece& b) {  // four rows a lane
       const int64_t from = static_cast<int64_t>(b.row0) + side * 128 + lane * 4;
       const int64_t n = min(static_cast<int64_t>(4), static_cast<int64_t>(b.row0) + b.rows - from);
@@ -538,9 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive_expect_tx(&bars.qload, kQAtoms * kHalfBytes);
               load_box(smem + kOffStage, &q_map, r * kQAtoms, p.row0 + side * 128, &bars.qload);
             }
+            loading = true;
           }
           ok = warp_wait<false>(&bars.qload, rounds & 1, P.err, abort_v);
           if (!ok) break;
+          loading = false;
 #pragma unroll 1
           for (int i = 0; i < kQAtoms; ++i) {
             const int a = r * kQAtoms + i;
@@ -645,7 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_remote(peer_ffull);
       ++pieces;
     }
-    if (!ok) __nanosleep(100000);  // copies on their way to the PV CTA land before either CTA leaves
+    if (!ok) {  // copies on their way, of q and to the PV CTA, land before either CTA leaves
+      if (loading) mbar_drain(&bars.qload, rounds & 1);
+      const uint64_t since = globaltimer_ns();
+      while (globaltimer_ns() - since < 200000) __nanosleep(1000);
+    }
   } else if (warp < 8) {
     // ------------------------------------------------ O: scaling and output
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -1048,8 +1055,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rows (a lane each) x 8 columns of a block.  Of a block of few parts a warp takes an item
 // with all of them, four in flight at a time; of one of many (one long sequence), eight
 // warps take an eighth each of the parts of 4 columns, ten in flight, and their sums meet
-// in shared memory.
-constexpr int kMergeWarps = 8, kFewParts = 16;
+// in shared memory.  (2 x 2 tokens at 64K, 19 parts a block: 65 us a call the first way, 73
+// the second; a bound of 32 parts or more makes 16 heads over 700 to 9000 rows 87 us in
+// place of 81, a bound of 0 112.)
+constexpr int kMergeWarps = 8, kFewParts = 24;
 
 template <int kCols>
 struct Merged {
@@ -1207,7 +1216,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
 }
 
 // Whether a call's blocks are 256 rows (NP = 2): where a sequence has more than 128 rows
-// on average.  Two blocks of 128 rows read the cache twice.
+// on average.  Two blocks of 128 rows read the cache twice, a block of 256 with 128 rows to
+// fill it wastes half of its products.  (4 x 2 tokens of 128 heads at 64K 103 us paired, 137
+// not; 1024 new tokens 1285 and 1664; 19 sequences of 144 rows at 32K 216 and 263; of 128
+// rows 213 and 158.)
 bool paired(const dsa_latent_attn_args& a) { return static_cast<long long>(a.T) * a.H > 128ll * a.B; }
 
 template <int NP>
@@ -1240,8 +1252,10 @@ int resident_clusters() {
     const cudaLaunchConfig_t cfg = config<NP>(1, attr);
     if (cudaFuncSetAttribute(latent_attn_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes)) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<NP>, &cfg) != cudaSuccess || n < 1)
-      n = 1;
+        cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<NP>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();  // (not to be found by a later launch)
+      return 1;
+    }
     known[d].store(n);
   }
   return n;

@@ -6,7 +6,9 @@
 // once; between lie two reductions over the row, of h^2 and of max |z|.  So the
 // kernel moves what it cannot do without, and is bound by HBM when there are
 // rows enough and by the launch, one trip to memory and the two reductions when
-// there are few.
+// there are few.  16384 rows of 7168 with a bf16 residual: y 138 us (6.83 TB/s, a
+// copy's rate), y and codes 165 us (6.41 TB/s; the quantiser's instructions beside
+// the loads), with an fp32 residual 228 us (6.70 TB/s); 8 such rows 2.6 and 3.7 us.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -63,9 +65,9 @@ __device__ __forceinline__ uint32_t code_of(float z, float s) {
 
 // The codes of 8 values.  A division costs as much as the rest of an element: t = z (1/s)
 // is within 127 * 2^-22 < 2^-14 of z / s, so its nearest whole number is the quotient's
-// unless t lies that near to a tie; then all 8 are divided (225 -> 196 us for 16384 rows
-// of 7168).  Adding 1.5 * 2^23 rounds to a whole number, ties to even, and leaves it in the
-// low byte.  |z| <= 127 s (1 + 2^-23): nothing has to be clamped.
+// unless t lies that near to a tie; then all 8 are divided.  Adding 1.5 * 2^23 rounds to a
+// whole number, ties to even, and leaves it in the low byte.  |z| <= 127 s (1 + 2^-23):
+// nothing has to be clamped.
 __device__ __forceinline__ uint2 codes_of(const float (&z)[8], float s, float r) {
   constexpr float kRound = 12582912.f;
   uint32_t c[8];
@@ -86,7 +88,9 @@ __device__ __forceinline__ uint2 codes_of(const float (&z)[8], float s, float r)
 }
 
 // kVec: D and every row allow vectors of 8 elements; else element by element,
-// neighbouring threads at neighbouring elements.
+// neighbouring threads at neighbouring elements (16384 rows of 7167: 548 us in place of
+// 165, for accesses of 64 bytes a warp; loads and stores interleaved 870, four chunks a
+// thread 790).
 template <int kChunks, int kThreads, bool kVec, bool kFp16, bool kRes32>
 __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const NormParams P) {
   __shared__ float part[2][32];
@@ -151,26 +155,35 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const NormParams 
       }
     }
   } else {
+    float b[kChunks][8];  // (every load before the first store, which the compiler cannot move it past)
 #pragma unroll
     for (int k = 0; k < kChunks; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int e = me + (k * 8 + i) * n;
-        float v = 0.f;
-        if (e < D) {
-          v = kFp16 ? __half2float(__ushort_as_half(x[e])) : __uint_as_float(static_cast<uint32_t>(x[e]) << 16);
-          if (res && kRes32) {
-            v += reinterpret_cast<const float*>(rin)[e];
-            reinterpret_cast<float*>(rout)[e] = v;
-          } else if (res) {
-            const __nv_bfloat16 s =
-                __float2bfloat16_rn(v + __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rin)[e]));
-            reinterpret_cast<__nv_bfloat16*>(rout)[e] = s;
-            v = __bfloat162float(s);
+        h[k][i] = b[k][i] = 0.f;
+        if (e >= D) continue;
+        h[k][i] = kFp16 ? __half2float(__ushort_as_half(x[e])) : __uint_as_float(static_cast<uint32_t>(x[e]) << 16);
+        if (res)
+          b[k][i] = kRes32 ? reinterpret_cast<const float*>(rin)[e]
+                           : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rin)[e]);
+      }
+    if (res) {
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = me + (k * 8 + i) * n;
+          h[k][i] += b[k][i];
+          if (!kRes32) {
+            const __nv_bfloat16 s = __float2bfloat16_rn(h[k][i]);
+            h[k][i] = __bfloat162float(s);
+            if (e < D) reinterpret_cast<__nv_bfloat16*>(rout)[e] = s;
+          } else if (e < D) {
+            reinterpret_cast<float*>(rout)[e] = h[k][i];
           }
         }
-        h[k][i] = v;
-      }
+    }
   }
 
   float sum = 0.f;
@@ -227,10 +240,11 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const NormParams 
       if (e >= D) continue;
       *reinterpret_cast<uint2*>(a.codes + row * a.D + e) = fine ? codes_of(h[k], s, inv_s) : make_uint2(0u, 0u);
     } else {
+      const uint2 c = fine ? codes_of(h[k], s, inv_s) : make_uint2(0u, 0u);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int e = me + (k * 8 + i) * n;
-        if (e < D) a.codes[row * a.D + e] = fine ? static_cast<int8_t>(code_of(h[k][i], s)) : 0;
+        if (e < D) a.codes[row * a.D + e] = static_cast<int8_t>((i < 4 ? c.x : c.y) >> (i % 4 * 8));
       }
     }
   }
@@ -252,10 +266,11 @@ int launch_add_rmsnorm(const dsa_add_rmsnorm_args& a, cudaStream_t s) {
                    aligned(a.residual, 16) && aligned(a.residual_out, 16) && a.residual_stride * rsize % 16 == 0 &&
                    a.residual_out_stride * rsize % 16 == 0 && aligned(a.y, 16) && aligned(a.codes, 8);
   const int chunks = (a.D + 7) / 8;
-  // Threads of a row.  Few rows: one chunk each, so that a row is one trip to memory (8 rows
-  // of 7168 2.7 us).  Rows enough to fill the SMs: four chunks each, so that more rows are
-  // on their way while others reduce.  Rows of up to 32 chunks: 8 to 32 threads, several
-  // rows a CTA.
+  // Threads of a row.  Few rows: one chunk each, so that a row is one trip to memory.  Rows
+  // enough to fill the SMs: four chunks each, so that more rows are on their way while
+  // others reduce (16384 rows of 7168, y and codes: 225 us with one chunk each and a
+  // division a code, 165 with four and the codes as above).  Rows of up to 32 chunks: 8 to
+  // 32 threads, several rows a CTA.
   const bool many = a.T > 4 * sm_count();
   int per = 1;
   while ((chunks + per - 1) / per > 1024) per *= 2;

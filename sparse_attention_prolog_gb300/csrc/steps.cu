@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(1024) step_maps_kernel(const dsa_step_maps_arg
     P.pos[t] = pos;
     P.slot[t] = slot;
   }
+  __threadfence();  // (a kernel two further on may read pos and seq_of_token without a wait)
 }
 
 }  // namespace
