@@ -475,7 +475,7 @@ static int check_latent_attn(const dsa_latent_attn_args* a) {
   if (a->B > 65535 || a->H > 1024 || a->cache_rows > INT32_MAX ||
       static_cast<long long>(a->T) * a->H >= INT32_MAX - 255)
     return DSA_ERR_UNSUPPORTED;
-  if (bad_ptr(a->q, 16) || bad_ptr(a->kv, 16) || bad_ptr(a->out, 16) || bad_ptr(a->kv_len, 4)) return DSA_ERR_INVALID_ARG;
+  if (bad_ptr(a->q, 16) || bad_ptr(a->kv, 16) || bad_ptr(a->out, 32) || bad_ptr(a->kv_len, 4)) return DSA_ERR_INVALID_ARG;
   if (!aligned(a->lse, 4) || !aligned(a->sink, 4) || !aligned(a->cu_tokens, 4)) return DSA_ERR_INVALID_ARG;
   if (a->block_table) {
     if (!aligned(a->block_table, 4) || a->block_size < 1) return DSA_ERR_INVALID_ARG;

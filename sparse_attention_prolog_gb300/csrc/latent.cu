@@ -24,14 +24,28 @@
 //       at a block's end.
 //
 // With NP = 1, a warp of the PV CTA fetches the rows of later tiles into the L2: the K ring
-// is one tile, and HBM's latency beside the products is longer than a tile's time (538 ->
-// 502 us for 32 sequences of 4096 to 131072 rows; from the QK CTA, whose own copies then
-// wait behind the fetches, it costs more than it gives).
+// is one tile, and HBM's latency beside the products is longer than a tile's time (542 ->
+// 502 us for 32 sequences of 4096 to 131072 rows; four tiles ahead 537, and from the QK CTA,
+// whose own copies then wait behind the fetches, it costs more than it gives).  It begins
+// when the first rows of V are there, or q would wait behind it (one token at 128K 61 -> 59
+// us; and two tiles ahead in place of three 57).
 //
 // What bounds such a kernel first is not a unit but the single threads that feed them:
 // every instruction of theirs takes some five clocks, so their loops are unrolled over a
 // tile's units with slots and phases that need no arithmetic, barriers have constant
-// addresses, and a tile has few units.
+// addresses, and a tile has few units (nine of K in place of three: 2.25 us a tile in place
+// of 1.97 with every row in the L2).  The loaders of K and of V are loops of their own for
+// the same reason (one loop with both: 2.25).
+//
+// Without its loads a tile takes 1.55 us, without its products 1.4, without either 1.17
+// (the softmax and P's way); with them NP = 1 takes 1.97 from the L2 and 2.1 from HBM, whose
+// rate allows 1.65.  What holds it is the K ring: an SM takes 64 bytes a clock from the L2,
+// so a tile of K needs 1.1 us on its way, and a slot is empty while its unit is multiplied.
+// NP = 2, whose rings are two tiles, takes 1.3 to 1.4 (its products alone 1.1).
+//
+// A block's q comes through the K ring, which it fills, and goes on into tensor memory: one
+// trip for all of it (through the three staging slots of P, three trips: one token over 1000
+// rows 25 us in place of 22, 8 x 64 tokens over 1000 rows 174 in place of 162).
 //
 // NP = 1: a cluster is one QK and one PV CTA.  NP = 2: two of each, for sequences
 // of more than 128 rows: the two QK CTAs run one MMA of M = 256 (cta_group::2), each
@@ -60,9 +74,10 @@ constexpr int kHalfBytes = 128 * 128;            // 64 columns of a P tile
 constexpr uint32_t kTmemS = 256;                 // QK: q's latent part in columns [0, 256), then two S buffers
 constexpr int kThreads = 384;                    // 8 softmax / output warps, a loader, an MMA issuer, two for news
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kNewsWarp = 11;
-// A cluster takes at least this many tiles: splitting further costs more in the
-// merge than it saves.
-constexpr int kMinTiles = 2;
+// A cluster's stretch has at least this many tiles.  (One token over 1000 rows: 22 us, with
+// at least six 31; with one, a call that needs no merge may get it: 4 heads over 256 rows 17
+// us in place of 16.)
+constexpr int kMinShare = 2;
 constexpr int kMaxClusters = 256;
 
 // The rings: slots of a unit, [atoms][rows][128 bytes].  K: three atoms of all rows of a
@@ -73,14 +88,17 @@ struct Ring {
   static constexpr int kKRows = kTile / NP, kKAtoms = 3, kKUnits = kAtomsK / kKAtoms;
   static constexpr int kKBytes = kKAtoms * kKRows * 128, kKSlots = kKUnits * NP;
   static constexpr int kKLoaders = NP == 1 ? 3 : 1;  // warps that load K, a share of a unit's atoms each
+  // A block's q fills the ring before its first tile: a load has the bytes that a loader's
+  // part of a unit of K has (an atom of 128 rows, or three of 64).
+  static constexpr int kQUnits = 3 * NP, kQAtoms = NP == 1 ? 1 : 3, kQLoads = 9 / kQAtoms * NP;
+  static constexpr int kQBytes = kKBytes / kKLoaders;
   static constexpr int kVRows = 64, kVAtoms = 4 / NP, kVUnits = 4;
   static constexpr int kVBytes = kVAtoms * kVRows * 128, kVSlots = kVUnits * NP;
 };
 constexpr int kMaxKSlots = 6, kMaxVSlots = 8;
 constexpr int kPSlots = 5, kStages = 3;  // slots of half a tile's P, in the PV CTA and where it is staged
-constexpr int kQRounds = 3, kQAtoms = 3; // a block's q comes through the staging slots
-constexpr int kAhead = 3;  // tiles between V's loads and the rows that are fetched into the L2
-static_assert(kQAtoms == kStages && kQRounds * kQAtoms == kAtomsK, "q's way");
+constexpr int kMaxQUnits = 6, kMaxQLoads = 9;
+constexpr int kAhead = 2;  // tiles between V's loads and the rows that are fetched into the L2
 
 // Shared memory of a QK CTA: K ring, staging slots of P, q's rotary part, OwnQk.  Of a PV
 // CTA: V ring, P slots, the rescale factors.  Behind them, in both, Shared.
@@ -111,6 +129,7 @@ struct LatentParams {
   float* lse;
   const float* sink;
   int clusters;
+  int start;        // tiles that a block's beginning counts as
   float* part_o;    // [2 clusters][64][128 NP][8]: the first and the last part of a stretch, 8 columns of all rows together
   float2* part_ml;  // [2 clusters][128 NP]: (maximum, sum) in log2 units
   int block_rows;   // 128 NP
@@ -126,7 +145,7 @@ struct __align__(8) Bars {
   uint64_t sfull[2], sempty[2];
   uint64_t pfree[kPSlots];        // QK: a P slot of the PV CTA is free
   uint64_t landed[kStages];       // QK: what a staging slot held has arrived there
-  uint64_t qload, qread;          // QK: three atoms of q are in the staging slots; every warp has read them
+  uint64_t qload[kMaxQLoads], qread[kMaxQUnits];  // QK: a part of q is in the K ring; a slot's part has been read
   uint64_t mready[4];             // QK: both halves' maxima are known, per pair of warps
   uint64_t qfull;                 // a block's q is in place
   uint64_t ffree;                 // QK: the final (m, l) have been read
@@ -165,10 +184,6 @@ struct Piece {
 template <int NP>
 struct Walker {
   static constexpr int kBlock = 128 * NP;
-  // What a block costs beside its tiles (its q, its output, the pipeline's start), in
-  // tiles: stretches are equal with it counted in front of each block.  (Without: 16 heads
-  // over 700 to 9000 rows 88 us in place of 80, 4 x 2 tokens at 64K 115 in place of 109.)
-  static constexpr int kStart = 2 + 2 * NP;
   long long left;
   int b, blk, off;
   int n, c0, len, nt, nb;
@@ -182,7 +197,7 @@ struct Walker {
       n = P.n_q;
     }
     len = min(max(__ldg(P.kv_len + b), 0), P.max_L);
-    nt = max(1, (len - 1) / kTile + 1) + kStart;  // kStart empty ones in front
+    nt = max(1, (len - 1) / kTile + 1) + P.start;  // so many empty ones in front
     nb = (n * P.H + kBlock - 1) / kBlock;
   }
   __device__ __forceinline__ void start(const LatentParams& P, int b0, long long at, long long count) {
@@ -211,7 +226,7 @@ struct Walker {
         off = 0;
         ++blk;
       }
-      if (stop <= kStart) continue;  // none of the block's tiles: it begins in the next stretch
+      if (stop <= P.start) continue;  // none of the block's tiles: it begins in the next stretch
       p.b = b;
       p.len = len;
       p.row0 = c0 * P.H + block * kBlock;
@@ -219,9 +234,9 @@ struct Walker {
       p.in_seq = block * kBlock;
       p.first_vis = len - n + 1;
       p.vis = max(0, p.first_vis + (block * kBlock + p.rows - 1) / P.H);
-      p.t0 = max(0, from - kStart);
-      p.t1 = max(p.t0, min(stop - kStart, (p.vis + kTile - 1) / kTile));
-      p.begins = from <= kStart;
+      p.t0 = max(0, from - P.start);
+      p.t1 = max(p.t0, min(stop - P.start, (p.vis + kTile - 1) / kTile));
+      p.begins = from <= P.start;
       p.ends = stop == nt;
       p.to_end = nt - stop;
       return true;
@@ -409,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.pcons[i], 1);
     }
     for (int i = 0; i < kStages; ++i) mbar_init(&bars.landed[i], 1);
-    mbar_init(&bars.qload, 1);
-    mbar_init(&bars.qread, 8);
+    for (int i = 0; i < R::kQLoads; ++i) mbar_init(&bars.qload[i], 1);
+    for (int i = 0; i < R::kQUnits; ++i) mbar_init(&bars.qread[i], 8 / NP);
     for (int i = 0; i < 4; ++i) mbar_init(&bars.mready[i], 2);
     mbar_init(&bars.qfull, 8 * NP);
     mbar_init(&bars.ffree, 8);
@@ -460,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (i < warp) before += sh.scan[i];
     total += sh.scan[i];
   }
-  const long long active = max(1ll, min(static_cast<long long>(P.clusters), total / (kMinTiles + Walker<NP>::kStart)));
+  const long long active = max(1ll, min(static_cast<long long>(P.clusters), total / kMinShare));
   // stretch c begins at share c + min(c, rest)
   const long long share = total / active, rest = total - share * active;
   const long long lo = cluster < active ? share * cluster + min(static_cast<long long>(cluster), rest) : total;
@@ -504,8 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t peer_pfull = mapa(smem_u32(&bars.pfull[0]), peer);
     const uint32_t peer_ffull = mapa(smem_u32(&bars.ffull), peer);
     const uint64_t scale2 = pack_f32x2(P.scale_log2, P.scale_log2), one2 = pack_f32x2(1.f, 1.f);
-    int G = 0, pieces = 0, rounds = 0;  // tiles, blocks and loads of q so far
-    bool loading = false;               // (warp 0) a load of q is on its way
+    int G = 0, pieces = 0, blocks = 0;  // tiles, pieces and blocks with tiles so far
     auto fetch_q = [&](const Piece& b) {  // four rows a lane
       const int64_t from = static_cast<int64_t>(b.row0) + side * 128 + lane * 4;
       const int64_t n = min(static_cast<int64_t>(4), static_cast<int64_t>(b.row0) + b.rows - from);
@@ -515,59 +529,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && w.next(P, p)) {
       const int nt = p.t1 - p.t0, in_block = side * 128 + row;
       if (nt > 0) {
-        // q, three atoms at a time through the staging slots (free once what they held
-        // has arrived): this row's latent atoms into tensor memory, half of them each
+        // q: this row's latent atoms go from the K ring into tensor memory, half of them each
         // group, the rotary atom into its own place.  The products that read the last
         // block's are complete: every warp has seen its last S.
-        if (warp == 7) {  // the later rounds' rows and the next block's come from the L2
-          if (G == 0) fetch_q(p);
+        if (warp == 7) {  // the next block's comes from the L2
           Walker<NP> after = w;
           Piece next;
           if (after.next(P, next)) fetch_q(next);
         }
-        if (warp == 0) {
-          for (int i = 0; ok && i < kStages; ++i) {
-            const int last = 2 * G - 1 - i;  // the last half that was staged, and the two before
-            ok = last < 0 || warp_wait<false>(&bars.landed[last % kStages], (last / kStages) & 1, P.err, abort_v);
-          }
-        }
-        for (int r = 0; ok && r < kQRounds; ++r, ++rounds) {
-          if (warp == 0) {
-            ok = rounds == 0 || warp_wait<false>(&bars.qread, (rounds & 1) ^ 1, P.err, abort_v);
-            if (!ok) break;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&bars.qload, kQAtoms * kHalfBytes);
-              load_box(smem + kOffStage, &q_map, r * kQAtoms, p.row0 + side * 128, &bars.qload);
-            }
-            loading = true;
-          }
-          ok = warp_wait<false>(&bars.qload, rounds & 1, P.err, abort_v);
-          if (!ok) break;
-          loading = false;
 #pragma unroll 1
-          for (int i = 0; i < kQAtoms; ++i) {
-            const int a = r * kQAtoms + i;
-            if ((a & 1) != g) continue;
-            const uint8_t* src = smem + kOffStage + i * kHalfBytes;
-            uint32_t v[32];
+        for (int a = g; ok && a < kAtomsK; a += 2) {
+          const int load = NP == 1 ? a : a / 3 * 2 + (row >> 6);  // (of a warp: its rows are of one part)
+          ok = warp_wait<false>(&bars.qload[load], blocks & 1, P.err, abort_v);
+          if (!ok) break;
+          const uint8_t* src = NP == 1 ? smem + a * kHalfBytes
+                                       : smem + ((G & 1) * R::kKUnits + load) % R::kKSlots * R::kKBytes + a % 3 * (kHalfBytes / 2);
+          uint32_t v[32];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint4 x = *reinterpret_cast<const uint4*>(src + sw128_off(row, c));
-              v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
-            }
-            if (a < kAtomsK - 1) {
-              tmem_st32(tmem + lane_off + a * 32, v);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4*>(smem + kOffQrope + sw128_off(row, c)) =
-                    make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-              fence_proxy_async_smem();
-            }
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + sw128_off(NP == 1 ? row : row & 63, c));
+            v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.qread);
+          if (a < kAtomsK - 1) {
+            tmem_st32(tmem + lane_off + a * 32, v);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(smem + kOffQrope + sw128_off(row, c)) =
+                  make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            fence_proxy_async_smem();
+          }
+          if (a + 2 >= a / 3 * 3 + 3) {  // this group's last of the slot
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.qread[NP == 1 ? a / 3 : load]);
+          }
         }
+        ++blocks;
         if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
@@ -648,8 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_remote(peer_ffull);
       ++pieces;
     }
-    if (!ok) {  // copies on their way, of q and to the PV CTA, land before either CTA leaves
-      if (loading) mbar_drain(&bars.qload, rounds & 1);
+    if (!ok) {  // copies on their way to the PV CTA land before either CTA leaves
       const uint64_t since = globaltimer_ns();
       while (globaltimer_ns() - since < 200000) __nanosleep(1000);
     }
@@ -758,8 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (in_block < p.rows) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(o + c0 + 8 * k) = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+            for (int k = 0; k < 2; ++k) st_global_v8(reinterpret_cast<float*>(o + c0 + 16 * k), pk + 8 * k);
           }
         }
       } else {
@@ -795,79 +790,120 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
     }
     if (tid == 0 && side == 0) P.desc[cluster] = make_int4(tail_row0, tail_rows, tail_parts, 0);
-  } else if (warp == kLoadWarp || (NP == 1 && role == 0 && warp > kMmaWarp)) {
-    // ------------------------------------------------------------ K or V
+  } else if (role == 0 && (warp == kLoadWarp || (NP == 1 && warp > kMmaWarp))) {
+    // ------------------------------------------------------------ q and K
     // Each lane has a box of the tile's rows (a page, or all rows of a unit): it looks up the
     // next tile's while it issues this one's.
-    const int box = role == 0 ? P.k_box : P.v_box, tile_rows = role == 0 ? R::kKRows : kTile;
-    const int boxes = tile_rows / box, skip = role == 0 ? side * R::kKRows : 0;  // boxes of a tile's rows that this CTA loads
-    const bool report = role == 1 && side == 0;  // (a PV CTA looks up every row)
-    const bool plain = box == (role == 0 ? R::kKRows : R::kVRows);  // a box has all rows of a unit, and its atoms
+    const int boxes = R::kKRows / P.k_box, from = side * R::kKRows + lane * P.k_box;
+    const bool plain = P.k_box == R::kKRows;  // a box has all rows of a unit, and its atoms
     const int which = warp == kLoadWarp ? 0 : warp - kMmaWarp;
-    int G = 0, issued = 0;
+    int G = 0, issued = 0, blocks = 0, q_issued = 0;  // tiles, units, blocks with tiles and loads of q so far
     bool ok = true;
-    auto look_up = [&](int t) {
-      return t < p.t1 && lane < boxes ? box_row(P, p, t * kTile + skip + lane * box, report) : 0;
-    };
+    auto look_up = [&](int t) { return t < p.t1 && lane < boxes ? box_row(P, p, t * kTile + from, false) : 0; };
     while (ok && w.next(P, p)) {
       if (p.t0 >= p.t1) continue;
       int row = look_up(p.t0);
-      for (int t = p.t0; t < p.t1; ++t, ++G) {
+      // q, into every slot of the ring, once the last block's is read and its K used up
+      if (lane == 0) {
+#pragma unroll 1
+        for (int u = 0; u < R::kQUnits; ++u)
+          ok = ok && (blocks == 0 || thread_wait<false>(&bars.qread[u], (blocks & 1) ^ 1, P.err, abort_v));
+#pragma unroll 1
+        for (int u = 0; ok && u < R::kQUnits; ++u) {
+          // (the phase that the slot's next unit of K waits for)
+          const int tile = NP == 1 ? G : G + u / R::kKUnits, slot = ((NP == 1 ? 0 : G & 1) * R::kKUnits + u) % R::kKSlots;
+          const int load = NP == 1 ? u * R::kKLoaders + which : u;
+          ok = thread_wait<false>(&bars.kempty[slot], ((NP == 1 ? tile : tile >> 1) & 1) ^ 1, P.err, abort_v);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars.qload[load], R::kQBytes);
+          load_box(smem + slot * R::kKBytes + which * R::kQBytes, &q_map, NP == 1 ? load : u / 2 * R::kQAtoms,
+                   p.row0 + side * 128 + (NP == 1 ? 0 : u % 2 * 64), &bars.qload[load]);
+          ++q_issued;
+        }
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int u = 0; u < R::kQUnits; ++u)
+        ok = ok && thread_wait<false>(&bars.qread[u], blocks & 1, P.err, abort_v);
+      ++blocks;
+      ok = __all_sync(0xffffffffu, ok);
+      for (int t = p.t0; ok && t < p.t1; ++t, ++G) {
+        const int next_row = look_up(t + 1);
+        if (lane < boxes) {
+          const int ring = NP == 1 ? 0 : G & 1;
+          const uint32_t use = ((NP == 1 ? G : G >> 1) & 1) ^ 1;
+#pragma unroll
+          for (int u = 0; u < R::kKUnits; ++u) {
+            constexpr int kAtoms = R::kKAtoms / R::kKLoaders;
+            const int slot = ring * R::kKUnits + u;
+            ok = ok && thread_wait<false>(&bars.kempty[slot], use, P.err, abort_v);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bars.kfull[slot], R::kKBytes / R::kKLoaders);
+            uint8_t* dst = smem + slot * R::kKBytes + (which * kAtoms * R::kKRows + lane * P.k_box) * 128;
+            if (plain) {
+              load_box(dst, &k_map, u * R::kKAtoms + which * kAtoms, row, &bars.kfull[slot]);
+            } else {
+#pragma unroll
+              for (int a = 0; a < kAtoms; ++a)
+                load_box(dst + a * R::kKRows * 128, &k_map, u * R::kKAtoms + which * kAtoms + a, row, &bars.kfull[slot]);
+            }
+            ++issued;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        row = next_row;
+      }
+    }
+    if (!ok && lane == 0) {  // copies in flight land before the CTA leaves
+      for (int i = max(0, issued - R::kKSlots); i < issued; ++i)
+        if (!mbar_drain(&bars.kfull[i % R::kKSlots], (i / R::kKSlots) & 1)) break;
+      constexpr int kMine = R::kQLoads / R::kKLoaders;  // loads of a block's q by this warp
+      for (int i = max(0, q_issued - kMine); i < q_issued; ++i)
+        if (!mbar_drain(&bars.qload[i % kMine * R::kKLoaders + which], (i / kMine) & 1)) break;
+    }
+  } else if (role == 1 && warp == kLoadWarp) {
+    // ------------------------------------------------------------------ V
+    const int boxes = kTile / P.v_box, per = boxes / 2;
+    const int group = lane >= per;  // this lane's box is in the units of rows 64 group ..
+    const bool plain = P.v_box == R::kVRows;
+    int G = 0, issued = 0;
+    bool ok = true;
+    auto look_up = [&](int t) { return t < p.t1 && lane < boxes ? box_row(P, p, t * kTile + lane * P.v_box, side == 0) : 0; };
+    while (ok && w.next(P, p)) {
+      if (p.t0 >= p.t1) continue;
+      int row = look_up(p.t0);
+      for (int t = p.t0; ok && t < p.t1; ++t, ++G) {
         const int next_row = look_up(t + 1);
         if (lane == 0) sh.progress = G;
         if (lane < boxes) {
           const int ring = NP == 1 ? 0 : G & 1;
           const uint32_t use = ((NP == 1 ? G : G >> 1) & 1) ^ 1;
-          if (role == 0) {
 #pragma unroll
-            for (int u = 0; u < R::kKUnits; ++u) {
-              constexpr int kAtoms = R::kKAtoms / R::kKLoaders;
-              const int slot = ring * R::kKUnits + u;
-              ok = ok && thread_wait<false>(&bars.kempty[slot], use, P.err, abort_v);
-              if (!ok) break;
-              if (lane == 0) mbar_arrive_expect_tx(&bars.kfull[slot], R::kKBytes / R::kKLoaders);
-              uint8_t* dst = smem + slot * R::kKBytes + (which * kAtoms * R::kKRows + lane * box) * 128;
+          for (int u = 0; u < R::kVUnits; ++u) {
+            const int slot = ring * R::kVUnits + u, atom = (u & 1) * 4 + side * R::kVAtoms;
+            ok = ok && thread_wait<false>(&bars.vempty[slot], use, P.err, abort_v);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bars.vfull[slot], R::kVBytes);
+            uint8_t* dst = smem + slot * R::kVBytes + (lane - group * per) * P.v_box * 128;
+            if (group == u >> 1) {
               if (plain) {
-                load_box(dst, &k_map, u * R::kKAtoms + which * kAtoms, row, &bars.kfull[slot]);
+                load_box(dst, &v_map, atom, row, &bars.vfull[slot]);
               } else {
 #pragma unroll
-                for (int a = 0; a < kAtoms; ++a)
-                  load_box(dst + a * R::kKRows * 128, &k_map, u * R::kKAtoms + which * kAtoms + a, row, &bars.kfull[slot]);
+                for (int a = 0; a < R::kVAtoms; ++a)
+                  load_box(dst + a * R::kVRows * 128, &v_map, atom + a, row, &bars.vfull[slot]);
               }
-              ++issued;
             }
-          } else {
-            const int per = boxes / 2, group = lane >= per;  // boxes of a unit; this lane's is in the units of rows 64 group ..
-#pragma unroll
-            for (int u = 0; u < R::kVUnits; ++u) {
-              const int slot = ring * R::kVUnits + u, atom = (u & 1) * 4 + side * R::kVAtoms;
-              ok = ok && thread_wait<false>(&bars.vempty[slot], use, P.err, abort_v);
-              if (!ok) break;
-              if (lane == 0) mbar_arrive_expect_tx(&bars.vfull[slot], R::kVBytes);
-              uint8_t* dst = smem + slot * R::kVBytes + (lane - group * per) * box * 128;
-              if (group == u >> 1) {
-                if (plain) {
-                  load_box(dst, &v_map, atom, row, &bars.vfull[slot]);
-                } else {
-#pragma unroll
-                  for (int a = 0; a < R::kVAtoms; ++a)
-                    load_box(dst + a * R::kVRows * 128, &v_map, atom + a, row, &bars.vfull[slot]);
-                }
-              }
-              ++issued;
-            }
+            ++issued;
           }
         }
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
         row = next_row;
       }
     }
-    if (!ok && lane == 0) {  // copies in flight land before the CTA leaves
-      const int slots = role == 0 ? R::kKSlots : R::kVSlots;
-      uint64_t* full = role == 0 ? bars.kfull : bars.vfull;
-      for (int i = max(0, issued - slots); i < issued; ++i)
-        if (!mbar_drain(&full[i % slots], (i / slots) & 1)) break;
+    if (!ok && lane == 0) {
+      for (int i = max(0, issued - R::kVSlots); i < issued; ++i)
+        if (!mbar_drain(&bars.vfull[i % R::kVSlots], (i / R::kVSlots) & 1)) break;
     }
   } else if (warp == kMmaWarp && side == 0 && elect_one()) {
     const uint16_t both = role == 0 ? 3 : 12;
@@ -1019,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = p.t0; ok && t < p.t1; ++t, ++G) {
         const int row = lane < kTile / 8 ? box_row(P, p, t * kTile + lane * 8, false) : static_cast<int>(P.cache_rows);
         const uint64_t since = globaltimer_ns();
-        while (ok && G > sh.progress + kAhead) {
+        while (ok && (G > sh.progress + kAhead || (G == 0 && sh.progress == 0 && !mbar_test(&bars.vfull[0], 0)))) {
           __nanosleep(64);
           ok = !*abort_v && globaltimer_ns() - since <= wait_limit_ns(P.err);
         }
@@ -1261,13 +1297,23 @@ int resident_clusters() {
   return n;
 }
 
+// The most blocks that the shape allows: every sequence but one may end in a block's first row.
+long long most_blocks(const dsa_latent_attn_args& a) {
+  const long long block = paired(a) ? 256 : 128;
+  return (static_cast<long long>(a.T) * a.H + std::min(a.T, a.B) * (block - 1)) / block;
+}
+
+// What a block costs beside its tiles (its q, its output, the pipeline's start), in tiles:
+// stretches are equal with it counted in front of each block.  (Without: 16 heads over 700
+// to 9000 rows 88 us in place of 81, 4 x 2 tokens at 64K 107 in place of 102.)  A single
+// block begins but once in any stretch.
+int start_tiles(const dsa_latent_attn_args& a) { return most_blocks(a) == 1 ? 0 : paired(a) ? 6 : 3; }
+
 // Clusters of a call: as many as the device holds, but no more than the most tiles
 // that the shape allows can keep busy.
 int cluster_count(const dsa_latent_attn_args& a) {
-  const int block = paired(a) ? 256 : 128;
-  const long long blocks = (static_cast<long long>(a.T) * a.H + block - 1) / block + a.B;
-  const long long tiles = blocks * ((static_cast<long long>(a.max_L) + kTile - 1) / kTile);
-  const long long most = paired(a) ? resident_clusters<2>() : resident_clusters<1>(), want = tiles / kMinTiles;
+  const long long tiles = most_blocks(a) * ((static_cast<long long>(a.max_L) + kTile - 1) / kTile + start_tiles(a));
+  const long long most = paired(a) ? resident_clusters<2>() : resident_clusters<1>(), want = tiles / kMinShare;
   return static_cast<int>(std::min<long long>(kMaxClusters, std::max(1ll, std::min(want, most))));
 }
 
@@ -1304,7 +1350,7 @@ int launch(LatentParams& P, const dsa_latent_attn_args& a, cudaStream_t s) {
   alignas(64) CUtensorMap k_map, v_map, q_map;
   if (!encode_boxes(k_map, a.kv, a.cache_rows, P.k_box, P.k_box == R::kKRows ? R::kKAtoms / R::kKLoaders : 1) ||
       !encode_boxes(v_map, a.kv, a.cache_rows, P.v_box, P.v_box == R::kVRows ? R::kVAtoms : 1) ||
-      !encode_boxes(q_map, a.q, static_cast<int64_t>(a.T) * a.H, 128, kQAtoms))
+      !encode_boxes(q_map, a.q, static_cast<int64_t>(a.T) * a.H, R::kKRows, R::kQAtoms))
     return DSA_ERR_CUDA;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = config<NP>(P.clusters, attr);
@@ -1335,6 +1381,7 @@ int launch_latent_attn(const dsa_latent_attn_args& a, void* ws, cudaStream_t s) 
   P.lse = a.lse;
   P.sink = a.sink;
   P.clusters = cluster_count(a);
+  P.start = start_tiles(a);
   P.block_rows = paired(a) ? 256 : 128;
   const Workspace at(P.clusters, P.block_rows);
   P.part_o = static_cast<float*>(ws);

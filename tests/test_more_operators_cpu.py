@@ -72,7 +72,7 @@ def test_latent_attn_refuses(lib):  # noqa: F811
     assert size() > 0 and call() == WORKSPACE and size(**paged) > 0 and size(cu_tokens=p[5], T=5) > 0
     for kw in ({"T": -1}, {"B": 0}, {"H": 0}, {"max_L": 0}, {"cache_rows": 0}, {"scale": 0.0}, {"scale": -1.0},
                {"scale": float("nan")}, {"scale": float("inf")}, {"n_q": 3}, {"n_q": 0}, {"T": 7}, {"cache_rows": 4 * 4096 - 1},
-               {"q": 0}, {"kv": 0}, {"out": 0}, {"kv_len": 0}, {"q": BASE + 8}, {"kv": BASE + 8}, {"out": BASE + 8},
+               {"q": 0}, {"kv": 0}, {"out": 0}, {"kv_len": 0}, {"q": BASE + 8}, {"kv": BASE + 8}, {"out": BASE + 16},
                {"kv_len": BASE + 2}, {"lse": BASE + 2}, {"sink": BASE + 2}, {"cu_tokens": BASE + 2},
                {**paged, "max_blocks": 63}, {**paged, "block_size": 0}, {**paged, "block_table": p[4] + 2}):
         assert call(**kw) == INVALID and size(**kw) == 0, kw
