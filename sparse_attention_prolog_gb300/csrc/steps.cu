@@ -4,10 +4,13 @@
 // Two running sums over the requests (tokens, new pages) decide everything: a
 // token finds its request, and a new page its own, by a binary search of them.
 // B is at most 8192, so every CTA forms both sums itself in shared memory (one
-// read of 8 B bytes, from L2 after the first CTA) and then fills its own stretch
-// of the tables; nothing passes between CTAs, and no page entry that this step
-// writes is read (a new page is looked up in the free list).  What bounds it is
-// the launch and three dependent trips to memory: lengths, page entries, stores.
+// read of 8 B bytes, from L2 after the first CTA, held in registers) and then
+// fills its own stretch of the tables; nothing passes between CTAs, and no page
+// entry that this step writes is read (a new page is looked up in the free list).
+// What bounds it is the launch and three dependent trips to memory: lengths, page
+// entries, stores.  In a graph 32 requests of a token take 3.0 us, 300 with five
+// prompt chunks 4.8, 4096 with forty 9.1 (lengths read again in every pass and
+// two tokens a thread: 3.6, 6.0 and 12.0).
 #include <cuda_runtime.h>
 #include "dsa_internal.h"
 #include "dsa_ptx.cuh"
@@ -44,42 +47,46 @@ __device__ __forceinline__ int owner(const int* run, int n, int v) {
   return lo;
 }
 
+// kEach: requests of a thread, which follow one another (read once, in registers).
+template <int kEach>
 __global__ void __launch_bounds__(1024) step_maps_kernel(const dsa_step_maps_args P, uint32_t* err) {
-  extern __shared__ int run[];  // tokens before request b [B + 1], then pages before it [B + 1]
+  extern __shared__ int run[];  // tokens before request b [B + 1], pages before it [B + 1], cached [B], pages held [B]
   __shared__ Sums warp_sum[32];
   __shared__ int cut_sh;       // the first request that is not served
   __shared__ int total_sh[2];  // tokens and pages of those that are
   int* run_tok = run;
   int* run_page = run + P.B + 1;
+  int* cached = run_page + P.B + 1;
+  int* held = cached + P.B;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   if (tid == 0) cut_sh = P.B;
   griddep_wait();
   const int head = P.free_head == nullptr ? 0 : __ldg(P.free_head);
   const long long avail = head < 0 ? -1 : static_cast<long long>(P.n_free) - head;
   const long long most = static_cast<long long>(P.max_blocks) * P.block_size;
-  const int each = (P.B + threads - 1) / threads;  // consecutive requests of a thread
-  const int b0 = min(P.B, tid * each), b1 = min(P.B, b0 + each);
+  const int b0 = tid * kEach;
 
-  auto request = [&](int b, int& c, int& f, int& old, int& last) {  // false: its lengths cannot be served
-    c = __ldg(P.cached + b);
-    f = __ldg(P.fresh + b);
-    old = last = 0;
-    if (c < 0 || f < 0 || static_cast<long long>(c) + f > most) return false;
-    old = c / P.block_size + (c % P.block_size != 0);
-    last = (c + f) / P.block_size + ((c + f) % P.block_size != 0);
-    return true;
-  };
-
+  int c[kEach], f[kEach], old[kEach], fresh_pages[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const bool on = b0 + i < P.B;
+    c[i] = on ? __ldg(P.cached + b0 + i) : 0;
+    f[i] = on ? __ldg(P.fresh + b0 + i) : 0;
+  }
   Sums own{0, 0};
   int first_bad = P.B;
-  for (int b = b0; b < b1; ++b) {
-    int c, f, old, last;
-    if (request(b, c, f, old, last)) {
-      own.tok += f;
-      own.page += last - old;
-    } else {
-      first_bad = min(first_bad, b);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    old[i] = fresh_pages[i] = 0;
+    if (b0 + i >= P.B) continue;
+    if (c[i] < 0 || f[i] < 0 || static_cast<long long>(c[i]) + f[i] > most) {  // lengths that cannot be served
+      first_bad = min(first_bad, b0 + i);
+      continue;
     }
+    old[i] = c[i] / P.block_size + (c[i] % P.block_size != 0);
+    fresh_pages[i] = (c[i] + f[i]) / P.block_size + ((c[i] + f[i]) % P.block_size != 0) - old[i];
+    own.tok += f[i];
+    own.page += fresh_pages[i];
   }
   Sums inc = warp_inclusive(own, lane);
   if (lane == 31) warp_sum[warp] = inc;
@@ -97,12 +104,12 @@ __global__ void __launch_bounds__(1024) step_maps_kernel(const dsa_step_maps_arg
   }
   {  // the first request whose running sums pass a limit
     Sums s = at;
-    for (int b = b0; b < b1 && b < first_bad; ++b) {
-      int c, f, old, last;
-      request(b, c, f, old, last);
-      s.tok += f;
-      s.page += last - old;
-      if (s.tok > P.T || s.page > avail) first_bad = b;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (b0 + i >= first_bad) break;
+      s.tok += f[i];
+      s.page += fresh_pages[i];
+      if (s.tok > P.T || s.page > avail) first_bad = b0 + i;
     }
   }
   if (first_bad < P.B) atomicMin(&cut_sh, first_bad);
@@ -113,13 +120,13 @@ __global__ void __launch_bounds__(1024) step_maps_kernel(const dsa_step_maps_arg
     total_sh[0] = static_cast<int>(all.tok);
     total_sh[1] = static_cast<int>(all.page);
   }
-  if (b0 <= cut && cut < b1) {  // sums before the cut
+  if (b0 <= cut && cut < min(P.B, b0 + kEach)) {  // sums before the cut
     Sums s = at;
-    for (int b = b0; b < cut; ++b) {
-      int c, f, old, last;
-      request(b, c, f, old, last);
-      s.tok += f;
-      s.page += last - old;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (b0 + i >= cut) break;
+      s.tok += f[i];
+      s.page += fresh_pages[i];
     }
     total_sh[0] = static_cast<int>(s.tok);
     total_sh[1] = static_cast<int>(s.page);
@@ -127,19 +134,22 @@ __global__ void __launch_bounds__(1024) step_maps_kernel(const dsa_step_maps_arg
   __syncthreads();
   const int tokens = total_sh[0], pages = total_sh[1];
   const bool writer = blockIdx.x == 0;
-  for (int b = b0; b < b1; ++b) {
-    int c, f, old, last;
-    request(b, c, f, old, last);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = b0 + i;
+    if (b >= P.B) break;
     const bool on = b < cut;
     run_tok[b] = on ? static_cast<int>(at.tok) : tokens;
     run_page[b] = on ? static_cast<int>(at.page) : pages;
-    if (on) {
-      at.tok += f;
-      at.page += last - old;
-    }
+    cached[b] = c[i];
+    held[b] = old[i];
     if (writer) {
       P.cu_tokens[b] = run_tok[b];
-      P.kv_len[b] = on ? c + f : c;
+      P.kv_len[b] = on ? c[i] + f[i] : c[i];
+    }
+    if (on) {
+      at.tok += f[i];
+      at.page += fresh_pages[i];
     }
   }
   if (tid == 0) {
@@ -158,8 +168,7 @@ __global__ void __launch_bounds__(1024) step_maps_kernel(const dsa_step_maps_arg
   const int stride = gridDim.x * threads;
   for (int p = blockIdx.x * threads + tid; p < pages; p += stride) {
     const int b = owner(run_page, P.B, p);
-    const int c = __ldg(P.cached + b);
-    const int j = c / P.block_size + (c % P.block_size != 0) + p - run_page[b];
+    const int j = held[b] + p - run_page[b];
     P.block_table[static_cast<size_t>(b) * P.max_blocks + j] = __ldg(P.free_pages + head + p);
   }
   const int pad_seq = tokens > 0 ? owner(run_tok, P.B, tokens - 1) : 0;
@@ -168,11 +177,10 @@ __global__ void __launch_bounds__(1024) step_maps_kernel(const dsa_step_maps_arg
     int64_t slot = -1;
     if (t < tokens) {
       seq = owner(run_tok, P.B, t);
-      const int c = __ldg(P.cached + seq);
-      pos = c + t - run_tok[seq];
-      const int j = pos / P.block_size, old = c / P.block_size + (c % P.block_size != 0);
-      const int page = j < old ? P.block_table[static_cast<size_t>(seq) * P.max_blocks + j]
-                               : __ldg(P.free_pages + head + run_page[seq] + j - old);
+      pos = cached[seq] + t - run_tok[seq];
+      const int j = pos / P.block_size;
+      const int page = j < held[seq] ? P.block_table[static_cast<size_t>(seq) * P.max_blocks + j]
+                                     : __ldg(P.free_pages + head + run_page[seq] + j - held[seq]);
       if (page >= 0)
         slot = static_cast<int64_t>(page) * P.block_size + pos % P.block_size;
       else
@@ -191,8 +199,9 @@ int launch_step_maps(const dsa_step_maps_args& a, cudaStream_t s) {
   uint32_t* err = error_word();
   if (!err) return DSA_ERR_CUDA;
   const int threads = a.B <= 256 ? 256 : 1024;
-  // every CTA forms the sums again, so none is started for less than two tokens a thread
-  const long long want = (static_cast<long long>(a.T) + 2 * threads - 1) / (2 * threads);
+  auto kern = a.B <= 1024 ? step_maps_kernel<1> : a.B <= 4096 ? step_maps_kernel<4> : step_maps_kernel<8>;
+  // every CTA forms the sums again, so none is started for less than a token a thread
+  const long long want = (static_cast<long long>(a.T) + threads - 1) / threads;
   const long long most = 2ll * sm_count() * (1024 / threads);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -200,17 +209,18 @@ int launch_step_maps(const dsa_step_maps_args& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most));
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = 2 * (static_cast<size_t>(a.B) + 1) * sizeof(int);
+  cfg.dynamicSmemBytes = (4 * static_cast<size_t>(a.B) + 2) * sizeof(int);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  static_assert(2 * (kMaxRequests + 1) * sizeof(int) <= 96 * 1024, "running sums");
+  static_assert(kMaxRequests == 8 * 1024, "requests of a CTA's threads");
+  static_assert((4 * kMaxRequests + 2) * sizeof(int) <= 200 * 1024, "running sums");
   if (cfg.dynamicSmemBytes > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(step_maps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(cfg.dynamicSmemBytes));
     if (e != cudaSuccess) return DSA_ERR_CUDA;
   }
-  return cuda_status(cudaLaunchKernelEx(&cfg, step_maps_kernel, a, err));
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, a, err));
 }
 
 }  // namespace dsa
