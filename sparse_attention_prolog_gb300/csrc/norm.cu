@@ -267,14 +267,15 @@ int launch_add_rmsnorm(const dsa_add_rmsnorm_args& a, cudaStream_t s) {
                    a.residual_out_stride * rsize % 16 == 0 && aligned(a.y, 16) && aligned(a.codes, 8);
   const int chunks = (a.D + 7) / 8;
   // Threads of a row.  Few rows: one chunk each, so that a row is one trip to memory.  Rows
-  // enough to fill the SMs: four chunks each, so that more rows are on their way while
-  // others reduce (16384 rows of 7168, y and codes: 225 us with one chunk each and a
-  // division a code, 165 with four and the codes as above).  Rows of up to 32 chunks: 8 to
-  // 32 threads, several rows a CTA.
+  // enough to fill the SMs: four chunks each, or two of shorter rows, so that more rows are
+  // on their way while others reduce (y and codes of 16384 rows: 7168 wide 225 us with one
+  // chunk each and a division a code, 165 with four and the codes as above; 2048 wide 59 and
+  // 51 with two, 1536 wide 45 and 40; 512 wide no difference).  Rows of up to 32 chunks: 8
+  // to 32 threads, several rows a CTA.
   const bool many = a.T > 4 * sm_count();
   int per = 1;
   while ((chunks + per - 1) / per > 1024) per *= 2;
-  if (many && vec && chunks > 256 && chunks <= 2048) per = 4;
+  if (many && vec && chunks > 64 && chunks <= 2048) per = chunks > 256 ? 4 : 2;
   int n = ((chunks + per - 1) / per + 31) / 32 * 32;
   if (n == 32) n = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
   const int rows = n <= 32 ? 256 / n : 1;
@@ -282,7 +283,7 @@ int launch_add_rmsnorm(const dsa_add_rmsnorm_args& a, cudaStream_t s) {
   const bool f = a.x_fp16, r = a.residual_fp32;
   auto kern = !vec ? (per == 1 ? pick<1, 1024, false>(f, r) : per == 2 ? pick<2, 1024, false>(f, r) : pick<4, 1024, false>(f, r))
               : per == 1 ? pick<1, 1024, true>(f, r)
-              : per == 2 ? pick<2, 1024, true>(f, r)
+              : per == 2 ? (n <= 128 ? pick<2, 128, true>(f, r) : pick<2, 1024, true>(f, r))
               : n <= 256 ? pick<4, 256, true>(f, r)
               : n <= 512 ? pick<4, 512, true>(f, r)
                          : pick<4, 1024, true>(f, r);
