@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -191,6 +192,11 @@ def load(path: str = LIB_PATH):
     lib.dsa_latent_attn.restype = c_int
     lib.dsa_add_rmsnorm.argtypes = [ctypes.POINTER(AddRmsnormArgs), c_ptr]
     lib.dsa_add_rmsnorm.restype = c_int
+    # the same entries for packed argument blocks
+    for name in ("step_maps", "add_rmsnorm"):
+        entry = lib["dsa_" + name]
+        entry.restype, entry.argtypes = c_int, [c_ptr, c_ptr]
+        setattr(lib, name + "_packed", entry)
     _lib = lib
     return lib
 
@@ -551,8 +557,13 @@ def dsa_latent_attn(args: LatentAttnArgs, workspace: Optional[torch.Tensor] = No
 
 
 # --------------------------------------------------------------- step maps
-def _plain(t: torch.Tensor, dtype, device: int) -> bool:
-    return t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+# The argument blocks of calls that are made as often as launches, packed (a ctypes struct costs 0.4 us more).
+_STEP_MAPS = struct.Struct("5i4x11P")       # StepMapsArgs
+_ADD_RMSNORM = struct.Struct("2if3i3q7P")   # AddRmsnormArgs
+
+
+def _unpackable(e) -> DSAError:
+    return DSAError(f"arguments: {e}")  # a size past 32 bits, a number that is none
 
 
 def dsa_step_maps(cached: torch.Tensor, fresh: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
@@ -563,17 +574,28 @@ def dsa_step_maps(cached: torch.Tensor, fresh: torch.Tensor, free_pages: torch.T
     [1] -> block_table int32 [B, max_blocks] (new pages entered), cu_tokens int32 [B + 1], kv_len int32 [B], counts
     int32 [3] (tokens, head after the step, requests served), seq_of_token and pos int32 [T], slot int64 [T] (see
     dsa.h)."""
-    device = _device("cached", cached)
-    n, i32, tokens, table = cached.shape, torch.int32, slot.shape, block_table.shape
-    # (one condition for the calls that pass, as a check of each tensor costs as much as a launch)
-    if not (len(n) == len(tokens) == 1 and fresh.shape == n and kv_len.shape == n and seq_of_token.shape == tokens
-            and pos.shape == tokens and len(table) == 2 and table[0] == n[0] and len(free_pages.shape) == 1
-            and cu_tokens.shape == (n[0] + 1,) and counts.shape == (3,) and slot.dtype is torch.int64
-            and -2 ** 31 <= block_size < 2 ** 31 and (free_head is None or _plain(free_head, i32, device) and free_head.shape == (1,))
-            and _plain(cached, i32, device) and _plain(fresh, i32, device) and _plain(free_pages, i32, device)
-            and _plain(block_table, i32, device) and _plain(cu_tokens, i32, device) and _plain(kv_len, i32, device)
-            and _plain(counts, i32, device) and _plain(seq_of_token, i32, device) and _plain(pos, i32, device)
-            and _plain(slot, torch.int64, device)):
+    device, n, tokens, table = cached.get_device(), cached.shape, slot.shape, block_table.shape
+    i32 = torch.int32
+    # (one condition for the calls that pass, written out: a function's call for each tensor costs as much as a launch)
+    if not (device >= 0 and device == torch._C._cuda_getDevice() and len(n) == len(tokens) == 1
+            and cached.dtype is i32 and cached.is_contiguous()
+            and fresh.shape == n and fresh.dtype is i32 and fresh.get_device() == device and fresh.is_contiguous()
+            and free_pages.dim() == 1 and free_pages.dtype is i32 and free_pages.get_device() == device
+            and free_pages.is_contiguous()
+            and len(table) == 2 and table[0] == n[0] and block_table.dtype is i32
+            and block_table.get_device() == device and block_table.is_contiguous()
+            and cu_tokens.shape == (n[0] + 1,) and cu_tokens.dtype is i32 and cu_tokens.get_device() == device
+            and cu_tokens.is_contiguous()
+            and kv_len.shape == n and kv_len.dtype is i32 and kv_len.get_device() == device and kv_len.is_contiguous()
+            and counts.shape == (3,) and counts.dtype is i32 and counts.get_device() == device and counts.is_contiguous()
+            and seq_of_token.shape == tokens and seq_of_token.dtype is i32 and seq_of_token.get_device() == device
+            and seq_of_token.is_contiguous()
+            and pos.shape == tokens and pos.dtype is i32 and pos.get_device() == device and pos.is_contiguous()
+            and slot.dtype is torch.int64 and slot.get_device() == device and slot.is_contiguous()
+            and -2 ** 31 <= block_size < 2 ** 31
+            and (free_head is None or free_head.shape == (1,) and free_head.dtype is i32
+                 and free_head.get_device() == device)):
+        device = _device("cached", cached)
         _fits_32(block_size=block_size)
         _tensor("cached", cached, i32, (None,), device)
         _tensor("slot", slot, torch.int64, (None,), device)
@@ -583,11 +605,17 @@ def dsa_step_maps(cached: torch.Tensor, fresh: torch.Tensor, free_pages: torch.T
                                ("pos", pos, tokens), ("free_head", free_head, (1,))):
             if t is not None:
                 _tensor(name, t, i32, shape, device)
-    args = StepMapsArgs(n[0], tokens[0], block_size, table[1], free_pages.shape[0], cached.data_ptr(), fresh.data_ptr(),
-                        free_pages.data_ptr(), None if free_head is None else free_head.data_ptr(),
-                        block_table.data_ptr(), cu_tokens.data_ptr(), kv_len.data_ptr(), counts.data_ptr(),
-                        seq_of_token.data_ptr(), pos.data_ptr(), slot.data_ptr())
-    _check(load().dsa_step_maps(ctypes.byref(args), _stream_of(device, stream)), "dsa_step_maps")
+    try:
+        args = _STEP_MAPS.pack(
+            n[0], tokens[0], block_size, table[1], free_pages.shape[0], cached.data_ptr(), fresh.data_ptr(),
+            free_pages.data_ptr(), 0 if free_head is None else free_head.data_ptr(), block_table.data_ptr(),
+            cu_tokens.data_ptr(), kv_len.data_ptr(), counts.data_ptr(), seq_of_token.data_ptr(), pos.data_ptr(),
+            slot.data_ptr())
+    except (struct.error, OverflowError) as e:
+        raise _unpackable(e) from None
+    code = load().step_maps_packed(args, _stream_of(device, stream))
+    if code:
+        _check(code, "dsa_step_maps")
 
 
 # --------------------------------------------------- residual and RMS norm
@@ -606,8 +634,9 @@ def dsa_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: 
     """x bf16 or fp16 [T, D], gamma fp32 [D], residual and residual_out bf16 or fp32 [T, D] (residual_out may be
     residual) -> residual_out = x + residual, and its RMS norm times gamma as y bf16 [T, D], as codes int8 [T, D] with
     scale fp32 [T], or both (see dsa.h).  x and the residuals may be rows of wider tensors."""
-    device = _device("x", x)
-    shape, kind, bf16 = x.shape, x.dtype, torch.bfloat16
+    device, shape, kind, bf16 = x.get_device(), x.shape, x.dtype, torch.bfloat16
+    if device < 0 or device != torch._C._cuda_getDevice():
+        _device("x", x)
     if len(shape) != 2 or kind is not bf16 and kind is not torch.float16:
         raise DSAError(f"x: {kind} {tuple(shape)}, expected bf16 or fp16 [T, D]")
     if (residual is None) != (residual_out is None) or (codes is None) != (scale is None):
@@ -618,19 +647,27 @@ def dsa_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: 
         r_kind = residual.dtype
         if r_kind is not bf16 and r_kind is not torch.float32:
             raise DSAError(f"residual: {r_kind}, expected bf16 or fp32")
-        strides = (strides[0], _rows("residual", residual, r_kind, shape, device),
+        r_stride = _rows("residual", residual, r_kind, shape, device)
+        strides = (strides[0], r_stride, r_stride if residual_out is residual else
                    _rows("residual_out", residual_out, r_kind, shape, device))
-    if not (gamma.shape == (D,) and _plain(gamma, torch.float32, device)):
+    if not (gamma.shape == (D,) and gamma.dtype is torch.float32 and gamma.get_device() == device
+            and gamma.is_contiguous()):
         _tensor("gamma", gamma, torch.float32, (D,), device)
-    if y is not None and not (y.shape == shape and _plain(y, bf16, device)):
+    if y is not None and not (y.dtype is bf16 and y.shape == shape and y.get_device() == device and y.is_contiguous()):
         _tensor("y", y, bf16, shape, device)
-    if codes is not None and not (codes.shape == shape and scale.shape == (T,) and _plain(codes, torch.int8, device)
-                                  and _plain(scale, torch.float32, device)):
+    if codes is not None and not (codes.dtype is torch.int8 and codes.shape == shape and codes.get_device() == device
+                                  and codes.is_contiguous() and scale.dtype is torch.float32 and scale.shape == (T,)
+                                  and scale.get_device() == device and scale.is_contiguous()):
         _tensor("codes", codes, torch.int8, shape, device)
         _tensor("scale", scale, torch.float32, (T,), device)
-    args = AddRmsnormArgs(T, D, eps, kind is not bf16, r_kind is not bf16, bool(round_scale), *strides, x.data_ptr(),
-                          None if residual is None else residual.data_ptr(),
-                          None if residual is None else residual_out.data_ptr(), gamma.data_ptr(),
-                          None if y is None else y.data_ptr(), None if codes is None else codes.data_ptr(),
-                          None if codes is None else scale.data_ptr())
-    _check(load().dsa_add_rmsnorm(ctypes.byref(args), _stream_of(device, stream)), "dsa_add_rmsnorm")
+    try:
+        args = _ADD_RMSNORM.pack(
+            T, D, eps, kind is not bf16, r_kind is not bf16, bool(round_scale), *strides, x.data_ptr(),
+            0 if residual is None else residual.data_ptr(), 0 if residual is None else residual_out.data_ptr(),
+            gamma.data_ptr(), 0 if y is None else y.data_ptr(), 0 if codes is None else codes.data_ptr(),
+            0 if codes is None else scale.data_ptr())
+    except (struct.error, OverflowError) as e:
+        raise _unpackable(e) from None
+    code = load().add_rmsnorm_packed(args, _stream_of(device, stream))
+    if code:
+        _check(code, "dsa_add_rmsnorm")

@@ -131,3 +131,15 @@ def test_the_most_requests(cuda_lib):
         got = np.stack([m.seq_of_token.cpu().numpy(), m.pos.cpu().numpy(), m.slot.cpu().numpy()], 1)
         assert np.array_equal(got[:k], want)
         assert bool((m.slot[k:] == -1).all()) and bool((m.pos[k:] == 0).all())
+
+
+def test_numbers_that_no_argument_block_holds(cuda_lib):
+    x, y = torch.zeros(2, 8, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 8, dtype=torch.bfloat16, device=DEV)
+    for eps in ("1e-6", None, -1.0, float("nan"), 1e300):
+        with pytest.raises(B.DSAError):
+            B.dsa_add_rmsnorm(x, torch.ones(8, device=DEV), eps, y=y)
+    i = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for size in (2 ** 31, 0, -1, 2.5):
+        with pytest.raises(B.DSAError):
+            B.dsa_step_maps(i, i, i, i.view(1, 1), size, i.new_zeros(2), i.clone(), i.new_zeros(3), i.clone(), i.clone(),
+                            torch.zeros(1, dtype=torch.int64, device=DEV))

@@ -37,6 +37,15 @@ def test_struct_layout_matches_header(lib, tmp_path):  # noqa: F811
             assert int(got[f"{cname}.{f}"]) == getattr(py, f).offset, f"{cname}.{f}"
 
 
+def test_packed_blocks_are_the_structs(lib):  # noqa: F811
+    a = B.StepMapsArgs(*range(1, 6), *[BASE + i * 64 for i in range(11)])
+    assert B._STEP_MAPS.pack(*[getattr(a, f) or 0 for f, _ in a._fields_]) == bytes(a)
+    a = B.AddRmsnormArgs(1, 2, 3.5, 1, 0, 1, 7, 8, 2 ** 40, *[BASE + i * 64 for i in range(7)])
+    assert B._ADD_RMSNORM.pack(*[getattr(a, f) or 0 for f, _ in a._fields_]) == bytes(a)
+    assert lib.step_maps_packed(B._STEP_MAPS.pack(-1, *[0] * 15), None) == INVALID
+    assert lib.step_maps_packed(B._STEP_MAPS.pack(*[0] * 16), None) == OK
+
+
 def _with(args, **kw):
     c = type(args).from_buffer_copy(args)
     for k, v in kw.items():
