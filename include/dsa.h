@@ -717,7 +717,8 @@ int dsa_latent_attn(const dsa_latent_attn_args* args, void* workspace, size_t wo
  * fp32 [D]; y bf16 [T, D] or NULL; codes int8 [T, D] and code_scale fp32 [T],
  * both NULL or both given; y or codes is given.  Strides are at least D.  Pointers
  * are aligned to their elements; rows that are all 16-byte aligned (codes: 8)
- * and D a multiple of 8 are read and written by vectors.  Nothing else overlaps.
+ * and D a multiple of 8 are read and written by vectors as they are, others by
+ * vectors and shifts (1.7 times as long).  Nothing else overlaps.
  * Supported: 1 <= D <= 32768, eps >= 0.  T = 0 is a no-op.  No workspace.
  * ---------------------------------------------------------------------- */
 typedef struct {

@@ -9,6 +9,7 @@
 // there are few.  16384 rows of 7168 with a bf16 residual: y 138 us (6.83 TB/s, a
 // copy's rate), y and codes 165 us (6.41 TB/s; the quantiser's instructions beside
 // the loads), with an fp32 residual 228 us (6.70 TB/s); 8 such rows 2.6 and 3.7 us.
+#include <algorithm>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -87,10 +88,98 @@ __device__ __forceinline__ uint2 codes_of(const float (&z)[8], float s, float r)
   return make_uint2(four(0), four(4));
 }
 
-// kVec: D and every row allow vectors of 8 elements; else element by element,
-// neighbouring threads at neighbouring elements (16384 rows of 7167: 548 us in place of
-// 165, for accesses of 64 bytes a warp; loads and stores interleaved 870, four chunks a
-// thread 790).
+// Rows whose arrays lie at any alignment.  A thread's 8 elements begin at e0 of the row
+// (which may be below 0 in its first chunk); elements outside [0, D) are neither read nor
+// written.  Inside a row the aligned vectors around the 8 are read and shifted; what they
+// have beside them is of the same row.
+__device__ __forceinline__ bool inside(int e0, int D) { return e0 >= 8 && e0 + 16 <= D; }
+template <int kWords>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[kWords], int words) {  // down by 0 to 3
+  if (words & 2)
+#pragma unroll
+    for (int i = 0; i < kWords - 2; ++i) w[i] = w[i + 2];
+  if (words & 1)
+#pragma unroll
+    for (int i = 0; i < kWords - 1; ++i) w[i] = w[i + 1];
+}
+__device__ __forceinline__ uint4 any_8x16(const uint16_t* row, int e0, int D) {
+  if (inside(e0, D)) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + e0);
+    const uint4* v = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+    const uint4 x = v[0];
+    if ((at & 15) == 0) return x;
+    const uint4 y = v[1];
+    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    shift_words(w, static_cast<int>(at >> 2) & 3);
+    if (at & 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = e0 + 2 * i;
+    w[i] = (e >= 0 && e < D ? row[e] : 0u) | (e + 1 >= 0 && e + 1 < D ? static_cast<uint32_t>(row[e + 1]) << 16 : 0u);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void any_8x32(const float* row, int e0, int D, float (&f)[8]) {
+  if (inside(e0, D)) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + e0);
+    const uint4* v = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+    const uint4 x = v[0], y = v[1], z = (at & 15) == 0 ? make_uint4(0, 0, 0, 0) : v[2];
+    uint32_t w[12] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+    shift_words(w, static_cast<int>(at >> 2) & 3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = e0 + i >= 0 && e0 + i < D ? row[e0 + i] : 0.f;
+}
+// 8 values of kBytes each, in words: by vectors where they are whole and aligned, 16-bit
+// ones by words where they are whole.
+template <int kBytes>
+__device__ __forceinline__ void put_8(void* row, int e0, int D, const uint32_t* w) {
+  uint8_t* at = static_cast<uint8_t*>(row) + static_cast<int64_t>(e0) * kBytes;
+  constexpr int kAlign = kBytes == 1 ? 8 : 16;
+  if (e0 >= 0 && e0 + 8 <= D && reinterpret_cast<uintptr_t>(at) % kAlign == 0) {
+    if (kBytes == 1) {
+      *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBytes / 2; ++i)
+        reinterpret_cast<uint4*>(at)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    return;
+  }
+  if (kBytes == 2 && e0 >= 0 && e0 + 8 <= D) {
+    if (reinterpret_cast<uintptr_t>(at) % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(at)[i] = w[i];
+    } else {
+      *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(w[0]);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(at + 2 + 4 * i) = __funnelshift_r(w[i], w[i + 1], 16);
+      *reinterpret_cast<uint16_t*>(at + 14) = static_cast<uint16_t>(w[3] >> 16);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (e0 + i < 0 || e0 + i >= D) continue;
+    if (kBytes == 1) at[i] = static_cast<uint8_t>(w[i / 4] >> (i % 4 * 8));
+    else if (kBytes == 2) reinterpret_cast<uint16_t*>(at)[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+    else reinterpret_cast<uint32_t*>(at)[i] = w[i];
+  }
+}
+
+// kVec: D and every row allow vectors of 8 elements.  Else chunks begin where the row of
+// y (or of the codes) is aligned, and what lies otherwise is shifted into place
+// (y and codes of 16384 rows of 7167: 277 us in place of 165, element by element 548; of
+// 7168 with rows of x and the residual 7169 apart 372, whose stores of the residual go by
+// words).
 template <int kChunks, int kThreads, bool kVec, bool kFp16, bool kRes32>
 __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const NormParams P) {
   __shared__ float part[2][32];
@@ -105,6 +194,11 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const NormParams 
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.x_stride;
   const uint8_t* rin = static_cast<const uint8_t*>(a.residual) + row * a.residual_stride * (kRes32 ? 4 : 2);
   uint8_t* rout = static_cast<uint8_t*>(a.residual_out) + row * a.residual_out_stride * (kRes32 ? 4 : 2);
+
+  // (of a row that needs the last chunk that the threads have, none is left for a skew)
+  const int skew = kVec || a.D + 7 > P.row_threads * kChunks * 8 ? 0
+                   : a.y ? static_cast<int>(reinterpret_cast<uintptr_t>(a.y + row * a.D) >> 1) & 7
+                         : static_cast<int>(reinterpret_cast<uintptr_t>(a.codes + row * a.D)) & 7;
 
   float h[kChunks][8];
   if (kVec) {
@@ -155,34 +249,47 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const NormParams 
       }
     }
   } else {
-    float b[kChunks][8];  // (every load before the first store, which the compiler cannot move it past)
+    uint4 xv[kChunks], rv[kChunks];
+    float rf[kRes32 ? kChunks : 1][8];
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k)
+    for (int k = 0; k < kChunks; ++k) {
+      const int e0 = (me + k * n) * 8 - skew;
+      xv[k] = any_8x16(x, e0, D);
+      if (res && !kRes32) rv[k] = any_8x16(reinterpret_cast<const uint16_t*>(rin), e0, D);
+      if (res && kRes32) any_8x32(reinterpret_cast<const float*>(rin), e0, D, rf[kRes32 ? k : 0]);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = me + (k * 8 + i) * n;
-        h[k][i] = b[k][i] = 0.f;
-        if (e >= D) continue;
-        h[k][i] = kFp16 ? __half2float(__ushort_as_half(x[e])) : __uint_as_float(static_cast<uint32_t>(x[e]) << 16);
-        if (res)
-          b[k][i] = kRes32 ? reinterpret_cast<const float*>(rin)[e]
-                           : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rin)[e]);
+    for (int k = 0; k < kChunks; ++k) {
+      const int e0 = (me + k * n) * 8 - skew;
+      const uint32_t w[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = pair_of<kFp16>(w[i]);
+        h[k][2 * i] = f.x;
+        h[k][2 * i + 1] = f.y;
       }
-    if (res) {
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k)
+      if (!res) continue;
+      if (kRes32) {
+        uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int e = me + (k * 8 + i) * n;
-          h[k][i] += b[k][i];
-          if (!kRes32) {
-            const __nv_bfloat16 s = __float2bfloat16_rn(h[k][i]);
-            h[k][i] = __bfloat162float(s);
-            if (e < D) reinterpret_cast<__nv_bfloat16*>(rout)[e] = s;
-          } else if (e < D) {
-            reinterpret_cast<float*>(rout)[e] = h[k][i];
-          }
+          h[k][i] += rf[kRes32 ? k : 0][i];
+          o[i] = __float_as_uint(h[k][i]);
         }
+        put_8<4>(rout, e0, D, o);
+      } else {
+        const uint32_t v[4] = {rv[k].x, rv[k].y, rv[k].z, rv[k].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = pair_of<false>(v[i]);
+          o[i] = bf16_pair(h[k][2 * i] + f.x, h[k][2 * i + 1] + f.y);
+          const float2 t = pair_of<false>(o[i]);
+          h[k][2 * i] = t.x;
+          h[k][2 * i + 1] = t.y;
+        }
+        put_8<2>(rout, e0, D, o);
+      }
     }
   }
 
@@ -212,14 +319,18 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const NormParams 
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max_abs_nan(top, h[k][i]);
     } else {
+      const int e0 = (me + k * n) * 8 - skew;
+      if (e0 >= D) continue;
+      float g[8];
+      any_8x32(a.gamma, e0, D, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int e = me + (k * 8 + i) * n;
-        if (e >= D) continue;
-        h[k][i] = h[k][i] * r * __ldg(a.gamma + e);
-        if (a.y) reinterpret_cast<__nv_bfloat16*>(a.y)[row * a.D + e] = __float2bfloat16_rn(h[k][i]);
-        top = max_abs_nan(top, h[k][i]);
+        h[k][i] = h[k][i] * r * g[i];
+        if (e0 + i >= 0 && e0 + i < D) top = max_abs_nan(top, h[k][i]);
       }
+      const uint32_t o[4] = {bf16_pair(h[k][0], h[k][1]), bf16_pair(h[k][2], h[k][3]), bf16_pair(h[k][4], h[k][5]),
+                             bf16_pair(h[k][6], h[k][7])};
+      if (a.y) put_8<2>(a.y + row * a.D, e0, D, o);
     }
   }
   if (a.codes == nullptr) return;
@@ -240,12 +351,11 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const NormParams 
       if (e >= D) continue;
       *reinterpret_cast<uint2*>(a.codes + row * a.D + e) = fine ? codes_of(h[k], s, inv_s) : make_uint2(0u, 0u);
     } else {
+      const int e0 = (me + k * n) * 8 - skew;
+      if (e0 >= D) continue;
       const uint2 c = fine ? codes_of(h[k], s, inv_s) : make_uint2(0u, 0u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = me + (k * 8 + i) * n;
-        if (e < D) a.codes[row * a.D + e] = static_cast<int8_t>((i < 4 ? c.x : c.y) >> (i % 4 * 8));
-      }
+      const uint32_t o[2] = {c.x, c.y};
+      put_8<1>(a.codes + row * a.D, e0, D, o);
     }
   }
 }
@@ -258,6 +368,15 @@ auto pick(bool fp16, bool res32) {
                        : add_rmsnorm_kernel<kChunks, kThreads, kVec, false, false>);
 }
 
+template <bool kVec>
+auto pick_size(int per, int n, bool f, bool r) {
+  return per == 1   ? pick<1, 1024, kVec>(f, r)
+         : per == 2 ? (n <= 160 ? pick<2, 160, kVec>(f, r) : pick<2, 1024, kVec>(f, r))
+         : n <= 256 ? pick<4, 256, kVec>(f, r)
+         : n <= 544 ? pick<4, 544, kVec>(f, r)
+                    : pick<4, 1024, kVec>(f, r);
+}
+
 }  // namespace
 
 int launch_add_rmsnorm(const dsa_add_rmsnorm_args& a, cudaStream_t s) {
@@ -265,7 +384,7 @@ int launch_add_rmsnorm(const dsa_add_rmsnorm_args& a, cudaStream_t s) {
   const bool vec = a.D % 8 == 0 && a.x_stride % 8 == 0 && aligned(a.x, 16) && aligned(a.gamma, 16) &&
                    aligned(a.residual, 16) && aligned(a.residual_out, 16) && a.residual_stride * rsize % 16 == 0 &&
                    a.residual_out_stride * rsize % 16 == 0 && aligned(a.y, 16) && aligned(a.codes, 8);
-  const int chunks = (a.D + 7) / 8;
+  const int chunks = vec ? a.D / 8 : std::min((a.D + 14) / 8, kMaxChunks * 1024);  // (room for a skew, but for the longest rows)
   // Threads of a row.  Few rows: one chunk each, so that a row is one trip to memory.  Rows
   // enough to fill the SMs: four chunks each, or two of shorter rows, so that more rows are
   // on their way while others reduce (y and codes of 16384 rows: 7168 wide 225 us with one
@@ -275,18 +394,13 @@ int launch_add_rmsnorm(const dsa_add_rmsnorm_args& a, cudaStream_t s) {
   const bool many = a.T > 4 * sm_count();
   int per = 1;
   while ((chunks + per - 1) / per > 1024) per *= 2;
-  if (many && vec && chunks > 64 && chunks <= 2048) per = chunks > 256 ? 4 : 2;
+  if (many && chunks > 64 && chunks <= 2048) per = chunks > 256 ? 4 : 2;
   int n = ((chunks + per - 1) / per + 31) / 32 * 32;
   if (n == 32) n = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
   const int rows = n <= 32 ? 256 / n : 1;
   NormParams P{a, n, 1.f / static_cast<float>(a.D)};
   const bool f = a.x_fp16, r = a.residual_fp32;
-  auto kern = !vec ? (per == 1 ? pick<1, 1024, false>(f, r) : per == 2 ? pick<2, 1024, false>(f, r) : pick<4, 1024, false>(f, r))
-              : per == 1 ? pick<1, 1024, true>(f, r)
-              : per == 2 ? (n <= 128 ? pick<2, 128, true>(f, r) : pick<2, 1024, true>(f, r))
-              : n <= 256 ? pick<4, 256, true>(f, r)
-              : n <= 512 ? pick<4, 512, true>(f, r)
-                         : pick<4, 1024, true>(f, r);
+  auto kern = vec ? pick_size<true>(per, n, f, r) : pick_size<false>(per, n, f, r);
   static_assert(kMaxChunks * 8 * 1024 >= 32768, "the longest row fits a CTA");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];

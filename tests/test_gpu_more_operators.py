@@ -86,6 +86,65 @@ def test_long_rows_of_any_alignment(D, off, x, res, cuda_lib):
     assert bool(((codes.double() * scale.double()[:, None] - z).abs() <= scale.double()[:, None] * (0.5 + 2.0 ** -9)).all())
 
 
+@pytest.mark.parametrize("D", [1, 7, 8, 9, 23, 24, 40, 41, 264, 517])
+@pytest.mark.parametrize("x_kind,r_kind", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float32),
+                                           (torch.bfloat16, None)])
+def test_every_alignment_of_every_array(D, x_kind, r_kind, cuda_lib):
+    """Rows of x, the residuals, gamma, y and the codes at offsets of their own, and what
+    lies before, between and behind the rows as it was.  Bounds as above; with the codes'
+    scale as the kernel gave it, a code is within half of one and 2^-9 (127 of the
+    value's 2^-18 and of the quotient's own roundings)."""
+    T = 5
+    rng = np.random.default_rng(D)
+    g = torch.Generator(device=DEV).manual_seed(D)
+
+    def rows(kind, off, stride, fill=None):
+        whole = torch.full((off + T * stride + 16,), 77, dtype=kind, device=DEV)
+        view = torch.as_strided(whole, (T, D), (stride, 1), off)
+        if fill is None:
+            view.copy_(torch.randn(T, D, device=DEV, generator=g))
+        return whole, view
+
+    def untouched(whole, off, stride):
+        mask = torch.ones_like(whole, dtype=torch.bool)
+        torch.as_strided(mask, (T, D), (stride, 1), off).zero_()
+        return bool((whole[mask] == 77).all())
+
+    for _ in range(24):
+        off = [int(v) for v in rng.integers(0, 17, 6)]
+        gap = [int(v) for v in rng.integers(0, 10, 3)]
+        _, x = rows(x_kind, off[0], D + gap[0])
+        gamma = torch.randn(D + off[5], device=DEV, generator=g)[off[5]:]
+        y_all, y = rows(torch.bfloat16, off[3], D, 0)
+        c_all, codes = rows(torch.int8, off[4], D, 0)
+        scale = torch.zeros(T, device=DEV)
+        res = out = None
+        h = x
+        if r_kind is not None:
+            r_all, res = rows(r_kind, off[1], D + gap[1])
+            in_place = rng.random() < 0.3
+            o_all, out = (r_all, res) if in_place else rows(r_kind, off[2], D + gap[2], 0)
+            h = (x.float() + res.float()).to(r_kind)
+        with_y, with_codes = rng.choice([True, True, False]), rng.choice([True, True, False])
+        if not with_y and not with_codes:
+            with_y = True
+        B.dsa_add_rmsnorm(x, gamma, 1e-5, res, out, y if with_y else None, codes if with_codes else None,
+                          scale if with_codes else None)
+        ok()
+        if r_kind is not None:
+            assert torch.equal(out, h)
+            assert untouched(o_all, *((off[1], D + gap[1]) if in_place else (off[2], D + gap[2])))
+        z = h.double()
+        z = z / (z.square().mean(1, keepdim=True) + 1e-5).sqrt() * gamma.double()
+        assert untouched(y_all, off[3], D) and untouched(c_all, off[4], D)
+        if with_y:
+            assert bool(((y.double() - z).abs() <= z.abs() * (2.0 ** -8 + 2.0 ** -18) + 2.0 ** -133).all())
+        if with_codes:
+            s = scale.double()[:, None]
+            assert bool(((scale.double() * 127 - z.abs().amax(1)).abs() <= z.abs().amax(1) * 2.0 ** -18).all())
+            assert bool(((codes.double() * s - z).abs() <= s * (0.5 + 2.0 ** -9)).all())
+
+
 def test_rows_past_4_gb(cuda_lib):
     """T * D past 2^31: the last rows' offsets need 64 bits."""
     T, D = 300_001, 7168
