@@ -804,7 +804,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto look_up = [&](int t) { return t < p.t1 && lane < boxes ? box_row(P, p, t * kTile + from, false) : 0; };
     while (ok && w.next(P, p)) {
       if (p.t0 >= p.t1) continue;
-      int row = look_up(p.t0);
       // q, into every slot of the ring, once the last block's is read and its K used up
       if (lane == 0) {
 #pragma unroll 1
@@ -824,6 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
+      int row = look_up(p.t0);  // (a trip to memory of its own, while q is on its way)
 #pragma unroll 1
       for (int u = 0; u < R::kQUnits; ++u)
         ok = ok && thread_wait<false>(&bars.qread[u], blocks & 1, P.err, abort_v);
