@@ -642,14 +642,18 @@ def dsa_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: 
     if (residual is None) != (residual_out is None) or (codes is None) != (scale is None):
         raise DSAError("dsa_add_rmsnorm: residual goes with residual_out, codes go with scale")
     T, D = shape
-    r_kind, strides = bf16, (_rows("x", x, kind, shape, device), 0, 0)
+    x_stride, inner = x.stride()
+    if inner != 1:
+        _tensor("x", x, kind, tuple(shape), device, last_dense=True)
+    if T == 1:  # (a single row has no stride of its own)
+        x_stride = max(D, x_stride)
+    r_kind, r_stride, out_stride = bf16, 0, 0
     if residual is not None:
         r_kind = residual.dtype
         if r_kind is not bf16 and r_kind is not torch.float32:
             raise DSAError(f"residual: {r_kind}, expected bf16 or fp32")
         r_stride = _rows("residual", residual, r_kind, shape, device)
-        strides = (strides[0], r_stride, r_stride if residual_out is residual else
-                   _rows("residual_out", residual_out, r_kind, shape, device))
+        out_stride = r_stride if residual_out is residual else _rows("residual_out", residual_out, r_kind, shape, device)
     if not (gamma.shape == (D,) and gamma.dtype is torch.float32 and gamma.get_device() == device
             and gamma.is_contiguous()):
         _tensor("gamma", gamma, torch.float32, (D,), device)
@@ -662,7 +666,7 @@ def dsa_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: 
         _tensor("scale", scale, torch.float32, (T,), device)
     try:
         args = _ADD_RMSNORM.pack(
-            T, D, eps, kind is not bf16, r_kind is not bf16, bool(round_scale), *strides, x.data_ptr(),
+            T, D, eps, kind is not bf16, r_kind is not bf16, bool(round_scale), x_stride, r_stride, out_stride, x.data_ptr(),
             0 if residual is None else residual.data_ptr(), 0 if residual is None else residual_out.data_ptr(),
             gamma.data_ptr(), 0 if y is None else y.data_ptr(), 0 if codes is None else codes.data_ptr(),
             0 if codes is None else scale.data_ptr())
