@@ -53,13 +53,16 @@ void* current_context() {
   }
   CUcontext c = nullptr;
   if (fn(&c) != CUDA_SUCCESS) return nullptr;
+  if (c == nullptr) {  // (a host thread's first call: cudaGetDevice binds no context, cudaSetDevice does)
+    int d = -1;
+    if (cudaGetDevice(&d) != cudaSuccess || cudaSetDevice(d) != cudaSuccess || fn(&c) != CUDA_SUCCESS) return nullptr;
+  }
   return c;
 }
 
 uint32_t* error_word() {
   const int d = current_device();
   if (d < 0) return nullptr;
-  // cudaGetDevice made the device's primary context current if none was.
   void* ctx = current_context();
   if (!ctx) return nullptr;
   std::lock_guard<std::mutex> lk(g_mu);

@@ -21,8 +21,9 @@ constexpr size_t kWaitLimitOffset = 8;
 // (resolved once per device and context).  nullptr if CUDA fails.
 uint32_t* error_word();
 
-// The calling thread's current CUDA context (a CUcontext), nullptr if none
-// or if the driver entry point is unavailable.
+// The calling thread's current CUDA context (a CUcontext): its device's primary
+// one where the thread has none yet.  nullptr if CUDA fails or the driver entry
+// point is unavailable.
 void* current_context();
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
