@@ -20,6 +20,7 @@ namespace dsa {
 namespace {
 
 constexpr int kMaxRequests = 8192;
+constexpr size_t shared_bytes(int requests) { return (4 * static_cast<size_t>(requests) + 2) * sizeof(int); }
 
 struct Sums {  // of a request's tokens and new pages
   long long tok, page;
@@ -207,7 +208,8 @@ int launch_step_maps(const dsa_step_maps_args& a, cudaStream_t s) {
   uint32_t* err = error_word();
   if (!err) return DSA_ERR_CUDA;
   const int threads = a.B <= 256 ? 256 : 1024;
-  auto kern = a.B <= 1024 ? step_maps_kernel<1> : a.B <= 4096 ? step_maps_kernel<4> : step_maps_kernel<8>;
+  const int each = a.B <= 1024 ? 1 : a.B <= 4096 ? 4 : 8;
+  auto kern = each == 1 ? step_maps_kernel<1> : each == 4 ? step_maps_kernel<4> : step_maps_kernel<8>;
   // every CTA forms the sums again, so none is started for less than a token a thread
   const long long want = (static_cast<long long>(a.T) + threads - 1) / threads;
   const long long most = 2ll * sm_count() * (1024 / threads);
@@ -217,17 +219,17 @@ int launch_step_maps(const dsa_step_maps_args& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most));
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = (4 * static_cast<size_t>(a.B) + 2) * sizeof(int);
+  cfg.dynamicSmemBytes = shared_bytes(a.B);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   static_assert(kMaxRequests == 8 * 1024, "requests of a CTA's threads");
-  static_assert((4 * kMaxRequests + 2) * sizeof(int) <= 200 * 1024, "running sums");
-  if (cfg.dynamicSmemBytes > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(cfg.dynamicSmemBytes));
-    if (e != cudaSuccess) return DSA_ERR_CUDA;
-  }
+  static_assert(shared_bytes(kMaxRequests) <= 200 * 1024 && shared_bytes(1024) <= 40 * 1024, "running sums");
+  // What the kernel may ever ask for, not what this call does: the limit is the kernel's, and
+  // a call of fewer requests in another host thread would lower it between here and the launch.
+  if (each > 1 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(shared_bytes(1024 * each))) != cudaSuccess)
+    return DSA_ERR_CUDA;
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, a, err));
 }
 

@@ -2,6 +2,7 @@
 call, and two threads' calls at once."""
 import threading
 
+import numpy as np
 import pytest
 import torch
 
@@ -45,3 +46,34 @@ def test_the_first_call_of_a_thread(cuda_lib):
     assert errors == [0]
     maps.check()
     attn.check()
+
+
+@pytest.mark.parametrize("sizes", [(4096, 2600), (8192, 4200), (1100, 4096, 2600, 8192)])
+def test_step_maps_of_different_sizes(sizes, cuda_lib):
+    """Requests whose running sums take different amounts of shared memory of the same
+    kernel (64 KB and 41, 128 and 66).  The packed blocks keep the threads inside the
+    library for most of the time."""
+    steps = []
+    for n in sizes:
+        rng = np.random.default_rng(n)
+        steps.append(Step(rng.integers(0, 64, n), np.arange(n) < 20, 64, 2, rng.permutation(2 * n), seed=n))
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    refused = [0] * len(sizes)
+
+    def loop(i):
+        s, d, stream = steps[i], steps[i].d, streams[i].cuda_stream
+        args = B._STEP_MAPS.pack(sizes[i], s.T, s.bs, 2, 2 * sizes[i], *[0 if d[k] is None else d[k].data_ptr() for k in (
+            "cached", "fresh", "free_pages", "free_head", "block_table", "cu_tokens", "kv_len", "counts", "seq_of_token",
+            "pos", "slot")])
+
+        def calls():
+            for _ in range(5000):
+                refused[i] += cuda_lib.step_maps_packed(args, stream) != 0
+        return calls
+
+    assert not at_once(*[loop(i) for i in range(len(sizes))])
+    torch.cuda.synchronize()
+    assert refused == [0] * len(sizes)
+    for s in steps:
+        s.check()
