@@ -615,7 +615,8 @@ int dsa_sparse_attn_kv4(const dsa_attn_kv4_args* args, void* workspace, size_t w
  * seq_of_token, pos int32 [T]; slot int64 [T].  free_head must not be an element
  * of counts, nor cached be kv_len: outputs are written while inputs are read,
  * so a loop keeps two of each and swaps them.
- * Supported: 1 <= B <= 8192, max_blocks * block_size < 2^31, block_size >= 1.
+ * Supported: 1 <= B <= 8192, max_blocks * block_size < 2^31, block_size >= 1,
+ * T and n_free at most 2^31 - 2^20.
  * T = 0 is allowed (no request with fresh > 0 is then served).  B = 0 is a
  * no-op.  No workspace.
  * ---------------------------------------------------------------------- */

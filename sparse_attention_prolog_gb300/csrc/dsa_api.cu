@@ -453,6 +453,9 @@ int dsa_step_maps(const dsa_step_maps_args* a, void* stream) {
   if (a->B == 0) return DSA_OK;
   if (a->block_size < 1 || a->max_blocks < 1) return DSA_ERR_INVALID_ARG;
   if (a->B > 8192 || static_cast<long long>(a->max_blocks) * a->block_size > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  // (an index of the kernel's loops goes past its end by up to a stride of 2 x SMs x 1024)
+  constexpr int kMost = INT32_MAX - (1 << 20) + 1;
+  if (a->T > kMost || a->n_free > kMost) return DSA_ERR_UNSUPPORTED;
   if (bad_ptr(a->cached, 4) || bad_ptr(a->fresh, 4) || bad_ptr(a->block_table, 4) || bad_ptr(a->cu_tokens, 4) ||
       bad_ptr(a->kv_len, 4) || bad_ptr(a->counts, 4) || !aligned(a->free_pages, 4) || !aligned(a->free_head, 4))
     return DSA_ERR_INVALID_ARG;

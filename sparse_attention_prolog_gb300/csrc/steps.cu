@@ -12,6 +12,7 @@
 // prompt chunks 4.6, 4096 with forty 8.2 (divisions by a page size that is a power
 // of two: 3.0, 4.8 and 9.1; lengths read again in every pass and two tokens a
 // thread as well: 3.6, 6.0 and 12.0).
+#include <algorithm>
 #include <cuda_runtime.h>
 #include "dsa_internal.h"
 #include "dsa_ptx.cuh"
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(1024) step_maps_kernel(const dsa_step_maps_arg
   }
   __syncthreads();
 
-  const int stride = gridDim.x * threads;
+  const int stride = gridDim.x * threads;  // (T and the pages end 2^20 below 2^31: the indexes stay inside)
   for (int p = blockIdx.x * threads + tid; p < pages; p += stride) {
     const int b = owner(run_page, P.B, p);
     const int j = held[b] + p - run_page[b];
@@ -212,7 +213,7 @@ int launch_step_maps(const dsa_step_maps_args& a, cudaStream_t s) {
   auto kern = each == 1 ? step_maps_kernel<1> : each == 4 ? step_maps_kernel<4> : step_maps_kernel<8>;
   // every CTA forms the sums again, so none is started for less than a token a thread
   const long long want = (static_cast<long long>(a.T) + threads - 1) / threads;
-  const long long most = 2ll * sm_count() * (1024 / threads);
+  const long long most = std::min(2ll * sm_count() * (1024 / threads), (1ll << 20) / threads);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
