@@ -672,7 +672,7 @@ int dsa_step_maps(const dsa_step_maps_args* args, void* stream);
  * (clamped) are recorded as DSA_ERR_DEVICE_DATA; rows of such a page read as
  * zeros.
  * Supported: T * H < 2^31 - 256, 1 <= H <= 1024, 1 <= B <= 65535, scale positive
- * and finite, cache_rows < 2^31, block_size 8, 16, 32 or a multiple of 64;
+ * and finite, cache_rows < 2^31, max_L <= 2^31 - 1024, block_size 8, 16, 32 or a multiple of 64;
  * q and kv 16-byte aligned, out 32-byte.
  * Workspace: dsa_latent_attn_workspace() bytes, 256-byte aligned, never in use
  * by two calls that may overlap; it need not be zeroed.

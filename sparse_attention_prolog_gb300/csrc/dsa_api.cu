@@ -478,7 +478,8 @@ static int check_latent_attn(const dsa_latent_attn_args* a) {
   if (a->B < 1 || a->H < 1 || a->max_L < 1 || a->cache_rows < 1 || !(a->scale > 0.f) || a->scale > FLT_MAX)
     return DSA_ERR_INVALID_ARG;
   if (a->cu_tokens == nullptr && (a->n_q < 1 || static_cast<long long>(a->B) * a->n_q != a->T)) return DSA_ERR_INVALID_ARG;
-  if (a->B > 65535 || a->H > 1024 || a->cache_rows > INT32_MAX ||
+  // (the kernel's row numbers go past a sequence's last one by a block and a tile)
+  if (a->B > 65535 || a->H > 1024 || a->cache_rows > INT32_MAX || a->max_L > INT32_MAX - 1023 ||
       static_cast<long long>(a->T) * a->H >= INT32_MAX - 255)
     return DSA_ERR_UNSUPPORTED;
   if (bad_ptr(a->q, 16) || bad_ptr(a->kv, 16) || bad_ptr(a->out, 32) || bad_ptr(a->kv_len, 4)) return DSA_ERR_INVALID_ARG;

@@ -17,3 +17,17 @@ def test_step_maps_leave_room_for_a_stride(lib, name):  # noqa: F811
         assert lib.dsa_step_maps(_with(a, **{name: n}), None) == UNSUPPORTED, n
     # (the largest is only looked at: something else is wrong with the call)
     assert lib.dsa_step_maps(_with(a, slot=a.slot + 4, **{name: 2 ** 31 - 2 ** 20}), None) == INVALID
+
+
+def test_latent_attn_leaves_room_behind_the_last_row(lib):  # noqa: F811
+    p = [BASE + i * FAR for i in range(8)]
+    a = B.LatentAttnArgs(8, 4, 2, 128, 64, 0.1, p[0], p[1], 4096, p[4], 64, 1, None, p[2], p[3], None, None)
+    for blocks, size in ((2 ** 25 - 1, 64), (2 ** 25 - 15, 64), (2 ** 27 - 63, 16)):
+        kw = {"max_blocks": blocks, "block_size": size, "max_L": blocks * size}
+        assert lib.dsa_latent_attn(_with(a, **kw), None, 0, None) == UNSUPPORTED, kw
+        assert lib.dsa_latent_attn_workspace(_with(a, **kw)) == 0
+    kw = {"max_blocks": 2 ** 25 - 16, "block_size": 64, "max_L": 2 ** 31 - 1024}
+    assert lib.dsa_latent_attn_workspace(_with(a, **kw)) > 0
+    # contiguous, where a sequence's rows are the cache's
+    kw = {"block_table": 0, "T": 1, "B": 1, "n_q": 1, "max_L": 2 ** 31 - 1023, "cache_rows": 2 ** 31 - 1}
+    assert lib.dsa_latent_attn(_with(a, **kw), None, 0, None) == UNSUPPORTED
