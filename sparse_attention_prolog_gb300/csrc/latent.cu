@@ -164,8 +164,11 @@ struct __align__(16) Shared {
   long long start_off;
   int start_b;
   uint32_t tmem;
-  int abort_flag;
+  int abort_flag;         // a wait has run out in this CTA, at the end in any of the cluster
   volatile int progress;  // tiles whose loads have begun, but one
+  // Copies begun, for a cluster that gives up: units of K and V by each lane, loads of q by
+  // each loader, tiles whose P a softmax warp has sent.
+  int k_begun[3][32], q_begun[3], v_begun[32], p_begun[8];
 };
 constexpr size_t kSmemBytes = kOffShared + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
@@ -373,10 +376,75 @@ __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Counts bytes on a barrier of this CTA as copied.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void st_global_v8(float* p, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// Of a cluster that gave up: waits until every copy into this CTA has landed, when all
+// threads of the cluster have stopped.  The lanes and warps that share a unit may have
+// stopped at different ones, and its barrier would never complete: what was not begun of a
+// unit that one of them did begin is counted here as landed.  (A copy into a slot was begun
+// after the slot's last use was complete, so only a ring's last units can be on their way,
+// and their phases are the barriers' current ones or just passed.)  Each wait has its limit.
+template <int NP>
+__device__ __noinline__ void settle(const LatentParams& P, Shared& sh, int role, uint32_t peer_p_begun) {
+  using R = Ring<NP>;
+  Bars& bars = sh.bars;
+  if (role == 0) {
+    const int boxes = R::kKRows / P.k_box;
+    constexpr int kBytes = R::kKBytes / R::kKLoaders;  // of a loader's part of a unit
+    int most = 0;
+    for (int w = 0; w < R::kKLoaders; ++w)
+      for (int l = 0; l < boxes; ++l) most = max(most, sh.k_begun[w][l]);
+    for (int i = max(0, most - R::kKSlots); i < most; ++i) {
+      uint64_t* full = &bars.kfull[i % R::kKSlots];
+      for (int w = 0; w < R::kKLoaders; ++w) {
+        if (sh.k_begun[w][0] <= i) mbar_arrive_expect_tx(full, kBytes);
+        for (int l = 0; l < boxes; ++l)
+          if (sh.k_begun[w][l] <= i) mbar_complete_tx(full, kBytes / boxes);
+      }
+      if (!mbar_drain(full, (i / R::kKSlots) & 1)) return;
+    }
+    constexpr int kMine = R::kQLoads / R::kKLoaders;  // loads of a block's q by a loader
+    for (int w = 0; w < R::kKLoaders; ++w)
+      for (int i = max(0, sh.q_begun[w] - kMine); i < sh.q_begun[w]; ++i)
+        if (!mbar_drain(&bars.qload[i % kMine * R::kKLoaders + w], (i / kMine) & 1)) return;
+  } else {
+    const int boxes = kTile / P.v_box, per = boxes / 2;
+    int most = 0;
+    for (int l = 0; l < boxes; ++l) most = max(most, sh.v_begun[l]);
+    for (int i = max(0, most - R::kVSlots); i < most; ++i) {
+      uint64_t* full = &bars.vfull[i % R::kVSlots];
+      const int group = i % R::kVUnits >> 1;  // whose lanes copy this unit
+      if (sh.v_begun[0] <= i) mbar_arrive_expect_tx(full, R::kVBytes);
+      for (int l = group * per; l < group * per + per; ++l)
+        if (sh.v_begun[l] <= i) mbar_complete_tx(full, R::kVBytes / per);
+      if (!mbar_drain(full, (i / R::kVSlots) & 1)) return;
+    }
+    for (int g = 0; g < 2; ++g) {  // P: half g of each tile, from four warps
+      int begun[4], tiles = 0;
+      for (int w = 0; w < 4; ++w) {
+        begun[w] = static_cast<int>(ld_cluster_u32(peer_p_begun + (4 * g + w) * 4));
+        tiles = max(tiles, begun[w]);
+      }
+      for (int t = max(0, tiles - 3); t < tiles; ++t) {  // (older halves have left their staging slots)
+        const int at = 2 * t + g;
+        uint64_t* full = &bars.pfull[at % kPSlots];
+        for (int w = 0; w < 4; ++w)
+          if (begun[w] <= t) mbar_complete_tx(full, p_bytes(at) / 4);
+        if (!mbar_drain(full, (at / kPSlots) & 1)) return;
+      }
+    }
+  }
 }
 
 template <int NP>
@@ -645,10 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_remote(peer_ffull);
       ++pieces;
     }
-    if (!ok) {  // copies on their way to the PV CTA land before either CTA leaves
-      const uint64_t since = globaltimer_ns();
-      while (globaltimer_ns() - since < 200000) __nanosleep(1000);
-    }
+    if (lane == 0) sh.p_begun[warp] = G;
+    tmem_st_wait();  // (q's, of a block that was given up)
   } else if (warp < 8) {
     // ------------------------------------------------ O: scaling and output
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -856,13 +922,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         row = next_row;
       }
     }
-    if (!ok && lane == 0) {  // copies in flight land before the CTA leaves
-      for (int i = max(0, issued - R::kKSlots); i < issued; ++i)
-        if (!mbar_drain(&bars.kfull[i % R::kKSlots], (i / R::kKSlots) & 1)) break;
-      constexpr int kMine = R::kQLoads / R::kKLoaders;  // loads of a block's q by this warp
-      for (int i = max(0, q_issued - kMine); i < q_issued; ++i)
-        if (!mbar_drain(&bars.qload[i % kMine * R::kKLoaders + which], (i / kMine) & 1)) break;
-    }
+    sh.k_begun[which][lane] = issued;
+    if (lane == 0) sh.q_begun[which] = q_issued;
   } else if (role == 1 && warp == kLoadWarp) {
     // ------------------------------------------------------------------ V
     const int boxes = kTile / P.v_box, per = boxes / 2;
@@ -903,10 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         row = next_row;
       }
     }
-    if (!ok && lane == 0) {
-      for (int i = max(0, issued - R::kVSlots); i < issued; ++i)
-        if (!mbar_drain(&bars.vfull[i % R::kVSlots], (i / R::kVSlots) & 1)) break;
-    }
+    sh.v_begun[lane] = issued;
   } else if (warp == kMmaWarp && side == 0 && elect_one()) {
     const uint16_t both = role == 0 ? 3 : 12;
     bool ok = true;
@@ -1084,7 +1142,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort_v)
+    for (int r = 0; r < 2 * NP; ++r) st_cluster_u32(mapa(smem_u32(&sh.abort_flag), r), 1);
   cluster_sync();  // no CTA leaves while another may still address it
+  if (*abort_v) {  // (the same in all of the cluster: nothing more is begun, what was begun lands)
+    if (tid == 0) settle<NP>(P, sh, role, mapa(smem_u32(sh.p_begun), side));
+    cluster_sync();
+  }
   if (warp == 0) free_tmem<NP>(tmem);
 }
 
