@@ -670,7 +670,8 @@ int dsa_step_maps(const dsa_step_maps_args* args, void* stream);
  * A page entry that is negative or names a page past cache_rows, a kv_len
  * outside [0, max_L] (clamped) and cu_tokens that decrease or leave [0, T]
  * (clamped) are recorded as DSA_ERR_DEVICE_DATA; rows of such a page read as
- * zeros.
+ * zeros, and of counts whose sequences overlap to more than T tokens in all none
+ * is attended.
  * Supported: T * H < 2^31 - 256, 1 <= H <= 1024, 1 <= B <= 65535, scale positive
  * and finite, cache_rows < 2^31, max_L <= 2^31 - 1024, block_size 8, 16, 32 or a multiple of 64;
  * q and kv 16-byte aligned, out 32-byte.

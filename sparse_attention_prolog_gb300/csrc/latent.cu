@@ -515,13 +515,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int each = (P.B + kThreads - 1) / kThreads;
   const int b0 = min(P.B, tid * each), b1 = min(P.B, b0 + each);
   long long mine = 0;
-  bool bad = false;
+  bool bad = false, falls = false;
   Walker<NP> w;
   for (w.b = b0; w.b < b1; ++w.b) {
     w.load(P);
     mine += static_cast<long long>(w.nb) * w.nt;
     if (P.cu != nullptr) {
       const int c0 = __ldg(P.cu + w.b), c1 = __ldg(P.cu + w.b + 1);
+      falls |= c1 < c0;
       bad |= c0 < 0 || c1 < c0 || c1 > P.T || (w.b == 0 && c0 != 0);
     }
     const int len = __ldg(P.kv_len + w.b);
@@ -536,12 +537,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (lane == 31) sh.scan[warp] = inc;
   tc_fence_before();
-  __syncthreads();
+  falls = __syncthreads_or(falls);
   tc_fence_after();
   long long before = inc - mine, total = 0;
   for (int i = 0; i < kThreads / 32; ++i) {
     if (i < warp) before += sh.scan[i];
     total += sh.scan[i];
+  }
+  if (falls) {  // counts that decrease: sequences may overlap, and be any multiple of T tokens
+    long long tokens = 0;
+    for (w.b = b0; w.b < b1; ++w.b) {
+      w.load(P);
+      tokens += w.n;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
+    __syncthreads();  // (the sums above have been read)
+    if (lane == 0) sh.scan[warp] = tokens;
+    __syncthreads();
+    tokens = 0;
+    for (int i = 0; i < kThreads / 32; ++i) tokens += sh.scan[i];
+    if (tokens > P.T) total = 0;
   }
   const long long active = max(1ll, min(static_cast<long long>(P.clusters), total / kMinShare));
   // stretch c begins at share c + min(c, rest)

@@ -59,3 +59,20 @@ def test_what_is_clamped_and_what_is_left(kv_len, cu, seen, cuda_lib):
     error, written = run(c, [300, 128], [0, 1, 3])
     assert error == 0 and written == [0, 1, 2]
     c.check()
+
+
+@pytest.mark.parametrize("n,cu", [
+    (6, [0, 5, 0, 5, 0, 5, 0]), (2, [5, 0, 5]), (3, [0, 4, 1, 4]), (1000, [0, 5] * 500 + [0]), (400, [0] * 399 + [5, 4]),
+])
+def test_counts_whose_sequences_overlap(n, cu, cuda_lib):
+    """Sequences of more tokens in all than there are rows (in garbage it may be any
+    multiple of them, and the call would last as much longer): none is attended.  Counts
+    that decrease without that are attended as they are clamped."""
+    c = Case([1] + [0] * (n - 1), [300] + [64] * (n - 1), 16, 64, pad=4, seed=8)
+    tokens = [max(0, b - a) for a, b in zip(cu, cu[1:])]
+    error, written = run(c, [300] + [64] * (n - 1), cu)
+    assert error == DATA_ERROR
+    assert written == ([] if sum(tokens) > c.T else list(range(5)))
+    error, written = run(c, [300] + [64] * (n - 1), [0] + [1] * n)
+    assert error == 0 and written == [0]
+    c.check()
