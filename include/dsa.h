@@ -673,8 +673,8 @@ int dsa_step_maps(const dsa_step_maps_args* args, void* stream);
  * zeros, and of counts whose sequences overlap to more than T tokens in all none
  * is attended.
  * Supported: T * H < 2^31 - 256, 1 <= H <= 1024, 1 <= B <= 65535, scale positive
- * and finite, cache_rows < 2^31, max_L <= 2^31 - 1024, block_size 8, 16, 32 or a multiple of 64;
- * q and kv 16-byte aligned, out 32-byte.
+ * and scale * log2(e) finite, cache_rows < 2^31, max_L <= 2^31 - 1024, block_size
+ * 8, 16, 32 or a multiple of 64; q and kv 16-byte aligned, out 32-byte.
  * Workspace: dsa_latent_attn_workspace() bytes, 256-byte aligned, never in use
  * by two calls that may overlap; it need not be zeroed.
  * ---------------------------------------------------------------------- */

@@ -135,6 +135,8 @@ using namespace dsa;
 
 namespace {
 
+constexpr float kLog2E = 1.4426950408889634f;
+
 bool bad_ptr(const void* p, size_t align) { return p == nullptr || !aligned(p, align); }
 
 int check_prolog(const dsa_prolog_args* a) {
@@ -475,7 +477,8 @@ int dsa_step_maps(const dsa_step_maps_args* a, void* stream) {
 static int check_latent_attn(const dsa_latent_attn_args* a) {
   if (!a || a->T < 0) return DSA_ERR_INVALID_ARG;
   if (a->T == 0) return DSA_OK;
-  if (a->B < 1 || a->H < 1 || a->max_L < 1 || a->cache_rows < 1 || !(a->scale > 0.f) || a->scale > FLT_MAX)
+  if (a->B < 1 || a->H < 1 || a->max_L < 1 || a->cache_rows < 1 || !(a->scale > 0.f) ||
+      a->scale * kLog2E > FLT_MAX)  // (the kernel takes the product)
     return DSA_ERR_INVALID_ARG;
   if (a->cu_tokens == nullptr && (a->n_q < 1 || static_cast<long long>(a->B) * a->n_q != a->T)) return DSA_ERR_INVALID_ARG;
   // (the kernel's row numbers go past a sequence's last one by a block and a tile)

@@ -31,3 +31,12 @@ def test_latent_attn_leaves_room_behind_the_last_row(lib):  # noqa: F811
     # contiguous, where a sequence's rows are the cache's
     kw = {"block_table": 0, "T": 1, "B": 1, "n_q": 1, "max_L": 2 ** 31 - 1023, "cache_rows": 2 ** 31 - 1}
     assert lib.dsa_latent_attn(_with(a, **kw), None, 0, None) == UNSUPPORTED
+
+
+def test_latent_attn_refuses_a_scale_that_overflows_in_base_2(lib):  # noqa: F811
+    p = [BASE + i * FAR for i in range(8)]
+    a = B.LatentAttnArgs(8, 4, 2, 128, 4096, 0.1, p[0], p[1], 4 * 4096, None, 0, 0, None, p[2], p[3], None, None)
+    for scale in (2.4e38, 3.4e38):  # times log2(e) past fp32's largest, 3.4028e38
+        assert lib.dsa_latent_attn(_with(a, scale=scale), None, 0, None) == INVALID
+        assert lib.dsa_latent_attn_workspace(_with(a, scale=scale)) == 0
+    assert lib.dsa_latent_attn_workspace(_with(a, scale=2.3e38)) > 0
