@@ -612,9 +612,10 @@ int dsa_sparse_attn_kv4(const dsa_attn_kv4_args* args, void* workspace, size_t w
  * Shapes: cached, fresh int32 [B]; free_pages int32 [n_free] (may be NULL if
  * n_free = 0), free_head int32 [1] or NULL; block_table int32 [B, max_blocks]
  * (in and out); cu_tokens int32 [B + 1]; kv_len int32 [B]; counts int32 [3];
- * seq_of_token, pos int32 [T]; slot int64 [T].  free_head must not be an element
- * of counts, nor cached be kv_len: outputs are written while inputs are read,
- * so a loop keeps two of each and swaps them.
+ * seq_of_token, pos int32 [T]; slot int64 [T].  Outputs are written while inputs
+ * are read, so no output may lie over an input or another output (free_head is
+ * no element of counts, cached is not kv_len): a loop keeps two of each and
+ * swaps them.
  * Supported: 1 <= B <= 8192, max_blocks * block_size < 2^31, block_size >= 1,
  * T and n_free at most 2^31 - 2^20.
  * T = 0 is allowed (no request with fresh > 0 is then served).  B = 0 is a

@@ -463,14 +463,22 @@ int dsa_step_maps(const dsa_step_maps_args* a, void* stream) {
     return DSA_ERR_INVALID_ARG;
   if (a->n_free > 0 && a->free_pages == nullptr) return DSA_ERR_INVALID_ARG;
   if (a->T > 0 && (bad_ptr(a->seq_of_token, 4) || bad_ptr(a->pos, 4) || bad_ptr(a->slot, 8))) return DSA_ERR_INVALID_ARG;
-  // inputs that are read while these outputs are written
-  const int32_t* outs[] = {a->cu_tokens, a->kv_len, a->counts};
-  const size_t lens[] = {static_cast<size_t>(a->B) + 1, static_cast<size_t>(a->B), 3};
-  auto meets = [](const int32_t* x, size_t n, const int32_t* y, size_t m) { return x && x < y + m && y < x + n; };
-  for (int i = 0; i < 3; ++i)
-    if (meets(a->cached, a->B, outs[i], lens[i]) || meets(a->fresh, a->B, outs[i], lens[i]) ||
-        meets(a->free_head, 1, outs[i], lens[i]))
-      return DSA_ERR_INVALID_ARG;
+  // Every CTA reads the inputs while others write: nothing written lies over them, or over another output.
+  struct Range {
+    uintptr_t at;
+    size_t bytes;
+  };
+  auto range = [](const void* p, size_t bytes) { return Range{reinterpret_cast<uintptr_t>(p), p ? bytes : 0}; };
+  const size_t b = static_cast<size_t>(a->B) * 4, t = static_cast<size_t>(a->T) * 4;
+  const Range all[] = {range(a->block_table, b * a->max_blocks), range(a->cu_tokens, b + 4), range(a->kv_len, b),
+                       range(a->counts, 12), range(a->seq_of_token, t), range(a->pos, t), range(a->slot, 2 * t),
+                       range(a->cached, b), range(a->fresh, b), range(a->free_pages, static_cast<size_t>(a->n_free) * 4),
+                       range(a->free_head, 4)};
+  constexpr int kWritten = 7, kAll = sizeof(all) / sizeof(all[0]);
+  for (int i = 0; i < kWritten; ++i)
+    for (int j = i + 1; j < kAll; ++j)
+      if (all[i].bytes && all[j].bytes && all[i].at < all[j].at + all[j].bytes && all[j].at < all[i].at + all[i].bytes)
+        return DSA_ERR_INVALID_ARG;
   return launch_step_maps(*a, static_cast<cudaStream_t>(stream));
 }
 

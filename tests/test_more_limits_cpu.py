@@ -40,3 +40,21 @@ def test_latent_attn_refuses_a_scale_that_overflows_in_base_2(lib):  # noqa: F81
         assert lib.dsa_latent_attn(_with(a, scale=scale), None, 0, None) == INVALID
         assert lib.dsa_latent_attn_workspace(_with(a, scale=scale)) == 0
     assert lib.dsa_latent_attn_workspace(_with(a, scale=2.3e38)) > 0
+
+
+def test_step_maps_refuse_arrays_over_one_another(lib):  # noqa: F811
+    """Every CTA reads the lengths and the list while the first ones write, so nothing
+    that is written may lie over what is read, or over what else is written."""
+    sizes = {"cached": 16, "fresh": 16, "free_pages": 400, "free_head": 4, "block_table": 4 * 4 * 32, "cu_tokens": 20,
+             "kv_len": 16, "counts": 12, "seq_of_token": 64, "pos": 64, "slot": 128}
+    written = list(sizes)[4:]
+    base = {f: BASE + i * FAR for i, f in enumerate(sizes)}
+    a = B.StepMapsArgs(4, 16, 64, 32, 100, *base.values())
+    call = lambda **kw: lib.dsa_step_maps(_with(a, **kw), None)  # noqa: E731
+    for out in written:
+        step = 8 if out == "slot" else 4
+        for other, n in sizes.items():
+            if other == out:
+                continue
+            for at in {0, -(-n // step) * step - step, -sizes[out] + step}:  # whole, its end, its beginning
+                assert call(**{out: base[other] + at}) == INVALID, (out, other, at)
