@@ -68,12 +68,19 @@ class PrologBuffers:
 class MlaBuffers:
     """Device copies of a workloads.MlaInputs plus the MLA Prolog's outputs
     (q_lora, q_lora_scale, q) and a latent cache of ``cache_rows`` rows.  x, pos
-    and slot may be given as device tensors (another kernel's outputs)."""
+    and slot may be given as device tensors (another kernel's outputs): bf16 [T,
+    D_x], int32 [T] and int64 [T]."""
 
     def __init__(self, p, device, cache_rows: int, kv_fill: float = 0.0, kv_cache: torch.Tensor = None,
                  x: torch.Tensor = None, pos: torch.Tensor = None, slot: torch.Tensor = None):
         self.p = p
         d = device
+        for name, t, dtype, shape in (("x", x, torch.bfloat16, (p.T, p.D_x)), ("pos", pos, torch.int32, (p.T,)),
+                                      ("slot", slot, torch.int64, (p.T,))):
+            if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                                      and t.device.type == torch.device(d).type):
+                raise B.DSAError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}; expected "
+                                 f"contiguous {dtype} {shape} on {d}")
         self.x = to_dev(p.x, d, "bf16") if x is None else x
         self.w_dq = to_dev(p.w_dq, d, "bf16")
         self.gamma_q = to_dev(p.gamma_q, d)
