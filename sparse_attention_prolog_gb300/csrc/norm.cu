@@ -368,10 +368,16 @@ auto pick(bool fp16, bool res32) {
                        : add_rmsnorm_kernel<kChunks, kThreads, kVec, false, false>);
 }
 
+// The instance for n threads of `per` chunks each.  Its bound on the threads leaves it as
+// many registers as they may have (1024: 64 each, 544: 120, fewer: 255): an instance is for
+// the thread counts that need no lower bound.  Two chunks each: up to 128 threads (rows of
+// up to 256 chunks, where there are many) or 513 and more (rows of over 1024 chunks).  Four:
+// 65 to 512 threads (many rows of up to 2048 chunks), or 513 and more (longer rows; up to
+// 544 takes in an unaligned row of 16384, which has a chunk more for its skew).
 template <bool kVec>
 auto pick_size(int per, int n, bool f, bool r) {
   return per == 1   ? pick<1, 1024, kVec>(f, r)
-         : per == 2 ? (n <= 160 ? pick<2, 160, kVec>(f, r) : pick<2, 1024, kVec>(f, r))
+         : per == 2 ? (n <= 128 ? pick<2, 128, kVec>(f, r) : pick<2, 1024, kVec>(f, r))
          : n <= 256 ? pick<4, 256, kVec>(f, r)
          : n <= 544 ? pick<4, 544, kVec>(f, r)
                     : pick<4, 1024, kVec>(f, r);
