@@ -28,6 +28,11 @@ void* current_context();
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Dynamic shared memory of a CTA with opt-in, less the kernel's static one.  A kernel's
+// limit is set to a size that no call exceeds, the same at every call: it is the kernel's,
+// not the call's, and a call of another host thread would lower it before this one's launch.
+constexpr size_t kSmemPerBlock = 232448;  // 227 KB, sm_103a
+
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Number of SMs of the current device (cached per device).

@@ -767,8 +767,6 @@ size_t indexer_smem(const IdxParams& P, int DI) {
   return n;
 }
 
-constexpr size_t kSmemPerBlock = 232448;  // 227 KB opt-in limit of sm_103a
-
 template <int HI, int DI>
 cudaError_t launch_hi(const IdxParams& P, const CUtensorMap& tmap, cudaStream_t s, bool& too_big) {
   const size_t smem = indexer_smem(P, DI);
@@ -777,7 +775,8 @@ cudaError_t launch_hi(const IdxParams& P, const CUtensorMap& tmap, cudaStream_t 
   if (e != cudaSuccess) return e;
   too_big = smem + fa.sharedSizeBytes > kSmemPerBlock;
   if (too_big) return cudaSuccess;
-  e = cudaFuncSetAttribute(indexer_kernel<HI, DI>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = cudaFuncSetAttribute(indexer_kernel<HI, DI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmemPerBlock - fa.sharedSizeBytes));
   if (e != cudaSuccess) return e;
   const long long items = static_cast<long long>(P.n_groups) * P.n_tiles;
   const int grid = static_cast<int>(items < sm_count() ? items : sm_count());

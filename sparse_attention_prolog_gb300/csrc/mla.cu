@@ -60,6 +60,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // ------------------------------------------------------------------ down
 constexpr int kDownThreads = 128;
 constexpr int kDownStages = 4;
+constexpr int kMaxKq = 2048;  // the largest K_q that the API takes
 constexpr uint32_t kDownAtomW = 128 * 128;  // [128 rows][64 bf16]
 
 struct DownParams {
@@ -506,8 +507,9 @@ int launch_mla(const dsa_mla_prolog_args& a, void* ws, cudaStream_t stream) {
     using L = decltype(layout);
     const int ns8 = L::stages(a.K_q, budget);
     cu.dynamicSmemBytes = L::smem(a.K_q, ns8);
+    // (the most that any K_q takes: see kSmemPerBlock)
     cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(cu.dynamicSmemBytes));
+                                         static_cast<int>(std::max(budget, L::smem(kMaxKq, 2))));
     if (r == cudaSuccess)
       r = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     return r == cudaSuccess ? cudaLaunchKernelEx(&cu, kern, maps, job, ns8) : r;

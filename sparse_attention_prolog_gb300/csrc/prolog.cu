@@ -516,7 +516,6 @@ int launch_prolog(const dsa_prolog_args& a, void* ws, cudaStream_t stream) {
                                                         : (const void*)prolog_kernel<2, 32>);
   cudaFuncAttributes fa{};
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return DSA_ERR_CUDA;
-  constexpr size_t kSmemPerBlock = 232448;  // 227 KB opt-in limit of sm_103a
   const size_t per_atom = 2 * kKwAtom + static_cast<size_t>(nx) * 128;
   const int fit_atoms = static_cast<int>((kSmemPerBlock - fa.sharedSizeBytes - 1024) / per_atom);
   const int atoms = a.D_x / 64;
@@ -581,7 +580,8 @@ int launch_prolog(const dsa_prolog_args& a, void* ws, cudaStream_t stream) {
   cfg.numAttrs = 2;
   cudaError_t e;
   auto go = [&](auto kern) {
-    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kSmemPerBlock - fa.sharedSizeBytes));
     return r == cudaSuccess ? cudaLaunchKernelEx(&cfg, kern, P, tm_wk, tm_wp, tm_x) : r;
   };
   if (a.d_I == 128) {

@@ -250,8 +250,8 @@ int launch_int8_gemm_wt(const dsa_int8_gemm_args& a, cudaStream_t s) {
 int launch_act_quant(const dsa_act_quant_args& a, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(a.N) * 2;
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(act_quant_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (smem > 48 * 1024)  // (the longest row's: see kSmemPerBlock)
+    e = cudaFuncSetAttribute(act_quant_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 32768);
   if (e != cudaSuccess) return cuda_status(e);
   act_quant_kernel<<<a.M, kQThreads, smem, s>>>(a.x, a.y, a.scale, a.N, a.round_scale);
   return cuda_status(cudaGetLastError());
