@@ -606,8 +606,8 @@ int dsa_sparse_attn_kv4(const dsa_attn_kv4_args* args, void* workspace, size_t w
  * tokens pass T, its new pages pass the list, its length passes max_blocks *
  * block_size, or a length is negative) is recorded as DSA_ERR_DEVICE_DATA, and
  * neither it nor any after it is served: they get no token and no page, and
- * kv_len = cached.  A negative free_head serves none.  A token whose page entry
- * is negative gets slot -1, recorded likewise.
+ * kv_len = cached.  A free_head that is negative or past the list serves none.  A
+ * token whose page entry is negative gets slot -1, recorded likewise.
  *
  * Shapes: cached, fresh int32 [B]; free_pages int32 [n_free] (may be NULL if
  * n_free = 0), free_head int32 [1] or NULL; block_table int32 [B, max_blocks]
@@ -721,7 +721,8 @@ int dsa_latent_attn(const dsa_latent_attn_args* args, void* workspace, size_t wo
  * both NULL or both given; y or codes is given.  Strides are at least D.  Pointers
  * are aligned to their elements; rows that are all 16-byte aligned (codes: 8)
  * and D a multiple of 8 are read and written by vectors as they are, others by
- * vectors and shifts (1.7 times as long).  Nothing else overlaps.
+ * vectors and shifts (1.7 times as long for dense rows, 2.3 times where the
+ * residual's rows lie at other alignments than y's).  Nothing else overlaps.
  * Supported: 1 <= D <= 32768, eps >= 0.  T = 0 is a no-op.  No workspace.
  * ---------------------------------------------------------------------- */
 typedef struct {

@@ -24,11 +24,11 @@
 //       at a block's end.
 //
 // With NP = 1, a warp of the PV CTA fetches the rows of later tiles into the L2: the K ring
-// is one tile, and HBM's latency beside the products is longer than a tile's time (542 ->
-// 502 us for 32 sequences of 4096 to 131072 rows; four tiles ahead 537, and from the QK CTA,
+// is one tile, and HBM's latency beside the products is longer than a tile's time (541 ->
+// 504 us for 32 sequences of 4096 to 131072 rows; four tiles ahead 537, and from the QK CTA,
 // whose own copies then wait behind the fetches, it costs more than it gives).  It begins
-// when the first rows of V are there, or q would wait behind it (one token at 128K 61 -> 59
-// us; and two tiles ahead in place of three 57).
+// when the first rows of V are there, or q would wait behind it (one token at 128K 58.5 ->
+// 57.3 us; three tiles ahead in place of two 58.7, four 61.2).
 //
 // What bounds such a kernel first is not a unit but the single threads that feed them:
 // every instruction of theirs takes some five clocks, so their loops are unrolled over a
@@ -44,8 +44,8 @@
 // NP = 2, whose rings are two tiles, takes 1.3 to 1.4 (its products alone 1.1).
 //
 // A block's q comes through the K ring, which it fills, and goes on into tensor memory: one
-// trip for all of it (through the three staging slots of P, three trips: one token over 1000
-// rows 22.4 us in place of 21.3).
+// trip for all of it (through the three staging slots of P, three trips, which cost one token
+// over 1000 rows 1 us).
 //
 // NP = 1: a cluster is one QK and one PV CTA.  NP = 2: two of each, for sequences
 // of more than 128 rows: the two QK CTAs run one MMA of M = 256 (cta_group::2), each
@@ -74,9 +74,9 @@ constexpr int kHalfBytes = 128 * 128;            // 64 columns of a P tile
 constexpr uint32_t kTmemS = 256;                 // QK: q's latent part in columns [0, 256), then two S buffers
 constexpr int kThreads = 384;                    // 8 softmax / output warps, a loader, an MMA issuer, two for news
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kRelayWarp = 10, kNewsWarp = 11;
-// A cluster's stretch has at least this many tiles.  (One token over 1000 rows: 22 us, with
-// at least six 31; with one, a call that needs no merge may get it: 4 heads over 256 rows 17
-// us in place of 16.)
+// A cluster's stretch has at least this many tiles.  (One token over 1000 rows: 22.9 us, with
+// at least six 29.3; with one, a call that needs no merge may get it: 4 heads over 256 rows
+// 16.0 us in place of 14.9.)
 constexpr int kMinShare = 2;
 constexpr int kMaxClusters = 256;
 
@@ -200,6 +200,8 @@ struct Walker {
       n = P.n_q;
     }
     len = min(max(__ldg(P.kv_len + b), 0), P.max_L);
+    // (the sequence's tiles for each of its blocks, though the first ones of a prompt see fewer: what
+    // that leaves idle is little behind a long context, a third and more where a prompt begins one)
     nt = max(1, (len - 1) / kTile + 1) + P.start;  // so many empty ones in front
     nb = (n * P.H + kBlock - 1) / kBlock;
   }
@@ -396,11 +398,11 @@ __device__ __forceinline__ void st_global_v8(float* p, const uint32_t* r) {
 // after the slot's last use was complete, so only a ring's last units can be on their way,
 // and their phases are the barriers' current ones or just passed.)  Each wait has its limit.
 template <int NP>
-__device__ __noinline__ void settle(const LatentParams& P, Shared& sh, int role, uint32_t peer_p_begun) {
+__device__ __noinline__ void settle(Shared& sh, int role, int k_box, int v_box, uint32_t peer_p_begun) {
   using R = Ring<NP>;
   Bars& bars = sh.bars;
   if (role == 0) {
-    const int boxes = R::kKRows / P.k_box;
+    const int boxes = R::kKRows / k_box;
     constexpr int kBytes = R::kKBytes / R::kKLoaders;  // of a loader's part of a unit
     int most = 0;
     for (int w = 0; w < R::kKLoaders; ++w)
@@ -419,7 +421,7 @@ __device__ __noinline__ void settle(const LatentParams& P, Shared& sh, int role,
       for (int i = max(0, sh.q_begun[w] - kMine); i < sh.q_begun[w]; ++i)
         if (!mbar_drain(&bars.qload[i % kMine * R::kKLoaders + w], (i / kMine) & 1)) return;
   } else {
-    const int boxes = kTile / P.v_box, per = boxes / 2;
+    const int boxes = kTile / v_box, per = boxes / 2;
     int most = 0;
     for (int l = 0; l < boxes; ++l) most = max(most, sh.v_begun[l]);
     for (int i = max(0, most - R::kVSlots); i < most; ++i) {
@@ -729,8 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_remote(peer_ffull);
       ++pieces;
     }
+    if (!ok) tmem_st_wait();  // (q's, of a block that was given up)
     if (lane == 0) sh.p_begun[warp] = G;
-    tmem_st_wait();  // (q's, of a block that was given up)
   } else if (warp < 8) {
     // ------------------------------------------------ O: scaling and output
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -823,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (in_block < p.rows && half == 0 && P.lse != nullptr) P.lse[orow] = lse2 * 0.69314718055994531f;
-        // (stores of 32 bytes a lane, whole sectors: 8 x 64 tokens over 1000 rows 162 us, with 16
+        // (stores of 32 bytes a lane, whole sectors: 8 x 64 tokens over 1000 rows 163 us, with 16
         // bytes 174; without any 147)
         __nv_bfloat16* o = P.out + orow * kDv;
 #pragma unroll 1
@@ -1162,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = 0; r < 2 * NP; ++r) st_cluster_u32(mapa(smem_u32(&sh.abort_flag), r), 1);
   cluster_sync();  // no CTA leaves while another may still address it
   if (*abort_v) {  // (the same in all of the cluster: nothing more is begun, what was begun lands)
-    if (tid == 0) settle<NP>(P, sh, role, mapa(smem_u32(sh.p_begun), side));
+    if (tid == 0) settle<NP>(sh, role, P.k_box, P.v_box, mapa(smem_u32(sh.p_begun), side));
     cluster_sync();
   }
   if (warp == 0) free_tmem<NP>(tmem);
@@ -1173,10 +1175,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rows (a lane each) x 8 columns of a block.  Of a block of few parts a warp takes an item
 // with all of them, four in flight at a time; of one of many (one long sequence), eight
 // warps take an eighth each of the parts of 4 columns, ten in flight, and their sums meet
-// in shared memory.  (2 x 2 tokens at 64K, 19 parts a block: 65 us a call the first way, 73
-// the second; a bound of 32 parts or more makes 16 heads over 700 to 9000 rows 87 us in
-// place of 81, a bound of 0 112.)
-constexpr int kMergeWarps = 8, kFewParts = 24;
+// in shared memory.  (At 64K rows: 3 tokens, 25 or 26 parts a block, 73.4 us a call the first
+// way, 76.7 the second; 2 x 2 tokens, 18 parts, 64.8 and 71.9; 2 tokens, 38 parts, 63.2 and
+// 59.8; 1 x 2 tokens, 36 parts, 52.9 and 50.7.  16 heads over 700 to 9000 rows, two or three
+// parts: 82 and 115.)
+constexpr int kMergeWarps = 8, kFewParts = 32;
 
 template <int kCols>
 struct Merged {
@@ -1335,9 +1338,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const __
 
 // Whether a call's blocks are 256 rows (NP = 2): where a sequence has more than 128 rows
 // on average.  Two blocks of 128 rows read the cache twice, a block of 256 with 128 rows to
-// fill it wastes half of its products.  (4 x 2 tokens of 128 heads at 64K 103 us paired, 137
-// not; 1024 new tokens 1285 and 1664; 19 sequences of 144 rows at 32K 216 and 263; of 128
-// rows 213 and 158.)
+// fill it wastes half of its products.  (4 x 2 tokens of 128 heads at 64K 99 us paired, 134
+// not; 1024 new tokens 1249 and 1744; 19 sequences of 144 rows at 32K 209 and 273; of 128
+// rows 208 and 157.)
 bool paired(const dsa_latent_attn_args& a) { return static_cast<long long>(a.T) * a.H > 128ll * a.B; }
 
 template <int NP>
@@ -1386,9 +1389,10 @@ long long most_blocks(const dsa_latent_attn_args& a) {
 }
 
 // What a block costs beside its tiles (its q, its output, the pipeline's start), in tiles:
-// stretches are equal with it counted in front of each block.  (Without: 16 heads over 700
-// to 9000 rows 88 us in place of 81, 4 x 2 tokens at 64K 107 in place of 102.)  A single
-// block begins but once in any stretch.
+// stretches are equal with it counted in front of each block.  (Without: 4 x 2 tokens at 64K
+// 104 us in place of 99, 2 x 2 tokens 67.7 in place of 64.7, 8 x 64 tokens over 1000 rows 166
+// in place of 163, 16 heads over 700 to 9000 rows 82.2 in place of 81.2.)  A single block
+// begins but once in any stretch.
 int start_tiles(const dsa_latent_attn_args& a) { return most_blocks(a) == 1 ? 0 : paired(a) ? 6 : 3; }
 
 // Clusters of a call: as many as the device holds, but no more than the most tiles

@@ -8,7 +8,8 @@
 // rows enough and by the launch, one trip to memory and the two reductions when
 // there are few.  16384 rows of 7168 with a bf16 residual: y 138 us (6.83 TB/s, a
 // copy's rate), y and codes 165 us (6.41 TB/s; the quantiser's instructions beside
-// the loads), with an fp32 residual 228 us (6.70 TB/s); 8 such rows 2.6 and 3.7 us.
+// the loads), both with an fp32 residual 228 us (6.70 TB/s); 8 such rows 2.4 to 2.8
+// and 3.9 us.
 #include <algorithm>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>

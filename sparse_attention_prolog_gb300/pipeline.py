@@ -75,14 +75,14 @@ class MlaBuffers:
                  x: torch.Tensor = None, pos: torch.Tensor = None, slot: torch.Tensor = None):
         self.p = p
         d = device
+        self.w_dq = to_dev(p.w_dq, d, "bf16")
         for name, t, dtype, shape in (("x", x, torch.bfloat16, (p.T, p.D_x)), ("pos", pos, torch.int32, (p.T,)),
                                       ("slot", slot, torch.int64, (p.T,))):
             if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                                      and t.device.type == torch.device(d).type):
+                                      and t.device == self.w_dq.device):
                 raise B.DSAError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}; expected "
-                                 f"contiguous {dtype} {shape} on {d}")
+                                 f"contiguous {dtype} {shape} on {self.w_dq.device}")
         self.x = to_dev(p.x, d, "bf16") if x is None else x
-        self.w_dq = to_dev(p.w_dq, d, "bf16")
         self.gamma_q = to_dev(p.gamma_q, d)
         self.w_dkv = to_dev(p.w_dkv, d, "bf16")
         self.gamma_kv = to_dev(p.gamma_kv, d)
