@@ -248,7 +248,10 @@ class StepMaps:
     take: block_table, cu_tokens, kv_len, seq_of_token, pos and slot (T rows; see
     dsa_step_maps), counts (tokens, free pages taken so far, requests served).
     A step reads one set of lengths and writes the other, and sets its free head
-    from its counts, so a captured run() has to be of an even number of steps."""
+    from its counts, so a captured run() has to be of an even number of steps.
+    Steps only take pages.  Between two steps a caller ends a request b of k pages
+    by writing them back in front of the head (h = counts[step][1]: free_pages[h -
+    k:h] = block_table[b, :k], then h - k into its place) and 0 into kv_len[b]."""
 
     def __init__(self, B_: int, T: int, block_size: int, max_blocks: int, free_pages: torch.Tensor):
         d = free_pages.device
